@@ -30,6 +30,7 @@ __all__ = [
     "bw_quantize_colwise_padded", "bw_grouped_gemm_fwd", "bw_grouped_gemm_dgrad",
     "bw_grouped_gemm_wgrad", "bw_quantize_1x128_pow2", "bw_quantize_128x128_pow2",
     "bw_quantize_colwise_padded_pow2", "bw_quantize_dual_padded",
+    "moe_route", "moe_experts", "moe_experts_workspace_size", "MOE_SYNC_WORDS", "lora_add", "lora_add_workspace_size",
 ]
 
 ELEM = {"e2m1": 1, "e4m3": 2}
@@ -100,6 +101,7 @@ def _ld(t: torch.Tensor, row_elems: int) -> int:
 
 
 _status = {}
+_ERR_TIMEOUT = 8  # MXG_ERR_TIMEOUT
 
 
 def status_tensor(device) -> torch.Tensor:
@@ -115,6 +117,8 @@ def check_status(status: torch.Tensor | None = None, device=None) -> int:
     """Synchronise, read and clear the device status word; raise on error."""
     st = status if status is not None else status_tensor(device or torch.cuda.current_device())
     code = _lib.load().mxg_check_status(_ptr(st), _stream(st.device))
+    if code == _ERR_TIMEOUT:
+        _moe_sync.clear()  # an abandoned moe_experts call may have left its words non-zero
     _ok(code, "device-side check")
     return code
 
@@ -619,6 +623,179 @@ def bw_grouped_gemm_wgrad(dYt: BWOperand, Xt: BWOperand, m_splits: torch.Tensor,
                                           total_rows, _ptr(out), _OUT[out.dtype],
                                           1 if accumulate else 0, _ptr(ws), ws.numel(), _ptr(st),
                                           _stream(dev)), "bw_grouped_gemm_wgrad")
+    if check:
+        check_status(st)
+    return out
+
+
+# ----------------------------------------------------------------------------- serving
+
+
+def _rows(t: torch.Tensor, name: str, cols: int | None = None):
+    """A 2-D tensor with contiguous rows (any row stride)."""
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be a 2-D tensor" + (f" of {cols} columns" if cols is not None else ""))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: elements of a row must be contiguous")
+    return t
+
+
+def _whole(t: torch.Tensor, name: str, shape, dtype):
+    """A contiguous tensor of the given shape and type."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    return t
+
+
+def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, ids: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None):
+    """Router logits [T, E] (BF16 or FP32) -> (int32 ids [T, top_k], FP32
+    weights [T, top_k]): each token's top_k experts, largest logit first and
+    equal logits in index order, with their softmax weights -- over the chosen
+    experts (``renormalize``) or over all of them.  Experts whose logit is -inf
+    or NaN are never chosen; slots left over have id -1 and weight 0."""
+    _need_cuda(logits, ids, weights)
+    _rows(logits, "logits")
+    if logits.dtype not in _OUT:
+        raise ValueError("logits must be bfloat16 or float32")
+    T, E = logits.shape
+    dev = logits.device
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if ids is None else \
+        _whole(ids, "ids", (T, top_k), torch.int32)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev) if weights is None else \
+        _whole(weights, "weights", (T, top_k), torch.float32)
+    _ok(_lib.load().moe_route(logits.data_ptr(), T, E, _ld(logits, E), _OUT[logits.dtype], top_k, int(renormalize),
+                              ids.data_ptr(), weights.data_ptr(), torch.cuda.current_stream(dev).cuda_stream),
+        "moe_route")
+    return ids, weights
+
+
+MOE_SYNC_WORDS = 1024  # MXG_MOE_SYNC_WORDS
+_moe_sync = {}
+
+
+def _moe_sync_words(dev, stream: int) -> torch.Tensor:
+    """The zeroed words that moe_experts calls on one stream share (every
+    completed call leaves them zero)."""
+    key = (dev.index, stream)
+    words = _moe_sync.get(key)
+    if words is None:
+        words = torch.zeros(MOE_SYNC_WORDS, dtype=torch.int32, device=dev)
+        # words first made during a stream capture belong to that graph (which zeroes them at every replay)
+        if not torch.cuda.is_current_stream_capturing():
+            _moe_sync[key] = words
+    return words
+
+
+def moe_experts_workspace_size(tokens: int, top_k: int, experts: int, hidden: int, inter: int) -> int:
+    return int(_lib.load().moe_experts_workspace_size(tokens, top_k, experts, hidden, inter))
+
+
+def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: MXOperand, W2: MXOperand,
+                out_dtype=torch.bfloat16, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                sync: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                check: bool = False) -> torch.Tensor:
+    """The expert layer of a few tokens over MX-quantized weights (decode):
+    out[t] = sum_j weights[t, j] * W2[e] silu_mul(W13[e] x[t]), e = ids[t, j].
+
+    ``x`` BF16 [T, H]; ``ids`` / ``weights`` [T, top_k] as from ``moe_route``
+    (a negative id is an empty slot); ``W13`` [E * 2I, H] (each expert's I gate
+    rows, then its I up rows) and ``W2`` [E * H, I] from
+    ``mx_quantize_rowwise_packed(..., groups=E)``, both "e2m1" or both "e4m3".
+    Activations are rounded to MXFP8 in front of each product, as the grouped
+    GEMMs of the same operands take them.  T * top_k <= 4096.
+
+    ``sync``: int32 zeros [MOE_SYNC_WORDS], only needed when calls on different
+    streams share a workspace handed in by the caller; by default each stream
+    keeps its own."""
+    _need_cuda(x, ids, weights, W13.data, W2.data, out, workspace, sync)
+    _rows(x, "x", W13.cols)
+    if x.dtype != torch.bfloat16:
+        raise ValueError("x must be bfloat16")
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, top_k]")
+    if W13.scale_layout != "packed" or W2.scale_layout != "packed":
+        raise ValueError("W13 and W2 need packed scales (mx_quantize_rowwise_packed with groups=experts)")
+    T, H = x.shape
+    k, I, dev = ids.shape[1], W2.cols, x.device
+    E = W2.rows // H
+    if W2.rows != E * H or W13.rows != E * 2 * I:
+        raise ValueError("W13 must be [E * 2I, H] and W2 [E * H, I]")
+    for w, cols in ((W13, H), (W2, I)):
+        if w.scale.numel() < w.rows // 128 * (cols // 128) * 512:
+            raise ValueError("packed scales are shorter than the weights need")
+    _whole(ids, "ids", (T, k), torch.int32)
+    _whole(weights, "weights", (T, k), torch.float32)
+    lib = _lib.load()
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=dev)
+    else:
+        _rows(out, "out", H)
+        if out.shape[0] != T or out.dtype not in _OUT:
+            raise ValueError("out must be [tokens, hidden], bfloat16 or float32")
+    ws = _workspace(0 if workspace is not None else lib.moe_experts_workspace_size(T, k, E, H, I), dev, workspace)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if sync is None:
+        sync = _moe_sync_words(dev, stream)
+    elif sync.dtype != torch.int32 or sync.numel() < MOE_SYNC_WORDS or not sync.is_contiguous():
+        raise ValueError(f"sync must be a contiguous int32 tensor of {MOE_SYNC_WORDS} words")
+    st = status if status is not None else status_tensor(dev)
+    a, b = W13.c(), W2.c()
+    _ok(lib.moe_experts(x.data_ptr(), T, _ld(x, H), ids.data_ptr(), weights.data_ptr(), k, E, ctypes.byref(a),
+                        ctypes.byref(b), out.data_ptr(), _ld(out, H), _OUT[out.dtype], ws.data_ptr(), ws.numel(),
+                        sync.data_ptr(), st.data_ptr(), stream), "moe_experts")
+    if check:
+        check_status(st)
+    return out
+
+
+def lora_add_workspace_size(tokens: int, K: int, rank: int) -> int:
+    return int(_lib.load().lora_add_workspace_size(tokens, K, rank))
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
+             scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+             check: bool = False) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a shared projection:
+    out[t] = y[t] + scale[a] * B[a] (A[a] x[t]) with a = ids[t]; out[t] = y[t]
+    for a negative id.
+
+    ``y`` [T, N] BF16 or FP32, the projection's output; ``x`` BF16 [T, K];
+    ``A`` BF16 [adapters, rank, K]; ``B`` BF16 [adapters, N, rank]; ``ids``
+    int32 [T]; ``scale`` FP32 [adapters] (None: 1).  ``out=y`` updates in
+    place.  rank is a multiple of 8 up to 128."""
+    _need_cuda(y, x, A, B, ids, scale, out, workspace)
+    _rows(y, "y")
+    _rows(x, "x")
+    if y.dtype not in _OUT or x.dtype != torch.bfloat16:
+        raise ValueError("y must be bfloat16 or float32 and x bfloat16")
+    if A.dim() != 3:
+        raise ValueError("A must be [adapters, rank, K]")
+    T, N = y.shape
+    n, R, K = A.shape
+    if x.shape[0] != T:
+        raise ValueError("x and y must have the same number of rows")
+    _rows(x, "x", K)
+    _whole(A, "A", (n, R, K), torch.bfloat16)
+    _whole(B, "B", (n, N, R), torch.bfloat16)
+    _whole(ids, "ids", (T,), torch.int32)
+    if scale is not None:
+        _whole(scale, "scale", (n,), torch.float32)
+    dev = y.device
+    lib = _lib.load()
+    if out is None:
+        out = torch.empty((T, N), dtype=y.dtype, device=dev)
+    else:
+        _rows(out, "out", N)
+        if out.shape[0] != T or out.dtype != y.dtype:
+            raise ValueError("out must have y's shape and type")
+    ws = _workspace(0 if workspace is not None else lib.lora_add_workspace_size(T, K, R), dev, workspace)
+    st = status if status is not None else status_tensor(dev)
+    _ok(lib.lora_add(y.data_ptr(), _ld(y, N), x.data_ptr(), _ld(x, K), A.data_ptr(), B.data_ptr(), ids.data_ptr(),
+                     scale.data_ptr() if scale is not None else None, T, N, K, R, n, _OUT[y.dtype], out.data_ptr(),
+                     _ld(out, N), ws.data_ptr(), ws.numel(), st.data_ptr(),
+                     torch.cuda.current_stream(dev).cuda_stream), "lora_add")
     if check:
         check_status(st)
     return out

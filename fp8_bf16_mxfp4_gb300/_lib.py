@@ -109,6 +109,15 @@ SIGNATURES = {
         c_i32, [ctypes.POINTER(BwOperandC), ctypes.POINTER(BwOperandC), c_vp, c_i32, c_i64, c_vp,
                 c_i32, c_i32, c_vp, c_size, c_vp, c_vp]),
     "bw_gemm_workspace_size": (c_size, [c_i32]),
+    "moe_route": (c_i32, [c_vp, c_i64, c_i32, c_i64, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]),
+    "moe_experts_workspace_size": (c_size, [c_i64, c_i32, c_i32, c_i64, c_i64]),
+    "moe_experts": (
+        c_i32, [c_vp, c_i64, c_i64, c_vp, c_vp, c_i32, c_i32, ctypes.POINTER(MxOperandC),
+                ctypes.POINTER(MxOperandC), c_vp, c_i64, c_i32, c_vp, c_size, c_vp, c_vp, c_vp]),
+    "lora_add_workspace_size": (c_size, [c_i64, c_i64, c_i32]),
+    "lora_add": (
+        c_i32, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i32, c_i32, c_i32, c_vp,
+                c_i64, c_vp, c_size, c_vp, c_vp]),
     "mxg_check_status": (c_i32, [c_vp, c_vp]),
     "mxg_status_string": (ctypes.c_char_p, [c_i32]),
     "mxg_set_wait_timeout_ns": (None, [c_u64]),

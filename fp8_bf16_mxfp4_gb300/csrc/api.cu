@@ -189,6 +189,7 @@ const char* mxg_status_string(mxg_status s) {
     case MXG_ERR_TIMEOUT: return "a bounded in-kernel wait ran out";
     case MXG_ERR_WORKSPACE: return "workspace missing or too small";
     case MXG_ERR_CAPACITY: return "padded rows exceed the output capacity";
+    case MXG_ERR_INDEX: return "an expert or adapter id is not below its count";
   }
   return "unknown status";
 }
@@ -804,6 +805,146 @@ mxg_status bw_grouped_gemm_wgrad(const mxg_bw_operand* dYt, const mxg_bw_operand
   return launch_grouped_bw_gemm(bw_args(MXG_PASS_WGRAD, G, dYt, Xt, d_m_splits, total_rows, N, K,
                                         out, K, out_dtype, accumulate ? 1 : 0, ws, d_status),
                                 static_cast<cudaStream_t>(stream), sms);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Serving: routing, the expert layer for a few tokens, low-rank adapters
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxTopK = 32;
+constexpr int64_t kMaxSlots = 4096;  // tokens * top_k of moe_experts
+constexpr int kMaxRank = 128;
+
+inline bool valid_out_dtype(int32_t d) { return d == MXG_OUT_BF16 || d == MXG_OUT_F32; }
+
+bool moe_sizes_ok(int64_t tokens, int32_t top_k, int32_t experts, int64_t hidden, int64_t inter) {
+  return tokens >= 0 && top_k >= 1 && top_k <= kMaxTopK && experts >= 1 && experts <= kMaxExperts &&
+         tokens <= kMaxSlots / top_k && hidden > 0 && inter > 0 && hidden % 128 == 0 && inter % 128 == 0 &&
+         hidden <= (1 << 20) && inter <= (1 << 20);
+}
+
+bool lora_sizes_ok(int64_t tokens, int64_t K, int32_t rank) {
+  return tokens >= 0 && tokens <= 0x7FFFFFFF && K > 0 && K % 8 == 0 && K <= 0x7FFFFFFF && rank >= 8 &&
+         rank % 8 == 0 && rank <= kMaxRank;
+}
+
+// One expert weight matrix of moe_experts: `rows` x `cols`, packed scales.
+mxg_status check_expert_weights(const mxg_mx_operand* w, int64_t rows, int64_t cols) {
+  const mxg_status st = check_operand(w, false, true);
+  if (st != MXG_OK) return st;
+  if (w->scale_layout != MXG_SCALE_PACKED) return MXG_ERR_UNSUPPORTED;
+  if (w->rows != rows || w->cols != cols) return MXG_ERR_SHAPE;
+  if (!aligned(w->data, 32) || w->ld % 32 != 0) return MXG_ERR_ALIGN;
+  return MXG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mxg_status moe_route(const void* logits, int64_t tokens, int32_t experts, int64_t ld_logits, int32_t dtype,
+                     int32_t top_k, int32_t renormalize, int32_t* ids, float* weights, void* stream) {
+  if (!valid_out_dtype(dtype)) return MXG_ERR_UNSUPPORTED;
+  if (tokens < 0 || tokens > 0x7FFFFFFF || experts < 1 || experts > kMaxExperts || top_k < 1 || top_k > kMaxTopK ||
+      top_k > experts || ld_logits < experts)
+    return MXG_ERR_SHAPE;
+  if (tokens == 0) return MXG_OK;
+  if (logits == nullptr || ids == nullptr || weights == nullptr) return MXG_ERR_NULL;
+  if (!aligned(logits, dtype == MXG_OUT_BF16 ? 2 : 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  mxg_status st = check_device({logits, ids, weights}, &dev, &sms);
+  if (st != MXG_OK) return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  return cuda_status(launch_moe_route(logits, tokens, experts, ld_logits, dtype == MXG_OUT_BF16, top_k,
+                                      renormalize != 0, ids, weights, static_cast<cudaStream_t>(stream), sms));
+}
+
+size_t moe_experts_workspace_size(int64_t tokens, int32_t top_k, int32_t experts, int64_t hidden, int64_t inter) {
+  if (!moe_sizes_ok(tokens, top_k, experts, hidden, inter)) return 0;
+  return moe_workspace_bytes(tokens, top_k, experts, hidden, inter);
+}
+
+mxg_status moe_experts(const void* x, int64_t tokens, int64_t ld_x, const int32_t* ids, const float* weights,
+                       int32_t top_k, int32_t experts, const mxg_mx_operand* W13, const mxg_mx_operand* W2,
+                       void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes, int32_t* d_sync,
+                       int32_t* d_status, void* stream) {
+  if (W13 == nullptr || W2 == nullptr || d_status == nullptr || d_sync == nullptr) return MXG_ERR_NULL;
+  const int64_t hidden = W13->cols, inter = W2->cols;
+  if (!moe_sizes_ok(tokens, top_k, experts, hidden, inter)) return MXG_ERR_SHAPE;
+  mxg_status st;
+  if ((st = check_expert_weights(W13, (int64_t)experts * 2 * inter, hidden)) != MXG_OK ||
+      (st = check_expert_weights(W2, (int64_t)experts * hidden, inter)) != MXG_OK)
+    return st;
+  if (W13->elem != W2->elem || !valid_out_dtype(out_dtype)) return MXG_ERR_UNSUPPORTED;
+  if (ld_x < hidden || ld_out < hidden) return MXG_ERR_SHAPE;
+  if (ld_x % 8 != 0 || ld_out % (out_dtype == MXG_OUT_BF16 ? 8 : 4) != 0) return MXG_ERR_ALIGN;
+  if (tokens == 0) return MXG_OK;
+  if (x == nullptr || ids == nullptr || weights == nullptr || out == nullptr) return MXG_ERR_NULL;
+  if (!aligned16(x) || !aligned16(out) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(d_sync, 4))
+    return MXG_ERR_ALIGN;
+  if (ws == nullptr || ws_bytes < moe_workspace_bytes(tokens, top_k, experts, hidden, inter)) return MXG_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if ((st = check_device({x, ids, weights, W13->data, W13->scale, W2->data, W2->scale, out, ws, d_sync, d_status},
+                         &dev, &sms)) != MXG_OK)
+    return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  MoeArgs a{};
+  a.x = static_cast<const uint16_t*>(x); a.ld_x = ld_x;
+  a.ids = ids; a.weights = weights;
+  a.T = (int)tokens; a.k = top_k; a.E = experts; a.H = (int)hidden; a.I = (int)inter;
+  a.elem = W13->elem;
+  a.w13 = static_cast<const uint8_t*>(W13->data); a.ld13 = W13->ld; a.s13 = W13->scale;
+  a.w2 = static_cast<const uint8_t*>(W2->data); a.ld2 = W2->ld; a.s2 = W2->scale;
+  a.out = out; a.ld_out = ld_out; a.out_dtype = out_dtype;
+  a.ws = ws; a.sync = d_sync; a.status = d_status;
+  return launch_moe_experts(a, static_cast<cudaStream_t>(stream), sms);
+}
+
+size_t lora_add_workspace_size(int64_t tokens, int64_t K, int32_t rank) {
+  if (!lora_sizes_ok(tokens, K, rank)) return 0;
+  return lora_workspace_bytes(tokens, K, rank);
+}
+
+mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, const void* A, const void* B,
+                    const int32_t* ids, const float* scale, int64_t tokens, int64_t N, int64_t K, int32_t rank,
+                    int32_t adapters, int32_t dtype, void* out, int64_t ld_out, void* ws, size_t ws_bytes,
+                    int32_t* d_status, void* stream) {
+  if (d_status == nullptr) return MXG_ERR_NULL;
+  if (!valid_out_dtype(dtype)) return MXG_ERR_UNSUPPORTED;
+  if (!lora_sizes_ok(tokens, K, rank) || N <= 0 || N % 8 != 0 || N > 0x7FFFFFFF || adapters < 1 || ld_x < K ||
+      ld_y < N || ld_out < N)
+    return MXG_ERR_SHAPE;
+  const int per16 = dtype == MXG_OUT_BF16 ? 8 : 4;
+  if (ld_x % 8 != 0 || ld_y % per16 != 0 || ld_out % per16 != 0) return MXG_ERR_ALIGN;
+  if (tokens == 0) return MXG_OK;
+  if (y == nullptr || x == nullptr || A == nullptr || B == nullptr || ids == nullptr || out == nullptr)
+    return MXG_ERR_NULL;
+  if (!aligned16(y) || !aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned16(out) || !aligned(ids, 4) ||
+      !aligned(scale, 4))
+    return MXG_ERR_ALIGN;
+  if (ws == nullptr || ws_bytes < lora_workspace_bytes(tokens, K, rank)) return MXG_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  mxg_status st = check_device({y, x, A, B, ids, scale, out, ws, d_status}, &dev, &sms);
+  if (st != MXG_OK) return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  LoraArgs a{};
+  a.y = y; a.ld_y = ld_y;
+  a.x = static_cast<const uint16_t*>(x); a.ld_x = ld_x;
+  a.A = static_cast<const uint16_t*>(A); a.B = static_cast<const uint16_t*>(B);
+  a.ids = ids; a.scale = scale;
+  a.T = tokens; a.N = N; a.K = K; a.R = rank; a.n = adapters;
+  a.dtype = dtype; a.out = out; a.ld_out = ld_out;
+  a.ws = static_cast<float*>(ws); a.status = d_status;
+  return cuda_status(launch_lora_add(a, static_cast<cudaStream_t>(stream), sms));
 }
 
 }  // extern "C"

@@ -107,4 +107,53 @@ struct BwGemmArgs {
 size_t bw_gemm_workspace_bytes(int G);
 mxg_status launch_grouped_bw_gemm(const BwGemmArgs& a, cudaStream_t stream, int num_sms);
 
+// Top-k routing.  See moe_route.cu.
+cudaError_t launch_moe_route(const void* logits, int64_t T, int E, int64_t ld, bool bf16, int k, bool renorm,
+                             int32_t* ids, float* weights, cudaStream_t stream, int num_sms);
+
+// The expert layer of a few tokens.  See moe_experts.cu.
+struct MoeArgs {
+  const uint16_t* x;
+  int64_t ld_x;
+  const int32_t* ids;
+  const float* weights;
+  int T, k, E, H, I;
+  int elem;  // weight format
+  const uint8_t* w13;
+  int64_t ld13;
+  const uint8_t* s13;  // packed scales
+  const uint8_t* w2;
+  int64_t ld2;
+  const uint8_t* s2;
+  void* out;
+  int64_t ld_out;
+  int out_dtype;
+  void* ws;
+  int32_t* sync;
+  int32_t* status;
+};
+size_t moe_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I);
+mxg_status launch_moe_experts(const MoeArgs& a, cudaStream_t stream, int num_sms);
+
+// Low-rank adapters.  See lora.cu.
+struct LoraArgs {
+  const void* y;
+  int64_t ld_y;
+  const uint16_t* x;
+  int64_t ld_x;
+  const uint16_t* A;
+  const uint16_t* B;
+  const int32_t* ids;
+  const float* scale;
+  int64_t T, N, K;
+  int R, n;
+  int dtype;
+  void* out;
+  int64_t ld_out;
+  float* ws;
+  int32_t* status;
+};
+size_t lora_workspace_bytes(int64_t T, int64_t K, int R);
+cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms);
+
 }  // namespace mxg

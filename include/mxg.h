@@ -67,7 +67,8 @@ typedef enum mxg_status {
   MXG_ERR_CUDA = 7,        /* a CUDA runtime call failed */
   MXG_ERR_TIMEOUT = 8,     /* device-side: a bounded wait ran out */
   MXG_ERR_WORKSPACE = 9,   /* workspace missing or smaller than required */
-  MXG_ERR_CAPACITY = 10    /* device-side: padded rows exceed the output capacity */
+  MXG_ERR_CAPACITY = 10,   /* device-side: padded rows exceed the output capacity */
+  MXG_ERR_INDEX = 11       /* device-side: an expert or adapter id is not below its count */
 } mxg_status;
 
 typedef enum mxg_elem { MXG_E2M1 = 1, MXG_E4M3 = 2 } mxg_elem;
@@ -461,6 +462,82 @@ mxg_status bw_grouped_gemm_wgrad(const mxg_bw_operand* dYt, const mxg_bw_operand
                                  void* out, int32_t out_dtype, int32_t accumulate, void* ws,
                                  size_t ws_bytes, int32_t* d_status, void* stream);
 size_t bw_gemm_workspace_size(int32_t G);
+
+/* --------------------------------------------------------------------------
+ * Serving: routing, the expert layer for a few tokens, low-rank adapters
+ *
+ * What a decode step of a mixture-of-experts model calls next to the GEMMs.
+ * Forward only.  Strides are in elements.
+ * ------------------------------------------------------------------------ */
+
+/* Top-k routing.  For every token t and its router logits l = logits[t, :]:
+ * the top_k experts with the largest l (equal logits: the lower expert first),
+ * in that order, and their weights
+ *   p_j = exp(l_j - max l),  weights[t, j] = p_j / sum over
+ *         the chosen experts (renormalize != 0) or all experts (0),
+ * computed in fp32 (an expert whose logit equals the maximum has p = 1, so a
+ * maximum of +inf shares the weight among the infinite ones).  A logit of -inf
+ * or NaN never is chosen and adds nothing: slots left over get id -1 and
+ * weight 0, and so do all slots of a token with no other logits.
+ *   logits  : [tokens, experts] of `dtype` (mxg_out_dtype: BF16 or FP32), row
+ *             stride ld_logits >= experts, aligned to the element
+ *   ids     : int32 [tokens, top_k]; weights: float [tokens, top_k]; contiguous
+ * 1 <= experts <= 512, 1 <= top_k <= min(experts, 32); tokens may be 0. */
+mxg_status moe_route(const void* logits, int64_t tokens, int32_t experts, int64_t ld_logits, int32_t dtype,
+                     int32_t top_k, int32_t renormalize, int32_t* ids, float* weights, void* stream);
+
+/* The expert layer of a few tokens (a decode step) over MX-quantized weights:
+ *   xq      = MXFP8(x[t])                    the bytes of mx_quantize_rowwise(x, MXG_E4M3)
+ *   g, u    = W13[e] xq                      rows [0, inter) and [inter, 2 inter) of expert e
+ *   hq      = MXFP8(g / (1 + exp(-g)) * u)   same rule, from the fp32 values
+ *   out[t]  = sum over slots j of weights[t, j] * (W2[e_j] hq_j),  e_j = ids[t, j]
+ * Products are exact, sums are in fp32 (slots in order), and the result is
+ * rounded once.  A slot with a negative id is empty; a token without slots
+ * gives zeros.  The result depends on the inputs only, not on timing.
+ *   x       : BF16 [tokens, hidden], row stride ld_x (% 8), 16-byte aligned
+ *   ids, weights : [tokens, top_k] contiguous (as from moe_route)
+ *   W13     : [experts * 2 * inter, hidden], W2: [experts * hidden, inter];
+ *             both MXG_E2M1 or both MXG_E4M3, scales packed with one segment
+ *             per expert (mx_quantize_rowwise_packed with G = experts);
+ *             data 32-byte aligned and ld % 32 == 0
+ *   out     : [tokens, hidden] of out_dtype, row stride ld_out, 16-byte
+ *             aligned rows
+ *   ws      : at least moe_experts_workspace_size(...) bytes, 256-byte aligned
+ *   d_sync  : MXG_MOE_SYNC_WORDS int32 words in device memory, zeroed by the
+ *             caller once.  Every completed call leaves them zero, so calls in
+ *             stream order share them; calls that may overlap need their own
+ *             ws and d_sync.  After MXG_ERR_TIMEOUT zero them again.
+ * hidden % 128 == 0, inter % 128 == 0, 1 <= experts <= 512, 1 <= top_k <= 32,
+ * tokens * top_k <= 4096 (tokens may be 0).  The weights of an expert are read
+ * once per 64 tokens routed to it: for hundreds of tokens per expert use the
+ * grouped GEMMs.  Device error: MXG_ERR_INDEX (an id >= experts; out is not
+ * written). */
+#define MXG_MOE_SYNC_WORDS 1024
+size_t moe_experts_workspace_size(int64_t tokens, int32_t top_k, int32_t experts, int64_t hidden, int64_t inter);
+mxg_status moe_experts(const void* x, int64_t tokens, int64_t ld_x, const int32_t* ids, const float* weights,
+                       int32_t top_k, int32_t experts, const mxg_mx_operand* W13, const mxg_mx_operand* W2,
+                       void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes, int32_t* d_sync,
+                       int32_t* d_status, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   out[t, :] = y[t, :] + scale[a] * B[a] (A[a] x[t, :]),   a = ids[t]
+ * with out = y for a negative id.  Sums are in fp32 and the result is rounded
+ * once to the output type.
+ *   y, out : [tokens, N] of `dtype` (mxg_out_dtype), row strides ld_y, ld_out
+ *            (rows 16-byte aligned: % 8 for BF16, % 4 for FP32); out may be y (in place), no other overlap
+ *   x      : BF16 [tokens, K], row stride ld_x (% 8), 16-byte aligned
+ *   A      : BF16 [adapters, rank, K], B: BF16 [adapters, N, rank]; contiguous,
+ *            16-byte aligned
+ *   ids    : int32 [tokens]; scale: float [adapters], NULL for 1
+ *   ws     : at least lora_add_workspace_size(...) bytes, 256-byte aligned
+ * K % 8 == 0, N % 8 == 0, rank a multiple of 8 up to 128 (pad adapters of a
+ * lower rank with zeros), adapters >= 1; tokens may be 0.  Device error:
+ * MXG_ERR_INDEX (an id >= adapters; that token's row of out is unspecified). */
+size_t lora_add_workspace_size(int64_t tokens, int64_t K, int32_t rank);
+mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, const void* A, const void* B,
+                    const int32_t* ids, const float* scale, int64_t tokens, int64_t N, int64_t K, int32_t rank,
+                    int32_t adapters, int32_t dtype, void* out, int64_t ld_out, void* ws, size_t ws_bytes,
+                    int32_t* d_status, void* stream);
 
 /* --------------------------------------------------------------------------
  * Status and configuration
