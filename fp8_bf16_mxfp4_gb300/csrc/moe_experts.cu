@@ -26,7 +26,7 @@
 //   warps 6-9  activations: each thread takes 32-element blocks of a token,
 //              rounds them to MXFP8 (up) or copies hq (down), and writes the
 //              swizzled tile and the scale bytes.
-// The stages of all units (expert, row tile, 64-token tile; in that order) are
+// The stages of all units (row tile, expert, 64-token tile; in that order) are
 // cut into one equal run per CTA, so every SM streams the same number of bytes
 // whatever the routing.  A unit cut by a run boundary is joined through
 // fp32 partials in global memory: the last of its CTAs to arrive (a counter
@@ -113,28 +113,18 @@ struct Runs {
 // Walks the segments (the part of one unit inside a run) of this CTA's run.
 struct Walker {
   int64_t s, end;
-  int e;
-  // the current segment
-  int unit, k0, k1, rt, tok0, n;
-  MXG_DEVINL bool next(const Runs& r, const int32_t* off, const int32_t* tile, int E, int row_tiles) {
+  // the current segment: unit, its stages [k0, k1), row tile, expert, tokens sorted[tok0 .. tok0 + n)
+  int unit, k0, k1, rt, e, tok0, n;
+  MXG_DEVINL bool next(const Runs& r, const int32_t* off, const int32_t* tile, int E) {
     if (s >= end) return false;
     unit = (int)(s / r.per_unit);
     k0 = (int)(s - (int64_t)unit * r.per_unit);
     k1 = (int)min((int64_t)r.per_unit, k0 + (end - s));
     s += k1 - k0;
-    if (e < 0) {  // last e whose first unit is not past `unit`
-      int lo = 0, hi = E - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tile[mid] * row_tiles <= unit) lo = mid; else hi = mid - 1;
-      }
-      e = lo;
-    }
-    while (unit >= tile[e + 1] * row_tiles) ++e;
-    const int tiles = tile[e + 1] - tile[e];
-    const int local = unit - tile[e] * row_tiles;
-    rt = local / tiles;
-    tok0 = (local - rt * tiles) * kTok;
+    rt = unit / tile[E];
+    const int ti = unit - rt * tile[E];
+    e = find_prefix(tile, E, ti);  // the last expert that starts at or before ti: it has tiles
+    tok0 = (ti - tile[e]) * kTok;
     n = min(kTok, off[e + 1] - off[e] - tok0);
     tok0 += off[e];
     return true;
@@ -268,7 +258,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   const int cta = blockIdx.x;
   const bool active = cta < runs.ctas;
   Walker w;
-  w.e = -1;
   w.s = active ? runs.start(cta) : 0;
   w.end = active ? runs.start(cta + 1) : 0;
 
@@ -280,7 +269,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       bool ok = true;
       constexpr uint32_t kTileTx = kFp4 ? kWTile / 2 : kWTile;  // the unpacking load counts its source bytes
       const int64_t rt_all = kDown ? (int64_t)p.E * (p.H >> 7) : (int64_t)p.E * 2 * (p.I >> 7);
-      while (ok && w.next(runs, off, tile, p.E, row_tiles)) {
+      while (ok && w.next(runs, off, tile, p.E)) {
         const int row0 = kDown ? w.e * p.H + w.rt * 256 : w.e * 2 * p.I + w.rt * 128;
         const int row1 = kDown ? row0 + 128 : row0 + p.I;
         const bool two = !kDown || w.rt * 256 + 128 < p.H;
@@ -313,7 +302,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       int stage = 0, count = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false;
-      while (ok && w.next(runs, off, tile, p.E, row_tiles)) {
+      while (ok && w.next(runs, off, tile, p.E)) {
         const int buf = count & 1;
         if (!ptx::mbar_wait(acc_empty(buf), ((count >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
         ptx::tc_fence_after();
@@ -385,7 +374,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      while (ok && w.next(runs, off, tile, p.E, row_tiles)) {
+      while (ok && w.next(runs, off, tile, p.E)) {
         const uint4* src[2];
         const uint8_t* ssrc[2];
         bool on[2];
@@ -491,8 +480,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int i = cta * 128 + quarter * 32 + lane; i < words; i += gridDim.x * 128) p.tok_cnt[i] = 0;
       }
       int count = 0;
-      while (w.next(runs, off, tile, p.E, row_tiles)) {
+      while (w.next(runs, off, tile, p.E)) {
         const int buf = count & 1;
+        float wt_lo = 0.0f, wt_hi = 0.0f;  // down: lane l has the weights of tokens l and l + 32
+        if constexpr (kDown) {
+          if (lane < w.n) wt_lo = __ldg(p.weights + sorted[w.tok0 + lane]);
+          if (lane + 32 < w.n) wt_hi = __ldg(p.weights + sorted[w.tok0 + lane + 32]);
+        }
         const bool ready = ptx::mbar_wait(acc_full(buf), (count >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
         if (!__all_sync(kFull, ready)) break;
         ptx::tc_fence_after();
@@ -502,47 +496,65 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         const int64_t u0 = (int64_t)w.unit * runs.per_unit;
         const bool whole = w.k0 == 0 && w.k1 == runs.per_unit;
 
-        // one token's pair of values (gate and up, or two output rows) of this lane
-        auto finish = [&](int c, float v0, float v1) {
-          const int slot = sorted[w.tok0 + c];
+        // 16 tokens' pairs of values (gate and up, or two output rows) of this
+        // lane's row; computed for all 16 so that they interleave, stored for
+        // the unit's tokens only
+        auto finish = [&](int c0, const float* v0, const float* v1) {
           if constexpr (kDown) {
-            const float wt = __ldg(p.weights + slot);
-            float* dst = p.rows + (int64_t)slot * p.H + w.rt * 256 + quarter * 32 + lane;
-            __stcg(dst, v0 * wt);
-            if (two) __stcg(dst + 128, v1 * wt);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (c0 + i < w.n) {
+                const float wt = __shfl_sync(kFull, c0 < 32 ? wt_lo : wt_hi, (c0 + i) & 31);
+                const int slot = sorted[w.tok0 + c0 + i];
+                float* dst = p.rows + (int64_t)slot * p.H + w.rt * 256 + quarter * 32 + lane;
+                __stcg(dst, v0[i] * wt);
+                if (two) __stcg(dst + 128, v1[i] * wt);
+              }
+            }
           } else {
-            const float h = v0 / (1.0f + expf(-v0)) * v1;
-            // the block of 32 channels is this warp's 32 lanes
-            const int ex = mx_exponent_f32(__reduce_max_sync(kFull, __float_as_uint(h) & 0x7FFFFFFFu));
-            const uint32_t code = cvt_e4m3x4(h * pow2_neg(ex), 0.0f, 0.0f, 0.0f) & 0xFFu;
-            p.hq[(int64_t)slot * p.I + w.rt * 128 + quarter * 32 + lane] = (uint8_t)code;
-            if (lane == 0) p.hs[(int64_t)slot * (p.I >> 5) + w.rt * 4 + quarter] = (uint8_t)(ex + 127);
+            uint32_t code[16];
+            int ex[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float h = v0[i] / (1.0f + expf(-v0[i])) * v1[i];
+              // the block of 32 channels is this warp's 32 lanes
+              ex[i] = mx_exponent_f32(__reduce_max_sync(kFull, __float_as_uint(h) & 0x7FFFFFFFu));
+              code[i] = cvt_e4m3x4(h * pow2_neg(ex[i]), 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (c0 + i < w.n) {
+                const int slot = sorted[w.tok0 + c0 + i];
+                p.hq[(int64_t)slot * p.I + w.rt * 128 + quarter * 32 + lane] = (uint8_t)code[i];
+                if (lane == 0) p.hs[(int64_t)slot * (p.I >> 5) + w.rt * 4 + quarter] = (uint8_t)(ex[i] + 127);
+              }
+            }
           }
         };
-        const int64_t part_row = (int64_t)256;
-        float* mine = p.part + ((int64_t)(2 * cta + (w.k0 == 0)) * p.part_tok) * part_row + quarter * 32 + lane;
+        float* mine = p.part + (int64_t)(2 * cta + (w.k0 == 0)) * p.part_tok * 256 + quarter * 32 + lane;
         for (int c0 = 0; c0 < w.n; c0 += 16) {
           uint32_t r0[16], r1[16];
           __syncwarp();
           ptx::tmem_ld_32x32b_x16(d0 + c0, r0);
-          if (two) ptx::tmem_ld_32x32b_x16(d1 + c0, r1);
+          ptx::tmem_ld_32x32b_x16(d1 + c0, r1);
           ptx::tmem_ld_wait();
           if (c0 + 16 >= w.n) {  // last read: hand the accumulator back
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(acc_empty(buf));
           }
+          float v0[16], v1[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (c0 + i < w.n) {
-              const float v0 = __uint_as_float(r0[i]), v1 = two ? __uint_as_float(r1[i]) : 0.0f;
-              if (whole) {
-                finish(c0 + i, v0, v1);
-              } else {
-                __stcg(mine + (c0 + i) * part_row, v0);
-                if (two) __stcg(mine + (c0 + i) * part_row + 128, v1);
+          for (int i = 0; i < 16; ++i) { v0[i] = __uint_as_float(r0[i]); v1[i] = __uint_as_float(r1[i]); }
+          if (whole) {
+            finish(c0, v0, v1);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c0 + i < w.n) {
+                __stcg(mine + (c0 + i) * 256, v0[i]);
+                if (two) __stcg(mine + (c0 + i) * 256 + 128, v1[i]);
               }
-            }
           }
         }
         if (!whole) {
@@ -555,22 +567,29 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           got = __shfl_sync(kFull, got, 0);
           if (got != (uint32_t)(last - first)) continue;
           __threadfence();
-          const float* base = p.part + quarter * 32 + lane;
-          const int64_t step = (int64_t)p.part_tok * part_row;
-          for (int c = 0; c < w.n; ++c) {
-            const float* src = base + (2 * first + 1) * step + c * part_row;
-            float v0 = __ldcg(src), v1 = two ? __ldcg(src + 128) : 0.0f;
-            src += step;  // buffer 2 * (first + 1)
-            for (int b = first + 1; b <= last; ++b, src += 2 * step) {
-              v0 += __ldcg(src);
-              if (two) v1 += __ldcg(src + 128);
+          const int64_t step = (int64_t)p.part_tok * 256;
+          for (int c0 = 0; c0 < w.n; c0 += 16) {
+            float v0[16], v1[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.0f;
+            // buffers 2 first + 1, 2 (first + 1), 2 (first + 2), ...
+            for (int b = first; b <= last; ++b) {
+              const float* src = p.part + (2 * b + (b == first)) * step + c0 * 256 + quarter * 32 + lane;
+              float a0[16], a1[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                a0[i] = c0 + i < w.n ? __ldcg(src + i * 256) : 0.0f;
+                a1[i] = two && c0 + i < w.n ? __ldcg(src + i * 256 + 128) : 0.0f;
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) { v0[i] += a0[i]; v1[i] += a1[i]; }
             }
-            finish(c, v0, v1);
+            finish(c0, v0, v1);
           }
         }
         if constexpr (kDown) {
           // this warp's rows of the unit's slots are in place; whoever brings
-          // a token's last slot sums the token's slots in order
+          // a token's last slot sums the token's slots
           __threadfence();
           __syncwarp();
           uint32_t* cnt = p.tok_cnt + (int64_t)(w.rt * 4 + quarter) * p.T;
@@ -586,27 +605,59 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             }
             uint32_t todo = __ballot_sync(kFull, done);
             if (todo) __threadfence();
+            // Four tokens at a time.  Lane 8 a + b reads rows 4 b .. 4 b + 3
+            // (16 bytes) of slots a, a + 4, ...; the four partial sums are
+            // then added across the lanes.
+            const int a = lane >> 3;
+            const int64_t r = w.rt * 256 + quarter * 32 + 4 * (lane & 7);
             while (todo) {
-              const int src_lane = __ffs(todo) - 1;
-              todo &= todo - 1;
-              const int tt = __shfl_sync(kFull, t, src_lane);
-              float a0 = 0.0f, a1 = 0.0f;
-              const int64_t r = w.rt * 256 + quarter * 32 + lane;
-              for (int j = 0; j < p.k; ++j) {
-                if ((mask[tt * mask_bytes + (j >> 3)] >> (j & 7)) & 1) {
-                  const float* s = p.rows + (int64_t)(tt * p.k + j) * p.H + r;
-                  a0 += __ldcg(s);
-                  if (two) a1 += __ldcg(s + 128);
+              int tt[4];
+              float4 s0[4], s1[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                tt[q] = todo ? __shfl_sync(kFull, t, __ffs(todo) - 1) : -1;
+                todo &= todo - 1;
+                s0[q] = s1[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              }
+              for (int j = a; j < ((p.k + 3) & ~3); j += 4) {
+                float4 x0[4], x1[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  x0[q] = x1[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                  if (tt[q] >= 0 && j < p.k && (mask[tt[q] * mask_bytes + (j >> 3)] >> (j & 7)) & 1) {
+                    const float4* src = reinterpret_cast<const float4*>(p.rows + (int64_t)(tt[q] * p.k + j) * p.H + r);
+                    x0[q] = __ldcg(src);
+                    if (two) x1[q] = __ldcg(src + 32);
+                  }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  s0[q].x += x0[q].x; s0[q].y += x0[q].y; s0[q].z += x0[q].z; s0[q].w += x0[q].w;
+                  s1[q].x += x1[q].x; s1[q].y += x1[q].y; s1[q].z += x1[q].z; s1[q].w += x1[q].w;
                 }
               }
-              if (p.out_f32) {
-                float* o = static_cast<float*>(p.out) + tt * p.ld_out + r;
-                o[0] = a0;
-                if (two) o[128] = a1;
-              } else {
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + tt * p.ld_out + r;
-                o[0] = __float2bfloat16_rn(a0);
-                if (two) o[128] = __float2bfloat16_rn(a1);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                float* f0 = &s0[q].x;
+                float* f1 = &s1[q].x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  f0[i] += __shfl_xor_sync(kFull, f0[i], 8);
+                  f0[i] += __shfl_xor_sync(kFull, f0[i], 16);
+                  f1[i] += __shfl_xor_sync(kFull, f1[i], 8);
+                  f1[i] += __shfl_xor_sync(kFull, f1[i], 16);
+                }
+                if (tt[q] >= 0 && a < (two ? 2 : 1)) {  // lanes 0-7 write the first tile's rows, 8-15 the second's
+                  const float4 o = a == 0 ? s0[q] : s1[q];
+                  const int64_t at = tt[q] * p.ld_out + r + 128 * a;
+                  if (p.out_f32) {
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o;
+                  } else {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                  }
+                }
               }
             }
           }
