@@ -30,7 +30,7 @@ __all__ = [
     "bw_quantize_colwise_padded", "bw_grouped_gemm_fwd", "bw_grouped_gemm_dgrad",
     "bw_grouped_gemm_wgrad", "bw_quantize_1x128_pow2", "bw_quantize_128x128_pow2",
     "bw_quantize_colwise_padded_pow2", "bw_quantize_dual_padded",
-    "moe_route", "moe_experts", "moe_experts_workspace_size", "MOE_SYNC_WORDS", "lora_add", "lora_add_workspace_size",
+    "moe_route", "moe_experts", "moe_experts_workspace_size", "lora_add", "lora_add_workspace_size",
 ]
 
 ELEM = {"e2m1": 1, "e4m3": 2}
@@ -101,7 +101,6 @@ def _ld(t: torch.Tensor, row_elems: int) -> int:
 
 
 _status = {}
-_ERR_TIMEOUT = 8  # MXG_ERR_TIMEOUT
 
 
 def status_tensor(device) -> torch.Tensor:
@@ -117,8 +116,6 @@ def check_status(status: torch.Tensor | None = None, device=None) -> int:
     """Synchronise, read and clear the device status word; raise on error."""
     st = status if status is not None else status_tensor(device or torch.cuda.current_device())
     code = _lib.load().mxg_check_status(_ptr(st), _stream(st.device))
-    if code == _ERR_TIMEOUT:
-        _moe_sync.clear()  # an abandoned moe_experts call may have left its words non-zero
     _ok(code, "device-side check")
     return code
 
@@ -670,31 +667,13 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, ids: t
     return ids, weights
 
 
-MOE_SYNC_WORDS = 1024  # MXG_MOE_SYNC_WORDS
-_moe_sync = {}
-
-
-def _moe_sync_words(dev, stream: int) -> torch.Tensor:
-    """The zeroed words that moe_experts calls on one stream share (every
-    completed call leaves them zero)."""
-    key = (dev.index, stream)
-    words = _moe_sync.get(key)
-    if words is None:
-        words = torch.zeros(MOE_SYNC_WORDS, dtype=torch.int32, device=dev)
-        # words first made during a stream capture belong to that graph (which zeroes them at every replay)
-        if not torch.cuda.is_current_stream_capturing():
-            _moe_sync[key] = words
-    return words
-
-
 def moe_experts_workspace_size(tokens: int, top_k: int, experts: int, hidden: int, inter: int) -> int:
     return int(_lib.load().moe_experts_workspace_size(tokens, top_k, experts, hidden, inter))
 
 
 def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: MXOperand, W2: MXOperand,
                 out_dtype=torch.bfloat16, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                sync: torch.Tensor | None = None, status: torch.Tensor | None = None,
-                check: bool = False) -> torch.Tensor:
+                status: torch.Tensor | None = None, check: bool = False) -> torch.Tensor:
     """The expert layer of a few tokens over MX-quantized weights (decode):
     out[t] = sum_j weights[t, j] * W2[e] silu_mul(W13[e] x[t]), e = ids[t, j].
 
@@ -703,12 +682,8 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
     rows, then its I up rows) and ``W2`` [E * H, I] from
     ``mx_quantize_rowwise_packed(..., groups=E)``, both "e2m1" or both "e4m3".
     Activations are rounded to MXFP8 in front of each product, as the grouped
-    GEMMs of the same operands take them.  T * top_k <= 4096.
-
-    ``sync``: int32 zeros [MOE_SYNC_WORDS], only needed when calls on different
-    streams share a workspace handed in by the caller; by default each stream
-    keeps its own."""
-    _need_cuda(x, ids, weights, W13.data, W2.data, out, workspace, sync)
+    GEMMs of the same operands take them.  T * top_k <= 4096."""
+    _need_cuda(x, ids, weights, W13.data, W2.data, out, workspace)
     _rows(x, "x", W13.cols)
     if x.dtype != torch.bfloat16:
         raise ValueError("x must be bfloat16")
@@ -735,15 +710,11 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
             raise ValueError("out must be [tokens, hidden], bfloat16 or float32")
     ws = _workspace(0 if workspace is not None else lib.moe_experts_workspace_size(T, k, E, H, I), dev, workspace)
     stream = torch.cuda.current_stream(dev).cuda_stream
-    if sync is None:
-        sync = _moe_sync_words(dev, stream)
-    elif sync.dtype != torch.int32 or sync.numel() < MOE_SYNC_WORDS or not sync.is_contiguous():
-        raise ValueError(f"sync must be a contiguous int32 tensor of {MOE_SYNC_WORDS} words")
     st = status if status is not None else status_tensor(dev)
     a, b = W13.c(), W2.c()
     _ok(lib.moe_experts(x.data_ptr(), T, _ld(x, H), ids.data_ptr(), weights.data_ptr(), k, E, ctypes.byref(a),
                         ctypes.byref(b), out.data_ptr(), _ld(out, H), _OUT[out.dtype], ws.data_ptr(), ws.numel(),
-                        sync.data_ptr(), st.data_ptr(), stream), "moe_experts")
+                        st.data_ptr(), stream), "moe_experts")
     if check:
         check_status(st)
     return out

@@ -823,7 +823,7 @@ inline bool valid_out_dtype(int32_t d) { return d == MXG_OUT_BF16 || d == MXG_OU
 bool moe_sizes_ok(int64_t tokens, int32_t top_k, int32_t experts, int64_t hidden, int64_t inter) {
   return tokens >= 0 && top_k >= 1 && top_k <= kMaxTopK && experts >= 1 && experts <= kMaxExperts &&
          tokens <= kMaxSlots / top_k && hidden > 0 && inter > 0 && hidden % 128 == 0 && inter % 128 == 0 &&
-         hidden <= (1 << 20) && inter <= (1 << 20);
+         hidden <= 65536 && inter <= 65536;  // 32-bit stage counts
 }
 
 bool lora_sizes_ok(int64_t tokens, int64_t K, int32_t rank) {
@@ -871,9 +871,9 @@ size_t moe_experts_workspace_size(int64_t tokens, int32_t top_k, int32_t experts
 
 mxg_status moe_experts(const void* x, int64_t tokens, int64_t ld_x, const int32_t* ids, const float* weights,
                        int32_t top_k, int32_t experts, const mxg_mx_operand* W13, const mxg_mx_operand* W2,
-                       void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes, int32_t* d_sync,
+                       void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes,
                        int32_t* d_status, void* stream) {
-  if (W13 == nullptr || W2 == nullptr || d_status == nullptr || d_sync == nullptr) return MXG_ERR_NULL;
+  if (W13 == nullptr || W2 == nullptr || d_status == nullptr) return MXG_ERR_NULL;
   const int64_t hidden = W13->cols, inter = W2->cols;
   if (!moe_sizes_ok(tokens, top_k, experts, hidden, inter)) return MXG_ERR_SHAPE;
   mxg_status st;
@@ -885,12 +885,11 @@ mxg_status moe_experts(const void* x, int64_t tokens, int64_t ld_x, const int32_
   if (ld_x % 8 != 0 || ld_out % (out_dtype == MXG_OUT_BF16 ? 8 : 4) != 0) return MXG_ERR_ALIGN;
   if (tokens == 0) return MXG_OK;
   if (x == nullptr || ids == nullptr || weights == nullptr || out == nullptr) return MXG_ERR_NULL;
-  if (!aligned16(x) || !aligned16(out) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(d_sync, 4))
-    return MXG_ERR_ALIGN;
+  if (!aligned16(x) || !aligned16(out) || !aligned(ids, 4) || !aligned(weights, 4)) return MXG_ERR_ALIGN;
   if (ws == nullptr || ws_bytes < moe_workspace_bytes(tokens, top_k, experts, hidden, inter)) return MXG_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return MXG_ERR_ALIGN;
   int dev = 0, sms = 0;
-  if ((st = check_device({x, ids, weights, W13->data, W13->scale, W2->data, W2->scale, out, ws, d_sync, d_status},
+  if ((st = check_device({x, ids, weights, W13->data, W13->scale, W2->data, W2->scale, out, ws, d_status},
                          &dev, &sms)) != MXG_OK)
     return st;
   DeviceGuard g(dev);
@@ -903,7 +902,7 @@ mxg_status moe_experts(const void* x, int64_t tokens, int64_t ld_x, const int32_
   a.w13 = static_cast<const uint8_t*>(W13->data); a.ld13 = W13->ld; a.s13 = W13->scale;
   a.w2 = static_cast<const uint8_t*>(W2->data); a.ld2 = W2->ld; a.s2 = W2->scale;
   a.out = out; a.ld_out = ld_out; a.out_dtype = out_dtype;
-  a.ws = ws; a.sync = d_sync; a.status = d_status;
+  a.ws = ws; a.status = d_status;
   return launch_moe_experts(a, static_cast<cudaStream_t>(stream), sms);
 }
 

@@ -129,7 +129,6 @@ struct MoeArgs {
   int64_t ld_out;
   int out_dtype;
   void* ws;
-  int32_t* sync;
   int32_t* status;
 };
 size_t moe_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I);

@@ -5,36 +5,37 @@
 //
 // With a handful of tokens per expert the layer is a stream of the used
 // experts' weights: 3 H I (1/2 or 1, + 1/32) bytes each, against which
-// activations, partial sums and arithmetic are small.  Two kernels:
+// activations, partial sums and arithmetic are small.  Four kernels:
 //
+//   quant x to MXFP8, once;
 //   up    units of 128 channels: the 128 gate rows and the 128 up rows of one
 //         expert, against its tokens; writes hq (MXFP8 codes and scales);
-//   down  units of 256 output rows of one expert; writes weighted fp32 rows
-//         per slot, and the warp that completes a token's last slot sums the
-//         slots in order and writes the output.
+//   down  units of 256 output rows of one expert; writes a weighted fp32 row
+//         per slot;
+//   sum   adds each token's slots in order and rounds once.
 //
 // Weights are the M operand of the tensor core (128 rows = TMEM lanes), the
 // expert's tokens the N operand (16 to 64 columns), so a few tokens fill the
 // tile: block-scaled tcgen05.mma (kind::mxf8f6f4, E4M3 activations against
-// E2M1 or E4M3 weights) needs no dequantization and no instruction issue per
-// weight.  One CTA per SM, 320 threads:
-//   warp 0     weight producer: TMA tiles (E2M1 unpacked to bytes on the way)
-//              and their packed scale chunks into a 5-stage ring, 128
-//              contraction elements a stage;
-//   warp 1     TMEM owner and MMA issuer: scale copies to TMEM and 8 MMAs a stage;
-//   warps 2-5  epilogue, one per TMEM lane quarter;
-//   warps 6-9  activations: each thread takes 32-element blocks of a token,
-//              rounds them to MXFP8 (up) or copies hq (down), and writes the
-//              swizzled tile and the scale bytes.
+// E2M1 or E4M3 weights) needs no dequantization and no instruction per weight.
+// One CTA per SM:
+//   warp 0       weight producer: E4M3 tiles by TMA, E2M1 tiles prefetched into
+//                L2 by TMA; packed scale chunks; 128 contraction elements a stage;
+//   warp 1       TMEM owner and MMA issuer: scale copies to TMEM and 8 MMAs a stage;
+//   warps 2-5    epilogue, one per TMEM lane quarter;
+//   warps 6-9    activations: the unit's tokens' codes and scale bytes;
+//   warps 10-13  E2M1 weights only: L2 to the tensor core's 4-bit layout.
 // The stages of all units (row tile, expert, 64-token tile; in that order) are
 // cut into one equal run per CTA, so every SM streams the same number of bytes
 // whatever the routing.  A unit cut by a run boundary is joined through
 // fp32 partials in global memory: the last of its CTAs to arrive (a counter
 // that wraps to zero) adds them in run order, so results do not depend on
-// timing.  Nothing waits for another CTA.  The down kernel is launched with
-// programmatic stream serialization: each of its CTAs starts on its SM as soon
-// as the up kernel's has left and streams W2 while the others finish; only its
-// activation and epilogue warps wait for the up kernel's results.
+// timing; a run takes its cut units first, so that the joins hide behind the
+// rest.  Nothing waits for another CTA.  All but the first kernel are launched
+// with programmatic stream serialization: they plan and start to stream their
+// weights while the kernel before still runs (a down CTA as soon as the up
+// kernel's has left its SM), and only their activation and epilogue warps wait
+// for its results.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -50,8 +51,8 @@ namespace mxg {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kMoeThreads = 320;
-constexpr int kMoeStages = 5;
+constexpr int kMoeThreads = 320;  // warps 0-9
+constexpr int kUnpackThreads = 128; // warps 10-13 (E2M1 weights)
 constexpr int kTok = 64;                  // tokens of one unit (TMEM columns of one accumulator)
 constexpr int kWTile = 128 * 128;         // one weight tile in shared memory (a byte per element)
 constexpr int kActTile = kTok * 128;
@@ -60,24 +61,36 @@ constexpr int kStageBytes = 2 * kWTile + kActTile;
 constexpr int kStageSf = 3 * kChunk;      // two weight chunks, one activation chunk
 constexpr int kMoeMaxSlots = 4096;
 constexpr int kMaxCtas = 160;             // partial buffers are sized for this many CTAs
+constexpr int kSyncWords = 4 * kMaxCtas;  // join counters: [CTAs][4]
 constexpr int kMoeTmemCols = 512;
 constexpr int kSfCol = 256;               // two accumulator buffers of 2 x 64 columns, then the scale slots
 constexpr int kSfSlot = 12;               // columns of one stage's scales
-constexpr int kMinStages = 2;             // shortest run of a CTA
+// A run is at least kMinStages long, and units of up to kWholeStages are not
+// cut: joining a cut unit costs about as much as that many stages.
+constexpr int kMinStages = 8;
+constexpr int kWholeStages = 8;
+constexpr int kPlanWarps = 8;             // warps 2-9 sort the slots
 
-constexpr int kSfOff = kMoeStages * kStageBytes;
-constexpr int kBarOff = kSfOff + kMoeStages * kStageSf;
-constexpr int kNumBars = 3 * kMoeStages + 5;
-constexpr int kMiscOff = kBarOff + kNumBars * 8;
-constexpr int kOffOff = kMiscOff + 32;                       // int32 [E + 1]: first sorted slot of each expert
-constexpr int kTileOff = kOffOff + (kMaxExperts + 4) * 4;    // int32 [E + 1]: first token tile of each expert
-constexpr int kPosOff = kTileOff + (kMaxExperts + 4) * 4;    // uint16 [E]: running position of the sort
-constexpr int kSortOff = kPosOff + kMaxExperts * 2;          // uint16 [slots]: slots by expert
-constexpr int kMaskOff = kSortOff + kMoeMaxSlots * 2;        // bytes: each token's used slots, (k + 7) / 8 bytes
-constexpr int kMoeSmem = kMaskOff + kMoeMaxSlots + 1024;     // + alignment slack
-static_assert(kBarOff % 8 == 0 && kMiscOff % 16 == 0, "barriers and TMEM address are aligned");
-static_assert(kMoeSmem <= 232448, "fits the 227 KB of dynamic shared memory of one CTA");
-static_assert(kSfCol + kMoeStages * kSfSlot <= kMoeTmemCols, "the scale slots fit the TMEM allocation");
+// Shared memory.  E2M1 stages hold half of their bytes' worth of weights (4-bit
+// elements in 16-byte slots), and the 8-byte copies that fill them land through
+// L1: with less than about 30 KB of it left they drop from 6.0 to 3.9 TB/s, so
+// there are four stages instead of five.
+template <bool kFp4>
+struct Lay {
+  static constexpr int kStages = kFp4 ? 4 : 5;
+  static constexpr int kSfOff = kStages * kStageBytes;
+  static constexpr int kBarOff = kSfOff + kStages * kStageSf;
+  static constexpr int kMiscOff = (kBarOff + (2 * kStages + 5) * 8 + 15) & ~15;
+  static constexpr int kOffOff = kMiscOff + 32;                     // int32 [E + 1]: first sorted slot of each expert
+  static constexpr int kTileOff = kOffOff + (kMaxExperts + 4) * 4;  // int32 [E + 1]: first token tile of each expert
+  static constexpr int kSortOff = kTileOff + (kMaxExperts + 4) * 4; // uint16 [slots]: slots by expert
+  static constexpr int kTotal = kSortOff + kMoeMaxSlots * 2 + 1024; // + alignment slack
+  static_assert(kBarOff % 8 == 0, "barriers are aligned");
+  static_assert(kTotal <= (kFp4 ? 195 : 227) * 1024, "fits, and leaves L1 for the E2M1 copies");
+  static_assert(kSfCol + kStages * kSfSlot <= kMoeTmemCols, "the scale slots fit the TMEM allocation");
+};
+static_assert(kMoeMaxSlots * 2 <= kActTile && kPlanWarps * kMaxExperts * 2 <= kActTile,
+              "the ids and the counts of the plan fit an activation tile each");
 
 struct MoeParams {
   const uint16_t* x;
@@ -86,41 +99,70 @@ struct MoeParams {
   const float* weights;
   int T, k, E, H, I;
   const uint8_t* ws;     // packed weight scales of this kernel's matrix
+  uint8_t* xq;           // [T, H] codes of x
+  uint8_t* xs;           // [T, H/32] scale bytes
   uint8_t* hq;           // [slots, I] codes
   uint8_t* hs;           // [slots, I/32] scale bytes
   float* rows;           // [slots, H] weighted down rows
-  uint32_t* tok_cnt;     // [row tiles][4][T] arrivals at a token's rows
+  int32_t* bad;          // set when an id is out of range
   float* part;           // [2 * CTAs][part_tok][256] partial sums of cut units
   int part_tok;
   uint32_t* sync;        // [CTAs][4] arrivals at a cut unit
   void* out;
   int64_t ld_out;
-  int out_f32;
   int32_t* status;
   uint64_t timeout_ns, drain_ns;
   uint32_t idesc;
+  const uint8_t* w;      // this kernel's weight codes (E2M1: read by warps 10-13)
+  int64_t ld_w;
 };
 
-// The contraction stages of all units cut into equal runs, one per CTA.
+// The contraction stages of all units cut into equal runs (to one grain), one per CTA.
 struct Runs {
-  int64_t total;  // stages of all units
   int per_unit;   // stages of one unit
-  int ctas;       // runs (every one has at least one stage)
-  MXG_DEVINL int64_t start(int b) const { return (int64_t)b * total / ctas; }
-  MXG_DEVINL int owner(int64_t s) const { return (int)(((s + 1) * ctas - 1) / total); }
+  int grain;      // runs start at multiples of this many stages
+  int ctas;       // runs (every one has at least one grain)
+  int q, r;       // grains of a run: q + 1 for the first r runs, q for the others
+  MXG_DEVINL Runs(int units, int per_unit_, int max_ctas) : per_unit(per_unit_) {
+    grain = per_unit <= kWholeStages ? per_unit : 1;
+    const int total = units * per_unit;
+    ctas = min(max_ctas, min((total + kMinStages - 1) / kMinStages, total / grain));
+    q = ctas > 0 ? total / grain / ctas : 0;
+    r = ctas > 0 ? total / grain - q * ctas : 0;
+  }
+  MXG_DEVINL int start(int b) const { return (b * q + min(b, r)) * grain; }
+  MXG_DEVINL int owner(int s) const {
+    const int g = s / grain;
+    return g < r * (q + 1) ? g / (q + 1) : r + (g - r * (q + 1)) / q;
+  }
 };
 
-// Walks the segments (the part of one unit inside a run) of this CTA's run.
+// Walks the segments (the part of one unit inside a run) of this CTA's run:
+// the cut unit at its start, the cut unit at its end, then the whole units.
 struct Walker {
-  int64_t s, end;
+  int s, end;           // what is left of the run
   // the current segment: unit, its stages [k0, k1), row tile, expert, tokens sorted[tok0 .. tok0 + n)
   int unit, k0, k1, rt, e, tok0, n;
   MXG_DEVINL bool next(const Runs& r, const int32_t* off, const int32_t* tile, int E) {
     if (s >= end) return false;
-    unit = (int)(s / r.per_unit);
-    k0 = (int)(s - (int64_t)unit * r.per_unit);
-    k1 = (int)min((int64_t)r.per_unit, k0 + (end - s));
-    s += k1 - k0;
+    const int first = s / r.per_unit, last = end / r.per_unit;
+    const int head = s - first * r.per_unit, tail = end - last * r.per_unit;
+    if (head != 0 || first == last) {  // up to the unit's end, or the run's
+      unit = first;
+      k0 = head;
+      k1 = first == last ? tail : r.per_unit;
+      s += k1 - k0;
+    } else if (tail != 0) {
+      unit = last;
+      k0 = 0;
+      k1 = tail;
+      end -= tail;
+    } else {
+      unit = first;
+      k0 = 0;
+      k1 = r.per_unit;
+      s += k1;
+    }
     rt = unit / tile[E];
     const int ti = unit - rt * tile[E];
     e = find_prefix(tile, E, ti);  // the last expert that starts at or before ti: it has tiles
@@ -134,48 +176,45 @@ struct Walker {
 // FP32 magnitude bits -> MX exponent of E4M3 (floor(log2) - 8, at least -127).
 MXG_DEVINL int mx_exponent_f32(uint32_t amax_bits) { return max((int)(amax_bits >> 23) - 127 - 8, -127); }
 
-// Eight BF16 values scaled by `sinv` -> eight E4M3 codes.
-MXG_DEVINL uint2 quantize8_e4m3(const uint4& w, float sinv) {
-  uint2 o;
-  o.x = cvt_e4m3x4(bf16lo_to_f32(w.x) * sinv, bf16hi_to_f32(w.x) * sinv, bf16lo_to_f32(w.y) * sinv,
-                   bf16hi_to_f32(w.y) * sinv);
-  o.y = cvt_e4m3x4(bf16lo_to_f32(w.z) * sinv, bf16hi_to_f32(w.z) * sinv, bf16lo_to_f32(w.w) * sinv,
-                   bf16hi_to_f32(w.w) * sinv);
-  return o;
-}
+__host__ __device__ constexpr int moe_threads(bool fp4) { return kMoeThreads + (fp4 ? kUnpackThreads : 0); }
 
 // kDown: the down kernel (else up).  kFp4: E2M1 weights (else E4M3).
 template <bool kDown, bool kFp4>
-__global__ void __launch_bounds__(kMoeThreads, 1)
-    moe_kernel(const __grid_constant__ CUtensorMap tmW, const MoeParams p) {
+__global__ void __launch_bounds__(moe_threads(kFp4), 1)
+    moe_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS, const MoeParams p) {
+  using L = Lay<kFp4>;
+  constexpr int kMoeStages = L::kStages;
+  constexpr int kSfOff = L::kSfOff;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = ptx::smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = p.T * p.k;
+  constexpr int kThreads = moe_threads(kFp4);
 
-  const uint32_t bar0 = sbase + kBarOff;
-  auto full_w = [&](int s) { return bar0 + 8u * s; };
-  auto full_a = [&](int s) { return bar0 + 8u * (kMoeStages + s); };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (2 * kMoeStages + s); };
-  auto acc_full = [&](int b) { return bar0 + 8u * (3 * kMoeStages + b); };
-  auto acc_empty = [&](int b) { return bar0 + 8u * (3 * kMoeStages + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (3 * kMoeStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMiscOff + 4);
-  int32_t* off = reinterpret_cast<int32_t*>(smem + kOffOff);
-  int32_t* tile = reinterpret_cast<int32_t*>(smem + kTileOff);
-  uint16_t* pos = reinterpret_cast<uint16_t*>(smem + kPosOff);
-  uint16_t* sorted = reinterpret_cast<uint16_t*>(smem + kSortOff);
-  uint8_t* mask = smem + kMaskOff;
+  const uint32_t bar0 = sbase + L::kBarOff;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kMoeStages + s); };
+  auto acc_full = [&](int b) { return bar0 + 8u * (2 * kMoeStages + b); };
+  auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kMoeStages + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kMoeStages + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+  int32_t* off = reinterpret_cast<int32_t*>(smem + L::kOffOff);
+  int32_t* tile = reinterpret_cast<int32_t*>(smem + L::kTileOff);
+  uint16_t* sorted = reinterpret_cast<uint16_t*>(smem + L::kSortOff);
 
   // ---------------------------------------------------------------- plan
-  // Every CTA counts the slots of each expert (the ids are a few KB).
-  for (int e = threadIdx.x; e < p.E; e += kMoeThreads) off[e] = 0;
+  // Every CTA sorts the slots by expert (the ids are a few KB), stably: warps
+  // 2-9 take a range of slots each and count its experts, the counts become
+  // running positions, and the slots are placed.  Ids and counts live in two
+  // activation tiles, which are first written after the sort.
+  int16_t* eid = reinterpret_cast<int16_t*>(smem + 2 * kWTile);
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + kStageBytes + 2 * kWTile);  // [8][E]
+  for (int i = threadIdx.x; i < (kPlanWarps * p.E + 1) / 2; i += kThreads) reinterpret_cast<uint32_t*>(cnt)[i] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMoeStages; ++s) {
-      ptx::mbar_init(full_w(s), 1);
-      ptx::mbar_init(full_a(s), 4);
+      ptx::mbar_init(full_bar(s), 5 + (kFp4 ? kUnpackThreads / 32 : 0));  // warps 0, 6-9 and 10-13
       ptx::mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -186,6 +225,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     *abort_flag = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmW);
+    ptx::prefetch_tmap(&tmS);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kMoeTmemCols);
@@ -193,27 +233,34 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   }
   __syncthreads();
   bool bad = false;
-  const int mask_bytes = (p.k + 7) >> 3;
-  for (int t = threadIdx.x; t < p.T; t += kMoeThreads) {
-    for (int b = 0; b < mask_bytes; ++b) {
-      uint32_t m = 0;
-      for (int j = b * 8; j < min(p.k, b * 8 + 8); ++j) {
-        const int e = __ldg(p.ids + t * p.k + j);
-        bad |= e >= p.E;
-        if (e >= 0 && e < p.E) {
-          m |= 1u << (j & 7);
-          atomicAdd(&off[e], 1);
-        }
-      }
-      mask[t * mask_bytes + b] = (uint8_t)m;
+  const int plan_warp = warp - 2;
+  const bool planner = plan_warp >= 0 && plan_warp < kPlanWarps;
+  const int per_warp = (((P + kPlanWarps - 1) / kPlanWarps) + 31) & ~31;
+  const int slot0 = min(P, plan_warp * per_warp), slot1 = min(P, slot0 + per_warp);
+  uint16_t* my_cnt = cnt + plan_warp * p.E;
+  if (planner) {
+    for (int i0 = slot0; i0 < slot1; i0 += 32) {
+      const int i = i0 + lane;
+      int e = i < slot1 ? __ldg(p.ids + i) : -1;
+      bad |= e >= p.E;
+      if (e < 0 || e >= p.E) e = -1;
+      if (i < slot1) eid[i] = (int16_t)e;
+      const uint32_t same = __match_any_sync(kFull, e);
+      if (e >= 0 && lane == __ffs(same) - 1) my_cnt[e] += (uint16_t)__popc(same);
+      __syncwarp();
     }
   }
   ptx::tc_fence_before();
   bad = __syncthreads_or(bad);
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (!kDown) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.bad = bad;
+  }
+  ptx::pdl_launch_dependents();
   if (bad) {  // every CTA sees it: nothing is written
     if (threadIdx.x == 0) report(p.status, MXG_ERR_INDEX);
+    ptx::pdl_wait();  // a kernel ends after the one before it: the sum kernel finds the flag in place
     if (warp == 1) ptx::tmem_dealloc(tmem, kMoeTmemCols);
     return;
   }
@@ -222,7 +269,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     int c = 0, nt = 0;
     for (int i = 0; i < per; ++i) {
       const int e = lane * per + i;
-      const int v = e < p.E ? off[e] : 0;
+      int v = 0;
+      if (e < p.E) {
+#pragma unroll
+        for (int q = 0; q < kPlanWarps; ++q) v += cnt[q * p.E + e];
+        off[e] = v;
+      }
       c += v;
       nt += (v + kTok - 1) / kTok;
     }
@@ -240,7 +292,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         const int v = off[e];
         off[e] = c;
         tile[e] = nt;
-        pos[e] = (uint16_t)c;
+        int at = c;
+#pragma unroll
+        for (int q = 0; q < kPlanWarps; ++q) {
+          const int m = cnt[q * p.E + e];
+          cnt[q * p.E + e] = (uint16_t)at;
+          at += m;
+        }
         c += v;
         nt += (v + kTok - 1) / kTok;
       }
@@ -248,13 +306,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     if (lane == 31) { off[p.E] = cs; tile[p.E] = ns; }
   }
   __syncthreads();
-  if constexpr (!kDown) ptx::pdl_launch_dependents();
 
   const int row_tiles = kDown ? (p.H + 255) >> 8 : p.I >> 7;
-  Runs runs;
-  runs.per_unit = (kDown ? p.I : p.H) >> 7;
-  runs.total = (int64_t)tile[p.E] * row_tiles * runs.per_unit;
-  runs.ctas = (int)min((int64_t)gridDim.x, (runs.total + kMinStages - 1) / kMinStages);
+  const Runs runs(tile[p.E] * row_tiles, (kDown ? p.I : p.H) >> 7, gridDim.x);
   const int cta = blockIdx.x;
   const bool active = cta < runs.ctas;
   Walker w;
@@ -267,23 +321,59 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_phase = 0;
       bool ok = true;
-      constexpr uint32_t kTileTx = kFp4 ? kWTile / 2 : kWTile;  // the unpacking load counts its source bytes
+      constexpr uint32_t kTileTx = kFp4 ? 0 : kWTile;  // E2M1 tiles come from warps 10-13
       const int64_t rt_all = kDown ? (int64_t)p.E * (p.H >> 7) : (int64_t)p.E * 2 * (p.I >> 7);
+      // E2M1: the stages to come are fetched into L2 four at a time, 256 bytes
+      // of every row, kAhead stages before they are asked for: a stage's ring
+      // slots cover too little of the memory's latency.
+      // The distance grows from the start, so that the first stages' own loads
+      // do not queue behind the prefetches.
+      constexpr int kAhead = 12;
+      Walker pw = w;
+      int pk = 0, pk1 = 0, prow0 = 0, prow1 = 0, ahead = 0, issued = 0;
+      bool ptwo = false, more = kFp4;
+      auto fetch_ahead = [&]() {
+        while (more && ahead < min(kAhead, issued)) {
+          if (pk >= pk1) {
+            more = pw.next(runs, off, tile, p.E);
+            if (!more) return;
+            pk = pw.k0;
+            pk1 = pw.k1;
+            prow0 = kDown ? pw.e * p.H + pw.rt * 256 : pw.e * 2 * p.I + pw.rt * 128;
+            prow1 = kDown ? prow0 + 128 : prow0 + p.I;
+            ptwo = !kDown || pw.rt * 256 + 128 < p.H;
+          }
+          ptx::tma_prefetch_2d(&tmW, pk * 64, prow0);
+          ptx::tma_prefetch_3d(&tmS, 0, prow0 >> 7, pk);
+          if (ptwo) {
+            ptx::tma_prefetch_2d(&tmW, pk * 64, prow1);
+            ptx::tma_prefetch_3d(&tmS, 0, prow1 >> 7, pk);
+          }
+          const int step = min(4, pk1 - pk);
+          pk += step;
+          ahead += step;
+        }
+      };
       while (ok && w.next(runs, off, tile, p.E)) {
         const int row0 = kDown ? w.e * p.H + w.rt * 256 : w.e * 2 * p.I + w.rt * 128;
         const int row1 = kDown ? row0 + 128 : row0 + p.I;
         const bool two = !kDown || w.rt * 256 + 128 < p.H;
         for (int kc = w.k0; kc < w.k1; ++kc) {
+          if constexpr (kFp4) fetch_ahead();
           if (!ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
-          const uint32_t fb = full_w(stage);
+          --ahead;
+          ++issued;
+          const uint32_t fb = full_bar(stage);
           ptx::mbar_arrive_expect_tx(fb, (kTileTx + kChunk) * (two ? 2u : 1u));
           armed |= 1u << stage;
           armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
           const uint32_t sw = sbase + stage * kStageBytes;
           const uint32_t sf = sbase + kSfOff + stage * kStageSf;
           const uint8_t* src = p.ws + (int64_t)kc * rt_all * kChunk;
-          ptx::tma_load_2d(sw, &tmW, kc * 128, row0, fb);
-          if (two) ptx::tma_load_2d(sw + kWTile, &tmW, kc * 128, row1, fb);
+          if constexpr (!kFp4) {
+            ptx::tma_load_2d(sw, &tmW, kc * 128, row0, fb);
+            if (two) ptx::tma_load_2d(sw + kWTile, &tmW, kc * 128, row1, fb);
+          }
           ptx::bulk_load(sf, src + (int64_t)(row0 >> 7) * kChunk, kChunk, fb);
           if (two) ptx::bulk_load(sf + kChunk, src + (int64_t)(row1 >> 7) * kChunk, kChunk, fb);
           if (++stage == kMoeStages) { stage = 0; phase ^= 1u; }
@@ -293,192 +383,195 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       for (int s = 0; s < kMoeStages; ++s)
         if ((armed >> s) & 1u) {
           volatile int no_abort = 0;
-          ptx::mbar_wait(full_w(s), (armed_phase >> s) & 1u, &no_abort, p.status, p.drain_ns);
+          ptx::mbar_wait(full_bar(s), (armed_phase >> s) & 1u, &no_abort, p.status, p.drain_ns);
         }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int stage = 0, count = 0;
-      uint32_t phase = 0;
-      bool ok = true, issued = false;
-      while (ok && w.next(runs, off, tile, p.E)) {
-        const int buf = count & 1;
-        if (!ptx::mbar_wait(acc_empty(buf), ((count >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns)) break;
-        ptx::tc_fence_after();
-        const uint32_t d0 = tmem + buf * 2 * kTok, d1 = d0 + kTok;
-        const bool two = !kDown || w.rt * 256 + 128 < p.H;
-        const uint32_t idesc_n = p.idesc | ((uint32_t)((w.n + 15) >> 4) << 18);  // N / 8, N a multiple of 16
-        for (int kc = w.k0; kc < w.k1; ++kc) {
-          if (!ptx::mbar_wait(full_w(stage), phase, abort_flag, p.status, p.timeout_ns) ||
-              !ptx::mbar_wait(full_a(stage), phase, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
-          ptx::tc_fence_after();
-          const uint32_t sw = sbase + stage * kStageBytes;
-          const uint32_t sf = sbase + kSfOff + stage * kStageSf;
-          const uint32_t tsf = tmem + kSfCol + stage * kSfSlot;
-          ptx::tc_cp_32x128b_warpx4(tsf, ptx::smem_desc(sf, 0, 128, 0));
-          if (two) ptx::tc_cp_32x128b_warpx4(tsf + 4, ptx::smem_desc(sf + kChunk, 0, 128, 0));
-          ptx::tc_cp_32x128b_warpx4(tsf + 8, ptx::smem_desc(sf + 2 * kChunk, 0, 128, 0));
-          const uint64_t a0 = ptx::smem_desc(sw, 16, 1024, 2), a1 = ptx::smem_desc(sw + kWTile, 16, 1024, 2);
-          const uint64_t b = ptx::smem_desc(sw + 2 * kWTile, 16, 1024, 2);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 32 contraction elements (32 bytes of each row) per MMA
-            const uint32_t idesc = idesc_n | (j << 4) | (j << 29);
-            const uint32_t acc = (kc != w.k0) || j != 0;
-            ptx::mma_mxf8f6f4(d0, a0 + 2 * j, b + 2 * j, idesc, tsf, tsf + 8, acc);
-            if (two) ptx::mma_mxf8f6f4(d1, a1 + 2 * j, b + 2 * j, idesc, tsf + 4, tsf + 8, acc);
-          }
-          issued = true;
-          ptx::tc_commit(empty_bar(stage));
-          if (++stage == kMoeStages) { stage = 0; phase ^= 1u; }
+    // The whole warp runs the loop and one lane issues (a lane that gives up a
+    // wait just leaves: nothing below needs the warp together).
+    const uint32_t el = ptx::elect_one();
+    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+    int stage = 0, count = 0;
+    uint32_t phase = 0;
+    bool ok = true, issued = false;
+    while (ok && w.next(runs, off, tile, p.E)) {
+      const int buf = count & 1;
+      ok = ptx::mbar_wait(acc_empty(buf), ((count >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const uint32_t d0 = tm + buf * 2 * kTok, d1 = d0 + kTok;
+      const bool two = !kDown || w.rt * 256 + 128 < p.H;
+      const uint32_t idesc_n = p.idesc | ((uint32_t)((w.n + 15) >> 4) << 18);  // N / 8, N a multiple of 16
+      for (int kc = w.k0; kc < w.k1; ++kc) {
+        if (!ptx::mbar_try_wait(full_bar(stage), phase)) {
+          ok = ptx::mbar_wait(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
+          if (!ok) break;
         }
-        if (!ok) break;
-        ptx::tc_commit(acc_full(buf));
-        ++count;
+        // The stage's plain stores (released by the barrier's arrivals) come
+        // before the MMAs' reads.  The fence is here and not at the writers,
+        // where it would wait for their loads in flight (1000 clocks a stage).
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_after();
+        const uint32_t sw = sbase + stage * kStageBytes;
+        const uint32_t sf = sbase + kSfOff + stage * kStageSf;
+        const uint32_t tsf = tm + kSfCol + stage * kSfSlot;
+        ptx::tc_cp_32x128b_warpx4_if(el, tsf, ptx::smem_desc(sf, 0, 128, 0));
+        if (two) ptx::tc_cp_32x128b_warpx4_if(el, tsf + 4, ptx::smem_desc(sf + kChunk, 0, 128, 0));
+        ptx::tc_cp_32x128b_warpx4_if(el, tsf + 8, ptx::smem_desc(sf + 2 * kChunk, 0, 128, 0));
+        const uint64_t a0 = ptx::smem_desc(sw, 16, 1024, 2), a1 = ptx::smem_desc(sw + kWTile, 16, 1024, 2);
+        const uint64_t b = ptx::smem_desc(sw + 2 * kWTile, 16, 1024, 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 32 contraction elements (32 bytes of each row) per MMA
+          const uint32_t idesc = idesc_n | (j << 4) | (j << 29);
+          const uint32_t acc = (kc != w.k0) || j != 0;
+          ptx::mma_mxf8f6f4_if(el, d0, a0 + 2 * j, b + 2 * j, idesc, tsf, tsf + 8, acc);
+          if (two) ptx::mma_mxf8f6f4_if(el, d1, a1 + 2 * j, b + 2 * j, idesc, tsf + 4, tsf + 8, acc);
+        }
+        issued = true;
+        ptx::tc_commit_if(el, empty_bar(stage));
+        if (++stage == kMoeStages) { stage = 0; phase ^= 1u; }
       }
-      if (issued) {  // every MMA has retired before TMEM is released
-        ptx::tc_commit(drain_bar);
-        volatile int no_abort = 0;
-        ptx::mbar_wait(drain_bar, 0, &no_abort, p.status, p.drain_ns);
+      if (!ok) break;
+      ptx::tc_commit_if(el, acc_full(buf));
+      ++count;
+    }
+    if (issued) {  // every MMA has retired before TMEM is released
+      ptx::tc_commit_if(el, drain_bar);
+      volatile int no_abort = 0;
+      ptx::mbar_wait(drain_bar, 0, &no_abort, p.status, p.drain_ns);
+    }
+  } else if (kFp4 && warp >= 10) {
+    // ------------------------------------------------------------ E2M1 weights
+    // The tensor core takes 4-bit elements as 8 bytes of 16 elements in a
+    // 16-byte slot.  A TMA load that unpacks to this moves a row in 2.9 ns
+    // whatever its length, 3.3 TB/s over the device for rows of 64 bytes;
+    // 8-byte asynchronous copies into the slots reach 6.1 TB/s.
+    // A thread copies piece c of rows r, r + 16, ... of either tile.
+    constexpr int kLag = 2;  // stages in flight before the oldest is handed over
+    const int tid = threadIdx.x - kMoeThreads;
+    const int c = tid & 7, r = tid >> 3;
+    const uint32_t slot = r * 128 + ((c ^ (r & 7)) << 4);
+    int stage = 0, gstage = 0, issued = 0, given = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    auto give = [&]() {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full_bar(gstage));
+      if (++gstage == kMoeStages) gstage = 0;
+      ++given;
+    };
+    while (ok && w.next(runs, off, tile, p.E)) {
+      const int64_t row0 = kDown ? (int64_t)w.e * p.H + w.rt * 256 : (int64_t)w.e * 2 * p.I + w.rt * 128;
+      const int64_t row1 = kDown ? row0 + 128 : row0 + p.I;
+      const bool two = !kDown || w.rt * 256 + 128 < p.H;
+      const uint8_t* src0 = p.w + (row0 + r) * p.ld_w + c * 8;
+      const uint8_t* src1 = p.w + (row1 + r) * p.ld_w + c * 8;
+      const int64_t step = 16 * p.ld_w;
+      for (int kc = w.k0; kc < w.k1; ++kc) {
+        const bool free = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
+        if (!__all_sync(kFull, free)) { ok = false; break; }
+        const uint32_t dst = sbase + stage * kStageBytes + slot;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ptx::cp_async_8(dst + i * 2048, src0 + kc * 64 + i * step);
+        if (two) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ptx::cp_async_8(dst + kWTile + i * 2048, src1 + kc * 64 + i * step);
+        }
+        ptx::cp_async_commit();
+        if (++issued > kLag) {
+          ptx::cp_async_wait<kLag>();
+          give();
+        }
+        if (++stage == kMoeStages) { stage = 0; phase ^= 1u; }
       }
     }
+    ptx::cp_async_wait<0>();
+    while (given < issued) give();
   } else {
     // the sorted slots are only needed by the activation and epilogue warps:
-    // warp 6 sorts (stable, so slots of an expert stay in order) while the
-    // first weights are on their way
-    if (warp == 6) {
-      for (int i0 = 0; i0 < P; i0 += 32) {
-        const int i = i0 + lane;
-        const int e = i < P ? __ldg(p.ids + i) : -1;
-        const uint32_t same = __match_any_sync(kFull, e);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        const int at = e >= 0 ? pos[e] + rank : 0;
-        __syncwarp();
-        if (e >= 0) {
-          sorted[at] = (uint16_t)i;
-          if (rank == 0) pos[e] = (uint16_t)(at + __popc(same));
-        }
-        __syncwarp();
+    // placed while the first weights are on their way
+    for (int i0 = slot0; i0 < slot1; i0 += 32) {
+      const int i = i0 + lane;
+      const int e = i < slot1 ? eid[i] : -1;
+      const uint32_t same = __match_any_sync(kFull, e);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      const int at = e >= 0 ? my_cnt[e] + rank : 0;
+      __syncwarp();
+      if (e >= 0) {
+        sorted[at] = (uint16_t)i;
+        if (rank == 0) my_cnt[e] = (uint16_t)(at + __popc(same));
       }
+      __syncwarp();
     }
     ptx::named_bar_sync(1, kMoeThreads - 64);
 
     if (warp >= 6) {
       // ---------------------------------------------------------- activations
-      // Item i of a stage: token i / 4 of the unit, 32-block i % 4; a thread
-      // takes items tid and tid + 128.  Two stages of loads are in flight.
-      if constexpr (kDown) ptx::pdl_wait();  // hq is complete
+      // Codes and scale bytes go from global to shared memory asynchronously; a
+      // stage is handed over kLag stages after its copies were issued.
+      // Item i of a stage is 32-block i % 4 of token i / 4; a thread takes items
+      // tid and tid + 128, and the scale word of token tid.
+      constexpr int kLag = kMoeStages - 2;
       const int tid = threadIdx.x - 6 * 32;
       const int blk = tid & 3;
-      constexpr int kVec = kDown ? 2 : 4;  // 16-byte loads of a block
-      int stage = 0;
+      const int width = kDown ? p.I : p.H;
+      const uint8_t* codes = kDown ? p.hq : p.xq;
+      const uint8_t* scales = kDown ? p.hs : p.xs;
+      int stage = 0, gstage = 0, issued = 0, given = 0;
       uint32_t phase = 0;
       bool ok = true;
+      auto give = [&]() {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full_bar(gstage));
+        if (++gstage == kMoeStages) gstage = 0;
+        ++given;
+      };
+      ptx::pdl_wait();  // the codes are complete
       while (ok && w.next(runs, off, tile, p.E)) {
-        const uint4* src[2];
-        const uint8_t* ssrc[2];
+        const uint8_t* src[2];
+        const uint8_t* ssrc = nullptr;
         bool on[2];
+        auto row_of = [&](int i) { return kDown ? (int)sorted[w.tok0 + i] : sorted[w.tok0 + i] / p.k; };
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int i = (tid >> 2) + 32 * q;
           on[q] = i < w.n;
-          const int slot = on[q] ? sorted[w.tok0 + i] : 0;
-          if constexpr (kDown) {
-            src[q] = reinterpret_cast<const uint4*>(p.hq + (int64_t)slot * p.I + blk * 32);
-            ssrc[q] = p.hs + (int64_t)slot * (p.I >> 5) + blk;
-          } else {
-            src[q] = reinterpret_cast<const uint4*>(p.x + (int64_t)(slot / p.k) * p.ld_x + blk * 32);
-            ssrc[q] = nullptr;
-          }
+          src[q] = codes + (int64_t)(on[q] ? row_of(i) : 0) * width + blk * 32;
         }
-        uint4 buf[2][2][kVec];
-        uint8_t sbuf[2][2];
-        auto load = [&](int kc, uint4 (*v)[kVec], uint8_t* sv) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            if (on[q]) {
-#pragma unroll
-              for (int i = 0; i < kVec; ++i)
-                v[q][i] = kDown ? __ldcg(src[q] + kc * 8 + i) : __ldg(src[q] + kc * 16 + i);
-              if constexpr (kDown) sv[q] = __ldcg(ssrc[q] + kc * 4);
-            }
-        };
-        auto store = [&](const uint4 (*v)[kVec], const uint8_t* sv) {
-          const uint32_t st = stage * kStageBytes + 2 * kWTile;
+        if (tid < w.n) ssrc = scales + (int64_t)row_of(tid) * (width >> 5);
+        for (int kc = w.k0; kc < w.k1; ++kc) {
+          const bool free = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
+          if (!__all_sync(kFull, free)) { ok = false; break; }
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             if (on[q]) {
               const int i = (tid >> 2) + 32 * q;
-              uint4 c0, c1;
-              uint8_t sc;
-              if constexpr (kDown) {
-                c0 = v[q][0];
-                c1 = v[q][1];
-                sc = sv[q];
-              } else {
-                uint32_t m = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  m = __vmaxu2(m, v[q][j].x & 0x7FFF7FFFu);
-                  m = __vmaxu2(m, v[q][j].y & 0x7FFF7FFFu);
-                  m = __vmaxu2(m, v[q][j].z & 0x7FFF7FFFu);
-                  m = __vmaxu2(m, v[q][j].w & 0x7FFF7FFFu);
-                }
-                const int ex = mx_exponent_from_amax_bits(max(m & 0xFFFFu, m >> 16), 8);
-                const float sinv = pow2_neg(ex);
-                const uint2 r0 = quantize8_e4m3(v[q][0], sinv), r1 = quantize8_e4m3(v[q][1], sinv);
-                const uint2 r2 = quantize8_e4m3(v[q][2], sinv), r3 = quantize8_e4m3(v[q][3], sinv);
-                c0 = make_uint4(r0.x, r0.y, r1.x, r1.y);
-                c1 = make_uint4(r2.x, r2.y, r3.x, r3.y);
-                sc = (uint8_t)(ex + 127);
-              }
-              uint8_t* row = smem + st + i * 128;  // 16-byte chunk c of row i sits at c ^ (i % 8)
-              *reinterpret_cast<uint4*>(row + ((2 * blk) ^ (i & 7)) * 16) = c0;
-              *reinterpret_cast<uint4*>(row + ((2 * blk + 1) ^ (i & 7)) * 16) = c1;
-              smem[kSfOff + stage * kStageSf + 2 * kChunk + (i & 31) * 16 + (i >> 5) * 4 + blk] = sc;
+              // 16-byte chunk c of row i sits at c ^ (i % 8)
+              const uint32_t row = sbase + stage * kStageBytes + 2 * kWTile + i * 128;
+              ptx::cp_async_16(row + ((2 * blk) ^ (i & 7)) * 16, src[q] + kc * 128);
+              ptx::cp_async_16(row + ((2 * blk + 1) ^ (i & 7)) * 16, src[q] + kc * 128 + 16);
             }
-        };
-        load(w.k0, buf[0], sbuf[0]);
-        if (w.k0 + 1 < w.k1) load(w.k0 + 1, buf[1], sbuf[1]);
-        for (int kc = w.k0; ok && kc < w.k1; kc += 2) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (kc + h < w.k1) {
-              const bool free = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
-              if (!__all_sync(kFull, free)) { ok = false; break; }
-              store(buf[h], sbuf[h]);
-              if (kc + h + 2 < w.k1) load(kc + h + 2, buf[h], sbuf[h]);
-              ptx::fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(full_a(stage));
-              if (++stage == kMoeStages) { stage = 0; phase ^= 1u; }
-            }
+          if (ssrc != nullptr)
+            ptx::cp_async_4(sbase + kSfOff + stage * kStageSf + 2 * kChunk + (tid & 31) * 16 + (tid >> 5) * 4,
+                            ssrc + kc * 4);
+          ptx::cp_async_commit();
+          if (++issued > kLag) {
+            ptx::cp_async_wait<kLag>();
+            give();
           }
+          if (++stage == kMoeStages) { stage = 0; phase ^= 1u; }
         }
       }
+      ptx::cp_async_wait<0>();
+      while (given < issued) give();
     } else {
       // ---------------------------------------------------------- epilogue (warps 2-5)
       // Warp q has TMEM lanes 32 q .. 32 q + 31: lane l is row 32 q + l of
       // either weight tile, a column is a token.  Each warp works alone.
       const int quarter = warp & 3;
       const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
-      if constexpr (kDown) {
-        ptx::pdl_wait();  // the counters and partial buffers are free, hq's writer is done
-        // tokens without slots: zeros
-        for (int t = cta; t < p.T; t += gridDim.x) {
-          uint32_t any = 0;
-          for (int b = 0; b < mask_bytes; ++b) any |= mask[t * mask_bytes + b];
-          if (any == 0)
-            for (int c = quarter * 32 + lane; c < p.H; c += 128) {
-              if (p.out_f32) static_cast<float*>(p.out)[t * p.ld_out + c] = 0.0f;
-              else static_cast<uint16_t*>(p.out)[t * p.ld_out + c] = 0;
-            }
-        }
-      } else {
-        // the down kernel's counters start at zero
-        const int words = ((p.H + 255) >> 8) * 4 * p.T;
-        for (int i = cta * 128 + quarter * 32 + lane; i < words; i += gridDim.x * 128) p.tok_cnt[i] = 0;
-      }
+      ptx::pdl_wait();  // the kernel before is done with the counters and partial buffers
       int count = 0;
       while (w.next(runs, off, tile, p.E)) {
         const int buf = count & 1;
@@ -493,18 +586,18 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         ++count;
         const uint32_t d0 = tq + buf * 2 * kTok, d1 = d0 + kTok;
         const bool two = !kDown || w.rt * 256 + 128 < p.H;
-        const int64_t u0 = (int64_t)w.unit * runs.per_unit;
+        const int u0 = w.unit * runs.per_unit;
         const bool whole = w.k0 == 0 && w.k1 == runs.per_unit;
 
-        // 16 tokens' pairs of values (gate and up, or two output rows) of this
-        // lane's row; computed for all 16 so that they interleave, stored for
+        // 8 tokens' pairs of values (gate and up, or two output rows) of this
+        // lane's row; computed for all 8 so that they interleave, stored for
         // the unit's tokens only
         auto finish = [&](int c0, const float* v0, const float* v1) {
           if constexpr (kDown) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
+              const float wt = __shfl_sync(kFull, c0 < 32 ? wt_lo : wt_hi, (c0 + i) & 31);
               if (c0 + i < w.n) {
-                const float wt = __shfl_sync(kFull, c0 < 32 ? wt_lo : wt_hi, (c0 + i) & 31);
                 const int slot = sorted[w.tok0 + c0 + i];
                 float* dst = p.rows + (int64_t)slot * p.H + w.rt * 256 + quarter * 32 + lane;
                 __stcg(dst, v0[i] * wt);
@@ -512,17 +605,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
               }
             }
           } else {
-            uint32_t code[16];
-            int ex[16];
+            uint32_t code[8];
+            int ex[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const float h = v0[i] / (1.0f + expf(-v0[i])) * v1[i];
               // the block of 32 channels is this warp's 32 lanes
               ex[i] = mx_exponent_f32(__reduce_max_sync(kFull, __float_as_uint(h) & 0x7FFFFFFFu));
               code[i] = cvt_e4m3x4(h * pow2_neg(ex[i]), 0.0f, 0.0f, 0.0f);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               if (c0 + i < w.n) {
                 const int slot = sorted[w.tok0 + c0 + i];
                 p.hq[(int64_t)slot * p.I + w.rt * 128 + quarter * 32 + lane] = (uint8_t)code[i];
@@ -532,25 +625,25 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           }
         };
         float* mine = p.part + (int64_t)(2 * cta + (w.k0 == 0)) * p.part_tok * 256 + quarter * 32 + lane;
-        for (int c0 = 0; c0 < w.n; c0 += 16) {
-          uint32_t r0[16], r1[16];
+        for (int c0 = 0; c0 < w.n; c0 += 8) {
+          uint32_t r0[8], r1[8];
           __syncwarp();
-          ptx::tmem_ld_32x32b_x16(d0 + c0, r0);
-          ptx::tmem_ld_32x32b_x16(d1 + c0, r1);
+          ptx::tmem_ld_32x32b_x8(d0 + c0, r0);
+          ptx::tmem_ld_32x32b_x8(d1 + c0, r1);
           ptx::tmem_ld_wait();
-          if (c0 + 16 >= w.n) {  // last read: hand the accumulator back
+          if (c0 + 8 >= w.n) {  // last read: hand the accumulator back
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(acc_empty(buf));
           }
-          float v0[16], v1[16];
+          float v0[8], v1[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) { v0[i] = __uint_as_float(r0[i]); v1[i] = __uint_as_float(r1[i]); }
+          for (int i = 0; i < 8; ++i) { v0[i] = __uint_as_float(r0[i]); v1[i] = __uint_as_float(r1[i]); }
           if (whole) {
             finish(c0, v0, v1);
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 8; ++i)
               if (c0 + i < w.n) {
                 __stcg(mine + (c0 + i) * 256, v0[i]);
                 if (two) __stcg(mine + (c0 + i) * 256 + 128, v1[i]);
@@ -568,98 +661,23 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           if (got != (uint32_t)(last - first)) continue;
           __threadfence();
           const int64_t step = (int64_t)p.part_tok * 256;
-          for (int c0 = 0; c0 < w.n; c0 += 16) {
-            float v0[16], v1[16];
+          for (int c0 = 0; c0 < w.n; c0 += 8) {
+            float v0[8], v1[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.0f;
+            for (int i = 0; i < 8; ++i) v0[i] = v1[i] = 0.0f;
             // buffers 2 first + 1, 2 (first + 1), 2 (first + 2), ...
             for (int b = first; b <= last; ++b) {
               const float* src = p.part + (2 * b + (b == first)) * step + c0 * 256 + quarter * 32 + lane;
-              float a0[16], a1[16];
+              float a0[8], a1[8];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
+              for (int i = 0; i < 8; ++i) {
                 a0[i] = c0 + i < w.n ? __ldcg(src + i * 256) : 0.0f;
                 a1[i] = two && c0 + i < w.n ? __ldcg(src + i * 256 + 128) : 0.0f;
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) { v0[i] += a0[i]; v1[i] += a1[i]; }
+              for (int i = 0; i < 8; ++i) { v0[i] += a0[i]; v1[i] += a1[i]; }
             }
             finish(c0, v0, v1);
-          }
-        }
-        if constexpr (kDown) {
-          // this warp's rows of the unit's slots are in place; whoever brings
-          // a token's last slot sums the token's slots
-          __threadfence();
-          __syncwarp();
-          uint32_t* cnt = p.tok_cnt + (int64_t)(w.rt * 4 + quarter) * p.T;
-#pragma unroll 1
-          for (int c0 = 0; c0 < w.n; c0 += 32) {
-            bool done = false;
-            int t = 0;
-            if (c0 + lane < w.n) {
-              t = sorted[w.tok0 + c0 + lane] / p.k;
-              int v = 0;
-              for (int b = 0; b < mask_bytes; ++b) v += __popc((uint32_t)mask[t * mask_bytes + b]);
-              done = atomicInc(cnt + t, (uint32_t)(v - 1)) == (uint32_t)(v - 1);
-            }
-            uint32_t todo = __ballot_sync(kFull, done);
-            if (todo) __threadfence();
-            // Four tokens at a time.  Lane 8 a + b reads rows 4 b .. 4 b + 3
-            // (16 bytes) of slots a, a + 4, ...; the four partial sums are
-            // then added across the lanes.
-            const int a = lane >> 3;
-            const int64_t r = w.rt * 256 + quarter * 32 + 4 * (lane & 7);
-            while (todo) {
-              int tt[4];
-              float4 s0[4], s1[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                tt[q] = todo ? __shfl_sync(kFull, t, __ffs(todo) - 1) : -1;
-                todo &= todo - 1;
-                s0[q] = s1[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              }
-              for (int j = a; j < ((p.k + 3) & ~3); j += 4) {
-                float4 x0[4], x1[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  x0[q] = x1[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                  if (tt[q] >= 0 && j < p.k && (mask[tt[q] * mask_bytes + (j >> 3)] >> (j & 7)) & 1) {
-                    const float4* src = reinterpret_cast<const float4*>(p.rows + (int64_t)(tt[q] * p.k + j) * p.H + r);
-                    x0[q] = __ldcg(src);
-                    if (two) x1[q] = __ldcg(src + 32);
-                  }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  s0[q].x += x0[q].x; s0[q].y += x0[q].y; s0[q].z += x0[q].z; s0[q].w += x0[q].w;
-                  s1[q].x += x1[q].x; s1[q].y += x1[q].y; s1[q].z += x1[q].z; s1[q].w += x1[q].w;
-                }
-              }
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                float* f0 = &s0[q].x;
-                float* f1 = &s1[q].x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  f0[i] += __shfl_xor_sync(kFull, f0[i], 8);
-                  f0[i] += __shfl_xor_sync(kFull, f0[i], 16);
-                  f1[i] += __shfl_xor_sync(kFull, f1[i], 8);
-                  f1[i] += __shfl_xor_sync(kFull, f1[i], 16);
-                }
-                if (tt[q] >= 0 && a < (two ? 2 : 1)) {  // lanes 0-7 write the first tile's rows, 8-15 the second's
-                  const float4 o = a == 0 ? s0[q] : s1[q];
-                  const int64_t at = tt[q] * p.ld_out + r + 128 * a;
-                  if (p.out_f32) {
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o;
-                  } else {
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                  }
-                }
-              }
-            }
           }
         }
       }
@@ -676,12 +694,104 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// x rounded to MXFP8, a 32-element block per thread (the rule and bytes of the
+// row-wise quantizer), and the counters of the joins zeroed.
+// ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 128;
+
+// Eight BF16 values scaled by `sinv` -> eight E4M3 codes.
+MXG_DEVINL uint2 quantize8_e4m3(const uint4& w, float sinv) {
+  uint2 o;
+  o.x = cvt_e4m3x4(bf16lo_to_f32(w.x) * sinv, bf16hi_to_f32(w.x) * sinv, bf16lo_to_f32(w.y) * sinv,
+                   bf16hi_to_f32(w.y) * sinv);
+  o.y = cvt_e4m3x4(bf16lo_to_f32(w.z) * sinv, bf16hi_to_f32(w.z) * sinv, bf16lo_to_f32(w.w) * sinv,
+                   bf16hi_to_f32(w.w) * sinv);
+  return o;
+}
+
+__global__ void __launch_bounds__(kQuantThreads) moe_quant_kernel(const MoeParams p) {
+  ptx::pdl_launch_dependents();
+  const int i = blockIdx.x * kQuantThreads + threadIdx.x;
+  if (i < kSyncWords) p.sync[i] = 0;
+  const int nb = p.H >> 5;
+  if (i >= p.T * nb) return;
+  const int t = i / nb, b = i - t * nb;
+  const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ld_x + b * 32);
+  uint4 v[4];
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = __ldg(src + j);
+    m = __vmaxu2(m, v[j].x & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v[j].y & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v[j].z & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v[j].w & 0x7FFF7FFFu);
+  }
+  const int ex = mx_exponent_from_amax_bits(max(m & 0xFFFFu, m >> 16), 8);
+  const float sinv = pow2_neg(ex);
+  const uint2 r0 = quantize8_e4m3(v[0], sinv), r1 = quantize8_e4m3(v[1], sinv);
+  const uint2 r2 = quantize8_e4m3(v[2], sinv), r3 = quantize8_e4m3(v[3], sinv);
+  uint4* dst = reinterpret_cast<uint4*>(p.xq + (int64_t)i * 32);
+  dst[0] = make_uint4(r0.x, r0.y, r1.x, r1.y);
+  dst[1] = make_uint4(r2.x, r2.y, r3.x, r3.y);
+  p.xs[i] = (uint8_t)(ex + 127);
+}
+
+// ---------------------------------------------------------------------------
+// Sum of each token's slots, in order; a token without slots gives zeros.
+// A thread takes four columns of a token; eight slots' rows are in flight.
+// ---------------------------------------------------------------------------
+constexpr int kSumThreads = 128;
+
+template <typename TOut>
+__global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const MoeParams p) {
+  const int t = blockIdx.x;
+  const int c = (blockIdx.y * kSumThreads + threadIdx.x) * 4;
+  ptx::pdl_wait();
+  if (c >= p.H || *p.bad) return;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t slot = (int64_t)t * p.k + j0 + j;
+      v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (j0 + j < p.k && __ldg(p.ids + slot) >= 0) v[j] = __ldcg(reinterpret_cast<const float4*>(p.rows + slot * p.H + c));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) { s.x += v[j].x; s.y += v[j].y; s.z += v[j].z; s.w += v[j].w; }
+  }
+  TOut* o = static_cast<TOut*>(p.out) + t * p.ld_out + c;
+  if constexpr (sizeof(TOut) == 4) {
+    *reinterpret_cast<float4*>(o) = s;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+    *reinterpret_cast<uint2*>(o) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+// 2-D byte map without swizzle.
+bool make_plain_tmap(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t ld, int box_inner, int box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct MoeWs {
-  uint8_t *hq, *hs;
+  uint8_t *xq, *xs, *hq, *hs;
+  uint32_t* sync;
   float* rows;
-  uint32_t* tok_cnt;
+  int32_t* bad;
   float* part;
   int part_tok;
   size_t total;
@@ -696,10 +806,13 @@ MoeWs moe_ws(int64_t T, int k, int64_t H, int64_t I, uint8_t* p) {
     o += ((size_t)n + 255) & ~(size_t)255;
     return r;
   };
+  w.sync = reinterpret_cast<uint32_t*>(take(kSyncWords * 4));
+  w.xq = take(T * H);
+  w.xs = take(T * (H / 32));
   w.hq = take(P * I);
   w.hs = take(P * (I / 32));
   w.rows = reinterpret_cast<float*>(take(P * H * 4));
-  w.tok_cnt = reinterpret_cast<uint32_t*>(take((H + 255) / 256 * 4 * T * 4));
+  w.bad = reinterpret_cast<int32_t*>(take(4));
   w.part_tok = (int)std::min<int64_t>(kTok, P);
   w.part = reinterpret_cast<float*>(take((int64_t)2 * kMaxCtas * w.part_tok * 256 * 4));
   w.total = o;
@@ -720,7 +833,8 @@ bool ensure_moe_attr(int dev) {
   std::lock_guard<std::mutex> lk(g_moe_mu);
   if (dev >= 0 && dev < kMoeMaxDevices && done[dev]) return true;
   for (int i = 0; i < 4; ++i)
-    if (cudaFuncSetAttribute(moe_fn(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmem) !=
+    if (cudaFuncSetAttribute(moe_fn(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             i & 2 ? Lay<true>::kTotal : Lay<false>::kTotal) !=
         cudaSuccess) {
       cudaGetLastError();
       return false;
@@ -748,10 +862,9 @@ mxg_status launch_moe_experts(const MoeArgs& a, cudaStream_t stream, int num_sms
   p.x = a.x; p.ld_x = a.ld_x;
   p.ids = a.ids; p.weights = a.weights;
   p.T = a.T; p.k = a.k; p.E = a.E; p.H = a.H; p.I = a.I;
-  p.hq = ws.hq; p.hs = ws.hs; p.rows = ws.rows; p.tok_cnt = ws.tok_cnt;
+  p.xq = ws.xq; p.xs = ws.xs; p.hq = ws.hq; p.hs = ws.hs; p.sync = ws.sync; p.rows = ws.rows; p.bad = ws.bad;
   p.part = ws.part; p.part_tok = ws.part_tok;
-  p.sync = reinterpret_cast<uint32_t*>(a.sync);
-  p.out = a.out; p.ld_out = a.ld_out; p.out_f32 = a.out_dtype == MXG_OUT_F32;
+  p.out = a.out; p.ld_out = a.ld_out;
   p.status = a.status;
   p.timeout_ns = wait_timeout_ns();
   p.drain_ns = std::max<uint64_t>(p.timeout_ns, 200000000ull);
@@ -759,30 +872,49 @@ mxg_status launch_moe_experts(const MoeArgs& a, cudaStream_t stream, int num_sms
   // both K-major, UE8M0 scales, M = 128; N is added per unit
   p.idesc = ((fp4 ? 5u : 0u) << 7) | (1u << 23) | ((128u >> 4) << 24);
 
-  const CUtensorMapDataType dt = fp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  CUtensorMap tm13, tm2;
-  if (!make_tmap(&tm13, a.w13, dt, a.H, (int64_t)a.E * 2 * a.I, a.ld13, 128, 128) ||
-      !make_tmap(&tm2, a.w2, dt, a.I, (int64_t)a.E * a.H, a.ld2, 128, 128))
-    return MXG_ERR_CUDA;
+  CUtensorMap tmW[2], tmS[2];  // E4M3: the stages' tiles; E2M1: 256 bytes of 128 rows for the L2 prefetch
+  for (int i = 0; i < 2; ++i) {
+    const uint8_t* w = i ? a.w2 : a.w13;
+    const int64_t rows = i ? (int64_t)a.E * a.H : (int64_t)a.E * 2 * a.I, cols = i ? a.I : a.H, ld = i ? a.ld2 : a.ld13;
+    const bool ok = fp4 ? make_plain_tmap(&tmW[i], w, cols / 2, rows, ld, 256, 128)
+                        : make_tmap(&tmW[i], w, CU_TENSOR_MAP_DATA_TYPE_UINT8, cols, rows, ld, 128, 128);
+    if (!ok || !make_scale_tmap(&tmS[i], i ? a.s2 : a.s13, rows / 128, cols / 128, 1, 4)) return MXG_ERR_CUDA;
+  }
 
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(num_sms, kMaxCtas));
-  cfg.blockDim = dim3(kMoeThreads);
-  cfg.dynamicSmemBytes = kMoeSmem;
-  cfg.stream = stream;
-  p.ws = a.s13;
-  {
-    void* args[] = {(void*)&tm13, (void*)&p};
-    if (cudaLaunchKernelExC(&cfg, moe_fn(false, fp4), args) != cudaSuccess) { cudaGetLastError(); return MXG_ERR_CUDA; }
-  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  p.ws = a.s2;
-  void* args[] = {(void*)&tm2, (void*)&p};
-  if (cudaLaunchKernelExC(&cfg, moe_fn(true, fp4), args) != cudaSuccess) { cudaGetLastError(); return MXG_ERR_CUDA; }
+  auto launch = [&](const void* fn, dim3 grid, int threads, int smem, void** args, bool overlap) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.numAttrs = overlap ? 1 : 0;
+    if (cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+  };
+  void* pargs[] = {(void*)&p};
+  const int64_t blocks = std::max<int64_t>((int64_t)a.T * (a.H / 32), kSyncWords);
+  if (!launch((const void*)moe_quant_kernel, dim3((unsigned)((blocks + kQuantThreads - 1) / kQuantThreads)),
+              kQuantThreads, 0, pargs, false))
+    return MXG_ERR_CUDA;
+  for (int i = 0; i < 2; ++i) {
+    p.ws = i ? a.s2 : a.s13;
+    p.w = i ? a.w2 : a.w13;
+    p.ld_w = i ? a.ld2 : a.ld13;
+    void* args[] = {(void*)&tmW[i], (void*)&tmS[i], (void*)&p};
+    if (!launch(moe_fn(i == 1, fp4), dim3((unsigned)std::min(num_sms, kMaxCtas)), moe_threads(fp4),
+                fp4 ? Lay<true>::kTotal : Lay<false>::kTotal, args, true))
+      return MXG_ERR_CUDA;
+  }
+  const void* sum = a.out_dtype == MXG_OUT_F32 ? (const void*)moe_sum_kernel<float>
+                                               : (const void*)moe_sum_kernel<__nv_bfloat16>;
+  if (!launch(sum, dim3((unsigned)a.T, (unsigned)((a.H / 4 + kSumThreads - 1) / kSumThreads)), kSumThreads, 0, pargs,
+              true))
+    return MXG_ERR_CUDA;
   return MXG_OK;
 }
 

@@ -502,21 +502,16 @@ mxg_status moe_route(const void* logits, int64_t tokens, int32_t experts, int64_
  *   out     : [tokens, hidden] of out_dtype, row stride ld_out, 16-byte
  *             aligned rows
  *   ws      : at least moe_experts_workspace_size(...) bytes, 256-byte aligned
- *   d_sync  : MXG_MOE_SYNC_WORDS int32 words in device memory, zeroed by the
- *             caller once.  Every completed call leaves them zero, so calls in
- *             stream order share them; calls that may overlap need their own
- *             ws and d_sync.  After MXG_ERR_TIMEOUT zero them again.
- * hidden % 128 == 0, inter % 128 == 0, 1 <= experts <= 512, 1 <= top_k <= 32,
- * tokens * top_k <= 4096 (tokens may be 0).  The weights of an expert are read
+ * hidden and inter multiples of 128 up to 65536, 1 <= experts <= 512, 1 <=
+ * top_k <= 32, tokens * top_k <= 4096 (tokens may be 0).  The weights of an expert are read
  * once per 64 tokens routed to it: for hundreds of tokens per expert use the
  * grouped GEMMs.  Device error: MXG_ERR_INDEX (an id >= experts; out is not
  * written). */
-#define MXG_MOE_SYNC_WORDS 1024
 size_t moe_experts_workspace_size(int64_t tokens, int32_t top_k, int32_t experts, int64_t hidden, int64_t inter);
 mxg_status moe_experts(const void* x, int64_t tokens, int64_t ld_x, const int32_t* ids, const float* weights,
                        int32_t top_k, int32_t experts, const mxg_mx_operand* W13, const mxg_mx_operand* W2,
-                       void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes, int32_t* d_sync,
-                       int32_t* d_status, void* stream);
+                       void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes, int32_t* d_status,
+                       void* stream);
 
 /* Low-rank adapters of many requests beside a shared projection:
  *   out[t, :] = y[t, :] + scale[a] * B[a] (A[a] x[t, :]),   a = ids[t]

@@ -45,15 +45,14 @@ def test_experts_refusals(lib):
     assert need > 0
     p = ctypes.byref
     w13, w2 = _op(E * 2 * I, H, 1), _op(E * H, I, 1)
-    #       x         T  ld_x ids      weights   k  E  W13     W2     out       ld dt ws        bytes sync      status
-    args = [vp(FAKE), 8, H, vp(FAKE), vp(FAKE), 2, E, p(w13), p(w2), vp(FAKE), H, 1, vp(FAKE), need, vp(FAKE), vp(FAKE),
-            None]
-    for at in (0, 3, 4, 7, 8, 9, 14, 15):
+    #       x         T  ld_x ids      weights   k  E  W13     W2     out       ld dt ws        bytes status
+    args = [vp(FAKE), 8, H, vp(FAKE), vp(FAKE), 2, E, p(w13), p(w2), vp(FAKE), H, 1, vp(FAKE), need, vp(FAKE), None]
+    for at in (0, 3, 4, 7, 8, 9, 14):
         refuse(f, args, at, None, 1)
     for at, value, code in ((1, -1, 2), (1, 2049, 2), (5, 0, 2), (5, 33, 2), (6, 0, 2), (6, 513, 2), (6, 3, 2),
                             (2, H - 8, 2), (2, H + 4, 3), (10, H - 8, 2), (10, H + 4, 3), (11, 0, 5), (12, None, 9),
                             (13, need - 1, 9), (0, vp(FAKE + 8), 3), (9, vp(FAKE + 8), 3), (12, vp(FAKE + 64), 3),
-                            (3, vp(FAKE + 1), 3), (14, vp(FAKE + 2), 3)):
+                            (3, vp(FAKE + 1), 3), (4, vp(FAKE + 2), 3)):
         refuse(f, args, at, value, code)
     for bad, code in ((_op(E * 2 * I, H, 1, layout=0), 5), (_op(E * 2 * I, H, 2), 5), (_op(E * 2 * I - 32, H, 1), 2),
                       (_op(E * 2 * I, H, 1, data=FAKE + 16), 3), (_op(E * 2 * I, H, 1, ld=144), 3),
@@ -62,7 +61,7 @@ def test_experts_refusals(lib):
     refuse(f, args, 8, p(_op(E * H, I + 128, 1)), 2)
     assert lib.moe_experts_workspace_size(2049, 2, E, H, I) == 0
     assert lib.moe_experts_workspace_size(8, 2, E, H + 32, I) == 0
-    assert f(None, 0, H, None, None, 2, E, p(w13), p(w2), None, H, 1, None, 0, vp(FAKE), vp(FAKE), None) == 0
+    assert f(None, 0, H, None, None, 2, E, p(w13), p(w2), None, H, 1, None, 0, vp(FAKE), None) == 0
 
 
 def test_lora_refusals(lib):
