@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
       // slots cover too little of the memory's latency.
       // The distance grows from the start, so that the first stages' own loads
       // do not queue behind the prefetches.
-      constexpr int kAhead = 12;
+      constexpr int kAhead = 6;
       Walker pw = w;
       int pk = 0, pk1 = 0, prow0 = 0, prow1 = 0, ahead = 0, issued = 0;
       bool ptwo = false, more = kFp4;
