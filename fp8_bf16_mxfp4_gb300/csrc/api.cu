@@ -827,7 +827,7 @@ bool moe_sizes_ok(int64_t tokens, int32_t top_k, int32_t experts, int64_t hidden
 }
 
 bool lora_sizes_ok(int64_t tokens, int64_t K, int32_t rank) {
-  return tokens >= 0 && tokens <= (1 << 22) - 64 && K > 0 && K % 8 == 0 && K <= 0x7FFFFFFF && rank >= 8 &&
+  return tokens >= 0 && tokens <= 65535 * 32 && K > 0 && K % 8 == 0 && K <= 0x7FFFFFFF && rank >= 8 &&
          rank % 8 == 0 && rank <= kMaxRank;
 }
 
