@@ -244,7 +244,6 @@ MXG_DEVINL void read_tile(Tile& s, const LoraArgs& a, int64_t t0) {
 // shrink: grid (K split, tiles, adapter groups).  The warps of a CTA take every
 // fourth 32-element block of its K range, up to 32 ranks at a time.
 __global__ void __launch_bounds__(kLoraThreads, 4) lora_shrink_tile_kernel(const LoraParams p) {
-  constexpr int kUnroll = 2;  // blocks in flight
   __shared__ Tile tile;
   __shared__ float red[kLoraWarps][kTile][33];
   ptx::pdl_launch_dependents();
@@ -255,13 +254,23 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_shrink_tile_kernel(const
   const int64_t kblocks = (a.K + 31) >> 5;
   const int64_t b0 = (int64_t)blockIdx.x * p.blocks;
   const int nb = (int)min((int64_t)p.blocks, kblocks - b0);
-  const uint16_t* xk = a.x + t0 * a.ld_x + b0 * 32 + 8 * tq;
-  const int kleft = (int)min(a.K - b0 * 32, (int64_t)nb * 32) - 8 * tq;  // of this lane's first block on
+  // rows past the batch are read from its last token (their products are not used)
+  const uint16_t* xr[kGroups][2];
+#pragma unroll
+  for (int m = 0; m < kGroups; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      xr[m][h] = a.x + min(t0 + m * 16 + g + 8 * h, a.T - 1) * a.ld_x + b0 * 32 + 8 * tq;
+  const int whole = (int)min((int64_t)nb, (a.K >> 5) - b0);  // blocks that do not end past K
   for (int o = blockIdx.z; o < tile.count; o += gridDim.z) {
     const uint32_t groups = tile.groups[o];
     for (int r0 = 0; r0 < a.R; r0 += 32) {
       const int nt = min(4, (a.R - r0) >> 3);
-      const uint16_t* ak = a.A + ((int64_t)tile.list[o] * a.R + r0 + g) * a.K + b0 * 32 + 8 * tq;
+      // products past the ranks are skipped; their loads repeat the first eight rows
+      const uint16_t* ar[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        ar[n] = a.A + ((int64_t)tile.list[o] * a.R + r0 + (n < nt ? 8 * n : 0) + g) * a.K + b0 * 32 + 8 * tq;
       float acc[kGroups][4][4];
 #pragma unroll
       for (int m = 0; m < kGroups; ++m)
@@ -269,40 +278,50 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_shrink_tile_kernel(const
         for (int n = 0; n < 4; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-      for (int b = warp; b < nb; b += kLoraWarps * kUnroll) {
-        uint4 xv[kUnroll][kGroups][2], av[kUnroll][4];
+      // two blocks' loads are in flight while a third is multiplied
+      uint4 xv[2][kGroups][2], av[2][4];
+      auto load = [&](int b, int q) {
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q) {
-          const int k = (b + q * kLoraWarps) * 32;
-          const bool in = k < kleft;
+        for (int n = 0; n < 4; ++n) av[q][n] = __ldg(reinterpret_cast<const uint4*>(ar[n] + b * 32));
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            av[q][n] = make_uint4(0, 0, 0, 0);
-            if (in && n < nt) av[q][n] = __ldg(reinterpret_cast<const uint4*>(ak + (int64_t)n * 8 * a.K + k));
+        for (int m = 0; m < kGroups; ++m)
+          if ((groups >> m) & 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) xv[q][m][h] = __ldg(reinterpret_cast<const uint4*>(xr[m][h] + b * 32));
           }
+      };
+      auto multiply = [&](int q) {
 #pragma unroll
-          for (int m = 0; m < kGroups; ++m)
+        for (int m = 0; m < kGroups; ++m)
+          if ((groups >> m) & 1) {
+            const uint4 lo = xv[q][m][0], hi = xv[q][m][1];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int row = m * 16 + g + 8 * h;
-              xv[q][m][h] = make_uint4(0, 0, 0, 0);
-              if (in && ((groups >> m) & 1) && t0 + row < a.T)
-                xv[q][m][h] = __ldg(reinterpret_cast<const uint4*>(xk + row * a.ld_x + k));
-            }
-        }
+            for (int n = 0; n < 4; ++n)
+              if (n < nt) {
+                mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, av[q][n].x, av[q][n].y);
+                mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, av[q][n].z, av[q][n].w);
+              }
+          }
+      };
+      if (warp < whole) load(warp, 0);
+      if (warp + kLoraWarps < whole) load(warp + kLoraWarps, 1);
+      for (int b = warp; b < whole; b += 2 * kLoraWarps) {
+        multiply(0);
+        if (b + 2 * kLoraWarps < whole) load(b + 2 * kLoraWarps, 0);
+        if (b + kLoraWarps < whole) multiply(1);
+        if (b + 3 * kLoraWarps < whole) load(b + 3 * kLoraWarps, 1);
+      }
+      if (whole < nb && warp == 0) {  // the block that ends past K: lanes without elements give zeros
+        const bool in = (b0 + whole) * 32 + 8 * tq < a.K;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q)
+        for (int n = 0; n < 4; ++n) av[0][n] = in ? __ldg(reinterpret_cast<const uint4*>(ar[n] + whole * 32)) : zero;
 #pragma unroll
-          for (int m = 0; m < kGroups; ++m)
-            if ((groups >> m) & 1) {
-              const uint4 lo = xv[q][m][0], hi = xv[q][m][1];
+        for (int m = 0; m < kGroups; ++m)
 #pragma unroll
-              for (int n = 0; n < 4; ++n)
-                if (n < nt) {
-                  mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, av[q][n].x, av[q][n].y);
-                  mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, av[q][n].z, av[q][n].w);
-                }
-            }
+          for (int h = 0; h < 2; ++h)
+            xv[0][m][h] = in ? __ldg(reinterpret_cast<const uint4*>(xr[m][h] + whole * 32)) : zero;
+        multiply(0);
       }
       // the four warps' sums, in order
 #pragma unroll
@@ -329,47 +348,92 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_shrink_tile_kernel(const
 }
 
 // expand: grid (column chunks, tiles, adapter groups).  A warp takes 32 columns
-// at a time; the next columns' y is on its way meanwhile.
+// at a time; the next columns' y and B are on their way meanwhile.
 template <typename TOut>
 struct Row8;  // 8 neighbouring columns of a row
 template <>
 struct Row8<__nv_bfloat16> {
   uint4 v;
-  MXG_DEVINL void load(const void* p, int64_t i) {
-    v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+  MXG_DEVINL void load(const void* p) { v = __ldcs(static_cast<const uint4*>(p)); }
+  MXG_DEVINL void store(void* p) const { __stcs(static_cast<uint4*>(p), v); }
+  // values j, j + 1 of the row
+  MXG_DEVINL void get(int j, float& lo, float& hi) const {
+    lo = bf16lo_to_f32((&v.x)[j >> 1]);
+    hi = bf16hi_to_f32((&v.x)[j >> 1]);
   }
-  MXG_DEVINL void store(void* p, int64_t i) const {
-    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i), v);
-  }
-  MXG_DEVINL void add(const float* d) {
-    uint32_t* w = &v.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 r =
-          __floats2bfloat162_rn(bf16lo_to_f32(w[i]) + d[2 * i], bf16hi_to_f32(w[i]) + d[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&r);
-    }
+  MXG_DEVINL void set(int j, float lo, float hi) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    (&v.x)[j >> 1] = *reinterpret_cast<const uint32_t*>(&r);
   }
 };
 template <>
 struct Row8<float> {
   float4 v[2];
-  MXG_DEVINL void load(const void* p, int64_t i) {
-    v[0] = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-    v[1] = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i) + 1);
+  MXG_DEVINL void load(const void* p) {
+    v[0] = __ldcs(static_cast<const float4*>(p));
+    v[1] = __ldcs(static_cast<const float4*>(p) + 1);
   }
-  MXG_DEVINL void store(void* p, int64_t i) const {
-    __stcs(reinterpret_cast<float4*>(static_cast<float*>(p) + i), v[0]);
-    __stcs(reinterpret_cast<float4*>(static_cast<float*>(p) + i) + 1, v[1]);
+  MXG_DEVINL void store(void* p) const {
+    __stcs(static_cast<float4*>(p), v[0]);
+    __stcs(static_cast<float4*>(p) + 1, v[1]);
   }
-  MXG_DEVINL void add(const float* d) {
-    float* w = &v[0].x;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] += d[i];
+  MXG_DEVINL void get(int j, float& lo, float& hi) const {
+    lo = (&v[0].x)[j];
+    hi = (&v[0].x)[j + 1];
+  }
+  MXG_DEVINL void set(int j, float lo, float hi) {
+    (&v[0].x)[j] = lo;
+    (&v[0].x)[j + 1] = hi;
   }
 };
 
-template <typename TOut>
+// One product's fragments of B for a chunk of kChunk ranks: 32 ranks are 16
+// bytes of a row a lane, 16 ranks 8 bytes, 8 ranks 4 bytes (half of the depth).
+template <int kChunk>
+struct Frag {
+  uint32_t v[kChunk / 8];
+  MXG_DEVINL void load(const uint16_t* row, int tq) {
+    const uint16_t* src = row + kChunk / 4 * tq;
+    if constexpr (kChunk == 32) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+      v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+    } else if constexpr (kChunk == 16) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+      v[0] = w.x; v[1] = w.y;
+    } else {
+      v[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    }
+  }
+};
+
+// acc += u * B over a chunk; u: this lane's row g (and g + 8, `pitch` 8 rows on)
+// of the 16-token group, in shared memory.
+template <int kChunk>
+MXG_DEVINL void chunk_products(float (*acc)[4], const uint16_t* u, int pitch, const Frag<kChunk>* b, int tq) {
+  const uint16_t* lo = u + kChunk / 4 * tq;
+  const uint16_t* hi = lo + 8 * pitch;
+  if constexpr (kChunk == 32) {
+    const uint4 l = *reinterpret_cast<const uint4*>(lo), h = *reinterpret_cast<const uint4*>(hi);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      mma_bf16(acc[n], l.x, h.x, l.y, h.y, b[n].v[0], b[n].v[1]);
+      mma_bf16(acc[n], l.z, h.z, l.w, h.w, b[n].v[2], b[n].v[3]);
+    }
+  } else if constexpr (kChunk == 16) {
+    const uint2 l = *reinterpret_cast<const uint2*>(lo), h = *reinterpret_cast<const uint2*>(hi);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) mma_bf16(acc[n], l.x, h.x, l.y, h.y, b[n].v[0], b[n].v[1]);
+  } else {
+    const uint32_t l = *reinterpret_cast<const uint32_t*>(lo), h = *reinterpret_cast<const uint32_t*>(hi);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) mma_bf16(acc[n], l, h, 0u, 0u, b[n].v[0], 0u);
+  }
+}
+
+// kChunk: the ranks are taken 32, 16 or 8 at a time (the largest that divides
+// R).  The loop over columns has no branches: fragments past the last column
+// repeat others, and 16-token groups without the adapter are multiplied too.
+template <typename TOut, int kChunk>
 __global__ void __launch_bounds__(kLoraThreads, 4) lora_expand_tile_kernel(const LoraParams p) {
   constexpr int kTerms = sizeof(TOut) == 2 ? 2 : 3;
   __shared__ Tile tile;
@@ -395,128 +459,79 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_expand_tile_kernel(const
   }
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  const int64_t first = (int64_t)blockIdx.x * p.cols + warp * 32;
-  const int64_t c1 = min(a.N, (int64_t)(blockIdx.x + 1) * p.cols);
-  for (int o = blockIdx.z; o < max(tile.count, 1); o += gridDim.z) {
-    const bool any = o < tile.count;
-    const uint32_t groups = any ? tile.groups[o] : 0u;
-    // this lane's rows: those of adapter o, and the ones without adapter in the first pass
-    bool mine[kGroups][2], sum[kGroups][2];
+  const int64_t c_first = (int64_t)blockIdx.x * p.cols + warp * 32;
+  // columns of this warp from its first on (N < 2^31)
+  const int left = (int)(min(a.N, (int64_t)(blockIdx.x + 1) * p.cols) - c_first);
+  const TOut* y0 = static_cast<const TOut*>(a.y) + (t0 + g) * a.ld_y + c_first + 8 * tq;
+  TOut* out0 = static_cast<TOut*>(a.out) + (t0 + g) * a.ld_out + c_first + 8 * tq;
+  const int64_t ystep = 8 * a.ld_y, ostep = 8 * a.ld_out;
+  // column g of product n is output column 8 (g / 2) + 2 n + g % 2
+  const int bcol = 8 * (g >> 1) + (g & 1);
+
+  if (blockIdx.z == 0 && (a.out != a.y || a.ld_out != a.ld_y)) {  // rows without an adapter
+    bool none[kGroups][2], any = false;
 #pragma unroll
-    for (int m = 0; m < kGroups; ++m)
+    for (int i = 0; i < 2 * kGroups; ++i) {
+      none[i >> 1][i & 1] = t0 + 8 * i + g < a.T && tile.ord[8 * i + g] < 0;
+      any |= none[i >> 1][i & 1];
+    }
+    if (__any_sync(kFull, any))
+      for (int c = 0; c + 8 * tq < left; c += kLoraWarps * 32)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = m * 16 + g + 8 * h;
-        const int ro = tile.ord[row];
-        sum[m][h] = any && ro == o;
-        mine[m][h] = t0 + row < a.T && (sum[m][h] || (ro < 0 && o == 0));
-      }
-    Row8<TOut> y[kGroups][2];
-    auto load = [&](int64_t c) {
+        for (int i = 0; i < 2 * kGroups; ++i)
+          if (none[i >> 1][i & 1]) {
+            Row8<TOut> v;
+            v.load(y0 + i * ystep + c);
+            v.store(out0 + i * ostep + c);
+          }
+  }
+
+  for (int o = blockIdx.z; o < tile.count; o += gridDim.z) {
+    const uint16_t* B = a.B + ((int64_t)tile.list[o] * a.N + c_first) * a.R;
+    bool mine[2 * kGroups];  // row 8 i + g belongs to the adapter
 #pragma unroll
-      for (int m = 0; m < kGroups; ++m)
+    for (int i = 0; i < 2 * kGroups; ++i) mine[i] = t0 + 8 * i + g < a.T && tile.ord[8 * i + g] == o;
+    Row8<TOut> y[2 * kGroups];
+    Frag<kChunk> b[4];
+    auto load_y = [&](int c) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (mine[m][h] && c + 8 * tq < c1) y[m][h].load(a.y, (t0 + m * 16 + g + 8 * h) * a.ld_y + c + 8 * tq);
+      for (int i = 0; i < 2 * kGroups; ++i)
+        if (mine[i] && c + 8 * tq < left) y[i].load(y0 + i * ystep + c);
     };
-    load(first);
-    for (int64_t c0 = first; c0 < c1; c0 += kLoraWarps * 32) {
+    auto load_b = [&](int c, int r) {
+      const uint16_t* row = B + (int64_t)(c + bcol < left ? c + bcol : 0) * a.R + r;
+      const int step = c + bcol < left ? 2 * a.R : 0;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) b[n].load(row + n * step, tq);
+    };
+    if (left <= 0) continue;
+    load_y(0);
+    load_b(0, 0);
+    for (int c = 0; c < left; c += kLoraWarps * 32) {
+      // the products add to y (a lane's columns 2 n, 2 n + 1 of product n)
       float acc[kGroups][4][4];
 #pragma unroll
-      for (int m = 0; m < kGroups; ++m)
+      for (int i = 0; i < 2 * kGroups; ++i)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 4; ++n) y[i].get(2 * n, acc[i >> 1][n][2 * (i & 1)], acc[i >> 1][n][2 * (i & 1) + 1]);
+      load_y(c + kLoraWarps * 32);
+      for (int r = 0; r < a.R; r += kChunk) {
+        if (r > 0) load_b(c, r);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-      if (any) {
-        // column g of product n is output column 8 (g / 2) + 2 n + g % 2
-        const int64_t col = c0 + 8 * (g >> 1) + (g & 1);
-        const uint16_t* bk = a.B + ((int64_t)tile.list[o] * a.N + col) * a.R;
-        const bool bin = c0 + 8 * (g >> 1) < c1;
-        int r0 = 0;
-        for (; r0 + 32 <= a.R; r0 += 32) {
-          uint4 bv[4];
+        for (int m = 0; m < kGroups; ++m)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            bv[n] = make_uint4(0, 0, 0, 0);
-            if (bin) bv[n] = __ldg(reinterpret_cast<const uint4*>(bk + (int64_t)2 * n * a.R + r0 + 8 * tq));
-          }
-#pragma unroll
-          for (int m = 0; m < kGroups; ++m)
-            if ((groups >> m) & 1) {
-#pragma unroll
-              for (int q = kTerms - 1; q >= 0; --q) {
-                const uint16_t* u = us + (q * kTile + m * 16 + g) * pitch + r0 + 8 * tq;
-                const uint4 lo = *reinterpret_cast<const uint4*>(u), hi = *reinterpret_cast<const uint4*>(u + 8 * pitch);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                  mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, bv[n].x, bv[n].y);
-                  mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, bv[n].z, bv[n].w);
-                }
-              }
-            }
-        }
-        if (a.R & 16) {  // 16 ranks: 8 bytes a lane
-          uint2 bv[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            bv[n] = make_uint2(0, 0);
-            if (bin) bv[n] = __ldg(reinterpret_cast<const uint2*>(bk + (int64_t)2 * n * a.R + r0 + 4 * tq));
-          }
-#pragma unroll
-          for (int m = 0; m < kGroups; ++m)
-            if ((groups >> m) & 1) {
-#pragma unroll
-              for (int q = kTerms - 1; q >= 0; --q) {
-                const uint16_t* u = us + (q * kTile + m * 16 + g) * pitch + r0 + 4 * tq;
-                const uint2 lo = *reinterpret_cast<const uint2*>(u), hi = *reinterpret_cast<const uint2*>(u + 8 * pitch);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, bv[n].x, bv[n].y);
-              }
-            }
-          r0 += 16;
-        }
-        if (a.R & 8) {  // 8 ranks: 4 bytes a lane, half of the product's depth
-          uint32_t bv[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-            bv[n] = bin ? __ldg(reinterpret_cast<const uint32_t*>(bk + (int64_t)2 * n * a.R + r0 + 2 * tq)) : 0u;
-#pragma unroll
-          for (int m = 0; m < kGroups; ++m)
-            if ((groups >> m) & 1) {
-#pragma unroll
-              for (int q = kTerms - 1; q >= 0; --q) {
-                const uint16_t* u = us + (q * kTile + m * 16 + g) * pitch + r0 + 2 * tq;
-                const uint32_t lo = *reinterpret_cast<const uint32_t*>(u);
-                const uint32_t hi = *reinterpret_cast<const uint32_t*>(u + 8 * pitch);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) mma_bf16(acc[m][n], lo, hi, 0u, 0u, bv[n], 0u);
-              }
-            }
-        }
+          for (int q = kTerms - 1; q >= 0; --q)
+            chunk_products<kChunk>(acc[m], us + (q * kTile + m * 16 + g) * pitch + r, pitch, b, tq);
       }
-      Row8<TOut> now[kGroups][2];
+      load_b(c + kLoraWarps * 32, 0);
 #pragma unroll
-      for (int m = 0; m < kGroups; ++m)
+      for (int i = 0; i < 2 * kGroups; ++i)
+        if (mine[i] && c + 8 * tq < left) {
+          Row8<TOut> v;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) now[m][h] = y[m][h];
-      load(c0 + kLoraWarps * 32);
-#pragma unroll
-      for (int m = 0; m < kGroups; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (mine[m][h] && c0 + 8 * tq < c1) {  // N is a multiple of 8
-            if (sum[m][h]) {
-              float d[8];
-#pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                d[2 * n] = acc[m][n][2 * h];
-                d[2 * n + 1] = acc[m][n][2 * h + 1];
-              }
-              now[m][h].add(d);
-            }
-            now[m][h].store(a.out, (t0 + m * 16 + g + 8 * h) * a.ld_out + c0 + 8 * tq);
-          }
+          for (int n = 0; n < 4; ++n) v.set(2 * n, acc[i >> 1][n][2 * (i & 1)], acc[i >> 1][n][2 * (i & 1) + 1]);
+          v.store(out0 + i * ostep + c);
+        }
     }
   }
 }
@@ -527,6 +542,13 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_expand_tile_kernel(const
 // Adapter bytes that the per-token kernels would read, from L2 where tokens
 // share them, against this limit.
 constexpr double kTokenBytes = 64e6;
+
+template <typename TOut>
+const void* expand_tile(int R) {
+  if (R % 32 == 0) return (const void*)lora_expand_tile_kernel<TOut, 32>;
+  if (R % 16 == 0) return (const void*)lora_expand_tile_kernel<TOut, 16>;
+  return (const void*)lora_expand_tile_kernel<TOut, 8>;
+}
 
 bool per_token(int64_t T, int64_t N, int64_t K, int R) {
   return (double)T * R * (double)(K + N) * 2.0 <= kTokenBytes && T <= 65535;
@@ -587,7 +609,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms)
     const int64_t chunks = std::max<int64_t>(1, 16 * (int64_t)num_sms / tiles);
     p.cols = (int)std::min<int64_t>(8192, std::max<int64_t>(128, (a.N / chunks + 127) / 128 * 128));
     shrink = (const void*)lora_shrink_tile_kernel;
-    expand = f32 ? (const void*)lora_expand_tile_kernel<float> : (const void*)lora_expand_tile_kernel<__nv_bfloat16>;
+    expand = f32 ? expand_tile<float>(a.R) : expand_tile<__nv_bfloat16>(a.R);
     sgrid = dim3((unsigned)p.ksplit, (unsigned)tiles, (unsigned)groups);
     egrid = dim3((unsigned)((a.N + p.cols - 1) / p.cols), (unsigned)tiles, (unsigned)groups);
     smem = (size_t)(f32 ? 3 : 2) * kTile * (a.R + 8) * 2;
