@@ -50,8 +50,7 @@ struct LoraParams {
 };
 
 MXG_DEVINL void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -290,18 +289,20 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_shrink_tile_kernel(const
             for (int h = 0; h < 2; ++h) xv[q][m][h] = __ldg(reinterpret_cast<const uint4*>(xr[m][h] + b * 32));
           }
       };
-      auto multiply = [&](int q) {
+      auto multiply = [&](int q) {  // eight independent products between dependent ones
 #pragma unroll
-        for (int m = 0; m < kGroups; ++m)
-          if ((groups >> m) & 1) {
-            const uint4 lo = xv[q][m][0], hi = xv[q][m][1];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-              if (n < nt) {
-                mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, av[q][n].x, av[q][n].y);
-                mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, av[q][n].z, av[q][n].w);
-              }
-          }
+          for (int m = 0; m < kGroups; ++m)
+            if ((groups >> m) & 1) {
+              const uint4 lo = xv[q][m][0], hi = xv[q][m][1];
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                if (n < nt) {
+                  if (h == 0) mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, av[q][n].x, av[q][n].y);
+                  else mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, av[q][n].z, av[q][n].w);
+                }
+            }
       };
       if (warp < whole) load(warp, 0);
       if (warp + kLoraWarps < whole) load(warp + kLoraWarps, 1);
@@ -354,8 +355,8 @@ struct Row8;  // 8 neighbouring columns of a row
 template <>
 struct Row8<__nv_bfloat16> {
   uint4 v;
-  MXG_DEVINL void load(const void* p) { v = __ldcs(static_cast<const uint4*>(p)); }
-  MXG_DEVINL void store(void* p) const { __stcs(static_cast<uint4*>(p), v); }
+  MXG_DEVINL void load(const void* p) { v = *static_cast<const uint4*>(p); }
+  MXG_DEVINL void store(void* p) const { *static_cast<uint4*>(p) = v; }
   // values j, j + 1 of the row
   MXG_DEVINL void get(int j, float& lo, float& hi) const {
     lo = bf16lo_to_f32((&v.x)[j >> 1]);
@@ -370,12 +371,12 @@ template <>
 struct Row8<float> {
   float4 v[2];
   MXG_DEVINL void load(const void* p) {
-    v[0] = __ldcs(static_cast<const float4*>(p));
-    v[1] = __ldcs(static_cast<const float4*>(p) + 1);
+    v[0] = *static_cast<const float4*>(p);
+    v[1] = *(static_cast<const float4*>(p) + 1);
   }
   MXG_DEVINL void store(void* p) const {
-    __stcs(static_cast<float4*>(p), v[0]);
-    __stcs(static_cast<float4*>(p) + 1, v[1]);
+    *static_cast<float4*>(p) = v[0];
+    *(static_cast<float4*>(p) + 1) = v[1];
   }
   MXG_DEVINL void get(int j, float& lo, float& hi) const {
     lo = (&v[0].x)[j];
@@ -415,10 +416,9 @@ MXG_DEVINL void chunk_products(float (*acc)[4], const uint16_t* u, int pitch, co
   if constexpr (kChunk == 32) {
     const uint4 l = *reinterpret_cast<const uint4*>(lo), h = *reinterpret_cast<const uint4*>(hi);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      mma_bf16(acc[n], l.x, h.x, l.y, h.y, b[n].v[0], b[n].v[1]);
-      mma_bf16(acc[n], l.z, h.z, l.w, h.w, b[n].v[2], b[n].v[3]);
-    }
+    for (int n = 0; n < 4; ++n) mma_bf16(acc[n], l.x, h.x, l.y, h.y, b[n].v[0], b[n].v[1]);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) mma_bf16(acc[n], l.z, h.z, l.w, h.w, b[n].v[2], b[n].v[3]);
   } else if constexpr (kChunk == 16) {
     const uint2 l = *reinterpret_cast<const uint2*>(lo), h = *reinterpret_cast<const uint2*>(hi);
 #pragma unroll
@@ -518,9 +518,9 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_expand_tile_kernel(const
       for (int r = 0; r < a.R; r += kChunk) {
         if (r > 0) load_b(c, r);
 #pragma unroll
-        for (int m = 0; m < kGroups; ++m)
+        for (int q = kTerms - 1; q >= 0; --q)
 #pragma unroll
-          for (int q = kTerms - 1; q >= 0; --q)
+          for (int m = 0; m < kGroups; ++m)
             chunk_products<kChunk>(acc[m], us + (q * kTile + m * 16 + g) * pitch + r, pitch, b, tq);
       }
       load_b(c + kLoraWarps * 32, 0);
