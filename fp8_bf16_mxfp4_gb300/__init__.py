@@ -626,22 +626,47 @@ def bw_grouped_gemm_wgrad(dYt: BWOperand, Xt: BWOperand, m_splits: torch.Tensor,
 
 
 # ----------------------------------------------------------------------------- serving
+#
+# These calls take microseconds on the device, so their checks are single
+# comparisons on the way through; what is wrong is worked out only on failure.
 
 
-def _rows(t: torch.Tensor, name: str, cols: int | None = None):
-    """A 2-D tensor with contiguous rows (any row stride)."""
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be a 2-D tensor" + (f" of {cols} columns" if cols is not None else ""))
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: elements of a row must be contiguous")
-    return t
+def _raw_stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _whole(t: torch.Tensor, name: str, shape, dtype):
-    """A contiguous tensor of the given shape and type."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
-    return t
+def _status_ptr(status, dev) -> int:
+    if status is not None:
+        return status.data_ptr()
+    st = _status.get(dev.index)
+    return (st if st is not None else status_tensor(dev)).data_ptr()
+
+
+def _row_ld(t: torch.Tensor, cols: int) -> int:
+    """Row stride of a 2-D tensor; its rows must be contiguous.  A tensor of at
+    most one row reports arbitrary strides: its width, rounded up to 8."""
+    if t.shape[0] > 1:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError("elements of a row must be contiguous")
+        return t.stride(0)
+    return (cols + 7) & ~7
+
+
+def _refuse(**named):
+    """Raise for the first argument that is not what it has to be: name =
+    (tensor, shape, dtype or dtypes, contiguous)."""
+    for name, (t, shape, dtypes, contiguous) in named.items():
+        if t is None:
+            continue
+        dtypes = dtypes if isinstance(dtypes, (tuple, dict)) else (dtypes,)
+        if not t.is_cuda:
+            raise ValueError("libmxg operates on CUDA tensors only")
+        if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+            raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)} of shape {list(shape)}, "
+                             f"got {t.dtype} of shape {list(t.shape)}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    raise ValueError("arguments do not fit together")
 
 
 def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, ids: torch.Tensor | None = None,
@@ -651,19 +676,26 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, ids: t
     equal logits in index order, with their softmax weights -- over the chosen
     experts (``renormalize``) or over all of them.  Experts whose logit is -inf
     or NaN are never chosen; slots left over have id -1 and weight 0."""
-    _need_cuda(logits, ids, weights)
-    _rows(logits, "logits")
-    if logits.dtype not in _OUT:
-        raise ValueError("logits must be bfloat16 or float32")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens, experts]")
     T, E = logits.shape
+    dtype = _OUT.get(logits.dtype)
     dev = logits.device
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if ids is None else \
-        _whole(ids, "ids", (T, top_k), torch.int32)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev) if weights is None else \
-        _whole(weights, "weights", (T, top_k), torch.float32)
-    _ok(_lib.load().moe_route(logits.data_ptr(), T, E, _ld(logits, E), _OUT[logits.dtype], top_k, int(renormalize),
-                              ids.data_ptr(), weights.data_ptr(), torch.cuda.current_stream(dev).cuda_stream),
-        "moe_route")
+    if dtype is None or not logits.is_cuda:
+        _refuse(logits=(logits, (T, E), _OUT, False))
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    elif ids.shape != (T, top_k) or ids.dtype != torch.int32 or not ids.is_contiguous() or not ids.is_cuda:
+        _refuse(ids=(ids, (T, top_k), torch.int32, True))
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    elif (weights.shape != (T, top_k) or weights.dtype != torch.float32 or not weights.is_contiguous()
+          or not weights.is_cuda):
+        _refuse(weights=(weights, (T, top_k), torch.float32, True))
+    code = _lib.load().moe_route(logits.data_ptr(), T, E, _row_ld(logits, E), dtype, top_k, renormalize,
+                                 ids.data_ptr(), weights.data_ptr(), _raw_stream(dev))
+    if code:
+        raise MXGError(code, "moe_route")
     return ids, weights
 
 
@@ -683,40 +715,40 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
     ``mx_quantize_rowwise_packed(..., groups=E)``, both "e2m1" or both "e4m3".
     Activations are rounded to MXFP8 in front of each product, as the grouped
     GEMMs of the same operands take them.  T * top_k <= 4096."""
-    _need_cuda(x, ids, weights, W13.data, W2.data, out, workspace)
-    _rows(x, "x", W13.cols)
-    if x.dtype != torch.bfloat16:
-        raise ValueError("x must be bfloat16")
-    if ids.dim() != 2:
-        raise ValueError("ids must be [tokens, top_k]")
+    if ids.dim() != 2 or x.dim() != 2:
+        raise ValueError("x must be [tokens, hidden] and ids [tokens, top_k]")
     if W13.scale_layout != "packed" or W2.scale_layout != "packed":
         raise ValueError("W13 and W2 need packed scales (mx_quantize_rowwise_packed with groups=experts)")
-    T, H = x.shape
-    k, I, dev = ids.shape[1], W2.cols, x.device
+    T, k = ids.shape
+    H, I, dev = W13.cols, W2.cols, x.device
     E = W2.rows // H
+    if (x.shape != (T, H) or x.dtype != torch.bfloat16 or weights.shape != (T, k) or ids.dtype != torch.int32
+            or weights.dtype != torch.float32 or not ids.is_contiguous() or not weights.is_contiguous()
+            or not (x.is_cuda and ids.is_cuda and weights.is_cuda)):
+        _refuse(x=(x, (T, H), torch.bfloat16, False), ids=(ids, (T, k), torch.int32, True),
+                weights=(weights, (T, k), torch.float32, True))
     if W2.rows != E * H or W13.rows != E * 2 * I:
         raise ValueError("W13 must be [E * 2I, H] and W2 [E * H, I]")
-    for w, cols in ((W13, H), (W2, I)):
-        if w.scale.numel() < w.rows // 128 * (cols // 128) * 512:
-            raise ValueError("packed scales are shorter than the weights need")
-    _whole(ids, "ids", (T, k), torch.int32)
-    _whole(weights, "weights", (T, k), torch.float32)
+    # a packed byte for every 32 weights (rows and columns are multiples of 128)
+    if W13.scale.numel() < W13.rows * (H // 32) or W2.scale.numel() < W2.rows * (I // 32):
+        raise ValueError("packed scales are shorter than the weights need")
+    if not (W13.data.is_cuda and W13.scale.is_cuda and W2.data.is_cuda and W2.scale.is_cuda):
+        raise ValueError("libmxg operates on CUDA tensors only")
     lib = _lib.load()
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype, device=dev)
-    else:
-        _rows(out, "out", H)
-        if out.shape[0] != T or out.dtype not in _OUT:
-            raise ValueError("out must be [tokens, hidden], bfloat16 or float32")
-    ws = _workspace(0 if workspace is not None else lib.moe_experts_workspace_size(T, k, E, H, I), dev, workspace)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    st = status if status is not None else status_tensor(dev)
+    if out.shape != (T, H) or out.dtype not in _OUT or not out.is_cuda:
+        _refuse(out=(out, (T, H), _OUT, False))
+    if workspace is None:
+        workspace = torch.empty(max(lib.moe_experts_workspace_size(T, k, E, H, I), 256), dtype=torch.uint8, device=dev)
     a, b = W13.c(), W2.c()
-    _ok(lib.moe_experts(x.data_ptr(), T, _ld(x, H), ids.data_ptr(), weights.data_ptr(), k, E, ctypes.byref(a),
-                        ctypes.byref(b), out.data_ptr(), _ld(out, H), _OUT[out.dtype], ws.data_ptr(), ws.numel(),
-                        st.data_ptr(), stream), "moe_experts")
+    code = lib.moe_experts(x.data_ptr(), T, _row_ld(x, H), ids.data_ptr(), weights.data_ptr(), k, E, ctypes.byref(a),
+                           ctypes.byref(b), out.data_ptr(), _row_ld(out, H), _OUT[out.dtype], workspace.data_ptr(),
+                           workspace.numel(), _status_ptr(status, dev), _raw_stream(dev))
+    if code:
+        raise MXGError(code, "moe_experts")
     if check:
-        check_status(st)
+        check_status(status, dev)
     return out
 
 
@@ -736,37 +768,35 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     ``A`` BF16 [adapters, rank, K]; ``B`` BF16 [adapters, N, rank]; ``ids``
     int32 [T]; ``scale`` FP32 [adapters] (None: 1).  ``out=y`` updates in
     place.  rank is a multiple of 8 up to 128."""
-    _need_cuda(y, x, A, B, ids, scale, out, workspace)
-    _rows(y, "y")
-    _rows(x, "x")
-    if y.dtype not in _OUT or x.dtype != torch.bfloat16:
-        raise ValueError("y must be bfloat16 or float32 and x bfloat16")
-    if A.dim() != 3:
-        raise ValueError("A must be [adapters, rank, K]")
+    if y.dim() != 2 or A.dim() != 3:
+        raise ValueError("y must be [tokens, N] and A [adapters, rank, K]")
     T, N = y.shape
     n, R, K = A.shape
-    if x.shape[0] != T:
-        raise ValueError("x and y must have the same number of rows")
-    _rows(x, "x", K)
-    _whole(A, "A", (n, R, K), torch.bfloat16)
-    _whole(B, "B", (n, N, R), torch.bfloat16)
-    _whole(ids, "ids", (T,), torch.int32)
-    if scale is not None:
-        _whole(scale, "scale", (n,), torch.float32)
+    bf16 = torch.bfloat16
+    dtype = _OUT.get(y.dtype)
+    if (x.shape != (T, K) or B.shape != (n, N, R) or ids.shape != (T,) or dtype is None or x.dtype != bf16
+            or A.dtype != bf16 or B.dtype != bf16 or ids.dtype != torch.int32 or not A.is_contiguous()
+            or not B.is_contiguous() or not ids.is_contiguous()
+            or not (y.is_cuda and x.is_cuda and A.is_cuda and B.is_cuda and ids.is_cuda)):
+        _refuse(y=(y, (T, N), _OUT, False), x=(x, (T, K), bf16, False), A=(A, (n, R, K), bf16, True),
+                B=(B, (n, N, R), bf16, True), ids=(ids, (T,), torch.int32, True))
+    if scale is not None and (scale.shape != (n,) or scale.dtype != torch.float32 or not scale.is_contiguous()
+                              or not scale.is_cuda):
+        _refuse(scale=(scale, (n,), torch.float32, True))
     dev = y.device
     lib = _lib.load()
     if out is None:
         out = torch.empty((T, N), dtype=y.dtype, device=dev)
-    else:
-        _rows(out, "out", N)
-        if out.shape[0] != T or out.dtype != y.dtype:
-            raise ValueError("out must have y's shape and type")
-    ws = _workspace(0 if workspace is not None else lib.lora_add_workspace_size(T, K, R), dev, workspace)
-    st = status if status is not None else status_tensor(dev)
-    _ok(lib.lora_add(y.data_ptr(), _ld(y, N), x.data_ptr(), _ld(x, K), A.data_ptr(), B.data_ptr(), ids.data_ptr(),
-                     scale.data_ptr() if scale is not None else None, T, N, K, R, n, _OUT[y.dtype], out.data_ptr(),
-                     _ld(out, N), ws.data_ptr(), ws.numel(), st.data_ptr(),
-                     torch.cuda.current_stream(dev).cuda_stream), "lora_add")
+    elif out.shape != (T, N) or out.dtype != y.dtype or not out.is_cuda:
+        _refuse(out=(out, (T, N), y.dtype, False))
+    if workspace is None:
+        workspace = torch.empty(max(lib.lora_add_workspace_size(T, K, R), 256), dtype=torch.uint8, device=dev)
+    code = lib.lora_add(y.data_ptr(), _row_ld(y, N), x.data_ptr(), _row_ld(x, K), A.data_ptr(), B.data_ptr(),
+                        ids.data_ptr(), None if scale is None else scale.data_ptr(), T, N, K, R, n, dtype,
+                        out.data_ptr(), _row_ld(out, N), workspace.data_ptr(), workspace.numel(),
+                        _status_ptr(status, dev), _raw_stream(dev))
+    if code:
+        raise MXGError(code, "lora_add")
     if check:
-        check_status(st)
+        check_status(status, dev)
     return out
