@@ -827,7 +827,7 @@ bool moe_sizes_ok(int64_t tokens, int32_t top_k, int32_t experts, int64_t hidden
 }
 
 bool lora_sizes_ok(int64_t tokens, int64_t K, int32_t rank) {
-  return tokens >= 0 && tokens <= 65535 * 32 && K > 0 && K % 8 == 0 && K <= 0x7FFFFFFF && rank >= 8 &&
+  return tokens >= 0 && tokens <= 65535 * 128 && K > 0 && K % 8 == 0 && K <= 0x7FFFFFFF && rank >= 8 &&
          rank % 8 == 0 && rank <= kMaxRank;
 }
 
@@ -917,7 +917,8 @@ mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, co
                     int32_t* d_status, void* stream) {
   if (d_status == nullptr) return MXG_ERR_NULL;
   if (!valid_out_dtype(dtype)) return MXG_ERR_UNSUPPORTED;
-  if (!lora_sizes_ok(tokens, K, rank) || N <= 0 || N % 8 != 0 || N > 0x7FFFFFFF || adapters < 1 || ld_x < K ||
+  if (!lora_sizes_ok(tokens, K, rank) || N <= 0 || N % 8 != 0 || N > 0x7FFFFFFF || adapters < 1 ||
+      adapters > 0x7FFFFFFF / N || adapters > 0x7FFFFFFF / rank || ld_x < K ||
       ld_y < N || ld_out < N)
     return MXG_ERR_SHAPE;
   const int per16 = dtype == MXG_OUT_BF16 ? 8 : 4;

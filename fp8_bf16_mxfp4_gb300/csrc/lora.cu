@@ -10,26 +10,24 @@
 // from L2; that is as fast as it gets while all adapters read for all tokens
 // are a few tens of MB, because every load of a CTA is in flight at once.
 //
-// Many tokens: a CTA takes a tile of 32 tokens as they come in the batch, and
-// for every adapter that occurs in the tile runs the tile's tokens against the
-// adapter's rows on the tensor core (mma.sync, BF16 x BF16 + FP32), which has
-// work for a few clocks per line loaded: products of rows that are not wanted
-// cost nothing, and there is no sorting.  A token's row belongs to one adapter,
-// so the adapters of a tile are shared out over CTAs without any sum across
-// them, and a row is selected, never masked by a product: an adapter's
-// infinities or NaN reach its own tokens only.  Fragments are loaded straight
-// from global memory, 16 bytes a lane: the contraction may be taken in any
-// order, so lane t of a row's four takes elements 8t .. 8t+7 of a 32-element
-// block for both operands.  In the expand the output columns are permuted the
-// same way, so that a lane has 8 neighbouring columns of a row.  u keeps its
-// fp32 accuracy as a sum of two BF16 terms (2^-17; BF16 output) or three
-// (2^-25; FP32 output).
+// Many tokens: a CTA takes a tile of 128 tokens as they come in the batch and
+// runs it against the adapters that occur in it on the tensor core (tcgen05,
+// BF16 x BF16 + FP32); products of rows that are not wanted cost nothing, and
+// there is no sorting.  A row of the result is selected, never masked by a
+// product: an adapter's infinities or NaN reach its own tokens only.  u keeps its
+// fp32 accuracy as a sum of two BF16 terms (2^-17; BF16 output) or three (2^-25;
+// FP32 output).  (mma.sync runs at 1/16 of the tcgen05 rate on GB300: a tile
+// form on it was held to 265 us by its pipe where this one takes @@ us, at 8192
+// tokens, 8192 x 28672, rank 32.)
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
+#include "gemm_common.cuh"
 #include "sm100_ptx.cuh"
 
 namespace mxg {
@@ -38,23 +36,15 @@ namespace {
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kLoraWarps = 4;
 constexpr int kLoraThreads = kLoraWarps * 32;
-constexpr int kGroups = 2;                // 16-token groups of a tile
-constexpr int kTile = 16 * kGroups;
 
 struct LoraParams {
   LoraArgs a;
   float* u;         // [ksplit][T][R] partial sums
   int ksplit;
-  int blocks;       // tiles: 32-element blocks of K per CTA of the shrink
+  int blocks;       // tiles: 64-element steps of K per CTA of the shrink
   int cols;         // tiles: columns per CTA of the expand
+  uint64_t timeout_ns, drain_ns;
 };
-
-MXG_DEVINL void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // ---------------------------------------------------------------------------
 // Few tokens: shrink, grid (K split, tokens, rank groups of 16).  A warp takes
@@ -207,332 +197,502 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_token_kernel(const L
 // ---------------------------------------------------------------------------
 // Many tokens
 // ---------------------------------------------------------------------------
+constexpr int kTile = 128;          // tokens of a tile (TMEM lanes)
+constexpr int kRowBytes = 128;      // one swizzled shared-memory row: 64 BF16 of the contraction
+constexpr int kTileBytes = kTile * kRowBytes;
+
 // The adapters of a tile of tokens, in order of first use.
 struct Tile {
-  int id[kTile];           // adapter of each token (-1: none)
-  int ord[kTile];          // its number in the list (-1: none)
-  int list[kTile];         // adapter by number
-  uint32_t groups[kTile];  // 16-token groups in which it occurs (bit mask)
+  int id[kTile];       // adapter of each token (-1: none)
+  int16_t ord[kTile];  // its number in the list (-1: none)
+  int list[kTile];     // adapter by number
   int count;
 };
 
+// All threads of the CTA (at least kTile).
 MXG_DEVINL void read_tile(Tile& s, const LoraArgs& a, int64_t t0) {
-  static_assert(kTile == 32, "a lane per token");
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int id = t0 + lane < a.T ? __ldg(a.ids + t0 + lane) : -1;
+  const int tid = threadIdx.x;
+  if (tid < kTile) {
+    int id = t0 + tid < a.T ? __ldg(a.ids + t0 + tid) : -1;
     if (id >= a.n) {
       report(a.status, MXG_ERR_INDEX);
       id = -1;
     }
-    const uint32_t same = __match_any_sync(kFull, id);
-    const int leader = __ffs(same) - 1;
-    const uint32_t firsts = __ballot_sync(kFull, id >= 0 && leader == lane);
-    const int o = id >= 0 ? __popc(firsts & ((1u << leader) - 1u)) : -1;
-    s.id[lane] = id;
-    s.ord[lane] = o;
-    if (id >= 0 && leader == lane) {
-      s.list[o] = id;
-      s.groups[o] = ((same & 0xFFFFu) ? 1u : 0u) | ((same >> 16) ? 2u : 0u);
-    }
-    if (lane == 0) s.count = __popc(firsts);
+    s.id[tid] = id;
+    s.ord[tid] = -1;
   }
+  __syncthreads();
+  int leader = tid;  // the first token with this one's adapter
+  if (tid < kTile && s.id[tid] >= 0)
+    for (leader = 0; s.id[leader] != s.id[tid]; ++leader) {}
+  if (tid < 32) {  // the leaders, numbered in order
+    int count = 0;
+    for (int base = 0; base < kTile; base += 32) {
+      const int i = base + tid, id = s.id[i];
+      bool first = id >= 0;
+      for (int j = 0; first && j < i; ++j) first = s.id[j] != id;
+      const uint32_t m = __ballot_sync(kFull, first);
+      if (first) {
+        const int o = count + __popc(m & ((1u << tid) - 1u));
+        s.list[o] = id;
+        s.ord[i] = (int16_t)o;
+      }
+      count += __popc(m);
+    }
+    if (tid == 0) s.count = count;
+  }
+  __syncthreads();
+  if (tid < kTile && s.id[tid] >= 0 && leader != tid) s.ord[tid] = s.ord[leader];
   __syncthreads();
 }
 
-// shrink: grid (K split, tiles, adapter groups).  The warps of a CTA take every
-// fourth 32-element block of its K range, up to 32 ranks at a time.
-__global__ void __launch_bounds__(kLoraThreads, 4) lora_shrink_tile_kernel(const LoraParams p) {
+// Instruction descriptor of kind::f16: BF16 x BF16 -> FP32, both K-major, M = 128.
+MXG_DEVINL uint32_t idesc_bf16(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// shrink: grid (K split, tiles), 192 threads: warp 0 loads (TMA), warp 1 issues
+// the MMAs, warps 2-5 store.  x is the M operand; the rows of up to 256 / R
+// adapters of the tile form one N operand, so x is read once for all of them.
+constexpr int kShrinkThreads = 192;
+constexpr int kShrinkRows = 256;  // adapter rows of one pass
+constexpr int kShrinkStage = kTileBytes + kShrinkRows * kRowBytes;
+constexpr int kShrinkStages = 4;
+constexpr int kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
+constexpr int kShrinkTmem = 256;
+
+__global__ void __launch_bounds__(kShrinkThreads, 1)
+    lora_shrink_tile_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
+                            const LoraParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   __shared__ Tile tile;
-  __shared__ float red[kLoraWarps][kTile][33];
+  __shared__ __align__(8) uint64_t bars[2 * kShrinkStages + 3];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const LoraArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kShrinkStages + s); };
+  const uint32_t acc_full = bar0 + 16u * kShrinkStages, acc_empty = acc_full + 8, drain = acc_full + 16;
   ptx::pdl_launch_dependents();
-  const LoraArgs& a = p.a;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kShrinkStages; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    ptx::mbar_init(acc_full, 1);
+    ptx::mbar_init(acc_empty, 4);
+    ptx::mbar_init(drain, 1);
+    abort_word = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmX);
+    ptx::prefetch_tmap(&tmA);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), kShrinkTmem);
+    ptx::tmem_relinquish();
+  }
   const int64_t t0 = (int64_t)blockIdx.y * kTile;
+  ptx::tc_fence_before();
   read_tile(tile, a, t0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  const int64_t kblocks = (a.K + 31) >> 5;
-  const int64_t b0 = (int64_t)blockIdx.x * p.blocks;
-  const int nb = (int)min((int64_t)p.blocks, kblocks - b0);
-  // rows past the batch are read from its last token (their products are not used)
-  const uint16_t* xr[kGroups][2];
-#pragma unroll
-  for (int m = 0; m < kGroups; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      xr[m][h] = a.x + min(t0 + m * 16 + g + 8 * h, a.T - 1) * a.ld_x + b0 * 32 + 8 * tq;
-  const int whole = (int)min((int64_t)nb, (a.K >> 5) - b0);  // blocks that do not end past K
-  for (int o = blockIdx.z; o < tile.count; o += gridDim.z) {
-    const uint32_t groups = tile.groups[o];
-    for (int r0 = 0; r0 < a.R; r0 += 32) {
-      const int nt = min(4, (a.R - r0) >> 3);
-      // products past the ranks are skipped; their loads repeat the first eight rows
-      const uint16_t* ar[4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        ar[n] = a.A + ((int64_t)tile.list[o] * a.R + r0 + (n < nt ? 8 * n : 0) + g) * a.K + b0 * 32 + 8 * tq;
-      float acc[kGroups][4][4];
-#pragma unroll
-      for (int m = 0; m < kGroups; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-      // two blocks' loads are in flight while a third is multiplied
-      uint4 xv[2][kGroups][2], av[2][4];
-      auto load = [&](int b, int q) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) av[q][n] = __ldg(reinterpret_cast<const uint4*>(ar[n] + b * 32));
-#pragma unroll
-        for (int m = 0; m < kGroups; ++m)
-          if ((groups >> m) & 1) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) xv[q][m][h] = __ldg(reinterpret_cast<const uint4*>(xr[m][h] + b * 32));
-          }
-      };
-      auto multiply = [&](int q) {  // eight independent products between dependent ones
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int m = 0; m < kGroups; ++m)
-            if ((groups >> m) & 1) {
-              const uint4 lo = xv[q][m][0], hi = xv[q][m][1];
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                if (n < nt) {
-                  if (h == 0) mma_bf16(acc[m][n], lo.x, hi.x, lo.y, hi.y, av[q][n].x, av[q][n].y);
-                  else mma_bf16(acc[m][n], lo.z, hi.z, lo.w, hi.w, av[q][n].z, av[q][n].w);
-                }
-            }
-      };
-      if (warp < whole) load(warp, 0);
-      if (warp + kLoraWarps < whole) load(warp + kLoraWarps, 1);
-      for (int b = warp; b < whole; b += 2 * kLoraWarps) {
-        multiply(0);
-        if (b + 2 * kLoraWarps < whole) load(b + 2 * kLoraWarps, 0);
-        if (b + kLoraWarps < whole) multiply(1);
-        if (b + 3 * kLoraWarps < whole) load(b + 3 * kLoraWarps, 1);
-      }
-      if (whole < nb && warp == 0) {  // the block that ends past K: lanes without elements give zeros
-        const bool in = (b0 + whole) * 32 + 8 * tq < a.K;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) av[0][n] = in ? __ldg(reinterpret_cast<const uint4*>(ar[n] + whole * 32)) : zero;
-#pragma unroll
-        for (int m = 0; m < kGroups; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            xv[0][m][h] = in ? __ldg(reinterpret_cast<const uint4*>(xr[m][h] + whole * 32)) : zero;
-        multiply(0);
-      }
-      // the four warps' sums, in order
-#pragma unroll
-      for (int m = 0; m < kGroups; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          float* d = &red[warp][m * 16 + g][n * 8 + 2 * tq];
-          d[0] = acc[m][n][0];
-          d[1] = acc[m][n][1];
-          d[8 * 33] = acc[m][n][2];
-          d[8 * 33 + 1] = acc[m][n][3];
-        }
-      __syncthreads();
-      for (int i = threadIdx.x; i < kTile * 32; i += kLoraThreads) {
-        const int row = i >> 5, r = i & 31;
-        if (tile.ord[row] == o && r < nt * 8) {
-          const float s = (red[0][row][r] + red[1][row][r]) + (red[2][row][r] + red[3][row][r]);
-          __stcg(p.u + ((int64_t)blockIdx.x * a.T + t0 + row) * a.R + r0 + r, s);
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int s0 = blockIdx.x * p.blocks;
+  const int s1 = (int)min((a.K + 63) / 64, (int64_t)s0 + p.blocks);  // 64-element steps of this CTA
+  const int per_pass = kShrinkRows / a.R;
+  const int count = tile.count;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_phase = 0;
+      bool ok = true;
+      for (int o0 = 0; ok && o0 < count; o0 += per_pass) {
+        const int na = min(per_pass, count - o0);
+        for (int k = s0; k < s1; ++k) {
+          if (!ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status, p.timeout_ns)) { ok = false; break; }
+          const uint32_t fb = full_bar(stage), sx = sbase + stage * kShrinkStage;
+          ptx::mbar_arrive_expect_tx(fb, (uint32_t)(kTileBytes + na * a.R * kRowBytes));
+          armed |= 1u << stage;
+          armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+          ptx::tma_load_2d(sx, &tmX, k * 64, (int)t0, fb);
+          for (int i = 0; i < na; ++i)
+            ptx::tma_load_2d(sx + kTileBytes + i * a.R * kRowBytes, &tmA, k * 64, tile.list[o0 + i] * a.R, fb);
+          if (++stage == kShrinkStages) { stage = 0; phase ^= 1u; }
         }
       }
-      __syncthreads();
+      for (int s = 0; s < kShrinkStages; ++s)  // no copies are left in flight
+        if ((armed >> s) & 1u) {
+          volatile int no_abort = 0;
+          ptx::mbar_wait(full_bar(s), (armed_phase >> s) & 1u, &no_abort, a.status, p.drain_ns);
+        }
     }
-  }
-}
-
-// expand: grid (column chunks, tiles, adapter groups).  A warp takes 32 columns
-// at a time; the next columns' y and B are on their way meanwhile.
-template <typename TOut>
-struct Row8;  // 8 neighbouring columns of a row
-template <>
-struct Row8<__nv_bfloat16> {
-  uint4 v;
-  MXG_DEVINL void load(const void* p) { v = *static_cast<const uint4*>(p); }
-  MXG_DEVINL void store(void* p) const { *static_cast<uint4*>(p) = v; }
-  // values j, j + 1 of the row
-  MXG_DEVINL void get(int j, float& lo, float& hi) const {
-    lo = bf16lo_to_f32((&v.x)[j >> 1]);
-    hi = bf16hi_to_f32((&v.x)[j >> 1]);
-  }
-  MXG_DEVINL void set(int j, float lo, float hi) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-    (&v.x)[j >> 1] = *reinterpret_cast<const uint32_t*>(&r);
-  }
-};
-template <>
-struct Row8<float> {
-  float4 v[2];
-  MXG_DEVINL void load(const void* p) {
-    v[0] = *static_cast<const float4*>(p);
-    v[1] = *(static_cast<const float4*>(p) + 1);
-  }
-  MXG_DEVINL void store(void* p) const {
-    *static_cast<float4*>(p) = v[0];
-    *(static_cast<float4*>(p) + 1) = v[1];
-  }
-  MXG_DEVINL void get(int j, float& lo, float& hi) const {
-    lo = (&v[0].x)[j];
-    hi = (&v[0].x)[j + 1];
-  }
-  MXG_DEVINL void set(int j, float lo, float hi) {
-    (&v[0].x)[j] = lo;
-    (&v[0].x)[j + 1] = hi;
-  }
-};
-
-// One product's fragments of B for a chunk of kChunk ranks: 32 ranks are 16
-// bytes of a row a lane, 16 ranks 8 bytes, 8 ranks 4 bytes (half of the depth).
-template <int kChunk>
-struct Frag {
-  uint32_t v[kChunk / 8];
-  MXG_DEVINL void load(const uint16_t* row, int tq) {
-    const uint16_t* src = row + kChunk / 4 * tq;
-    if constexpr (kChunk == 32) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
-      v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-    } else if constexpr (kChunk == 16) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-      v[0] = w.x; v[1] = w.y;
-    } else {
-      v[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+  } else if (warp == 1) {
+    const uint32_t el = ptx::elect_one();
+    int stage = 0, pass = 0;
+    uint32_t phase = 0;
+    bool ok = true, issued = false;
+    for (int o0 = 0; ok && o0 < count; o0 += per_pass, ++pass) {
+      const uint32_t idesc = idesc_bf16((min(per_pass, count - o0) * a.R + 15) & ~15);
+      ok = ptx::mbar_wait(acc_empty, (pass & 1u) ^ 1u, abort_flag, a.status, p.timeout_ns);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      for (int k = s0; k < s1; ++k) {
+        ok = ptx::mbar_wait(full_bar(stage), phase, abort_flag, a.status, p.timeout_ns);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint64_t xd = ptx::smem_desc(sbase + stage * kShrinkStage, 16, 1024, 2);
+        const uint64_t ad = ptx::smem_desc(sbase + stage * kShrinkStage + kTileBytes, 16, 1024, 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ptx::mma_f16_if(el, tmem, xd + 2 * j, ad + 2 * j, idesc, k != s0 || j != 0);
+        issued = true;
+        ptx::tc_commit_if(el, empty_bar(stage));
+        if (++stage == kShrinkStages) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+      ptx::tc_commit_if(el, acc_full);
     }
-  }
-};
-
-// acc += u * B over a chunk; u: this lane's row g (and g + 8, `pitch` 8 rows on)
-// of the 16-token group, in shared memory.
-template <int kChunk>
-MXG_DEVINL void chunk_products(float (*acc)[4], const uint16_t* u, int pitch, const Frag<kChunk>* b, int tq) {
-  const uint16_t* lo = u + kChunk / 4 * tq;
-  const uint16_t* hi = lo + 8 * pitch;
-  if constexpr (kChunk == 32) {
-    const uint4 l = *reinterpret_cast<const uint4*>(lo), h = *reinterpret_cast<const uint4*>(hi);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) mma_bf16(acc[n], l.x, h.x, l.y, h.y, b[n].v[0], b[n].v[1]);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) mma_bf16(acc[n], l.z, h.z, l.w, h.w, b[n].v[2], b[n].v[3]);
-  } else if constexpr (kChunk == 16) {
-    const uint2 l = *reinterpret_cast<const uint2*>(lo), h = *reinterpret_cast<const uint2*>(hi);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) mma_bf16(acc[n], l.x, h.x, l.y, h.y, b[n].v[0], b[n].v[1]);
+    if (issued) {  // every MMA has retired before TMEM is released
+      ptx::tc_commit_if(el, drain);
+      volatile int no_abort = 0;
+      ptx::mbar_wait(drain, 0, &no_abort, a.status, p.drain_ns);
+    }
   } else {
-    const uint32_t l = *reinterpret_cast<const uint32_t*>(lo), h = *reinterpret_cast<const uint32_t*>(hi);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) mma_bf16(acc[n], l, h, 0u, 0u, b[n].v[0], 0u);
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const int ord = tile.ord[row];
+    const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
+    float* dst = p.u + ((int64_t)blockIdx.x * a.T + t0 + row) * a.R;
+    int pass = 0;
+    for (int o0 = 0; o0 < count; o0 += per_pass, ++pass) {
+      const bool ready = ptx::mbar_wait(acc_full, pass & 1u, abort_flag, a.status, p.timeout_ns);
+      if (!__all_sync(kFull, ready)) break;
+      ptx::tc_fence_after();
+      const int na = min(per_pass, count - o0);
+      for (int i = 0; i < na; ++i) {
+        const bool mine = ord == o0 + i;
+        if (!__any_sync(kFull, mine)) continue;
+        for (int r = 0; r < a.R; r += 8) {
+          uint32_t v[8];
+          ptx::tmem_ld_32x32b_x8(tq + i * a.R + r, v);
+          ptx::tmem_ld_wait();
+          if (mine) ptx::st_global_v8(dst + r, v);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(acc_empty);
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kShrinkTmem);
   }
 }
 
-// kChunk: the ranks are taken 32, 16 or 8 at a time (the largest that divides
-// R).  The loop over columns has no branches: fragments past the last column
-// repeat others, and 16-token groups without the adapter are multiplied too.
-template <typename TOut, int kChunk>
-__global__ void __launch_bounds__(kLoraThreads, 4) lora_expand_tile_kernel(const LoraParams p) {
-  constexpr int kTerms = sizeof(TOut) == 2 ? 2 : 3;
+// expand: grid (column chunks, tiles, adapter groups), 320 threads: warp 0 loads
+// blocks of 128 columns of B (TMA), warp 1 issues u * B^T into one of two TMEM
+// accumulators, warps 2-9 add y.  u is the M operand, as kTerms BF16 terms; a
+// token's row of u is its own adapter's, and of the product with another
+// adapter's B the row is not used.
+// An epilogue warp has 32 rows and half of the block's columns.  Its y moves in
+// pieces of 32 rows x 128 bytes through a ring of shared-memory buffers, so that
+// global memory sees whole lines and two pieces are always on their way.
+constexpr int kExpThreads = 320;
+constexpr int kExpCols = 128;
+constexpr int kPiecePitch = kRowBytes + 16;
+constexpr int kPieceBytes = 32 * kPiecePitch;
+constexpr int kExpTmem = 256;
+
+template <typename TOut>
+struct Exp {
+  static constexpr int kTerms = sizeof(TOut) == 2 ? 2 : 3;
+  static constexpr int kStages = sizeof(TOut) == 2 ? 3 : 2;  // 128 columns x 64 ranks of B each
+  static constexpr int kPieces = sizeof(TOut) == 2 ? 3 : 2;
+  static int smem(int R) { return (kTerms * ((R + 63) / 64) + kStages) * kTileBytes + 8 * kPieces * kPieceBytes + 1024; }
+};
+
+// y + d for the 16 bytes of a row's piece, rounded once.
+template <typename TOut>
+MXG_DEVINL uint4 add16(const uint4& y, const float* d);
+template <>
+MXG_DEVINL uint4 add16<__nv_bfloat16>(const uint4& y, const float* d) {
+  uint4 o;
+  const uint32_t* w = &y.x;
+  uint32_t* r = &o.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(bf16lo_to_f32(w[i]) + d[2 * i], bf16hi_to_f32(w[i]) + d[2 * i + 1]);
+    r[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return o;
+}
+template <>
+MXG_DEVINL uint4 add16<float>(const uint4& y, const float* d) {
+  return make_uint4(__float_as_uint(__uint_as_float(y.x) + d[0]), __float_as_uint(__uint_as_float(y.y) + d[1]),
+                    __float_as_uint(__uint_as_float(y.z) + d[2]), __float_as_uint(__uint_as_float(y.w) + d[3]));
+}
+
+template <typename TOut>
+__global__ void __launch_bounds__(kExpThreads, 1)
+    lora_expand_tile_kernel(const __grid_constant__ CUtensorMap tmB, const LoraParams p) {
+  constexpr int kTerms = Exp<TOut>::kTerms, kStages = Exp<TOut>::kStages, kPieces = Exp<TOut>::kPieces;
+  constexpr int kPieceCols = kRowBytes / (int)sizeof(TOut);  // 64 or 32
+  constexpr int kPer = 64 / kPieceCols;                      // pieces of a warp's 64 columns
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - ptx::smem_u32(smem_raw));
   __shared__ Tile tile;
-  extern __shared__ __align__(16) uint16_t us[];  // [kTerms][kTile][R + 8]: scale * u as a sum of BF16 terms
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
   const LoraArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+  auto acc_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
+  auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
+  const uint32_t drain = bar0 + 8u * (2 * kStages + 4);
+  const int atoms = (a.R + 63) >> 6;                       // 64-rank rows of u and B
+  const int ubytes = kTerms * atoms * kTileBytes;          // [term][atom][128 rows]
   const int64_t t0 = (int64_t)blockIdx.y * kTile;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(acc_full(b), 1);
+      ptx::mbar_init(acc_empty(b), 8);
+    }
+    ptx::mbar_init(drain, 1);
+    abort_word = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), kExpTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
   read_tile(tile, a, t0);
-  if (blockIdx.z > 0 && (int)blockIdx.z >= tile.count) return;
-  const int pitch = a.R + 8;
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int count = tile.count;
+  const bool idle = (int)blockIdx.z >= max(count, 1);  // no adapter for this CTA
+  // u: ranks past R up to the product's depth are zero
   ptx::pdl_wait();
-  for (int i = threadIdx.x; i < kTile * a.R; i += kLoraThreads) {
-    const int row = i / a.R, r = i - row * a.R;
-    const int o = tile.ord[row];
-    if (o < 0 || o % (int)gridDim.z != (int)blockIdx.z) continue;
-    float s = sum_u(p, t0 + row, r);
-    if (a.scale != nullptr) s *= __ldg(a.scale + tile.id[row]);
+  const int depth = (a.R + 15) & ~15;
+  for (int i = threadIdx.x; !idle && i < kTile * (depth >> 3); i += kExpThreads) {
+    const int row = i / (depth >> 3), r0 = (i - row * (depth >> 3)) * 8;
+    float v[8] = {};
+    if (tile.ord[row] >= 0 && r0 < a.R) {
+      const float* src = p.u + (t0 + row) * a.R + r0;
+      for (int k = 0; k < p.ksplit; ++k) {
+        const float4 lo = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)k * a.T * a.R));
+        const float4 hi = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)k * a.T * a.R) + 1);
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+      }
+      const float sc = a.scale != nullptr ? __ldg(a.scale + tile.id[row]) : 1.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= sc;
+    }
+    // 16-byte chunk c of a row sits at c ^ (row % 8)
+    const int at = (r0 >> 6) * kTileBytes + row * kRowBytes + ((((r0 & 63) >> 3) ^ (row & 7)) << 4);
 #pragma unroll
     for (int q = 0; q < kTerms; ++q) {
-      const __nv_bfloat16 h = __float2bfloat16_rn(s);
-      us[(q * kTile + row) * pitch + r] = *reinterpret_cast<const uint16_t*>(&h);
-      s -= __bfloat162float(h);
-    }
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  const int64_t c_first = (int64_t)blockIdx.x * p.cols + warp * 32;
-  // columns of this warp from its first on (N < 2^31)
-  const int left = (int)(min(a.N, (int64_t)(blockIdx.x + 1) * p.cols) - c_first);
-  const TOut* y0 = static_cast<const TOut*>(a.y) + (t0 + g) * a.ld_y + c_first + 8 * tq;
-  TOut* out0 = static_cast<TOut*>(a.out) + (t0 + g) * a.ld_out + c_first + 8 * tq;
-  const int64_t ystep = 8 * a.ld_y, ostep = 8 * a.ld_out;
-  // column g of product n is output column 8 (g / 2) + 2 n + g % 2
-  const int bcol = 8 * (g >> 1) + (g & 1);
-
-  if (blockIdx.z == 0 && (a.out != a.y || a.ld_out != a.ld_y)) {  // rows without an adapter
-    bool none[kGroups][2], any = false;
+      uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 2 * kGroups; ++i) {
-      none[i >> 1][i & 1] = t0 + 8 * i + g < a.T && tile.ord[8 * i + g] < 0;
-      any |= none[i >> 1][i & 1];
-    }
-    if (__any_sync(kFull, any))
-      for (int c = 0; c + 8 * tq < left; c += kLoraWarps * 32)
-#pragma unroll
-        for (int i = 0; i < 2 * kGroups; ++i)
-          if (none[i >> 1][i & 1]) {
-            Row8<TOut> v;
-            v.load(y0 + i * ystep + c);
-            v.store(out0 + i * ostep + c);
-          }
-  }
-
-  for (int o = blockIdx.z; o < tile.count; o += gridDim.z) {
-    const uint16_t* B = a.B + ((int64_t)tile.list[o] * a.N + c_first) * a.R;
-    bool mine[2 * kGroups];  // row 8 i + g belongs to the adapter
-#pragma unroll
-    for (int i = 0; i < 2 * kGroups; ++i) mine[i] = t0 + 8 * i + g < a.T && tile.ord[8 * i + g] == o;
-    Row8<TOut> y[2 * kGroups];
-    Frag<kChunk> b[4];
-    auto load_y = [&](int c) {
-#pragma unroll
-      for (int i = 0; i < 2 * kGroups; ++i)
-        if (mine[i] && c + 8 * tq < left) y[i].load(y0 + i * ystep + c);
-    };
-    auto load_b = [&](int c, int r) {
-      const uint16_t* row = B + (int64_t)(c + bcol < left ? c + bcol : 0) * a.R + r;
-      const int step = c + bcol < left ? 2 * a.R : 0;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) b[n].load(row + n * step, tq);
-    };
-    if (left <= 0) continue;
-    load_y(0);
-    load_b(0, 0);
-    for (int c = 0; c < left; c += kLoraWarps * 32) {
-      // the products add to y (a lane's columns 2 n, 2 n + 1 of product n)
-      float acc[kGroups][4][4];
-#pragma unroll
-      for (int i = 0; i < 2 * kGroups; ++i)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) y[i].get(2 * n, acc[i >> 1][n][2 * (i & 1)], acc[i >> 1][n][2 * (i & 1) + 1]);
-      load_y(c + kLoraWarps * 32);
-      for (int r = 0; r < a.R; r += kChunk) {
-        if (r > 0) load_b(c, r);
-#pragma unroll
-        for (int q = kTerms - 1; q >= 0; --q)
-#pragma unroll
-          for (int m = 0; m < kGroups; ++m)
-            chunk_products<kChunk>(acc[m], us + (q * kTile + m * 16 + g) * pitch + r, pitch, b, tq);
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        v[2 * j] -= bf16lo_to_f32(w[j]);
+        v[2 * j + 1] -= bf16hi_to_f32(w[j]);
       }
-      load_b(c + kLoraWarps * 32, 0);
-#pragma unroll
-      for (int i = 0; i < 2 * kGroups; ++i)
-        if (mine[i] && c + 8 * tq < left) {
-          Row8<TOut> v;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) v.set(2 * n, acc[i >> 1][n][2 * (i & 1)], acc[i >> 1][n][2 * (i & 1) + 1]);
-          v.store(out0 + i * ostep + c);
+      *reinterpret_cast<uint4*>(smem + q * atoms * kTileBytes + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  ptx::fence_proxy_async_smem();
+  __syncthreads();
+
+  const int64_t c0 = (int64_t)blockIdx.x * p.cols;
+  const int ncols = (int)(min(a.N, c0 + p.cols) - c0);
+  const int blocks = (ncols + kExpCols - 1) / kExpCols;
+  const int o_first = blockIdx.z, o_step = gridDim.z;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_phase = 0;
+      bool ok = true;
+      for (int o = o_first; ok && o < count; o += o_step) {
+        // rows past the adapter's last column belong to the next one (or lie past the tensor and read as zero)
+        const int64_t row0 = (int64_t)tile.list[o] * a.N + c0;
+        for (int b = 0; ok && b < blocks; ++b)
+          for (int q = 0; q < atoms; ++q) {
+            ok = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status, p.timeout_ns);
+            if (!ok) break;
+            const uint32_t fb = full_bar(stage);
+            ptx::mbar_arrive_expect_tx(fb, kTileBytes);
+            armed |= 1u << stage;
+            armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+            ptx::tma_load_2d(sbase + ubytes + stage * kTileBytes, &tmB, q * 64, (int)(row0 + b * kExpCols), fb);
+            if (++stage == kStages) { stage = 0; phase ^= 1u; }
+          }
+      }
+      for (int s = 0; s < kStages; ++s)
+        if ((armed >> s) & 1u) {
+          volatile int no_abort = 0;
+          ptx::mbar_wait(full_bar(s), (armed_phase >> s) & 1u, &no_abort, a.status, p.drain_ns);
         }
     }
+  } else if (warp == 1) {
+    const uint32_t el = ptx::elect_one();
+    const uint32_t idesc = idesc_bf16(kExpCols);
+    int stage = 0, n = 0;
+    uint32_t phase = 0;
+    bool ok = true, issued = false;
+    for (int o = o_first; ok && o < count; o += o_step)
+      for (int b = 0; ok && b < blocks; ++b, ++n) {
+        ok = ptx::mbar_wait(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u, abort_flag, a.status, p.timeout_ns);
+        if (!ok) break;
+        const uint32_t d = tmem + (n & 1) * kExpCols;
+        for (int at = 0; at < atoms; ++at) {
+          ok = ptx::mbar_wait(full_bar(stage), phase, abort_flag, a.status, p.timeout_ns);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint64_t bd = ptx::smem_desc(sbase + ubytes + stage * kTileBytes, 16, 1024, 2);
+          const int steps = min(4, (depth - at * 64) >> 4);
+          for (int q = kTerms - 1; q >= 0; --q) {  // the smallest term first
+            const uint64_t ud = ptx::smem_desc(sbase + (q * atoms + at) * kTileBytes, 16, 1024, 2);
+            for (int j = 0; j < steps; ++j)
+              ptx::mma_f16_if(el, d, ud + 2 * j, bd + 2 * j, idesc, at != 0 || q != kTerms - 1 || j != 0);
+          }
+          issued = true;
+          ptx::tc_commit_if(el, empty_bar(stage));
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+        if (ok) ptx::tc_commit_if(el, acc_full(n & 1));
+      }
+    if (issued) {
+      ptx::tc_commit_if(el, drain);
+      volatile int no_abort = 0;
+      ptx::mbar_wait(drain, 0, &no_abort, a.status, p.drain_ns);
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
+    uint8_t* ring = smem + ubytes + kStages * kTileBytes + (warp - 2) * kPieces * kPieceBytes;
+    const uint32_t ring_a = sbase + ubytes + kStages * kTileBytes + (warp - 2) * kPieces * kPieceBytes;
+    // moving: lane l has 16 bytes (l % 8) of rows l / 8, l / 8 + 4, ...; adding: row l
+    const int mrow = lane >> 3, mcol = (lane & 7) * (16 / (int)sizeof(TOut));
+    const int64_t row0 = t0 + quarter * 32;
+    const TOut* ybase = static_cast<const TOut*>(a.y) + row0 * a.ld_y + c0 + half * 64 + mcol;
+    TOut* obase = static_cast<TOut*>(a.out) + row0 * a.ld_out + c0 + half * 64 + mcol;
+    const bool in_place = a.out == a.y && a.ld_out == a.ld_y;
+    uint32_t rows = 0;  // bit i: row mrow + 4 i is moved in this pass
+    auto pick = [&](int o) {
+      rows = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = mrow + 4 * i;
+        if (row0 + r < a.T && tile.ord[quarter * 32 + r] == o) rows |= 1u << i;
+      }
+    };
+    if (blockIdx.z == 0 && !in_place) {  // rows without an adapter are copied
+      pick(-1);
+      if (__any_sync(kFull, rows != 0))
+        for (int c = 0; c < ncols; c += kExpCols)
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            const int col = c + q * kPieceCols;
+            if (half * 64 + col + mcol < ncols) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if ((rows >> i) & 1)
+                  *reinterpret_cast<uint4*>(obase + (mrow + 4 * i) * a.ld_out + col) =
+                      *reinterpret_cast<const uint4*>(ybase + (mrow + 4 * i) * a.ld_y + col);
+            }
+          }
+    }
+    int n = 0;  // accumulators taken
+    for (int o = o_first; o < count; o += o_step) {
+      pick(o);
+      const bool wanted = __any_sync(kFull, rows != 0);
+      const int pieces = wanted ? blocks * kPer : 0;
+      auto fetch = [&](int k) {  // piece k of the pass into its buffer
+        if (k < pieces) {
+          const int col = (k / kPer) * kExpCols + (k % kPer) * kPieceCols;
+          const uint32_t dst = ring_a + (k % kPieces) * kPieceBytes + mrow * kPiecePitch + (lane & 7) * 16;
+          if (half * 64 + col + mcol < ncols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((rows >> i) & 1)
+                ptx::cp_async_16(dst + 4 * i * kPiecePitch, ybase + (mrow + 4 * i) * a.ld_y + col);
+          }
+        }
+        ptx::cp_async_commit();
+      };
+#pragma unroll
+      for (int k = 0; k < kPieces - 1; ++k) fetch(k);
+      bool ok = true;
+      for (int b = 0; b < blocks; ++b, ++n) {
+        ok = ptx::mbar_wait(acc_full(n & 1), (n >> 1) & 1u, abort_flag, a.status, p.timeout_ns);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        float d[64];
+        if (wanted) {
+          ptx::tmem_ld_32x32b_x32(tq + (n & 1) * kExpCols, reinterpret_cast<uint32_t*>(d));
+          ptx::tmem_ld_32x32b_x32(tq + (n & 1) * kExpCols + 32, reinterpret_cast<uint32_t*>(d) + 32);
+          ptx::tmem_ld_wait();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(acc_empty(n & 1));
+        if (!wanted) continue;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const int k = b * kPer + q;
+          fetch(k + kPieces - 1);
+          ptx::cp_async_wait<kPieces - 1>();
+          __syncwarp();
+          uint8_t* piece = ring + (k % kPieces) * kPieceBytes;
+          uint4* mine = reinterpret_cast<uint4*>(piece + lane * kPiecePitch);
+          constexpr int kVals = 16 / (int)sizeof(TOut);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mine[j] = add16<TOut>(mine[j], d + q * kPieceCols + j * kVals);
+          __syncwarp();
+          const int col = b * kExpCols + q * kPieceCols;
+          if (half * 64 + col + mcol < ncols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((rows >> i) & 1)
+                *reinterpret_cast<uint4*>(obase + (mrow + 4 * i) * a.ld_out + col) =
+                    *reinterpret_cast<const uint4*>(piece + (mrow + 4 * i) * kPiecePitch + (lane & 7) * 16);
+          }
+          __syncwarp();
+        }
+      }
+      ptx::cp_async_wait<0>();
+      if (!ok) break;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kExpTmem);
   }
 }
 
@@ -542,31 +702,69 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_expand_tile_kernel(const
 // Adapter bytes that the per-token kernels would read, from L2 where tokens
 // share them, against this limit.
 constexpr double kTokenBytes = 64e6;
-
-template <typename TOut>
-const void* expand_tile(int R) {
-  if (R % 32 == 0) return (const void*)lora_expand_tile_kernel<TOut, 32>;
-  if (R % 16 == 0) return (const void*)lora_expand_tile_kernel<TOut, 16>;
-  return (const void*)lora_expand_tile_kernel<TOut, 8>;
-}
+constexpr int kLoraSms = 152;
 
 bool per_token(int64_t T, int64_t N, int64_t K, int R) {
   return (double)T * R * (double)(K + N) * 2.0 <= kTokenBytes && T <= 65535;
 }
 
-// Tiles: 32-element blocks of K per shrink CTA, a multiple of the warps, so
-// that there are about eight CTAs per SM if K allows.
-int shrink_blocks(int64_t T, int64_t K) {
-  const int64_t tiles = (T + kTile - 1) / kTile;
-  const int64_t kblocks = (K + 31) / 32;
-  const int64_t split = std::max<int64_t>(1, (8 * 152 + tiles - 1) / tiles);
-  const int64_t per = std::max<int64_t>((kblocks + split - 1) / split, 2 * kLoraWarps);
-  return (int)std::min<int64_t>((per + kLoraWarps - 1) / kLoraWarps * kLoraWarps, 1 << 20);
+// Tiles: 64-element steps of K per shrink CTA.  Among the splits that leave
+// eight steps a CTA (and at most sixteen splits), the one that fills its last
+// wave of CTAs best.
+int shrink_steps(int64_t T, int64_t K) {
+  const int64_t tiles = (T + kTile - 1) / kTile, steps = (K + 63) / 64;
+  int64_t best = steps;
+  double best_eff = 0.0;
+  for (int64_t split = 1; split <= 16 && (split == 1 || steps / split >= 8); ++split) {
+    const int64_t per = (steps + split - 1) / split;
+    const int64_t ctas = tiles * ((steps + per - 1) / per);
+    const double eff = (double)(tiles * steps) / (double)((ctas + kLoraSms - 1) / kLoraSms * kLoraSms * per);
+    if (eff > best_eff * 1.02) {
+      best_eff = eff;
+      best = per;
+    }
+  }
+  return (int)best;
 }
 
 int64_t tile_splits(int64_t T, int64_t K) {
-  const int64_t per = shrink_blocks(T, K);
-  return ((K + 31) / 32 + per - 1) / per;
+  const int64_t per = shrink_steps(T, K);
+  return ((K + 63) / 64 + per - 1) / per;
+}
+
+constexpr int kLoraMaxDevices = 64;
+std::mutex g_lora_mu;
+
+// The dynamic shared-memory opt-in of the tile kernels, once per device.
+cudaError_t ensure_lora_attr() {
+  static bool done[kLoraMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(g_lora_mu);
+  if (dev < kLoraMaxDevices && done[dev]) return cudaSuccess;
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute((const void*)lora_shrink_tile_kernel, attr, kShrinkSmem)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute((const void*)lora_expand_tile_kernel<float>, attr, Exp<float>::smem(128))) != cudaSuccess ||
+      (e = cudaFuncSetAttribute((const void*)lora_expand_tile_kernel<__nv_bfloat16>, attr,
+                                Exp<__nv_bfloat16>::smem(128))) != cudaSuccess)
+    return e;
+  if (dev < kLoraMaxDevices) done[dev] = true;
+  return cudaSuccess;
+}
+
+cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** args, bool overlap, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace
@@ -582,46 +780,45 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms)
   p.a = a;
   p.u = a.ws;
   const bool f32 = a.dtype == MXG_OUT_F32;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kLoraThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  const void *shrink, *expand;
-  dim3 sgrid, egrid;
-  size_t smem = 0;
+  cudaError_t e;
   if (per_token(a.T, a.N, a.K, a.R)) {
     p.ksplit = (int)((a.K + kTokK - 1) / kTokK);
-    shrink = (const void*)lora_shrink_token_kernel;
-    expand = f32 ? (const void*)lora_expand_token_kernel<float> : (const void*)lora_expand_token_kernel<__nv_bfloat16>;
-    sgrid = dim3((unsigned)p.ksplit, (unsigned)a.T, (unsigned)((a.R + kTokR - 1) / kTokR));
-    egrid = dim3((unsigned)((a.N + kLoraThreads * kTokCols - 1) / (kLoraThreads * kTokCols)), (unsigned)a.T);
-  } else {
-    const int64_t tiles = (a.T + kTile - 1) / kTile;
-    if (tiles > 65535) return cudaErrorInvalidConfiguration;
-    // adapters of a tile over CTAs: more where there are few tiles
-    const int groups = std::min<int>(a.n, tiles < 64 ? 8 : 2);
-    p.blocks = shrink_blocks(a.T, a.K);
-    p.ksplit = (int)tile_splits(a.T, a.K);
-    // columns per CTA: as many as leave about sixteen CTAs per SM, in steps of 128
-    const int64_t chunks = std::max<int64_t>(1, 16 * (int64_t)num_sms / tiles);
-    p.cols = (int)std::min<int64_t>(8192, std::max<int64_t>(128, (a.N / chunks + 127) / 128 * 128));
-    shrink = (const void*)lora_shrink_tile_kernel;
-    expand = f32 ? expand_tile<float>(a.R) : expand_tile<__nv_bfloat16>(a.R);
-    sgrid = dim3((unsigned)p.ksplit, (unsigned)tiles, (unsigned)groups);
-    egrid = dim3((unsigned)((a.N + p.cols - 1) / p.cols), (unsigned)tiles, (unsigned)groups);
-    smem = (size_t)(f32 ? 3 : 2) * kTile * (a.R + 8) * 2;
+    void* args[] = {(void*)&p};
+    e = launch((const void*)lora_shrink_token_kernel,
+               dim3((unsigned)p.ksplit, (unsigned)a.T, (unsigned)((a.R + kTokR - 1) / kTokR)), kLoraThreads, 0, args,
+               false, stream);
+    if (e != cudaSuccess) return e;
+    return launch(f32 ? (const void*)lora_expand_token_kernel<float> : (const void*)lora_expand_token_kernel<__nv_bfloat16>,
+                  dim3((unsigned)((a.N + kLoraThreads * kTokCols - 1) / (kLoraThreads * kTokCols)), (unsigned)a.T),
+                  kLoraThreads, 0, args, true, stream);
   }
-  void* args[] = {(void*)&p};
-  cfg.gridDim = sgrid;
-  cudaError_t e = cudaLaunchKernelExC(&cfg, shrink, args);
+  const int64_t tiles = (a.T + kTile - 1) / kTile;
+  if ((e = ensure_lora_attr()) != cudaSuccess) return e;
+  p.blocks = shrink_steps(a.T, a.K);
+  p.ksplit = (int)tile_splits(a.T, a.K);
+  p.timeout_ns = wait_timeout_ns();
+  p.drain_ns = std::max<uint64_t>(p.timeout_ns, 200000000ull);
+  // columns per CTA: a few blocks, so that a CTA's start (its u) is spread over
+  // some work, in about three waves or more; the adapters of a tile go to
+  // several CTAs where there are few tiles
+  const int64_t chunks = std::max<int64_t>(1, 3 * (int64_t)num_sms / tiles);
+  const int64_t blocks = (a.N + kExpCols - 1) / kExpCols;
+  p.cols = (int)std::min<int64_t>(16, std::max<int64_t>(1, (blocks + chunks - 1) / chunks)) * kExpCols;
+  const int groups = std::min<int>(a.n, tiles < 16 ? 8 : 1);
+  CUtensorMap tmX, tmA, tmB;
+  const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!make_tmap(&tmX, a.x, dt, a.K, a.T, a.ld_x * 2, 64, kTile) ||
+      !make_tmap(&tmA, a.A, dt, a.K, (int64_t)a.n * a.R, a.K * 2, 64, a.R) ||
+      !make_tmap(&tmB, a.B, dt, a.R, (int64_t)a.n * a.N, (int64_t)a.R * 2, 64, kExpCols))
+    return cudaErrorInvalidValue;
+  void* sargs[] = {(void*)&tmX, (void*)&tmA, (void*)&p};
+  e = launch((const void*)lora_shrink_tile_kernel, dim3((unsigned)p.ksplit, (unsigned)tiles), kShrinkThreads, kShrinkSmem,
+             sargs, false, stream);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = egrid;
-  cfg.dynamicSmemBytes = smem;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelExC(&cfg, expand, args);
+  void* eargs[] = {(void*)&tmB, (void*)&p};
+  return launch(f32 ? (const void*)lora_expand_tile_kernel<float> : (const void*)lora_expand_tile_kernel<__nv_bfloat16>,
+                dim3((unsigned)((a.N + p.cols - 1) / p.cols), (unsigned)tiles, (unsigned)groups), kExpThreads,
+                (size_t)(f32 ? Exp<float>::smem(a.R) : Exp<__nv_bfloat16>::smem(a.R)), eargs, true, stream);
 }
 
 }  // namespace mxg

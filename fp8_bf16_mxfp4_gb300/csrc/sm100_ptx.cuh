@@ -505,6 +505,16 @@ MXG_DEVINL void mma_mxf8f6f4_if(uint32_t e, uint32_t d, uint64_t adesc, uint64_t
       : "memory");
 }
 
+MXG_DEVINL void mma_f16_if(uint32_t e, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
+      : "memory");
+}
+
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading
 // and stride byte offsets (16-byte units), fixed version bits 46-48 = 0b001,
 // base offset 0, swizzle mode in bits 61-63 (0 none, 2 = 128-byte swizzle).

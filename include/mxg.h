@@ -525,7 +525,8 @@ mxg_status moe_experts(const void* x, int64_t tokens, int64_t ld_x, const int32_
  *   ids    : int32 [tokens]; scale: float [adapters], NULL for 1
  *   ws     : at least lora_add_workspace_size(...) bytes, 256-byte aligned
  * K % 8 == 0, N % 8 == 0, rank a multiple of 8 up to 128 (pad adapters of a
- * lower rank with zeros), adapters >= 1, 0 <= tokens <= 2097120.  Device error:
+ * lower rank with zeros), adapters >= 1, adapters * N and adapters *
+ * rank below 2^31, 0 <= tokens <= 8388480.  Device error:
  * MXG_ERR_INDEX (an id >= adapters; that token's row of out is unspecified). */
 size_t lora_add_workspace_size(int64_t tokens, int64_t K, int32_t rank);
 mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, const void* A, const void* B,

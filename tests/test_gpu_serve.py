@@ -249,6 +249,54 @@ def test_lora(T, K, N, R, n, runs, dtype):
     check_lora(T, K, N, R, n, dtype, runs)
 
 
+# more adapter reads than the per-token form takes on: 128-token tiles
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,K,N,R,n,runs", [
+    (129, 2056, 2064, 128, 70, 1), (130, 4104, 4120, 64, 3, 1), (257, 8200, 520, 16, 40, 1), (300, 2048, 2048, 32, 1, 1),
+    (600, 1160, 2056, 72, 9, 5), (1000, 1000, 1544, 24, 5, 37), (2000, 520, 600, 40, 2, 500), (4000, 520, 600, 8, 9, 100),
+    (700, 72, 3080, 56, 12, 128), (1200, 3080, 72, 96, 4, 1)])
+def test_lora_tiles(T, K, N, R, n, runs, dtype):
+    assert T * R * (K + N) * 2 > 64e6
+    check_lora(T, K, N, R, n, dtype, runs)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_lora_tiles_strides_in_place_and_no_scale(dtype):
+    check_lora(400, 1032, 1544, 40, 5, dtype, pad=24, runs=3)
+    check_lora(400, 1032, 1544, 40, 5, dtype, pad=8, runs=3, inplace=True)
+    check_lora(400, 1032, 1544, 40, 5, dtype, runs=90, inplace=True, scale=False)
+
+
+def test_lora_tiles_select_rows():
+    """Infinities and NaN of an adapter, or of a token, stay with its tokens."""
+    mxg = _mxg()
+    g = torch.Generator().manual_seed(6)
+    T, K, N, R, n = 300, 1800, 2000, 32, 5
+    to = lambda t: t.to(torch.bfloat16).to(DEV)  # noqa: E731
+    x, y = to(torch.randn(T, K, generator=g)), to(torch.randn(T, N, generator=g))
+    A, B = to(torch.randn(n, R, K, generator=g) * 0.03), to(torch.randn(n, N, R, generator=g))
+    ids = torch.randint(-1, n, (T,), generator=g).to(torch.int32)
+    ids[ids == 4] = 1  # adapter 4 is not used
+    want = mxg.lora_add(y, x, A, B, ids.to(DEV), check=True)
+    assert torch.equal(want[(ids < 0).to(DEV)], y[(ids < 0).to(DEV)])
+    A[4], B[4] = float("nan"), float("nan")
+    assert torch.equal(mxg.lora_add(y, x, A, B, ids.to(DEV), check=True), want)
+    A[2], B[2] = float("inf"), float("nan")
+    x[ids == -1] = float("nan")
+    hit = int((ids == 3).nonzero()[0])
+    x[hit] = float("nan")
+    got = mxg.lora_add(y, x, A, B, ids.to(DEV), check=True)
+    keep = (ids != 2).to(DEV)
+    keep[hit] = False
+    assert torch.equal(got[keep], want[keep]) and bool(got[~keep].isnan().all())
+    bad = ids.clone()
+    bad[150] = n
+    mxg.lora_add(y, x, A, B, bad.to(DEV))
+    with pytest.raises(mxg.MXGError) as e:
+        mxg.check_status()
+    assert e.value.code == 11
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_lora_strides_in_place_and_no_scale(dtype):
     check_lora(37, 520, 264, 16, 5, dtype, pad=24)
