@@ -17,7 +17,7 @@
 // product: an adapter's infinities or NaN reach its own tokens only.  u keeps its
 // fp32 accuracy as a sum of two BF16 terms (2^-17; BF16 output) or three (2^-25;
 // FP32 output).  (mma.sync runs at 1/16 of the tcgen05 rate on GB300: a tile
-// form on it was held to 265 us by its pipe where this one takes @@ us, at 8192
+// form on it was held to 264 us by its pipe where this one takes 240 us, at 8192
 // tokens, 8192 x 28672, rank 32.)
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -496,11 +496,22 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     float v[8] = {};
     if (tile.ord[row] >= 0 && r0 < a.R) {
       const float* src = p.u + (t0 + row) * a.R + r0;
-      for (int k = 0; k < p.ksplit; ++k) {
-        const float4 lo = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)k * a.T * a.R));
-        const float4 hi = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)k * a.T * a.R) + 1);
-        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+      for (int k0 = 0; k0 < p.ksplit; k0 += 4) {
+        float4 w[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          w[k][0] = w[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k0 + k < p.ksplit) {
+            const float4* part = reinterpret_cast<const float4*>(src + (int64_t)(k0 + k) * a.T * a.R);
+            w[k][0] = __ldcg(part);
+            w[k][1] = __ldcg(part + 1);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[0] += w[k][0].x; v[1] += w[k][0].y; v[2] += w[k][0].z; v[3] += w[k][0].w;
+          v[4] += w[k][1].x; v[5] += w[k][1].y; v[6] += w[k][1].z; v[7] += w[k][1].w;
+        }
       }
       const float sc = a.scale != nullptr ? __ldg(a.scale + tile.id[row]) : 1.0f;
 #pragma unroll
@@ -798,12 +809,20 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms)
   p.ksplit = (int)tile_splits(a.T, a.K);
   p.timeout_ns = wait_timeout_ns();
   p.drain_ns = std::max<uint64_t>(p.timeout_ns, 200000000ull);
-  // columns per CTA: a few blocks, so that a CTA's start (its u) is spread over
-  // some work, in about three waves or more; the adapters of a tile go to
+  // columns per CTA: the split that ends soonest in whole waves of CTAs, with
+  // a CTA's start (its u) counted as four blocks; the adapters of a tile go to
   // several CTAs where there are few tiles
-  const int64_t chunks = std::max<int64_t>(1, 3 * (int64_t)num_sms / tiles);
   const int64_t blocks = (a.N + kExpCols - 1) / kExpCols;
-  p.cols = (int)std::min<int64_t>(16, std::max<int64_t>(1, (blocks + chunks - 1) / chunks)) * kExpCols;
+  int64_t best = blocks, best_cost = INT64_MAX;
+  for (int64_t per = blocks; per >= 1; per = std::min(per - 1, (blocks + (blocks + per - 1) / per) / ((blocks + per - 1) / per + 1))) {
+    const int64_t ctas = tiles * ((blocks + per - 1) / per);
+    const int64_t cost = (ctas + num_sms - 1) / num_sms * (per + 4);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = per;
+    }
+  }
+  p.cols = (int)best * kExpCols;
   const int groups = std::min<int>(a.n, tiles < 16 ? 8 : 1);
   CUtensorMap tmX, tmA, tmB;
   const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

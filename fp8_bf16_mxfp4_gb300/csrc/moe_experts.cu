@@ -52,7 +52,7 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMoeThreads = 320;  // warps 0-9
-constexpr int kUnpackThreads = 128; // warps 10-13 (E2M1 weights)
+constexpr int kUnpackThreads = 128;  // warps 10-13 (E2M1 weights)
 constexpr int kTok = 64;                  // tokens of one unit (TMEM columns of one accumulator)
 constexpr int kWTile = 128 * 128;         // one weight tile in shared memory (a byte per element)
 constexpr int kActTile = kTok * 128;
@@ -65,10 +65,10 @@ constexpr int kSyncWords = 4 * kMaxCtas;  // join counters: [CTAs][4]
 constexpr int kMoeTmemCols = 512;
 constexpr int kSfCol = 256;               // two accumulator buffers of 2 x 64 columns, then the scale slots
 constexpr int kSfSlot = 12;               // columns of one stage's scales
-// A run is at least kMinStages long, and units of up to kWholeStages are not
-// cut: joining a cut unit costs about as much as that many stages.
-constexpr int kMinStages = 8;
-constexpr int kWholeStages = 8;
+// Joining a cut unit costs about as much as kJoinStages stages, and a run of
+// cut units is at least kMinStages long.
+constexpr int kJoinStages = 6;
+constexpr int kMinStages = 4;
 constexpr int kPlanWarps = 8;             // warps 2-9 sort the slots
 
 // Shared memory.  E2M1 stages hold half of their bytes' worth of weights (4-bit
@@ -124,9 +124,12 @@ struct Runs {
   int ctas;       // runs (every one has at least one grain)
   int q, r;       // grains of a run: q + 1 for the first r runs, q for the others
   MXG_DEVINL Runs(int units, int per_unit_, int max_ctas) : per_unit(per_unit_) {
-    grain = per_unit <= kWholeStages ? per_unit : 1;
+    // whole units to every CTA, or units cut into equal runs: what ends sooner
     const int total = units * per_unit;
-    ctas = min(max_ctas, min((total + kMinStages - 1) / kMinStages, total / grain));
+    const int whole = (units + max_ctas - 1) / max_ctas * per_unit;
+    const int cut = max((total + max_ctas - 1) / max_ctas, kMinStages) + kJoinStages;
+    grain = whole <= cut ? per_unit : 1;
+    ctas = min(max_ctas, grain > 1 || per_unit == 1 ? units : (total + kMinStages - 1) / kMinStages);
     q = ctas > 0 ? total / grain / ctas : 0;
     r = ctas > 0 ? total / grain - q * ctas : 0;
   }
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
   for (int i = threadIdx.x; i < (kPlanWarps * p.E + 1) / 2; i += kThreads) reinterpret_cast<uint32_t*>(cnt)[i] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMoeStages; ++s) {
-      ptx::mbar_init(full_bar(s), 5 + (kFp4 ? kUnpackThreads / 32 : 0));  // warps 0, 6-9 and 10-13
+      ptx::mbar_init(full_bar(s), 1 + 128 + (kFp4 ? kUnpackThreads : 0));  // warp 0; the threads of warps 6-9, 10-13
       ptx::mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -448,19 +451,12 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
     // whatever its length, 3.3 TB/s over the device for rows of 64 bytes;
     // 8-byte asynchronous copies into the slots reach 6.1 TB/s.
     // A thread copies piece c of rows r, r + 16, ... of either tile.
-    constexpr int kLag = 2;  // stages in flight before the oldest is handed over
     const int tid = threadIdx.x - kMoeThreads;
     const int c = tid & 7, r = tid >> 3;
     const uint32_t slot = r * 128 + ((c ^ (r & 7)) << 4);
-    int stage = 0, gstage = 0, issued = 0, given = 0;
+    int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    auto give = [&]() {
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(full_bar(gstage));
-      if (++gstage == kMoeStages) gstage = 0;
-      ++given;
-    };
     while (ok && w.next(runs, off, tile, p.E)) {
       const int64_t row0 = kDown ? (int64_t)w.e * p.H + w.rt * 256 : (int64_t)w.e * 2 * p.I + w.rt * 128;
       const int64_t row1 = kDown ? row0 + 128 : row0 + p.I;
@@ -469,8 +465,8 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
       const uint8_t* src1 = p.w + (row1 + r) * p.ld_w + c * 8;
       const int64_t step = 16 * p.ld_w;
       for (int kc = w.k0; kc < w.k1; ++kc) {
-        const bool free = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
-        if (!__all_sync(kFull, free)) { ok = false; break; }
+        ok = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
+        if (!ok) break;
         const uint32_t dst = sbase + stage * kStageBytes + slot;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ptx::cp_async_8(dst + i * 2048, src0 + kc * 64 + i * step);
@@ -478,16 +474,11 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) ptx::cp_async_8(dst + kWTile + i * 2048, src1 + kc * 64 + i * step);
         }
-        ptx::cp_async_commit();
-        if (++issued > kLag) {
-          ptx::cp_async_wait<kLag>();
-          give();
-        }
+        ptx::cp_async_arrive(full_bar(stage));
         if (++stage == kMoeStages) { stage = 0; phase ^= 1u; }
       }
     }
-    ptx::cp_async_wait<0>();
-    while (given < issued) give();
+    ptx::cp_async_wait_all();
   } else {
     // the sorted slots are only needed by the activation and epilogue warps:
     // placed while the first weights are on their way
@@ -508,25 +499,17 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
 
     if (warp >= 6) {
       // ---------------------------------------------------------- activations
-      // Codes and scale bytes go from global to shared memory asynchronously; a
-      // stage is handed over kLag stages after its copies were issued.
+      // Codes and scale bytes go from global to shared memory asynchronously.
       // Item i of a stage is 32-block i % 4 of token i / 4; a thread takes items
       // tid and tid + 128, and the scale word of token tid.
-      constexpr int kLag = kMoeStages - 2;
       const int tid = threadIdx.x - 6 * 32;
       const int blk = tid & 3;
       const int width = kDown ? p.I : p.H;
       const uint8_t* codes = kDown ? p.hq : p.xq;
       const uint8_t* scales = kDown ? p.hs : p.xs;
-      int stage = 0, gstage = 0, issued = 0, given = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      auto give = [&]() {
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(full_bar(gstage));
-        if (++gstage == kMoeStages) gstage = 0;
-        ++given;
-      };
       ptx::pdl_wait();  // the codes are complete
       while (ok && w.next(runs, off, tile, p.E)) {
         const uint8_t* src[2];
@@ -541,8 +524,8 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
         }
         if (tid < w.n) ssrc = scales + (int64_t)row_of(tid) * (width >> 5);
         for (int kc = w.k0; kc < w.k1; ++kc) {
-          const bool free = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
-          if (!__all_sync(kFull, free)) { ok = false; break; }
+          ok = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
+          if (!ok) break;
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             if (on[q]) {
@@ -555,16 +538,11 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
           if (ssrc != nullptr)
             ptx::cp_async_4(sbase + kSfOff + stage * kStageSf + 2 * kChunk + (tid & 31) * 16 + (tid >> 5) * 4,
                             ssrc + kc * 4);
-          ptx::cp_async_commit();
-          if (++issued > kLag) {
-            ptx::cp_async_wait<kLag>();
-            give();
-          }
+          ptx::cp_async_arrive(full_bar(stage));
           if (++stage == kMoeStages) { stage = 0; phase ^= 1u; }
         }
       }
-      ptx::cp_async_wait<0>();
-      while (given < issued) give();
+      ptx::cp_async_wait_all();
     } else {
       // ---------------------------------------------------------- epilogue (warps 2-5)
       // Warp q has TMEM lanes 32 q .. 32 q + 31: lane l is row 32 q + l of

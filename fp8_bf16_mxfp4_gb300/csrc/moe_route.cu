@@ -69,17 +69,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const TIn* 
       for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
     }
     int my_id = -1;  // lane j: slot j
-    float my_p = 0.0f;
+    uint32_t my_key = 0;
     for (int j = 0; j < k; ++j) {
       const uint32_t m = __reduce_max_sync(kFull, best);
       if (m == 0) break;  // nothing left to choose (warp-uniform)
-      int at = 0x7FFFFFFF;
-      if (best == m) {
+      int e;
+      if constexpr (kPer == 1) {
+        e = __ffs(__ballot_sync(kFull, best == m)) - 1;
+      } else {
+        int at = 0x7FFFFFFF;
+        if (best == m) {
 #pragma unroll
-        for (int i = kPer - 1; i >= 0; --i)
-          if (key[i] == m) at = lane + 32 * i;
+          for (int i = kPer - 1; i >= 0; --i)
+            if (key[i] == m) at = lane + 32 * i;
+        }
+        e = __reduce_min_sync(kFull, at);
       }
-      const int e = __reduce_min_sync(kFull, at);
       if ((e & 31) == lane) {  // the winner's lane drops it
         best = 0;
 #pragma unroll
@@ -90,9 +95,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const TIn* 
       }
       if (lane == j) {
         my_id = e;
-        my_p = route_exp(key_value(m), top);
+        my_key = m;
       }
     }
+    const float my_p = my_id >= 0 ? route_exp(key_value(my_key), top) : 0.0f;
     if (renorm) {
       total = my_p;
 #pragma unroll

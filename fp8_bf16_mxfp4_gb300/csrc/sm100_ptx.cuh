@@ -453,9 +453,16 @@ MXG_DEVINL void cp_async_8(uint32_t dst, const void* src) {
 MXG_DEVINL void cp_async_4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+MXG_DEVINL void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 MXG_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 MXG_DEVINL void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Arrive on an mbarrier (counted among its expected arrivals) once every
+// cp.async that this thread has issued so far has completed.
+MXG_DEVINL void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 // Programmatic dependent launch: let the next kernel of the stream start its
 // prologue; wait until the kernel before has completed and its writes are
