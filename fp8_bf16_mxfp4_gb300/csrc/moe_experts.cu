@@ -65,10 +65,7 @@ constexpr int kSyncWords = 4 * kMaxCtas;  // join counters: [CTAs][4]
 constexpr int kMoeTmemCols = 512;
 constexpr int kSfCol = 256;               // two accumulator buffers of 2 x 64 columns, then the scale slots
 constexpr int kSfSlot = 12;               // columns of one stage's scales
-// Joining a cut unit costs about as much as kJoinStages stages, and a run of
-// cut units is at least kMinStages long.
-constexpr int kJoinStages = 6;
-constexpr int kMinStages = 4;
+constexpr int kMinStages = 4;             // shortest run of cut units
 constexpr int kPlanWarps = 8;             // warps 2-9 sort the slots
 
 // Shared memory.  E2M1 stages hold half of their bytes' worth of weights (4-bit
@@ -123,11 +120,13 @@ struct Runs {
   int grain;      // runs start at multiples of this many stages
   int ctas;       // runs (every one has at least one grain)
   int q, r;       // grains of a run: q + 1 for the first r runs, q for the others
-  MXG_DEVINL Runs(int units, int per_unit_, int max_ctas) : per_unit(per_unit_) {
+  MXG_DEVINL Runs(int units, int per_unit_, int tokens, int max_ctas) : per_unit(per_unit_) {
     // whole units to every CTA, or units cut into equal runs: what ends sooner
     const int total = units * per_unit;
     const int whole = (units + max_ctas - 1) / max_ctas * per_unit;
-    const int cut = max((total + max_ctas - 1) / max_ctas, kMinStages) + kJoinStages;
+    // (a join takes as long as about 4 + tokens / 2 stages, hidden where the run has whole units to follow)
+    const int run = max((total + max_ctas - 1) / max_ctas, kMinStages);
+    const int cut = run + (run >= 2 * per_unit ? 2 : 4 + tokens / 2);
     grain = whole <= cut ? per_unit : 1;
     ctas = min(max_ctas, grain > 1 || per_unit == 1 ? units : (total + kMinStages - 1) / kMinStages);
     q = ctas > 0 ? total / grain / ctas : 0;
@@ -311,7 +310,7 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
   __syncthreads();
 
   const int row_tiles = kDown ? (p.H + 255) >> 8 : p.I >> 7;
-  const Runs runs(tile[p.E] * row_tiles, (kDown ? p.I : p.H) >> 7, gridDim.x);
+  const Runs runs(tile[p.E] * row_tiles, (kDown ? p.I : p.H) >> 7, off[p.E] / max(tile[p.E], 1), gridDim.x);
   const int cta = blockIdx.x;
   const bool active = cta < runs.ctas;
   Walker w;
@@ -564,13 +563,71 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
         ++count;
         const uint32_t d0 = tq + buf * 2 * kTok, d1 = d0 + kTok;
         const bool two = !kDown || w.rt * 256 + 128 < p.H;
-        const int u0 = w.unit * runs.per_unit;
         const bool whole = w.k0 == 0 && w.k1 == runs.per_unit;
-
-        // 8 tokens' pairs of values (gate and up, or two output rows) of this
-        // lane's row; computed for all 8 so that they interleave, stored for
-        // the unit's tokens only
-        auto finish = [&](int c0, const float* v0, const float* v1) {
+        auto read = [&](int c0, float* v0, float* v1) {  // 8 tokens' pairs of values of this lane's row
+          __syncwarp();
+          ptx::tmem_ld_32x32b_x8(d0 + c0, reinterpret_cast<uint32_t*>(v0));
+          ptx::tmem_ld_32x32b_x8(d1 + c0, reinterpret_cast<uint32_t*>(v1));
+          ptx::tmem_ld_wait();
+          if (c0 + 8 >= w.n) {  // last read: hand the accumulator back
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(acc_empty(buf));
+          }
+        };
+        int first = 0, last = -1;  // the CTAs of a cut unit
+        if (!whole) {
+          float* mine = p.part + (int64_t)(2 * cta + (w.k0 == 0)) * p.part_tok * 256 + quarter * 32 + lane;
+          for (int c0 = 0; c0 < w.n; c0 += 8) {
+            float v0[8], v1[8];
+            read(c0, v0, v1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c0 + i < w.n) {
+                __stcg(mine + (c0 + i) * 256, v0[i]);
+                if (two) __stcg(mine + (c0 + i) * 256 + 128, v1[i]);
+              }
+          }
+          first = runs.owner(w.unit * runs.per_unit);
+          last = runs.owner(w.unit * runs.per_unit + runs.per_unit - 1);
+          __threadfence();
+          __syncwarp();
+          uint32_t got = 0;
+          if (lane == 0) got = atomicInc(p.sync + (first + 1) * 4 + quarter, (uint32_t)(last - first));
+          got = __shfl_sync(kFull, got, 0);
+          if (got != (uint32_t)(last - first)) continue;
+          __threadfence();
+        }
+        // Eight tokens at a time (all eight are computed, so that they
+        // interleave, and the unit's stored).  The last CTA of a cut unit adds
+        // the partials in run order: buffers 2 first + 1, 2 (first + 1), ...
+        for (int c0 = 0; c0 < w.n; c0 += 8) {
+          float v0[8], v1[8];
+          if (whole) {
+            read(c0, v0, v1);
+          } else {
+            constexpr int kSegs = 3;  // partials in flight
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v0[i] = v1[i] = 0.0f;
+            for (int b = first; b <= last; b += kSegs) {
+              float a0[kSegs][8], a1[kSegs][8];
+#pragma unroll
+              for (int g = 0; g < kSegs; ++g) {
+                const float* src = p.part + (int64_t)(2 * (b + g) + (b + g == first)) * p.part_tok * 256 + c0 * 256 +
+                                   quarter * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const bool in = b + g <= last && c0 + i < w.n;
+                  a0[g][i] = in ? __ldcg(src + i * 256) : 0.0f;
+                  a1[g][i] = in && two ? __ldcg(src + i * 256 + 128) : 0.0f;
+                }
+              }
+#pragma unroll
+              for (int g = 0; g < kSegs; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) { v0[i] += a0[g][i]; v1[i] += a1[g][i]; }
+            }
+          }
           if constexpr (kDown) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -587,7 +644,7 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
             int ex[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float h = v0[i] / (1.0f + expf(-v0[i])) * v1[i];
+              const float h = __fdividef(v0[i], 1.0f + expf(-v0[i])) * v1[i];
               // the block of 32 channels is this warp's 32 lanes
               ex[i] = mx_exponent_f32(__reduce_max_sync(kFull, __float_as_uint(h) & 0x7FFFFFFFu));
               code[i] = cvt_e4m3x4(h * pow2_neg(ex[i]), 0.0f, 0.0f, 0.0f);
@@ -600,62 +657,6 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
                 if (lane == 0) p.hs[(int64_t)slot * (p.I >> 5) + w.rt * 4 + quarter] = (uint8_t)(ex[i] + 127);
               }
             }
-          }
-        };
-        float* mine = p.part + (int64_t)(2 * cta + (w.k0 == 0)) * p.part_tok * 256 + quarter * 32 + lane;
-        for (int c0 = 0; c0 < w.n; c0 += 8) {
-          uint32_t r0[8], r1[8];
-          __syncwarp();
-          ptx::tmem_ld_32x32b_x8(d0 + c0, r0);
-          ptx::tmem_ld_32x32b_x8(d1 + c0, r1);
-          ptx::tmem_ld_wait();
-          if (c0 + 8 >= w.n) {  // last read: hand the accumulator back
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(acc_empty(buf));
-          }
-          float v0[8], v1[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) { v0[i] = __uint_as_float(r0[i]); v1[i] = __uint_as_float(r1[i]); }
-          if (whole) {
-            finish(c0, v0, v1);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c0 + i < w.n) {
-                __stcg(mine + (c0 + i) * 256, v0[i]);
-                if (two) __stcg(mine + (c0 + i) * 256 + 128, v1[i]);
-              }
-          }
-        }
-        if (!whole) {
-          // join: the last of the unit's CTAs adds the partials in run order
-          const int first = runs.owner(u0), last = runs.owner(u0 + runs.per_unit - 1);
-          __threadfence();
-          __syncwarp();
-          uint32_t got = 0;
-          if (lane == 0) got = atomicInc(p.sync + (first + 1) * 4 + quarter, (uint32_t)(last - first));
-          got = __shfl_sync(kFull, got, 0);
-          if (got != (uint32_t)(last - first)) continue;
-          __threadfence();
-          const int64_t step = (int64_t)p.part_tok * 256;
-          for (int c0 = 0; c0 < w.n; c0 += 8) {
-            float v0[8], v1[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v0[i] = v1[i] = 0.0f;
-            // buffers 2 first + 1, 2 (first + 1), 2 (first + 2), ...
-            for (int b = first; b <= last; ++b) {
-              const float* src = p.part + (2 * b + (b == first)) * step + c0 * 256 + quarter * 32 + lane;
-              float a0[8], a1[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                a0[i] = c0 + i < w.n ? __ldcg(src + i * 256) : 0.0f;
-                a1[i] = two && c0 + i < w.n ? __ldcg(src + i * 256 + 128) : 0.0f;
-              }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) { v0[i] += a0[i]; v1[i] += a1[i]; }
-            }
-            finish(c0, v0, v1);
           }
         }
       }
