@@ -403,8 +403,6 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t d0 = tm + buf * 2 * kTok, d1 = d0 + kTok;
-      const bool two = !kDown || w.rt * 256 + 128 < p.H;
-      const uint32_t idesc_n = p.idesc | ((uint32_t)((w.n + 15) >> 4) << 18);  // N / 8, N a multiple of 16
       for (int kc = w.k0; kc < w.k1; ++kc) {
         if (!ptx::mbar_try_wait(full_bar(stage), phase)) {
           ok = ptx::mbar_wait(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
@@ -419,16 +417,19 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
         const uint32_t sf = sbase + kSfOff + stage * kStageSf;
         const uint32_t tsf = tm + kSfCol + stage * kSfSlot;
         ptx::tc_cp_32x128b_warpx4_if(el, tsf, ptx::smem_desc(sf, 0, 128, 0));
-        if (two) ptx::tc_cp_32x128b_warpx4_if(el, tsf + 4, ptx::smem_desc(sf + kChunk, 0, 128, 0));
+        ptx::tc_cp_32x128b_warpx4_if(el, tsf + 4, ptx::smem_desc(sf + kChunk, 0, 128, 0));
         ptx::tc_cp_32x128b_warpx4_if(el, tsf + 8, ptx::smem_desc(sf + 2 * kChunk, 0, 128, 0));
+        // Always both tiles (the second of the last row tile may be stale, and
+        // its rows are not stored) and the same N: a branch or an operand that
+        // depends on the unit costs a third more per stage.
         const uint64_t a0 = ptx::smem_desc(sw, 16, 1024, 2), a1 = ptx::smem_desc(sw + kWTile, 16, 1024, 2);
         const uint64_t b = ptx::smem_desc(sw + 2 * kWTile, 16, 1024, 2);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // 32 contraction elements (32 bytes of each row) per MMA
-          const uint32_t idesc = idesc_n | (j << 4) | (j << 29);
+          const uint32_t idesc = p.idesc | (j << 4) | (j << 29);
           const uint32_t acc = (kc != w.k0) || j != 0;
           ptx::mma_mxf8f6f4_if(el, d0, a0 + 2 * j, b + 2 * j, idesc, tsf, tsf + 8, acc);
-          if (two) ptx::mma_mxf8f6f4_if(el, d1, a1 + 2 * j, b + 2 * j, idesc, tsf + 4, tsf + 8, acc);
+          ptx::mma_mxf8f6f4_if(el, d1, a1 + 2 * j, b + 2 * j, idesc, tsf + 4, tsf + 8, acc);
         }
         issued = true;
         ptx::tc_commit_if(el, empty_bar(stage));
@@ -603,6 +604,9 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
         // the partials in run order: buffers 2 first + 1, 2 (first + 1), ...
         for (int c0 = 0; c0 < w.n; c0 += 8) {
           float v0[8], v1[8];
+          int64_t slot[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) slot[i] = sorted[w.tok0 + min(c0 + i, w.n - 1)];
           if (whole) {
             read(c0, v0, v1);
           } else {
@@ -633,8 +637,7 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
             for (int i = 0; i < 8; ++i) {
               const float wt = __shfl_sync(kFull, c0 < 32 ? wt_lo : wt_hi, (c0 + i) & 31);
               if (c0 + i < w.n) {
-                const int slot = sorted[w.tok0 + c0 + i];
-                float* dst = p.rows + (int64_t)slot * p.H + w.rt * 256 + quarter * 32 + lane;
+                float* dst = p.rows + slot[i] * p.H + w.rt * 256 + quarter * 32 + lane;
                 __stcg(dst, v0[i] * wt);
                 if (two) __stcg(dst + 128, v1[i] * wt);
               }
@@ -652,9 +655,8 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if (c0 + i < w.n) {
-                const int slot = sorted[w.tok0 + c0 + i];
-                p.hq[(int64_t)slot * p.I + w.rt * 128 + quarter * 32 + lane] = (uint8_t)code[i];
-                if (lane == 0) p.hs[(int64_t)slot * (p.I >> 5) + w.rt * 4 + quarter] = (uint8_t)(ex[i] + 127);
+                p.hq[slot[i] * p.I + w.rt * 128 + quarter * 32 + lane] = (uint8_t)code[i];
+                if (lane == 0) p.hs[slot[i] * (p.I >> 5) + w.rt * 4 + quarter] = (uint8_t)(ex[i] + 127);
               }
             }
           }
@@ -848,8 +850,8 @@ mxg_status launch_moe_experts(const MoeArgs& a, cudaStream_t stream, int num_sms
   p.timeout_ns = wait_timeout_ns();
   p.drain_ns = std::max<uint64_t>(p.timeout_ns, 200000000ull);
   // instruction descriptor: weights (A) E2M1 or E4M3, activations (B) E4M3,
-  // both K-major, UE8M0 scales, M = 128; N is added per unit
-  p.idesc = ((fp4 ? 5u : 0u) << 7) | (1u << 23) | ((128u >> 4) << 24);
+  // both K-major, UE8M0 scales, M = 128, N for the most tokens of a unit
+  p.idesc = ((fp4 ? 5u : 0u) << 7) | ((uint32_t)((ws.part_tok + 15) / 16) << 18) | (1u << 23) | ((128u >> 4) << 24);
 
   CUtensorMap tmW[2], tmS[2];  // E4M3: the stages' tiles; E2M1: 256 bytes of 128 rows for the L2 prefetch
   for (int i = 0; i < 2; ++i) {
