@@ -14,6 +14,7 @@ Layouts (row-major, K-major operands):
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -635,6 +636,24 @@ def _raw_stream(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+_scratch_buffers = {}
+_SCRATCH_KEEP = 64 << 20
+
+
+def _scratch(nbytes: int, dev, stream: int) -> torch.Tensor:
+    """A call's workspace when the caller gives none.  An allocation costs as
+    much host time as the launches, so each stream keeps one buffer of up to
+    64 MiB (calls on a stream are ordered, and each writes what it reads); a
+    captured graph gets memory of its own pool."""
+    if nbytes <= _SCRATCH_KEEP and not torch._C._cuda_isCurrentStreamCapturing():
+        key = (dev.index, stream)
+        buf = _scratch_buffers.get(key)
+        if buf is None or buf.numel() < nbytes:
+            buf = _scratch_buffers[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+        return buf
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
 def _status_ptr(status, dev) -> int:
     if status is not None:
         return status.data_ptr()
@@ -699,6 +718,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, ids: t
     return ids, weights
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_experts_workspace_size(tokens: int, top_k: int, experts: int, hidden: int, inter: int) -> int:
     return int(_lib.load().moe_experts_workspace_size(tokens, top_k, experts, hidden, inter))
 
@@ -739,12 +759,13 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
         out = torch.empty((T, H), dtype=out_dtype, device=dev)
     if out.shape != (T, H) or out.dtype not in _OUT or not out.is_cuda:
         _refuse(out=(out, (T, H), _OUT, False))
+    stream = _raw_stream(dev)
     if workspace is None:
-        workspace = torch.empty(max(lib.moe_experts_workspace_size(T, k, E, H, I), 256), dtype=torch.uint8, device=dev)
+        workspace = _scratch(moe_experts_workspace_size(T, k, E, H, I), dev, stream)
     a, b = W13.c(), W2.c()
     code = lib.moe_experts(x.data_ptr(), T, _row_ld(x, H), ids.data_ptr(), weights.data_ptr(), k, E, ctypes.byref(a),
                            ctypes.byref(b), out.data_ptr(), _row_ld(out, H), _OUT[out.dtype], workspace.data_ptr(),
-                           workspace.numel(), _status_ptr(status, dev), _raw_stream(dev))
+                           workspace.numel(), _status_ptr(status, dev), stream)
     if code:
         raise MXGError(code, "moe_experts")
     if check:
@@ -752,6 +773,7 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def lora_add_workspace_size(tokens: int, K: int, rank: int) -> int:
     return int(_lib.load().lora_add_workspace_size(tokens, K, rank))
 
@@ -789,12 +811,13 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
         out = torch.empty((T, N), dtype=y.dtype, device=dev)
     elif out.shape != (T, N) or out.dtype != y.dtype or not out.is_cuda:
         _refuse(out=(out, (T, N), y.dtype, False))
+    stream = _raw_stream(dev)
     if workspace is None:
-        workspace = torch.empty(max(lib.lora_add_workspace_size(T, K, R), 256), dtype=torch.uint8, device=dev)
+        workspace = _scratch(lora_add_workspace_size(T, K, R), dev, stream)
     code = lib.lora_add(y.data_ptr(), _row_ld(y, N), x.data_ptr(), _row_ld(x, K), A.data_ptr(), B.data_ptr(),
                         ids.data_ptr(), None if scale is None else scale.data_ptr(), T, N, K, R, n, dtype,
                         out.data_ptr(), _row_ld(out, N), workspace.data_ptr(), workspace.numel(),
-                        _status_ptr(status, dev), _raw_stream(dev))
+                        _status_ptr(status, dev), stream)
     if code:
         raise MXGError(code, "lora_add")
     if check:

@@ -337,6 +337,30 @@ def test_lora_an_unused_adapter_is_not_read_into_others():
     assert torch.equal(got[keep], want[keep]) and bool(got[2::4].isnan().all())
 
 
+def test_workspaces_kept_by_streams_do_not_meet():
+    """Calls of several sizes and operators interleaved on three streams give
+    what they give alone."""
+    mxg = _mxg()
+    cases = []
+    for n, (T, H, I) in enumerate(((3, 256, 128), (40, 384, 256), (70, 256, 256))):
+        args, got, _ = check_experts(T, 4, 2, H, I, "e2m1" if n % 2 else "e4m3", seed=40 + n)
+        g = torch.Generator().manual_seed(n)
+        to = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+        lora = (to(T, 520), to(T, H), to(3, 16, H), to(3, 520, 16), torch.arange(T, dtype=torch.int32, device=DEV) % 3)
+        cases.append((args, got, lora, mxg.lora_add(*lora, check=True)))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = []
+    for r in range(6):
+        for i, s in enumerate(streams):
+            args, got, lora, want = cases[(i + r) % 3]
+            with torch.cuda.stream(s):
+                outs.append((mxg.moe_experts(*args), got))
+                outs.append((mxg.lora_add(*lora), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+
+
 def test_lora_bad_id_is_reported():
     mxg = _mxg()
     y = torch.zeros(20, 64, dtype=torch.bfloat16, device=DEV)
