@@ -664,11 +664,10 @@ def _status_ptr(status, dev) -> int:
 def _row_ld(t: torch.Tensor, cols: int) -> int:
     """Row stride of a 2-D tensor; its rows must be contiguous.  A tensor of at
     most one row reports arbitrary strides: its width, rounded up to 8."""
-    if t.shape[0] > 1:
-        if cols > 1 and t.stride(1) != 1:
-            raise ValueError("elements of a row must be contiguous")
-        return t.stride(0)
-    return (cols + 7) & ~7
+    rows = t.shape[0]
+    if rows > 0 and cols > 1 and t.stride(1) != 1:
+        raise ValueError("elements of a row must be contiguous")
+    return t.stride(0) if rows > 1 else (cols + 7) & ~7
 
 
 def _refuse(**named):

@@ -396,3 +396,113 @@ def test_lora_side_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(cap, mxg.lora_add(y, x, A, B, ids, check=True)) and not torch.equal(cap, want)
+
+
+# --------------------------------------------------------------------------- bounds and refusals
+
+BAND = 4096
+
+
+def banded(nbytes):
+    """nbytes of 256-byte aligned device memory between sentinel bands."""
+    n = (nbytes + 255) // 256 * 256
+    buf = torch.full((BAND + n + BAND,), 0xA5, dtype=torch.uint8, device=DEV)
+    return buf, buf[BAND: BAND + nbytes]
+
+
+def bands_hold(buf, nbytes):
+    return bool((buf[:BAND] == 0xA5).all()) and bool((buf[BAND + nbytes:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("T,E,k,H,I,fmt,how", [(1, 2, 2, 256, 128, "e2m1", "all"), (1, 1, 1, 1152, 1152, "e4m3", "all"),
+                                               (130, 3, 2, 384, 256, "e2m1", "one"), (33, 12, 3, 640, 384, "e4m3", "holes")])
+def test_experts_write_only_their_output_and_workspace(T, E, k, H, I, fmt, how):
+    mxg = _mxg()
+    args, got, _ = check_experts(T, E, k, H, I, fmt, how)
+    need = mxg.moe_experts_workspace_size(T, k, E, H, I)
+    wbuf, ws = banded(need)
+    obuf, ob = banded(T * H * 2)
+    out = ob.view(torch.bfloat16).view(T, H)
+    assert torch.equal(mxg.moe_experts(*args, out=out, workspace=ws, check=True), got)
+    assert bands_hold(wbuf, need) and bands_hold(obuf, T * H * 2)
+
+
+@pytest.mark.parametrize("T,K,N,R,n", [(1, 264, 72, 8, 2), (19, 1032, 520, 24, 5), (300, 2048, 2056, 32, 4), (129, 4104, 4120, 72, 9)])
+def test_lora_writes_only_its_output_and_workspace(T, K, N, R, n):
+    mxg = _mxg()
+    g = torch.Generator().manual_seed(T)
+    to = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    args = (to(T, N), to(T, K), to(n, R, K), to(n, N, R), (torch.arange(T, device=DEV) % n).to(torch.int32))
+    want = mxg.lora_add(*args, check=True)
+    need = mxg.lora_add_workspace_size(T, K, R)
+    wbuf, ws = banded(need)
+    ld = N + 8  # padding between rows
+    obuf, ob = banded((T * ld - 8) * 2)
+    out = ob.view(torch.bfloat16).as_strided((T, N), (ld, 1))
+    assert torch.equal(mxg.lora_add(*args, out=out, workspace=ws, check=True), want)
+    assert bands_hold(wbuf, need) and bands_hold(obuf, (T * ld - 8) * 2)
+    gaps = ob.view(torch.int16).as_strided((T - 1, 8), (ld, 1), BAND // 2 + N) if T > 1 else None
+    assert gaps is None or bool((gaps == 0xA5A5 - 0x10000).all())
+
+
+def test_route_writes_only_its_outputs():
+    mxg = _mxg()
+    x = torch.randn(37, 33, device=DEV)
+    ids, w = mxg.moe_route(x, 5)
+    ibuf, ib = banded(37 * 5 * 4)
+    wbuf, wb = banded(37 * 5 * 4)
+    mxg.moe_route(x, 5, ids=ib.view(torch.int32).view(37, 5), weights=wb.view(torch.float32).view(37, 5))
+    assert torch.equal(ib.view(torch.int32).view(37, 5), ids) and torch.equal(wb.view(torch.float32).view(37, 5), w)
+    assert bands_hold(ibuf, 37 * 20) and bands_hold(wbuf, 37 * 20)
+
+
+def test_binding_refusals():
+    mxg = _mxg()
+    bf = torch.bfloat16
+    z = lambda *s, d=bf: torch.zeros(*s, dtype=d, device=DEV)  # noqa: E731
+    i32 = lambda *s: z(*s, d=torch.int32)  # noqa: E731
+    f32 = lambda *s: z(*s, d=torch.float32)  # noqa: E731
+    for bad in (lambda: mxg.moe_route(f32(4, 16)[:, ::2], 2), lambda: mxg.moe_route(f32(1, 16)[:, ::2], 2),
+                lambda: mxg.moe_route(z(4, 8, d=torch.float16), 2), lambda: mxg.moe_route(f32(8), 2),
+                lambda: mxg.moe_route(f32(4, 8), 2, ids=i32(4, 3)), lambda: mxg.moe_route(f32(4, 8), 2, weights=z(4, 2))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(mxg.MXGError):
+        mxg.moe_route(f32(4, 8), 9)
+    w13 = mxg.mx_quantize_rowwise_packed(z(2 * 256, 256), "e2m1", groups=2)
+    w2 = mxg.mx_quantize_rowwise_packed(z(2 * 256, 128), "e2m1", groups=2)
+    ok = dict(x=z(3, 256), ids=i32(3, 2), weights=f32(3, 2), W13=w13, W2=w2)
+    mxg.moe_experts(**ok, check=True)
+    plain = mxg.mx_quantize_rowwise(z(2 * 256, 256), "e2m1")
+    # the quantizer allocates for every split (2560 bytes); 512 x 128 weights need 512 * 128 / 32 = 2048 of them
+    assert w2.scale.numel() == 2560
+    mxg.moe_experts(**{**ok, "W2": mxg.MXOperand(w2.data, w2.scale[:-512], "e2m1", 128, "packed")}, check=True)
+    short = mxg.MXOperand(w2.data, w2.scale[:-513], "e2m1", 128, "packed")
+    for k, v in (("x", z(3, 512)[:, ::2]), ("x", z(1, 512)[:, ::2]), ("x", f32(3, 256)), ("x", z(4, 256)), ("ids", i32(2, 3).t()),
+                 ("ids", z(3, 2, d=torch.int64)), ("weights", f32(3, 1)), ("W13", plain), ("W13", w2), ("W2", short),
+                 ("out", z(3, 128)), ("out", z(3, 256, d=torch.float16)), ("out", z(3, 512)[:, ::2])):
+        with pytest.raises(ValueError):
+            mxg.moe_experts(**{**ok, k: v})
+    with pytest.raises(mxg.MXGError):
+        mxg.moe_experts(**ok, workspace=z(256, d=torch.uint8))
+    ok = dict(y=z(3, 64), x=z(3, 128), A=z(2, 8, 128), B=z(2, 64, 8), ids=i32(3), scale=f32(2))
+    mxg.lora_add(**ok, check=True)
+    for k, v in (("y", z(3, 128)[:, ::2]), ("y", z(3, 64, d=torch.float16)), ("x", z(3, 120)), ("x", f32(3, 128)), ("A", z(2, 128, 8).transpose(1, 2)),
+                 ("B", z(2, 64, 16)[:, :, ::2]), ("B", z(3, 64, 8)), ("ids", z(3, d=torch.int64)), ("ids", i32(6)[::2]),
+                 ("scale", f32(3)), ("scale", z(2)), ("out", z(3, 64, d=torch.float32))):
+        with pytest.raises(ValueError):
+            mxg.lora_add(**{**ok, k: v})
+    for k, v in (("A", z(2, 12, 128)), ("A", z(2, 136, 128))):  # ranks not a multiple of 8, or past 128
+        with pytest.raises(mxg.MXGError):
+            mxg.lora_add(**{**ok, "A": v, "B": z(2, 64, v.shape[1])})
+
+
+def test_example_runs_the_operators_together(capsys):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_moe_block.py")
+    spec = importlib.util.spec_from_file_location("serve_moe_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    us = example.main(["--tokens", "5", "--hidden", "512", "--inter", "256", "--experts", "6", "--top-k", "2", "--steps", "3"])
+    assert us > 0 and "experts used" in capsys.readouterr().out
