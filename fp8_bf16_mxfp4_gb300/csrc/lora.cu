@@ -1,24 +1,29 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   out[t] = y[t] + scale[a] * B[a] (A[a] x[t]),  a = ids[t].
 //
-// Two kernels: shrink, u[t] = A[a] x[t], split over K, fp32 partials to the
-// workspace; expand, which sums the partials in order and adds scale * B u to y.
+// shrink: u[t] = A[a] x[t], split over K, fp32 partials to the workspace;
+// expand: sums the partials in order and adds scale * B u to y.
 // Both are bound by memory: x, y, and R (K + N) values of each adapter used.
 //
 // Few tokens: a CTA works for one token, reads the token's adapter rows 16 bytes
 // a lane and multiplies in fp32.  Tokens that share an adapter read it again,
-// from L2; that is as fast as it gets while all adapters read for all tokens
-// are a few tens of MB, because every load of a CTA is in flight at once.
+// from L2; every load of a CTA is in flight at once.  64 tokens of 64 adapters
+// (K = N = 7168, rank 16): 6.2 us, two thirds of it the two launches; one token
+// 3.7 us.
 //
-// Many tokens: a CTA takes a tile of 128 tokens as they come in the batch and
-// runs it against the adapters that occur in it on the tensor core (tcgen05,
-// BF16 x BF16 + FP32); products of rows that are not wanted cost nothing, and
-// there is no sorting.  A row of the result is selected, never masked by a
+// Many tokens: the tokens are ordered by adapter (a third kernel), and a CTA
+// runs a tile of 128 of them against the adapters that occur in it on the
+// tensor core (tcgen05, BF16 x BF16 + FP32); products of rows that are not
+// wanted cost little.  A row of the result is selected, never masked by a
 // product: an adapter's infinities or NaN reach its own tokens only.  u keeps its
 // fp32 accuracy as a sum of two BF16 terms (2^-17; BF16 output) or three (2^-25;
-// FP32 output).  (mma.sync runs at 1/16 of the tcgen05 rate on GB300: a tile
-// form on it was held to 264 us by its pipe where this one takes 240 us, at 8192
-// tokens, 8192 x 28672, rank 32.)
+// FP32 output).
+//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 248 us, 4.4 TB/s
+//   of the 1.09 GB it has to move (160 us at the copy rate).  Expand is about
+//   three quarters of that; reads and writes of y share DRAM at 67 to 80 %.
+//   Left in the batch's order the same takes 240 us, but 1024 tokens of 64 mixed
+//   adapters (4096 x 4096, rank 16) take 200 us instead of 32.
+//   mma.sync runs at 1/16 of the tcgen05 rate here: a form on it took 264 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -39,7 +44,8 @@ constexpr int kLoraThreads = kLoraWarps * 32;
 
 struct LoraParams {
   LoraArgs a;
-  float* u;         // [ksplit][T][R] partial sums
+  float* u;         // [ksplit][T][R] partial sums (tiles: rows in the order of `order`)
+  int32_t* order;   // tiles: [T] tokens, by adapter within each segment
   int ksplit;
   int blocks;       // tiles: 64-element steps of K per CTA of the shrink
   int cols;         // tiles: columns per CTA of the expand
@@ -201,48 +207,124 @@ constexpr int kTile = 128;          // tokens of a tile (TMEM lanes)
 constexpr int kRowBytes = 128;      // one swizzled shared-memory row: 64 BF16 of the contraction
 constexpr int kTileBytes = kTile * kRowBytes;
 
-// The adapters of a tile of tokens, in order of first use.
+// Order of the tokens: within each segment of 8192, by adapter, tokens without
+// one last; a CTA per segment counts, sums and places.  So a tile meets about
+// 1 + adapters / 64 adapters instead of up to 128.  The order among a
+// segment's tokens of one adapter goes by the atomics; a token's result does not
+// depend on its place.  Where the counters do not fit, the order is the batch's.
+constexpr int kSegment = 8192;
+constexpr int kOrderThreads = 1024;
+constexpr int kOrderPer = kSegment / kOrderThreads;
+constexpr int kCounters = 8192;  // adapters + 1 at most
+constexpr int kCountPer = kCounters / kOrderThreads;
+
+__global__ void __launch_bounds__(kOrderThreads) lora_order_kernel(const LoraParams p) {
+  __shared__ int count[kCounters];
+  __shared__ int warp_sum[32];
+  ptx::pdl_launch_dependents();
+  const LoraArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t t0 = (int64_t)blockIdx.x * kSegment;
+  const bool sort = a.n < kCounters;
+  int bucket[kOrderPer], rank[kOrderPer];
+#pragma unroll
+  for (int i = 0; i < kOrderPer; ++i) {
+    const int64_t t = t0 + i * kOrderThreads + tid;
+    const int id = t < a.T ? __ldg(a.ids + t) : -1;
+    if (id >= a.n) report(a.status, MXG_ERR_INDEX);
+    bucket[i] = t >= a.T ? -1 : id < 0 || id >= a.n ? a.n : id;  // -1: no token
+  }
+  if (!sort) {
+#pragma unroll
+    for (int i = 0; i < kOrderPer; ++i) {
+      const int64_t t = t0 + i * kOrderThreads + tid;
+      if (t < a.T) p.order[t] = (int32_t)t;
+    }
+    return;
+  }
+  for (int i = tid; i <= a.n; i += kOrderThreads) count[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kOrderPer; ++i) {
+    if (t0 + i * kOrderThreads >= a.T) continue;
+    const uint32_t same = __match_any_sync(kFull, bucket[i]);
+    const int leader = __ffs(same) - 1;
+    int base = 0;
+    if (lane == leader && bucket[i] >= 0) base = atomicAdd(&count[bucket[i]], __popc(same));
+    rank[i] = __shfl_sync(kFull, base, leader) + __popc(same & ((1u << lane) - 1u));
+  }
+  __syncthreads();
+  // exclusive sums: a thread has kCountPer counters in a row
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kCountPer; ++i) {
+    const int b = tid * kCountPer + i;
+    if (b <= a.n) sum += count[b];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  const int before = __reduce_add_sync(kFull, lane < warp ? warp_sum[lane] : 0);
+  int at = before + incl - sum;
+#pragma unroll
+  for (int i = 0; i < kCountPer; ++i) {
+    const int b = tid * kCountPer + i;
+    if (b <= a.n) {
+      const int c = count[b];
+      count[b] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kOrderPer; ++i) {
+    const int64_t t = t0 + i * kOrderThreads + tid;
+    if (bucket[i] >= 0) p.order[t0 + count[bucket[i]] + rank[i]] = (int32_t)t;
+  }
+}
+
+// The tokens of a tile and the adapters of their runs.
 struct Tile {
-  int id[kTile];       // adapter of each token (-1: none)
-  int16_t ord[kTile];  // its number in the list (-1: none)
-  int list[kTile];     // adapter by number
+  int tok[kTile];      // token (-1: past the last)
+  int id[kTile];       // its adapter (-1: none)
+  int16_t ord[kTile];  // the number of its run in the list (-1: none)
+  int list[kTile];     // adapter of each run
+  int warp_runs[4];
   int count;
 };
 
-// All threads of the CTA (at least kTile).
-MXG_DEVINL void read_tile(Tile& s, const LoraArgs& a, int64_t t0) {
-  const int tid = threadIdx.x;
+// All threads of the CTA (at least kTile), once the order is written.
+MXG_DEVINL void read_tile(Tile& s, const LoraParams& p, int64_t t0) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  int id = -1;
   if (tid < kTile) {
-    int id = t0 + tid < a.T ? __ldg(a.ids + t0 + tid) : -1;
-    if (id >= a.n) {
-      report(a.status, MXG_ERR_INDEX);
-      id = -1;
-    }
+    const int tok = t0 + tid < p.a.T ? __ldcg(p.order + t0 + tid) : -1;
+    if (tok >= 0) id = __ldg(p.a.ids + tok);
+    if (id >= p.a.n) id = -1;  // reported with the order
+    s.tok[tid] = tok;
     s.id[tid] = id;
-    s.ord[tid] = -1;
   }
   __syncthreads();
-  int leader = tid;  // the first token with this one's adapter
-  if (tid < kTile && s.id[tid] >= 0)
-    for (leader = 0; s.id[leader] != s.id[tid]; ++leader) {}
-  if (tid < 32) {  // the leaders, numbered in order
-    int count = 0;
-    for (int base = 0; base < kTile; base += 32) {
-      const int i = base + tid, id = s.id[i];
-      bool first = id >= 0;
-      for (int j = 0; first && j < i; ++j) first = s.id[j] != id;
-      const uint32_t m = __ballot_sync(kFull, first);
-      if (first) {
-        const int o = count + __popc(m & ((1u << tid) - 1u));
-        s.list[o] = id;
-        s.ord[i] = (int16_t)o;
-      }
-      count += __popc(m);
-    }
-    if (tid == 0) s.count = count;
+  uint32_t starts = 0;
+  bool first = false;
+  if (tid < kTile) {
+    first = id >= 0 && (tid == 0 || s.id[tid - 1] != id);
+    starts = __ballot_sync(kFull, first);
+    if (lane == 0) s.warp_runs[tid >> 5] = __popc(starts);
   }
   __syncthreads();
-  if (tid < kTile && s.id[tid] >= 0 && leader != tid) s.ord[tid] = s.ord[leader];
+  if (tid < kTile) {
+    int o = __popc(starts & (0xFFFFFFFFu >> (31 - lane))) - 1;
+    for (int w = 0; w < (tid >> 5); ++w) o += s.warp_runs[w];
+    s.ord[tid] = (int16_t)(id >= 0 ? o : -1);
+    if (first) s.list[o] = id;
+    if (tid == kTile - 1) s.count = o + 1;
+  }
   __syncthreads();
 }
 
@@ -251,10 +333,11 @@ MXG_DEVINL uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// shrink: grid (K split, tiles), 192 threads: warp 0 loads (TMA), warp 1 issues
-// the MMAs, warps 2-5 store.  x is the M operand; the rows of up to 256 / R
-// adapters of the tile form one N operand, so x is read once for all of them.
-constexpr int kShrinkThreads = 192;
+// shrink: grid (K split, tiles, passes), 320 threads: warp 0 loads A (TMA), warp 1 issues
+// the MMAs, warps 2-5 store, warps 6-9 gather the tokens' rows of x.  x is the M
+// operand; the rows of up to 256 / R adapters of the tile form one N operand, a
+// pass; passes go to several CTAs where there are few tiles.
+constexpr int kShrinkThreads = 320;
 constexpr int kShrinkRows = 256;  // adapter rows of one pass
 constexpr int kShrinkStage = kTileBytes + kShrinkRows * kRowBytes;
 constexpr int kShrinkStages = 4;
@@ -262,8 +345,7 @@ constexpr int kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
 constexpr int kShrinkTmem = 256;
 
 __global__ void __launch_bounds__(kShrinkThreads, 1)
-    lora_shrink_tile_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
-                            const LoraParams p) {
+    lora_shrink_tile_kernel(const __grid_constant__ CUtensorMap tmA, const LoraParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   __shared__ Tile tile;
@@ -280,7 +362,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   ptx::pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kShrinkStages; ++s) {
-      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(full_bar(s), 1 + kTile);  // warp 0; the threads of warps 6-9
       ptx::mbar_init(empty_bar(s), 1);
     }
     ptx::mbar_init(acc_full, 1);
@@ -288,7 +370,6 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     ptx::mbar_init(drain, 1);
     abort_word = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&tmX);
     ptx::prefetch_tmap(&tmA);
   }
   if (warp == 1) {
@@ -297,12 +378,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   }
   const int64_t t0 = (int64_t)blockIdx.y * kTile;
   ptx::tc_fence_before();
-  read_tile(tile, a, t0);
+  ptx::pdl_wait();
+  read_tile(tile, p, t0);
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int s0 = blockIdx.x * p.blocks;
   const int s1 = (int)min((a.K + 63) / 64, (int64_t)s0 + p.blocks);  // 64-element steps of this CTA
   const int per_pass = kShrinkRows / a.R;
+  const int o_first = blockIdx.z * per_pass, o_step = gridDim.z * per_pass;
   const int count = tile.count;
 
   if (warp == 0) {
@@ -310,15 +393,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_phase = 0;
       bool ok = true;
-      for (int o0 = 0; ok && o0 < count; o0 += per_pass) {
+      for (int o0 = o_first; ok && o0 < count; o0 += o_step) {
         const int na = min(per_pass, count - o0);
         for (int k = s0; k < s1; ++k) {
           if (!ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status, p.timeout_ns)) { ok = false; break; }
           const uint32_t fb = full_bar(stage), sx = sbase + stage * kShrinkStage;
-          ptx::mbar_arrive_expect_tx(fb, (uint32_t)(kTileBytes + na * a.R * kRowBytes));
+          ptx::mbar_arrive_expect_tx(fb, (uint32_t)(na * a.R * kRowBytes));
           armed |= 1u << stage;
           armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-          ptx::tma_load_2d(sx, &tmX, k * 64, (int)t0, fb);
           for (int i = 0; i < na; ++i)
             ptx::tma_load_2d(sx + kTileBytes + i * a.R * kRowBytes, &tmA, k * 64, tile.list[o0 + i] * a.R, fb);
           if (++stage == kShrinkStages) { stage = 0; phase ^= 1u; }
@@ -335,7 +417,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     int stage = 0, pass = 0;
     uint32_t phase = 0;
     bool ok = true, issued = false;
-    for (int o0 = 0; ok && o0 < count; o0 += per_pass, ++pass) {
+    for (int o0 = o_first; ok && o0 < count; o0 += o_step, ++pass) {
       const uint32_t idesc = idesc_bf16((min(per_pass, count - o0) * a.R + 15) & ~15);
       ok = ptx::mbar_wait(acc_empty, (pass & 1u) ^ 1u, abort_flag, a.status, p.timeout_ns);
       if (!ok) break;
@@ -343,6 +425,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
       for (int k = s0; k < s1; ++k) {
         ok = ptx::mbar_wait(full_bar(stage), phase, abort_flag, a.status, p.timeout_ns);
         if (!ok) break;
+        ptx::fence_proxy_async_smem();
         ptx::tc_fence_after();
         const uint64_t xd = ptx::smem_desc(sbase + stage * kShrinkStage, 16, 1024, 2);
         const uint64_t ad = ptx::smem_desc(sbase + stage * kShrinkStage + kTileBytes, 16, 1024, 2);
@@ -360,6 +443,35 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
       volatile int no_abort = 0;
       ptx::mbar_wait(drain, 0, &no_abort, a.status, p.drain_ns);
     }
+  } else if (warp >= 6) {
+    // 16 bytes c of rows tid / 8, tid / 8 + 16, ...; chunk c of a row sits at c ^ (row % 8)
+    const int tid = threadIdx.x - 6 * 32, c = tid & 7, r0 = tid >> 3;
+    const uint32_t at = sbase + r0 * kRowBytes + ((c ^ (r0 & 7)) << 4);
+    const uint16_t* src[8];
+    uint32_t on = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = r0 + 16 * i;
+      const bool used = tile.ord[row] >= 0;
+      on |= (uint32_t)used << i;
+      src[i] = a.x + (int64_t)(used ? tile.tok[row] : 0) * a.ld_x + c * 8;
+    }
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int o0 = o_first; ok && o0 < count; o0 += o_step)
+      for (int k = s0; k < s1; ++k) {
+        ok = ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.status, p.timeout_ns);
+        if (!ok) break;
+        const bool in = k * 64 + c * 8 < a.K;  // past K: zeros
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((on >> i) & 1u)
+            ptx::cp_async_16_fill(at + stage * kShrinkStage + i * 16 * kRowBytes, in ? src[i] + k * 64 : a.x, in ? 16 : 0);
+        ptx::cp_async_arrive(full_bar(stage));
+        if (++stage == kShrinkStages) { stage = 0; phase ^= 1u; }
+      }
+    ptx::cp_async_wait_all();
   } else {
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
@@ -367,7 +479,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
     float* dst = p.u + ((int64_t)blockIdx.x * a.T + t0 + row) * a.R;
     int pass = 0;
-    for (int o0 = 0; o0 < count; o0 += per_pass, ++pass) {
+    for (int o0 = o_first; o0 < count; o0 += o_step, ++pass) {
       const bool ready = ptx::mbar_wait(acc_full, pass & 1u, abort_flag, a.status, p.timeout_ns);
       if (!__all_sync(kFull, ready)) break;
       ptx::tc_fence_after();
@@ -483,13 +595,13 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
-  read_tile(tile, a, t0);
+  ptx::pdl_wait();
+  read_tile(tile, p, t0);
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int count = tile.count;
   const bool idle = (int)blockIdx.z >= max(count, 1);  // no adapter for this CTA
   // u: ranks past R up to the product's depth are zero
-  ptx::pdl_wait();
   const int depth = (a.R + 15) & ~15;
   for (int i = threadIdx.x; !idle && i < kTile * (depth >> 3); i += kExpThreads) {
     const int row = i / (depth >> 3), r0 = (i - row * (depth >> 3)) * 8;
@@ -606,17 +718,18 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     const uint32_t ring_a = sbase + ubytes + kStages * kTileBytes + (warp - 2) * kPieces * kPieceBytes;
     // moving: lane l has 16 bytes (l % 8) of rows l / 8, l / 8 + 4, ...; adding: row l
     const int mrow = lane >> 3, mcol = (lane & 7) * (16 / (int)sizeof(TOut));
-    const int64_t row0 = t0 + quarter * 32;
-    const TOut* ybase = static_cast<const TOut*>(a.y) + row0 * a.ld_y + c0 + half * 64 + mcol;
-    TOut* obase = static_cast<TOut*>(a.out) + row0 * a.ld_out + c0 + half * 64 + mcol;
+    const TOut* ybase = static_cast<const TOut*>(a.y) + c0 + half * 64 + mcol;
+    TOut* obase = static_cast<TOut*>(a.out) + c0 + half * 64 + mcol;
+    int64_t tok[8];  // of rows mrow + 4 i
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tok[i] = tile.tok[quarter * 32 + mrow + 4 * i];
     const bool in_place = a.out == a.y && a.ld_out == a.ld_y;
     uint32_t rows = 0;  // bit i: row mrow + 4 i is moved in this pass
     auto pick = [&](int o) {
       rows = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = mrow + 4 * i;
-        if (row0 + r < a.T && tile.ord[quarter * 32 + r] == o) rows |= 1u << i;
+        if (tok[i] >= 0 && tile.ord[quarter * 32 + mrow + 4 * i] == o) rows |= 1u << i;
       }
     };
     if (blockIdx.z == 0 && !in_place) {  // rows without an adapter are copied
@@ -630,8 +743,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 if ((rows >> i) & 1)
-                  *reinterpret_cast<uint4*>(obase + (mrow + 4 * i) * a.ld_out + col) =
-                      *reinterpret_cast<const uint4*>(ybase + (mrow + 4 * i) * a.ld_y + col);
+                  *reinterpret_cast<uint4*>(obase + tok[i] * a.ld_out + col) =
+                      *reinterpret_cast<const uint4*>(ybase + tok[i] * a.ld_y + col);
             }
           }
     }
@@ -648,7 +761,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if ((rows >> i) & 1)
-                ptx::cp_async_16(dst + 4 * i * kPiecePitch, ybase + (mrow + 4 * i) * a.ld_y + col);
+                ptx::cp_async_16(dst + 4 * i * kPiecePitch, ybase + tok[i] * a.ld_y + col);
           }
         }
         ptx::cp_async_commit();
@@ -688,7 +801,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if ((rows >> i) & 1)
-                *reinterpret_cast<uint4*>(obase + (mrow + 4 * i) * a.ld_out + col) =
+                *reinterpret_cast<uint4*>(obase + tok[i] * a.ld_out + col) =
                     *reinterpret_cast<const uint4*>(piece + (mrow + 4 * i) * kPiecePitch + (lane & 7) * 16);
           }
           __syncwarp();
@@ -710,9 +823,15 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// Adapter bytes that the per-token kernels would read, from L2 where tokens
-// share them, against this limit.
-constexpr double kTokenBytes = 64e6;
+// The per-token kernels read T R (K + N) BF16 values of adapters, from L2 where
+// tokens share them, at 6 to 8 TB/s; the tiles take 16 to 50 us before the size
+// shows.  Per token against tiles, in us:
+//   4096 x 4096, rank 16, 64 adapters: 256 tokens (67 MB) 11 / 31, 512 (134 MB)
+//   19 / 32, 1024 (268 MB) 36 / 32; with 8 adapters 11 / 16, 18 / 16, 33 / 17
+//   4096 x 4096, rank 64, 16 adapters: 64 tokens (67 MB) 21 / 20, 128 (134 MB)
+//   26 / 21, 256 (268 MB) 49 / 22
+//   2048 x 8192, rank 32, 32 adapters: 256 tokens (168 MB) 26 / 29, 512 47 / 31
+constexpr double kTokenBytes = 150e6;
 constexpr int kLoraSms = 152;
 
 bool per_token(int64_t T, int64_t N, int64_t K, int R) {
@@ -783,7 +902,7 @@ cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** a
 size_t lora_workspace_bytes(int64_t T, int64_t K, int R) {
   T = std::max<int64_t>(T, 1);
   const int64_t split = std::max<int64_t>(tile_splits(T, K), T <= 65535 ? (K + kTokK - 1) / kTokK : 0);
-  return (size_t)(split * T * R) * sizeof(float);
+  return (size_t)(split * T * R) * sizeof(float) + (size_t)T * sizeof(int32_t);  // u, order
 }
 
 cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms) {
@@ -807,32 +926,40 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms)
   if ((e = ensure_lora_attr()) != cudaSuccess) return e;
   p.blocks = shrink_steps(a.T, a.K);
   p.ksplit = (int)tile_splits(a.T, a.K);
+  const int64_t met = std::min<int64_t>(kTile, 1 + a.n / tiles);  // about what a tile of sorted tokens meets
+  const int64_t passes = (met * a.R + kShrinkRows - 1) / kShrinkRows;
+  const int64_t pass_groups = std::max<int64_t>(1, std::min(passes, num_sms / (tiles * p.ksplit)));
+  p.order = reinterpret_cast<int32_t*>(a.ws + (int64_t)p.ksplit * a.T * a.R);
   p.timeout_ns = wait_timeout_ns();
   p.drain_ns = std::max<uint64_t>(p.timeout_ns, 200000000ull);
-  // columns per CTA: the split that ends soonest in whole waves of CTAs, with
-  // a CTA's start (its u) counted as four blocks; the adapters of a tile go to
-  // several CTAs where there are few tiles
+  // The split of columns, and of a tile's adapters, that ends soonest in whole
+  // waves of CTAs, with a CTA's start (its u) counted as four blocks.
   const int64_t blocks = (a.N + kExpCols - 1) / kExpCols;
-  int64_t best = blocks, best_cost = INT64_MAX;
-  for (int64_t per = blocks; per >= 1; per = std::min(per - 1, (blocks + (blocks + per - 1) / per) / ((blocks + per - 1) / per + 1))) {
-    const int64_t ctas = tiles * ((blocks + per - 1) / per);
-    const int64_t cost = (ctas + num_sms - 1) / num_sms * (per + 4);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = per;
+  int64_t best = blocks, groups = 1, best_cost = INT64_MAX;
+  for (int64_t g = 1; g <= met; g = g < met ? std::min(2 * g, met) : g + 1)
+    for (int64_t per = blocks; per >= 1;
+         per = std::min(per - 1, (blocks + (blocks + per - 1) / per) / ((blocks + per - 1) / per + 1))) {
+      const int64_t ctas = tiles * ((blocks + per - 1) / per) * g;
+      const int64_t cost = (ctas + num_sms - 1) / num_sms * (per * ((met + g - 1) / g) + 4);
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = per;
+        groups = g;
+      }
     }
-  }
   p.cols = (int)best * kExpCols;
-  const int groups = std::min<int>(a.n, tiles < 16 ? 8 : 1);
-  CUtensorMap tmX, tmA, tmB;
+  CUtensorMap tmA, tmB;
   const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!make_tmap(&tmX, a.x, dt, a.K, a.T, a.ld_x * 2, 64, kTile) ||
-      !make_tmap(&tmA, a.A, dt, a.K, (int64_t)a.n * a.R, a.K * 2, 64, a.R) ||
+  if (!make_tmap(&tmA, a.A, dt, a.K, (int64_t)a.n * a.R, a.K * 2, 64, a.R) ||
       !make_tmap(&tmB, a.B, dt, a.R, (int64_t)a.n * a.N, (int64_t)a.R * 2, 64, kExpCols))
     return cudaErrorInvalidValue;
-  void* sargs[] = {(void*)&tmX, (void*)&tmA, (void*)&p};
-  e = launch((const void*)lora_shrink_tile_kernel, dim3((unsigned)p.ksplit, (unsigned)tiles), kShrinkThreads, kShrinkSmem,
-             sargs, false, stream);
+  void* oargs[] = {(void*)&p};
+  e = launch((const void*)lora_order_kernel, dim3((unsigned)((a.T + kSegment - 1) / kSegment)), kOrderThreads, 0, oargs,
+             false, stream);
+  if (e != cudaSuccess) return e;
+  void* sargs[] = {(void*)&tmA, (void*)&p};
+  e = launch((const void*)lora_shrink_tile_kernel, dim3((unsigned)p.ksplit, (unsigned)tiles, (unsigned)pass_groups),
+             kShrinkThreads, kShrinkSmem, sargs, true, stream);
   if (e != cudaSuccess) return e;
   void* eargs[] = {(void*)&tmB, (void*)&p};
   return launch(f32 ? (const void*)lora_expand_tile_kernel<float> : (const void*)lora_expand_tile_kernel<__nv_bfloat16>,

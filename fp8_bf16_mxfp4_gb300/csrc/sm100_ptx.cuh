@@ -447,6 +447,10 @@ MXG_DEVINL void fence_proxy_async_smem() {
 MXG_DEVINL void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// The first `bytes` (0..16) of 16 from src, zeros behind them.
+MXG_DEVINL void cp_async_16_fill(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 MXG_DEVINL void cp_async_8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }

@@ -361,6 +361,29 @@ def test_workspaces_kept_by_streams_do_not_meet():
     assert all(torch.equal(a, b) for a, b in outs)
 
 
+def test_calls_of_threads_on_one_stream_do_not_meet():
+    """Two threads that enqueue on the same stream do not share a workspace."""
+    import threading
+    mxg = _mxg()
+    bf = torch.bfloat16
+    g = torch.Generator().manual_seed(12)
+    to = lambda *s: torch.randn(*s, generator=g).to(bf).to(DEV)  # noqa: E731
+    sets = [(to(T, 520), to(T, 512), to(3, 16, 512), to(3, 520, 16), torch.arange(T, dtype=torch.int32, device=DEV) % 3)
+            for T in (40, 40)]
+    wants = [mxg.lora_add(*s, check=True) for s in sets]
+    wrong = [0, 0]
+
+    def work(i):
+        for _ in range(200):
+            wrong[i] += not torch.equal(mxg.lora_add(*sets[i]), wants[i])
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert wrong == [0, 0]
+    mxg.check_status()
+
+
 def test_lora_bad_id_is_reported():
     mxg = _mxg()
     y = torch.zeros(20, 64, dtype=torch.bfloat16, device=DEV)
@@ -396,6 +419,51 @@ def test_lora_side_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(cap, mxg.lora_add(y, x, A, B, ids, check=True)) and not torch.equal(cap, want)
+
+
+# batches that tiles of sorted tokens take: few tiles with many adapters, K splits, one pass and several
+@pytest.mark.parametrize("T,K,N,R,n,runs", [
+    (129, 3144, 3200, 128, 300, 1), (250, 2056, 2064, 104, 130, 1), (511, 4104, 2056, 32, 40, 1), (640, 72, 3080, 56, 12, 128),
+    (1500, 3080, 72, 96, 4, 1), (2000, 1032, 1544, 40, 2, 500), (4001, 520, 608, 24, 90, 1),
+    (8192, 512, 520, 64, 64, 1),    # one segment, every adapter in every 128 tokens of the batch
+    (8193, 1032, 264, 128, 3, 1),   # a segment of one token
+    (16391, 72, 1032, 64, 200, 5),  # three segments, K inside one 64-element step
+    (700, 4104, 8, 128, 9, 1),      # columns inside one block
+    (9000, 264, 248, 128, 1, 9000),
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_lora_mixed_batches(T, K, N, R, n, runs, dtype):
+    check_lora(T, K, N, R, n, dtype, runs)
+
+
+def test_lora_adapters_past_the_sorted_count():
+    mxg = _mxg()
+    T, K, N, R = 2048, 512, 8, 128
+    g = torch.Generator().manual_seed(3)
+    to = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    few = (to(5, R, K), to(5, N, R))
+    y, x = to(T, N), to(T, K)
+    ids = torch.randint(-1, 5, (T,), generator=g).to(torch.int32).to(DEV)
+    want = mxg.lora_add(y, x, *few, ids, check=True)
+    for n in (8190, 8191, 8192, 8200):  # the same adapters at the end of a long list
+        A = torch.zeros(n, R, K, dtype=torch.bfloat16, device=DEV)
+        B = torch.zeros(n, N, R, dtype=torch.bfloat16, device=DEV)
+        A[-5:], B[-5:] = few
+        many = torch.where(ids < 0, ids, ids + n - 5)
+        assert torch.equal(mxg.lora_add(y, x, A, B, many, check=True), want)
+
+
+def test_lora_results_do_not_depend_on_the_place_in_the_batch():
+    mxg = _mxg()
+    T, K, N, R, n = 1500, 1024, 1544, 96, 40
+    g = torch.Generator().manual_seed(4)
+    to = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    y, x, A, B = to(T, N), to(T, K), to(n, R, K), to(n, N, R)
+    ids = torch.randint(-1, n, (T,), generator=g).to(torch.int32).to(DEV)
+    want = mxg.lora_add(y, x, A, B, ids, check=True)
+    for _ in range(3):
+        perm = torch.randperm(T, generator=g).to(DEV)
+        assert torch.equal(mxg.lora_add(y[perm], x[perm], A, B, ids[perm], check=True), want[perm])
 
 
 # --------------------------------------------------------------------------- bounds and refusals
