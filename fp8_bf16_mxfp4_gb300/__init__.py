@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -636,20 +637,27 @@ def _raw_stream(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-_scratch_buffers = {}
+class _Scratch(threading.local):
+    def __init__(self):
+        self.buffers = {}
+
+
+_scratch_kept = _Scratch()
 _SCRATCH_KEEP = 64 << 20
 
 
 def _scratch(nbytes: int, dev, stream: int) -> torch.Tensor:
     """A call's workspace when the caller gives none.  An allocation costs as
-    much host time as the launches, so each stream keeps one buffer of up to
-    64 MiB (calls on a stream are ordered, and each writes what it reads); a
-    captured graph gets memory of its own pool."""
+    much host time as the launches, so each thread keeps one buffer of up to
+    64 MiB for each stream (a thread's calls on a stream are ordered, and each
+    writes what it reads; calls of two threads interleave); a captured graph
+    gets memory of its own pool."""
     if nbytes <= _SCRATCH_KEEP and not torch._C._cuda_isCurrentStreamCapturing():
+        kept = _scratch_kept.buffers
         key = (dev.index, stream)
-        buf = _scratch_buffers.get(key)
+        buf = kept.get(key)
         if buf is None or buf.numel() < nbytes:
-            buf = _scratch_buffers[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+            buf = kept[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
         return buf
     return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
