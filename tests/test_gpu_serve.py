@@ -574,3 +574,58 @@ def test_example_runs_the_operators_together(capsys):
     spec.loader.exec_module(example)
     us = example.main(["--tokens", "5", "--hidden", "512", "--inter", "256", "--experts", "6", "--top-k", "2", "--steps", "3"])
     assert us > 0 and "experts used" in capsys.readouterr().out
+
+
+# --------------------------------------------------------------------------- offsets past 32 bits
+
+
+def test_lora_offsets_past_32_bits():
+    """More than 2^31 elements of y and 2^32 bytes of x and out, padded rows; sampled rows against the oracle."""
+    T, K, N, R, n = 70003, 72, 32776, 64, 3
+    ld_x = 33000  # 4.6 GB of rows of which a few columns are used
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    x = torch.empty(T, ld_x, dtype=torch.bfloat16, device=DEV)[:, :K]
+    x.copy_(torch.randn(T, K, generator=g, device=DEV))
+    y = torch.empty(T, N, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    A = (torch.randn(n, R, K, generator=g, device=DEV) * K ** -0.5).to(torch.bfloat16)
+    B = (torch.randn(n, N, R, generator=g, device=DEV) * R ** -0.5).to(torch.bfloat16)
+    ids = torch.randint(-1, n, (T,), generator=g, device=DEV).to(torch.int32)
+    got = _mxg().lora_add(y, x, A, B, ids, check=True)
+    rows = [0, 1, 65535, 65536, 69999, 70000, 70001, 70002]
+    want, bound = serve.lora_add(f64(y[rows]), f64(x[rows]), f64(A), f64(B), ids[rows].tolist(), [1.0] * n)
+    tol = bound + np.abs(want) * 2.0 ** -8 + 2.0 ** -126
+    assert (np.abs(f64(got[rows]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_experts_offsets_past_32_bits(fmt):
+    """The last experts of weights with more than 2^32 (E2M1: 2^31) bytes of
+    codes give what the same experts give in a list of their own: the work is
+    split by the experts used."""
+    mxg = _mxg()
+    E, H, I, T, few = 70, 4096, 8192, 5, 3
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    per = 2 if fmt == "e2m1" else 1
+
+    def operand(rows, cols):
+        data = torch.zeros(rows, cols // per, dtype=torch.uint8, device=DEV)
+        scale = torch.full((cols // 128, rows // 128, 512), 127, dtype=torch.uint8, device=DEV)
+        last = rows // E * few
+        data[-last:].random_(0, 256, generator=g)
+        if fmt == "e4m3":
+            data[-last:] &= 0xB7  # no NaN, magnitudes below 2
+        scale[:, -(last // 128):].random_(116, 122, generator=g)
+        return (mxg.MXOperand(data, scale.view(-1), fmt, cols, "packed"),
+                mxg.MXOperand(data[-last:], scale[:, -(last // 128):].contiguous().view(-1), fmt, cols, "packed"))
+
+    w13, w13_few = operand(E * 2 * I, H)
+    w2, w2_few = operand(E * H, I)
+    x = torch.randn(T, H, generator=g, device=DEV).to(torch.bfloat16)
+    ids = torch.tensor([[0, 1], [2, 0], [1, 2], [-1, 2], [1, -1]], dtype=torch.int32, device=DEV)
+    w = torch.rand(T, 2, generator=g, device=DEV)
+    want = mxg.moe_experts(x, ids, w, w13_few, w2_few, check=True)
+    got = mxg.moe_experts(x, torch.where(ids < 0, ids, ids + E - few), w, w13, w2, check=True)
+    assert bool(want.isfinite().all()) and float(want.float().abs().max()) > 0
+    assert torch.equal(got, want)
