@@ -18,10 +18,10 @@
 // product: an adapter's infinities or NaN reach its own tokens only.  u keeps its
 // fp32 accuracy as a sum of two BF16 terms (2^-17; BF16 output) or three (2^-25;
 // FP32 output).
-//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 248 us, 4.4 TB/s
+//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 242 us, 4.5 TB/s
 //   of the 1.09 GB it has to move (160 us at the copy rate).  Expand is about
 //   three quarters of that; reads and writes of y share DRAM at 67 to 80 %.
-//   Left in the batch's order the same takes 240 us, but 1024 tokens of 64 mixed
+//   Left in the batch's order the same takes about 5 us less, but 1024 tokens of 64 mixed
 //   adapters (4096 x 4096, rank 16) take 200 us instead of 32.
 //   mma.sync runs at 1/16 of the tcgen05 rate here: a form on it took 264 us.
 #include <cuda.h>
@@ -839,18 +839,17 @@ bool per_token(int64_t T, int64_t N, int64_t K, int R) {
 }
 
 // Tiles: 64-element steps of K per shrink CTA.  Among the splits that leave
-// eight steps a CTA (and at most sixteen splits), the one that fills its last
-// wave of CTAs best.
+// eight steps a CTA (and at most sixteen splits), the one that ends soonest in
+// whole waves of CTAs, with a CTA's start counted as eight steps.
 int shrink_steps(int64_t T, int64_t K) {
   const int64_t tiles = (T + kTile - 1) / kTile, steps = (K + 63) / 64;
-  int64_t best = steps;
-  double best_eff = 0.0;
+  int64_t best = steps, best_cost = INT64_MAX;
   for (int64_t split = 1; split <= 16 && (split == 1 || steps / split >= 8); ++split) {
     const int64_t per = (steps + split - 1) / split;
     const int64_t ctas = tiles * ((steps + per - 1) / per);
-    const double eff = (double)(tiles * steps) / (double)((ctas + kLoraSms - 1) / kLoraSms * kLoraSms * per);
-    if (eff > best_eff * 1.02) {
-      best_eff = eff;
+    const int64_t cost = (ctas + kLoraSms - 1) / kLoraSms * (per + 8);
+    if (cost < best_cost) {
+      best_cost = cost;
       best = per;
     }
   }
