@@ -18,7 +18,7 @@
 // product: an adapter's infinities or NaN reach its own tokens only.  u keeps its
 // fp32 accuracy as a sum of two BF16 terms (2^-17; BF16 output) or three (2^-25;
 // FP32 output).
-//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 242 us, 4.5 TB/s
+//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 240 us, 4.5 TB/s
 //   of the 1.09 GB it has to move (160 us at the copy rate).  Expand is about
 //   three quarters of that; reads and writes of y share DRAM at 67 to 80 %.
 //   Left in the batch's order the same takes about 5 us less, but 1024 tokens of 64 mixed
