@@ -18,7 +18,7 @@
 // product: an adapter's infinities or NaN reach its own tokens only.  u keeps its
 // fp32 accuracy as a sum of two BF16 terms (2^-17; BF16 output) or three (2^-25;
 // FP32 output).
-//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 240 us, 4.5 TB/s
+//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 237 us, 4.6 TB/s
 //   of the 1.09 GB it has to move (160 us at the copy rate).  Expand is about
 //   three quarters of that; reads and writes of y share DRAM at 67 to 80 %.
 //   Left in the batch's order the same takes about 5 us less, but 1024 tokens of 64 mixed
@@ -760,8 +760,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           if (half * 64 + col + mcol < ncols) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if ((rows >> i) & 1)
-                ptx::cp_async_16(dst + 4 * i * kPiecePitch, ybase + tok[i] * a.ld_y + col);
+              ptx::cp_async_16_if((rows >> i) & 1, dst + 4 * i * kPiecePitch, ybase + tok[i] * a.ld_y + col);
           }
         }
         ptx::cp_async_commit();
@@ -800,9 +799,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           if (half * 64 + col + mcol < ncols) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if ((rows >> i) & 1)
-                *reinterpret_cast<uint4*>(obase + tok[i] * a.ld_out + col) =
-                    *reinterpret_cast<const uint4*>(piece + (mrow + 4 * i) * kPiecePitch + (lane & 7) * 16);
+              ptx::st_v4_if((rows >> i) & 1, obase + tok[i] * a.ld_out + col,
+                            *reinterpret_cast<const uint4*>(piece + (mrow + 4 * i) * kPiecePitch + (lane & 7) * 16));
           }
           __syncwarp();
         }
@@ -925,7 +923,10 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms)
   if ((e = ensure_lora_attr()) != cudaSuccess) return e;
   p.blocks = shrink_steps(a.T, a.K);
   p.ksplit = (int)tile_splits(a.T, a.K);
-  const int64_t met = std::min<int64_t>(kTile, 1 + a.n / tiles);  // about what a tile of sorted tokens meets
+  // About what a tile of sorted tokens meets, with room for one more where it
+  // meets several (a CTA that gets a second adapter takes twice as long: 512
+  // tokens of 64 adapters, 4096 x 4096, rank 16: 40 us without the room, 36 with).
+  const int64_t met = a.n < tiles ? 1 : std::min<int64_t>({kTile, a.n, 2 + a.n / tiles});
   const int64_t passes = (met * a.R + kShrinkRows - 1) / kShrinkRows;
   const int64_t pass_groups = std::max<int64_t>(1, std::min(passes, num_sms / (tiles * p.ksplit)));
   p.order = reinterpret_cast<int32_t*>(a.ws + (int64_t)p.ksplit * a.T * a.R);

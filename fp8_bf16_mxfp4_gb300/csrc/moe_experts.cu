@@ -42,10 +42,10 @@
 // the tensor core's layout at full rate (it moves a row of up to 128 bytes in
 // 2.9 ns an SM, so 64-byte rows stop at 3.3 TB/s); 8-byte copies out of L2 bring
 // them at about 20 bytes a clock an SM: 13 tokens, top 8 of 32 experts,
-// 7168 x 2048: 130 us, 5.6 TB/s; 128 tokens 154 us, joins and epilogues growing
+// 7168 x 2048: 130 us, 5.6 TB/s; 128 tokens 152 us, joins and epilogues growing
 // with the tokens; 1 token 50 us for 0.19 GB, of which the four kernels' plans
 // and tails are a third.  A small layer (33 tokens, top 3 of 12, 1152 x 640,
-// 27 MB) takes 16 us, nearly all of it latency.
+// 27 MB) takes 15.5 us, nearly all of it latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -598,11 +598,11 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
             float v0[8], v1[8];
             read(c0, v0, v1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c0 + i < w.n) {
-                __stcg(mine + (c0 + i) * 256, v0[i]);
-                if (two) __stcg(mine + (c0 + i) * 256 + 128, v1[i]);
-              }
+            for (int i = 0; i < 8; ++i) {
+              const bool in = c0 + i < w.n;
+              ptx::st_cg_f32_if(in, mine + (c0 + i) * 256, v0[i]);
+              ptx::st_cg_f32_if(in && two, mine + (c0 + i) * 256 + 128, v1[i]);
+            }
           }
           first = runs.owner(w.unit * runs.per_unit);
           last = runs.owner(w.unit * runs.per_unit + runs.per_unit - 1);
@@ -615,7 +615,8 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
           __threadfence();
         }
         // Eight tokens at a time (all eight are computed, so that they
-        // interleave, and the unit's stored).  The last CTA of a cut unit adds
+        // interleave, and the unit's stored, under predicates: a branch for each
+        // store took 1100 clocks for eight tokens).  The last CTA of a cut unit adds
         // the partials in run order: buffers 2 first + 1, 2 (first + 1), ...
         for (int c0 = 0; c0 < w.n; c0 += 8) {
           float v0[8], v1[8];
@@ -651,11 +652,10 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float wt = __shfl_sync(kFull, c0 < 32 ? wt_lo : wt_hi, (c0 + i) & 31);
-              if (c0 + i < w.n) {
-                float* dst = p.rows + slot[i] * p.H + w.rt * 256 + quarter * 32 + lane;
-                __stcg(dst, v0[i] * wt);
-                if (two) __stcg(dst + 128, v1[i] * wt);
-              }
+              const bool in = c0 + i < w.n;
+              float* dst = p.rows + slot[i] * p.H + w.rt * 256 + quarter * 32 + lane;
+              ptx::st_cg_f32_if(in, dst, v0[i] * wt);
+              ptx::st_cg_f32_if(in && two, dst + 128, v1[i] * wt);
             }
           } else {
             uint32_t code[8];
@@ -667,13 +667,15 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
               ex[i] = mx_exponent_f32(__reduce_max_sync(kFull, __float_as_uint(h) & 0x7FFFFFFFu));
               code[i] = cvt_e4m3x4(h * pow2_neg(ex[i]), 0.0f, 0.0f, 0.0f);
             }
+            int my_ex = 0;  // lane i has the scale of token i
+            int64_t my_slot = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if (c0 + i < w.n) {
-                p.hq[slot[i] * p.I + w.rt * 128 + quarter * 32 + lane] = (uint8_t)code[i];
-                if (lane == 0) p.hs[slot[i] * (p.I >> 5) + w.rt * 4 + quarter] = (uint8_t)(ex[i] + 127);
-              }
+              ptx::st_u8_if(c0 + i < w.n, p.hq + slot[i] * p.I + w.rt * 128 + quarter * 32 + lane, code[i]);
+              my_ex = lane == i ? ex[i] : my_ex;
+              my_slot = lane == i ? slot[i] : my_slot;
             }
+            ptx::st_u8_if(lane < 8 && c0 + lane < w.n, p.hs + my_slot * (p.I >> 5) + w.rt * 4 + quarter, my_ex + 127);
           }
         }
       }

@@ -451,6 +451,11 @@ MXG_DEVINL void cp_async_16(uint32_t dst, const void* src) {
 MXG_DEVINL void cp_async_16_fill(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+MXG_DEVINL void cp_async_16_if(uint32_t pred, uint32_t dst, const void* src) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q cp.async.cg.shared.global [%1], [%2], 16;\n\t}" ::"r"(pred),
+               "r"(dst), "l"(src)
+               : "memory");
+}
 MXG_DEVINL void cp_async_8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -466,6 +471,21 @@ MXG_DEVINL void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N
 // cp.async that this thread has issued so far has completed.
 MXG_DEVINL void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Stores under a predicate (no branch).
+MXG_DEVINL void st_cg_f32_if(uint32_t pred, float* p, float v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q st.global.cg.f32 [%1], %2;\n\t}" ::"r"(pred), "l"(p), "f"(v)
+               : "memory");
+}
+MXG_DEVINL void st_v4_if(uint32_t pred, void* p, const uint4& v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q st.global.v4.b32 [%1], {%2, %3, %4, %5};\n\t}" ::"r"(pred),
+               "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+MXG_DEVINL void st_u8_if(uint32_t pred, uint8_t* p, uint32_t v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q st.global.u8 [%1], %2;\n\t}" ::"r"(pred), "l"(p), "r"(v)
+               : "memory");
 }
 
 // Programmatic dependent launch: let the next kernel of the stream start its
