@@ -227,6 +227,11 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
   // activation tiles, which are first written after the sort.
   int16_t* eid = reinterpret_cast<int16_t*>(smem + 2 * kWTile);
   uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + kStageBytes + 2 * kWTile);  // [8][E]
+  const int plan_warp = warp - 2;
+  const bool planner = plan_warp >= 0 && plan_warp < kPlanWarps;
+  const int per_warp = (((P + kPlanWarps - 1) / kPlanWarps) + 31) & ~31;
+  const int slot0 = min(P, plan_warp * per_warp), slot1 = min(P, slot0 + per_warp);
+  int next_id = planner && slot0 + lane < slot1 ? __ldg(p.ids + slot0 + lane) : -1;  // on its way during the set-up
   for (int i = threadIdx.x; i < (kPlanWarps * p.E + 1) / 2; i += kThreads) reinterpret_cast<uint32_t*>(cnt)[i] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMoeStages; ++s) {
@@ -249,15 +254,12 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
   }
   __syncthreads();
   bool bad = false;
-  const int plan_warp = warp - 2;
-  const bool planner = plan_warp >= 0 && plan_warp < kPlanWarps;
-  const int per_warp = (((P + kPlanWarps - 1) / kPlanWarps) + 31) & ~31;
-  const int slot0 = min(P, plan_warp * per_warp), slot1 = min(P, slot0 + per_warp);
   uint16_t* my_cnt = cnt + plan_warp * p.E;
   if (planner) {
     for (int i0 = slot0; i0 < slot1; i0 += 32) {
       const int i = i0 + lane;
-      int e = i < slot1 ? __ldg(p.ids + i) : -1;
+      int e = next_id;
+      next_id = i + 32 < slot1 ? __ldg(p.ids + i + 32) : -1;
       bad |= e >= p.E;
       if (e < 0 || e >= p.E) e = -1;
       if (i < slot1) eid[i] = (int16_t)e;
