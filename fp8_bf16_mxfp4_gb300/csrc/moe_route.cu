@@ -41,7 +41,9 @@ MXG_DEVINL float load_logit(const __nv_bfloat16* p) {
   return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
 }
 
-// kPer: logits per lane (experts <= 32 * kPer).
+// kPer: logits per lane, the least that holds the experts (<= 32 * kPer): 16384
+// tokens of 32 experts, top 8, take 7.6 us with one, 8.5 with two and 26.7 with
+// sixteen; 4096 tokens of 128 experts 5.2 with four and 10.2 with sixteen.
 template <typename TIn, int kPer>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const TIn* __restrict__ logits, int64_t T, int E,
                                                                      int64_t ld, int k, bool renorm,
