@@ -419,11 +419,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     bool ok = true, issued = false;
     for (int o0 = o_first; ok && o0 < count; o0 += o_step, ++pass) {
       const uint32_t idesc = idesc_bf16((min(per_pass, count - o0) * a.R + 15) & ~15);
-      ok = ptx::mbar_wait(acc_empty, (pass & 1u) ^ 1u, abort_flag, a.status, p.timeout_ns);
+      ok = ptx::mbar_wait_warp(acc_empty, (pass & 1u) ^ 1u, abort_flag, a.status, p.timeout_ns);
       if (!ok) break;
       ptx::tc_fence_after();
       for (int k = s0; k < s1; ++k) {
-        ok = ptx::mbar_wait(full_bar(stage), phase, abort_flag, a.status, p.timeout_ns);
+        ok = ptx::mbar_wait_warp(full_bar(stage), phase, abort_flag, a.status, p.timeout_ns);
         if (!ok) break;
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_after();
@@ -686,11 +686,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     bool ok = true, issued = false;
     for (int o = o_first; ok && o < count; o += o_step)
       for (int b = 0; ok && b < blocks; ++b, ++n) {
-        ok = ptx::mbar_wait(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u, abort_flag, a.status, p.timeout_ns);
+        ok = ptx::mbar_wait_warp(acc_empty(n & 1), ((n >> 1) & 1u) ^ 1u, abort_flag, a.status, p.timeout_ns);
         if (!ok) break;
         const uint32_t d = tmem + (n & 1) * kExpCols;
         for (int at = 0; at < atoms; ++at) {
-          ok = ptx::mbar_wait(full_bar(stage), phase, abort_flag, a.status, p.timeout_ns);
+          ok = ptx::mbar_wait_warp(full_bar(stage), phase, abort_flag, a.status, p.timeout_ns);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint64_t bd = ptx::smem_desc(sbase + ubytes + stage * kTileBytes, 16, 1024, 2);

@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop and one lane issues (a lane that gives up a
-    // wait just leaves: nothing below needs the warp together).
+    // The whole warp runs the loop in step (each wait ends in a vote) and one
+    // lane issues and hands the stages back.
     const uint32_t el = ptx::elect_one();
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
     int stage = 0, count = 0;
@@ -416,15 +416,13 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
     bool ok = true, issued = false;
     while (ok && w.next(runs, off, tile, p.E)) {
       const int buf = count & 1;
-      ok = ptx::mbar_wait(acc_empty(buf), ((count >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns);
+      ok = ptx::mbar_wait_warp(acc_empty(buf), ((count >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns);
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t d0 = tm + buf * 2 * kTok, d1 = d0 + kTok;
       for (int kc = w.k0; kc < w.k1; ++kc) {
-        if (!ptx::mbar_try_wait(full_bar(stage), phase)) {
-          ok = ptx::mbar_wait(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
-          if (!ok) break;
-        }
+        ok = ptx::mbar_wait_warp(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
+        if (!ok) break;
         // The stage's plain stores (released by the barrier's arrivals) come
         // before the MMAs' reads.  The fence is here and not at the writers,
         // where it would wait for their loads in flight (1000 clocks a stage).

@@ -65,6 +65,17 @@ MXG_DEVINL bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, in
   }
 }
 
+// As mbar_wait, for a whole warp in step: no lane returns before every lane has
+// seen the phase (or one has given up: then none has).  For a warp of which one
+// lane hands a ring's stages on: without the vote that lane could run ahead until
+// the ring has come round, and a lane left behind would wait for a phase that is
+// past.
+MXG_DEVINL bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status,
+                               uint64_t timeout_ns) {
+  const bool ok = mbar_wait(bar, parity, abort, status, timeout_ns);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // As mbar_wait, for waiters off the critical path: each try_wait may suspend
 // the thread for up to `suspend_ns` (it resumes when the phase completes), so
 // that a long wait does not take issue slots from the warps that share its
