@@ -1,0 +1,108 @@
+"""Infinities, NaN, overflow and the precision of intermediates in the serving
+operators, at sizes that take each of their forms."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serve
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF16_MAX = (2.0 - 2.0 ** -7) * 2.0 ** 127
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def _mxg():
+    import fp8_bf16_mxfp4_gb300 as mxg
+    return mxg
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+# --------------------------------------------------------------------------- adapters
+
+# tokens, K, N, rank, adapters: the first takes the per-token form (its adapters' reads, T * R * (K + N) values of
+# 2 bytes, stay below 150 MB), the second 128-token tiles
+FORMS = {"per_token": (60, 264, 1544, 16, 4), "tiles": (600, 1800, 2416, 32, 4), "tiles_wide_rank": (400, 264, 1544, 128, 4)}
+assert all((T * R * (K + N) * 2 > 150e6) == name.startswith("tiles") for name, (T, K, N, R, n) in FORMS.items())
+
+
+def adapters(form, dtype, seed=0):
+    T, K, N, R, n = FORMS[form]
+    g = torch.Generator().manual_seed(seed + T)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16)  # noqa: E731
+    x, y = rnd(T, K), rnd(T, N).to(dtype)
+    A, B = (rnd(n, R, K) * K ** -0.5).to(torch.bfloat16), (rnd(n, N, R) * R ** -0.5).to(torch.bfloat16)
+    ids = torch.randint(-1, n, (T,), generator=g).to(torch.int32)
+    return y, x, A, B, ids
+
+
+def check(y, x, A, B, ids, scale=None):
+    """lora_add against the definition in 64 bits: where that is infinite or NaN, so is the result."""
+    dtype = y.dtype
+    sc = [1.0] * A.shape[0] if scale is None else scale.tolist()
+    with np.errstate(invalid="ignore", over="ignore"):
+        want, bound = serve.lora_add(f64(y), f64(x), f64(A), f64(B), ids.tolist(), sc)
+        to = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+        got = f64(_mxg().lora_add(to(y), to(x), to(A), to(B), to(ids), to(scale), check=True))
+        fin = np.isfinite(want)
+        tol = bound + np.abs(want) * (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23) + 2.0 ** -126
+        assert np.array_equal(np.isnan(got), np.isnan(want)), f"{(np.isnan(got) != np.isnan(want)).sum()} differ in NaN"
+        inf = np.isinf(want)
+        assert np.array_equal(got[inf], want[inf])
+        assert (np.abs(got[fin] - want[fin]) <= tol[fin]).all()
+    return want
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_lora_infinite_and_overflowing_products(form, dtype):
+    """A x that is infinite, or finite but past the largest BF16, against a finite B."""
+    y, x, A, B, ids = adapters(form, dtype)
+    A[2] = 0
+    A[2, :, :2] = 1.0                         # adapter 2: x0 + x1 in every rank
+    B[2] = B[2].abs().clamp(min=2.0 ** -6) * 2.0 ** -120  # exact, of one sign, and keeps the sums in range
+    at = (torch.arange(len(ids)) % 7 == 1).nonzero().flatten()
+    ids[at] = 2
+    x[at] = 0
+    x[at[0::4], 0] = BF16_MAX                 # past the largest BF16 by 3/4 of its step: finite in FP32
+    x[at[0::4], 1] = 1.5 * 2.0 ** 119
+    x[at[1::4], 0] = -BF16_MAX
+    x[at[1::4], 1] = -1.5 * 2.0 ** 119
+    x[at[2::4], 0] = float("inf")
+    x[at[3::4], 1] = -float("inf")
+    want = check(y, x, A, B, ids)
+    assert np.isinf(want[at[2::4]]).all() and np.isfinite(want[at[0::4]]).all()
+    rest = torch.ones(len(ids), dtype=torch.bool)
+    rest[at] = False
+    assert np.isfinite(want[rest]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_lora_infinite_columns(form, dtype):
+    """Infinities and NaN in B, against A x of either sign, with and without a part below BF16's step, and zero."""
+    y, x, A, B, ids = adapters(form, dtype, seed=1)
+    N = B.shape[1]
+    B[1, 5, 3], B[1, N - 1, 0], B[1, 129, 1], B[1, 300, 2] = float("inf"), -float("inf"), float("inf"), float("nan")
+    A[1, 1] = 0
+    A[1, 1, 0] = 1.0                          # rank 1: A x = x0, a BF16 value
+    one = (ids == 1).nonzero().flatten()
+    x[one[0], 0] = 0                          # 0 * inf
+    x[one[1]] = float("nan")
+    x[one[2], 0] = float("inf")               # infinite in every rank that uses it
+    want = check(y, x, A, B, ids)
+    assert np.isinf(want[one[3:]][:, [5, N - 1, 129]]).all() and np.isnan(want[one, 300]).all()
+    assert np.isnan(want[one[0], 129]) and np.isnan(want[one[1]]).all()
+    cols = [c for c in range(N) if c not in (5, N - 1, 129, 300)]
+    assert np.isfinite(want[one[3:]][:, cols]).all()
+    assert np.isfinite(want[(ids != 1).numpy()]).all()
