@@ -189,6 +189,15 @@ struct Walker {
   }
 };
 
+// g / (1 + exp(-g)), by exp(-|g|): exp(-g) would pass the FP32 range below -88.7,
+// where the quotient does not.  The divisor is in [1, 2], where the fast division
+// is within 2 units; the result is rounded to 4 bits next.  A rounded division
+// takes 33 tokens of a small layer (1152 x 640) from 16.9 to 18.0 us.
+MXG_DEVINL float silu(float g) {
+  const float e = expf(-fabsf(g));
+  return __fdividef(g < 0.0f ? g * e : g, 1.0f + e);
+}
+
 // FP32 magnitude bits -> MX exponent of E4M3 (floor(log2) - 8, at least -127).
 MXG_DEVINL int mx_exponent_f32(uint32_t amax_bits) { return max((int)(amax_bits >> 23) - 127 - 8, -127); }
 
@@ -662,7 +671,7 @@ __global__ void __launch_bounds__(moe_threads(kFp4), 1)
             int ex[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float h = __fdividef(v0[i], 1.0f + expf(-v0[i])) * v1[i];
+              const float h = silu(v0[i]) * v1[i];
               // the block of 32 channels is this warp's 32 lanes
               ex[i] = mx_exponent_f32(__reduce_max_sync(kFull, __float_as_uint(h) & 0x7FFFFFFFu));
               code[i] = cvt_e4m3x4(h * pow2_neg(ex[i]), 0.0f, 0.0f, 0.0f);

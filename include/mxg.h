@@ -491,8 +491,11 @@ mxg_status moe_route(const void* logits, int64_t tokens, int32_t experts, int64_
  *   g, u    = W13[e] xq                      rows [0, inter) and [inter, 2 inter) of expert e
  *   hq      = MXFP8(g / (1 + exp(-g)) * u)   same rule, from the fp32 values
  *   out[t]  = sum over slots j of weights[t, j] * (W2[e_j] hq_j),  e_j = ids[t, j]
- * Products are exact, sums are in fp32, and the result is rounded once.  A slot with a negative id is empty; a token without slots
- * gives zeros.  The result depends on the inputs only, not on timing.
+ * Products are exact, sums are in fp32, and the result is rounded once; the
+ * quotient by 1 + exp(-g) is within a few fp32 units for every g (it is taken by
+ * exp(-|g|), so that it does not vanish where exp(-g) overflows).  A slot with a
+ * negative id is empty; a token without slots gives zeros.  The result depends
+ * on the inputs only, not on timing.
  *   x       : BF16 [tokens, hidden], row stride ld_x (% 8), 16-byte aligned
  *   ids, weights : [tokens, top_k] contiguous (as from moe_route)
  *   W13     : [experts * 2 * inter, hidden], W2: [experts * hidden, inter];

@@ -106,3 +106,49 @@ def test_lora_infinite_columns(form, dtype):
     cols = [c for c in range(N) if c not in (5, N - 1, 129, 300)]
     assert np.isfinite(want[one[3:]][:, cols]).all()
     assert np.isfinite(want[(ids != 1).numpy()]).all()
+
+
+# --------------------------------------------------------------------------- experts
+
+
+def operand(w, fmt, groups):
+    """float64 weights that the format holds exactly -> packed operand on the device."""
+    import oracle
+    from gpu_util import u8_to_dev
+    t = torch.from_numpy(w).to(torch.bfloat16)
+    assert np.array_equal(f64(t), w)
+    data, scale = oracle.quantize_mx_rowwise(t.view(torch.int16).numpy().view(np.uint16), fmt)
+    codes = oracle.unpack_e2m1(data) if fmt == "e2m1" else data
+    assert np.array_equal(oracle.dequantize_mx(codes, scale, fmt), w)
+    packed = oracle.pack_scales_mma(scale, [w.shape[0] // groups] * groups)
+    return _mxg().MXOperand(u8_to_dev(data), u8_to_dev(packed), fmt, w.shape[1], "packed")
+
+
+def silu_rounded(g, u):
+    """silu(g) * u rounded to MXFP8 from exact g and u, and how far fp32 arithmetic may land from it: a few units of
+    the result (16, as in the oracle), and the step of a subnormal exp and silu."""
+    with np.errstate(over="ignore"):
+        h = g / (1.0 + np.exp(-g)) * u
+    return serve.mxfp8_f64(h, 16 * serve.U * np.abs(h) + np.abs(u) * (np.abs(g) + 1) * 2.0 ** -148)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("up", [0, 100])
+def test_experts_gates_far_below_zero(fmt, up):
+    """Gates at which exp(-g) is near the end of the FP32 range or past it, where silu(g) is tiny and not zero."""
+    H = I = 128
+    # each block of 32 channels has one gate: 64 a + 16 b + c / 16 with weights of 4 bits
+    parts = [(-64, -24, 8), (-64, -24, 0), (-64, -24, -8), (-64, -24, -32)]
+    x = np.zeros((1, H))
+    x[0, :3] = 1, 1, 2.0 ** -4
+    w13 = np.zeros((2 * I, H))
+    w13[:I, :3] = np.repeat(np.array(parts, float), 32, 0)
+    w13[I:, 0] = 2.0 ** up * np.where(np.arange(I) % 3 == 1, -1.5, 1.0)
+    g, u = x[0] @ w13[:I].T, x[0] @ w13[I:].T
+    assert sorted(set(g)) == [-90, -88.5, -88, -87.5]
+    want, off = silu_rounded(g[None], u[None])
+    got = _mxg().moe_experts(torch.from_numpy(x).to(torch.bfloat16).to(DEV), torch.zeros(1, 1, dtype=torch.int32, device=DEV),
+                             torch.ones(1, 1, device=DEV), operand(w13, fmt, 1), operand(np.eye(H, I), fmt, 1),
+                             out_dtype=torch.float32, check=True)
+    assert (want != 0).all()
+    assert (np.abs(f64(got) - want) <= off + serve.U * np.abs(want)).all()
