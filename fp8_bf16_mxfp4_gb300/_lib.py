@@ -114,6 +114,7 @@ SIGNATURES = {
     "moe_experts": (
         c_i32, [c_vp, c_i64, c_i64, c_vp, c_vp, c_i32, c_i32, ctypes.POINTER(MxOperandC),
                 ctypes.POINTER(MxOperandC), c_vp, c_i64, c_i32, c_vp, c_size, c_vp, c_vp]),
+    "lora_add_form": (c_i32, [c_i64, c_i64, c_i64, c_i32]),
     "lora_add_workspace_size": (c_size, [c_i64, c_i64, c_i32]),
     "lora_add": (
         c_i32, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i32, c_i32, c_i32, c_vp,

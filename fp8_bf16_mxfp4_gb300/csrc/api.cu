@@ -831,6 +831,8 @@ bool lora_sizes_ok(int64_t tokens, int64_t K, int32_t rank) {
          rank % 8 == 0 && rank <= kMaxRank;
 }
 
+bool lora_columns_ok(int64_t N) { return N > 0 && N % 8 == 0 && N <= 0x7FFFFFFF; }
+
 // One expert weight matrix of moe_experts: `rows` x `cols`, packed scales.
 mxg_status check_expert_weights(const mxg_mx_operand* w, int64_t rows, int64_t cols) {
   const mxg_status st = check_operand(w, false, true);
@@ -911,13 +913,18 @@ size_t lora_add_workspace_size(int64_t tokens, int64_t K, int32_t rank) {
   return lora_workspace_bytes(tokens, K, rank);
 }
 
+int32_t lora_add_form(int64_t tokens, int64_t N, int64_t K, int32_t rank) {
+  if (!lora_sizes_ok(tokens, K, rank) || !lora_columns_ok(N)) return 0;
+  return lora_per_token(tokens, N, K, rank) ? 1 : 2;
+}
+
 mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, const void* A, const void* B,
                     const int32_t* ids, const float* scale, int64_t tokens, int64_t N, int64_t K, int32_t rank,
                     int32_t adapters, int32_t dtype, void* out, int64_t ld_out, void* ws, size_t ws_bytes,
                     int32_t* d_status, void* stream) {
   if (d_status == nullptr) return MXG_ERR_NULL;
   if (!valid_out_dtype(dtype)) return MXG_ERR_UNSUPPORTED;
-  if (!lora_sizes_ok(tokens, K, rank) || N <= 0 || N % 8 != 0 || N > 0x7FFFFFFF || adapters < 1 ||
+  if (!lora_sizes_ok(tokens, K, rank) || !lora_columns_ok(N) || adapters < 1 ||
       adapters > 0x7FFFFFFF / N || adapters > 0x7FFFFFFF / rank || ld_x < K ||
       ld_y < N || ld_out < N)
     return MXG_ERR_SHAPE;

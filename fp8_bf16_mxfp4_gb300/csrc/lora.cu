@@ -930,10 +930,6 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 constexpr double kTokenBytes = 150e6;
 constexpr int kLoraSms = 152;
 
-bool per_token(int64_t T, int64_t N, int64_t K, int R) {
-  return (double)T * R * (double)(K + N) * 2.0 <= kTokenBytes && T <= 65535;
-}
-
 // Tiles: 64-element steps of K per shrink CTA.  Among the splits that leave
 // eight steps a CTA (and at most sixteen splits), the one that ends soonest in
 // whole waves of CTAs, with a CTA's start counted as eight steps.
@@ -994,6 +990,10 @@ cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void** a
 
 }  // namespace
 
+bool lora_per_token(int64_t T, int64_t N, int64_t K, int R) {
+  return (double)T * R * (double)(K + N) * 2.0 <= kTokenBytes && T <= 65535;
+}
+
 size_t lora_workspace_bytes(int64_t T, int64_t K, int R) {
   T = std::max<int64_t>(T, 1);
   const int64_t split = std::max<int64_t>(tile_splits(T, K), T <= 65535 ? (K + kTokK - 1) / kTokK : 0);
@@ -1006,7 +1006,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms)
   p.u = a.ws;
   const bool f32 = a.dtype == MXG_OUT_F32;
   cudaError_t e;
-  if (per_token(a.T, a.N, a.K, a.R)) {
+  if (lora_per_token(a.T, a.N, a.K, a.R)) {
     p.ksplit = (int)((a.K + kTokK - 1) / kTokK);
     void* args[] = {(void*)&p};
     e = launch((const void*)lora_shrink_token_kernel,

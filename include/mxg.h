@@ -530,7 +530,14 @@ mxg_status moe_experts(const void* x, int64_t tokens, int64_t ld_x, const int32_
  * K % 8 == 0, N % 8 == 0, rank a multiple of 8 up to 128 (pad adapters of a
  * lower rank with zeros), adapters >= 1, adapters * N and adapters *
  * rank below 2^31, 0 <= tokens <= 8388480.  Device error:
- * MXG_ERR_INDEX (an id >= adapters; that token's row of out is unspecified). */
+ * MXG_ERR_INDEX (an id >= adapters; that token's row of out is unspecified).
+ *
+ * There are two forms, chosen by the sizes alone; lora_add_form says which a call
+ * takes: 1, a CTA per token, or 2, tiles of 128 tokens on the tensor cores (0: the
+ * sizes are refused).  In the second, scale * (A x) enters the second product
+ * with 16 significant bits for a BF16 output and 24 for an FP32 one; the first
+ * is in fp32 throughout. */
+int32_t lora_add_form(int64_t tokens, int64_t N, int64_t K, int32_t rank);
 size_t lora_add_workspace_size(int64_t tokens, int64_t K, int32_t rank);
 mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, const void* A, const void* B,
                     const int32_t* ids, const float* scale, int64_t tokens, int64_t N, int64_t K, int32_t rank,

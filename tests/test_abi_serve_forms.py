@@ -1,0 +1,27 @@
+"""lora_add_form: which kernels a call takes, from its sizes (no GPU)."""
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from fp8_bf16_mxfp4_gb300 import build, _lib
+    build.build()
+    return _lib.load()
+
+
+def test_lora_form(lib):
+    f = lib.lora_add_form
+    assert f(1, 4096, 7168, 16) == 1 and f(8192, 28672, 8192, 32) == 2 and f(0, 8, 8, 8) == 1
+    assert f(1, 2 ** 24, 2 ** 24, 128) == 2                    # one token of a huge adapter
+    assert f(65535, 8, 8, 8) == 1 and f(65536, 8, 8, 8) == 2   # the per-token grids' limit
+    # the adapters' reads, 2 T R (K + N) bytes, of the per-token form: at most 150 MB
+    assert 2 * 3125 * 8 * (1000 + 2000) == 150e6
+    assert f(3125, 1000, 2000, 8) == 1 and f(3126, 1000, 2000, 8) == 2
+
+
+def test_lora_form_of_refused_sizes(lib):
+    f = lib.lora_add_form
+    for bad in ((-1, 64, 64, 8), (65535 * 128 + 1, 64, 64, 8), (4, 60, 64, 8), (4, 0, 64, 8), (4, 64, 60, 8), (4, 64, 0, 8),
+                (4, 64, 64, 0), (4, 64, 64, 12), (4, 64, 64, 136), (4, 2 ** 31, 64, 8)):
+        assert f(*bad) == 0, bad
