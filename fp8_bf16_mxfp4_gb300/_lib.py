@@ -126,6 +126,7 @@ SIGNATURES = {
     "mxg_set_gemm_cta_group": (c_i32, [c_i32]),
     "mxg_get_gemm_cta_group": (c_i32, []),
     "mxg_diag_bounded_wait": (c_i32, [c_vp, c_u64, c_vp]),
+    "mxg_diag_lora_tile_adapters": (c_i32, [c_i64, c_i32]),
     "mxg_version": (c_i32, []),
 }
 

@@ -913,6 +913,10 @@ size_t lora_add_workspace_size(int64_t tokens, int64_t K, int32_t rank) {
   return lora_workspace_bytes(tokens, K, rank);
 }
 
+int32_t mxg_diag_lora_tile_adapters(int64_t tokens, int32_t adapters) {
+  return tokens < 1 || adapters < 1 ? 0 : (int32_t)lora_tile_adapters(tokens, adapters);
+}
+
 int32_t lora_add_form(int64_t tokens, int64_t N, int64_t K, int32_t rank) {
   if (!lora_sizes_ok(tokens, K, rank) || !lora_columns_ok(N)) return 0;
   return lora_per_token(tokens, N, K, rank) ? 1 : 2;

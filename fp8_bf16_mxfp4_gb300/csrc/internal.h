@@ -152,6 +152,7 @@ struct LoraArgs {
   float* ws;
   int32_t* status;
 };
+int64_t lora_tile_adapters(int64_t T, int64_t n);  // that the tile form's split is planned for
 bool lora_per_token(int64_t T, int64_t N, int64_t K, int R);
 size_t lora_workspace_bytes(int64_t T, int64_t K, int R);
 cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms);

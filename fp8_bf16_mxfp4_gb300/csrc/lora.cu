@@ -209,7 +209,7 @@ constexpr int kTileBytes = kTile * kRowBytes;
 
 // Order of the tokens: within each segment of 8192, by adapter, tokens without
 // one last; a CTA per segment counts, sums and places.  So a tile meets about
-// 1 + adapters / 64 adapters instead of up to 128.  The order among a
+// 1 + adapters / (tiles of its segment, 64 at most) instead of up to 128.  The order among a
 // segment's tokens of one adapter goes by the atomics; a token's result does not
 // depend on its place.  Where the counters do not fit, the order is the batch's.
 constexpr int kSegment = 8192;
@@ -994,6 +994,15 @@ bool lora_per_token(int64_t T, int64_t N, int64_t K, int R) {
   return (double)T * R * (double)(K + N) * 2.0 <= kTokenBytes && T <= 65535;
 }
 
+// About what a tile of sorted tokens meets, with room for one more where it
+// meets several (a CTA that gets a second adapter takes twice as long: 512
+// tokens of 64 adapters, 4096 x 4096, rank 16: 40 us without the room, 36 with).
+// Tokens are sorted within a segment, whose tiles share its adapters out.
+int64_t lora_tile_adapters(int64_t T, int64_t n) {
+  const int64_t tiles = std::min<int64_t>((T + kTile - 1) / kTile, kSegment / kTile);
+  return n < tiles ? 1 : std::min<int64_t>({kTile, n, 2 + n / tiles});
+}
+
 size_t lora_workspace_bytes(int64_t T, int64_t K, int R) {
   T = std::max<int64_t>(T, 1);
   const int64_t split = std::max<int64_t>(tile_splits(T, K), T <= 65535 ? (K + kTokK - 1) / kTokK : 0);
@@ -1021,10 +1030,7 @@ cudaError_t launch_lora_add(const LoraArgs& a, cudaStream_t stream, int num_sms)
   if ((e = ensure_lora_attr()) != cudaSuccess) return e;
   p.blocks = shrink_steps(a.T, a.K);
   p.ksplit = (int)tile_splits(a.T, a.K);
-  // About what a tile of sorted tokens meets, with room for one more where it
-  // meets several (a CTA that gets a second adapter takes twice as long: 512
-  // tokens of 64 adapters, 4096 x 4096, rank 16: 40 us without the room, 36 with).
-  const int64_t met = a.n < tiles ? 1 : std::min<int64_t>({kTile, a.n, 2 + a.n / tiles});
+  const int64_t met = lora_tile_adapters(a.T, a.n);
   const int64_t passes = (met * a.R + kShrinkRows - 1) / kShrinkRows;
   const int64_t pass_groups = std::max<int64_t>(1, std::min(passes, num_sms / (tiles * p.ksplit)));
   p.order = reinterpret_cast<int32_t*>(a.ws + (int64_t)p.ksplit * a.T * a.R);

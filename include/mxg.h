@@ -578,6 +578,10 @@ int32_t mxg_get_gemm_cta_group(void);
  * usable.  Returns the launch status (enqueue only). */
 mxg_status mxg_diag_bounded_wait(int32_t* d_status, uint64_t timeout_ns, void* stream);
 
+/* Diagnostic: the number of adapters per tile of 128 tokens that lora_add plans
+ * its work for (tokens on adapters at random), 0 where either is below 1. */
+int32_t mxg_diag_lora_tile_adapters(int64_t tokens, int32_t adapters);
+
 /* ABI version: major*10000 + minor*100 + patch. */
 int32_t mxg_version(void);
 

@@ -25,3 +25,20 @@ def test_lora_form_of_refused_sizes(lib):
     for bad in ((-1, 64, 64, 8), (65535 * 128 + 1, 64, 64, 8), (4, 60, 64, 8), (4, 0, 64, 8), (4, 64, 60, 8), (4, 64, 0, 8),
                 (4, 64, 64, 0), (4, 64, 64, 12), (4, 64, 64, 136), (4, 2 ** 31, 64, 8)):
         assert f(*bad) == 0, bad
+
+
+@pytest.mark.parametrize("T,n", [(1024, 64), (2000, 30), (8192, 64), (8192, 500), (8193, 64), (16384, 100), (16384, 500),
+                                 (65536, 64), (65536, 500), (65536, 512), (65536, 1000), (100000, 700)])
+def test_planned_adapters_of_a_tile(lib, T, n):
+    """The adapters that a tile meets: tokens on adapters at random, sorted within segments of 8192, cut into tiles of
+    128.  The plan has room for one more than the average, and never less than the average."""
+    import numpy as np
+    ids = np.random.default_rng(T + n).integers(0, n, T)
+    met = [len(set(tile)) for s in range(0, T, 8192) for seg in [np.sort(ids[s:s + 8192])]
+           for tile in np.split(seg, range(128, len(seg), 128))]
+    plan = lib.mxg_diag_lora_tile_adapters(T, n)
+    assert np.mean(met) - 0.5 <= plan <= np.mean(met) + 2, (plan, np.mean(met))
+
+
+def test_planned_adapters_of_no_tile(lib):
+    assert lib.mxg_diag_lora_tile_adapters(0, 4) == 0 and lib.mxg_diag_lora_tile_adapters(4, 0) == 0
