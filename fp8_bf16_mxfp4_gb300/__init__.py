@@ -19,6 +19,7 @@ import threading
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 
@@ -695,20 +696,36 @@ def _refuse(**named):
     raise ValueError("arguments do not fit together")
 
 
+def _refuse_grad(name: str):
+    """No gradient goes through these calls: an input that asks for one is refused instead of being detached."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name} is forward only and an input requires grad: detach it, or call under torch.no_grad()")
+
+
+def _written(t: torch.Tensor):
+    """Tell autograd that the caller's tensor was written, as torch's in-place operations do."""
+    if not t.is_inference():
+        increment_version(t)
+
+
 def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, ids: torch.Tensor | None = None,
               weights: torch.Tensor | None = None):
     """Router logits [T, E] (BF16 or FP32) -> (int32 ids [T, top_k], FP32
     weights [T, top_k]): each token's top_k experts, largest logit first and
     equal logits in index order, with their softmax weights -- over the chosen
     experts (``renormalize``) or over all of them.  Experts whose logit is -inf
-    or NaN are never chosen; slots left over have id -1 and weight 0."""
+    or NaN are never chosen; slots left over have id -1 and weight 0.
+    Forward only."""
     if logits.dim() != 2:
         raise ValueError("logits must be [tokens, experts]")
+    if logits.requires_grad or (weights is not None and weights.requires_grad):
+        _refuse_grad("moe_route")
     T, E = logits.shape
     dtype = _OUT.get(logits.dtype)
     dev = logits.device
     if dtype is None or not logits.is_cuda:
         _refuse(logits=(logits, (T, E), _OUT, False))
+    ids_given, weights_given = ids, weights
     if ids is None:
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     elif ids.shape != (T, top_k) or ids.dtype != torch.int32 or not ids.is_contiguous() or not ids.is_cuda:
@@ -722,6 +739,10 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, ids: t
                                  ids.data_ptr(), weights.data_ptr(), _raw_stream(dev))
     if code:
         raise MXGError(code, "moe_route")
+    if ids_given is not None:
+        _written(ids)
+    if weights_given is not None:
+        _written(weights)
     return ids, weights
 
 
@@ -741,9 +762,11 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
     rows, then its I up rows) and ``W2`` [E * H, I] from
     ``mx_quantize_rowwise_packed(..., groups=E)``, both "e2m1" or both "e4m3".
     Activations are rounded to MXFP8 in front of each product, as the grouped
-    GEMMs of the same operands take them.  T * top_k <= 4096."""
+    GEMMs of the same operands take them.  T * top_k <= 4096.  Forward only."""
     if ids.dim() != 2 or x.dim() != 2:
         raise ValueError("x must be [tokens, hidden] and ids [tokens, top_k]")
+    if x.requires_grad or weights.requires_grad or (out is not None and out.requires_grad):
+        _refuse_grad("moe_experts")
     if W13.scale_layout != "packed" or W2.scale_layout != "packed":
         raise ValueError("W13 and W2 need packed scales (mx_quantize_rowwise_packed with groups=experts)")
     T, k = ids.shape
@@ -762,6 +785,7 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
     if not (W13.data.is_cuda and W13.scale.is_cuda and W2.data.is_cuda and W2.scale.is_cuda):
         raise ValueError("libmxg operates on CUDA tensors only")
     lib = _lib.load()
+    given = out
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype, device=dev)
     if out.shape != (T, H) or out.dtype not in _OUT or not out.is_cuda:
@@ -775,6 +799,8 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
                            workspace.numel(), _status_ptr(status, dev), stream)
     if code:
         raise MXGError(code, "moe_experts")
+    if given is not None:
+        _written(out)
     if check:
         check_status(status, dev)
     return out
@@ -796,9 +822,12 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     ``y`` [T, N] BF16 or FP32, the projection's output; ``x`` BF16 [T, K];
     ``A`` BF16 [adapters, rank, K]; ``B`` BF16 [adapters, N, rank]; ``ids``
     int32 [T]; ``scale`` FP32 [adapters] (None: 1).  ``out=y`` updates in
-    place.  rank is a multiple of 8 up to 128."""
+    place.  rank is a multiple of 8 up to 128.  Forward only."""
     if y.dim() != 2 or A.dim() != 3:
         raise ValueError("y must be [tokens, N] and A [adapters, rank, K]")
+    if (y.requires_grad or x.requires_grad or A.requires_grad or B.requires_grad
+            or (scale is not None and scale.requires_grad) or (out is not None and out.requires_grad)):
+        _refuse_grad("lora_add")
     T, N = y.shape
     n, R, K = A.shape
     bf16 = torch.bfloat16
@@ -814,6 +843,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
         _refuse(scale=(scale, (n,), torch.float32, True))
     dev = y.device
     lib = _lib.load()
+    given = out
     if out is None:
         out = torch.empty((T, N), dtype=y.dtype, device=dev)
     elif out.shape != (T, N) or out.dtype != y.dtype or not out.is_cuda:
@@ -827,6 +857,8 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                         _status_ptr(status, dev), stream)
     if code:
         raise MXGError(code, "lora_add")
+    if given is not None:
+        _written(out)
     if check:
         check_status(status, dev)
     return out
