@@ -665,6 +665,8 @@ def _scratch(nbytes: int, dev, stream: int) -> torch.Tensor:
 
 def _status_ptr(status, dev) -> int:
     if status is not None:
+        if status.dtype != torch.int32:
+            raise ValueError("status must be int32")
         return status.data_ptr()
     st = _status.get(dev.index)
     return (st if st is not None else status_tensor(dev)).data_ptr()
@@ -751,6 +753,22 @@ def moe_experts_workspace_size(tokens: int, top_k: int, experts: int, hidden: in
     return int(_lib.load().moe_experts_workspace_size(tokens, top_k, experts, hidden, inter))
 
 
+def _expert_weights(w: MXOperand) -> _lib.MxOperandC:
+    """The C form of one expert weight matrix: rows of codes, and a packed byte
+    for every 32 weights (rows and columns are multiples of 128)."""
+    data, scale, cols = w.data, w.scale, w.cols
+    rows, ld = data.shape[0], data.stride(0)
+    if w.scale_layout != "packed":
+        raise ValueError("W13 and W2 need packed scales (mx_quantize_rowwise_packed with groups=experts)")
+    if data.shape[1:] != (_codes_cols(w.elem, cols),) or data.stride(-1) != 1:
+        raise ValueError("codes of W13 and W2 must be rows of their columns, contiguous in a row")
+    if scale.numel() < rows * (cols // 32) or not scale.is_contiguous():
+        raise ValueError("packed scales must be contiguous and as many as the weights need")
+    if not (data.is_cuda and scale.is_cuda):
+        raise ValueError("libmxg operates on CUDA tensors only")
+    return _lib.MxOperandC(data.data_ptr(), scale.data_ptr(), rows, cols, ld, cols // 32, ELEM[w.elem], 1)
+
+
 def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: MXOperand, W2: MXOperand,
                 out_dtype=torch.bfloat16, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                 status: torch.Tensor | None = None, check: bool = False) -> torch.Tensor:
@@ -767,23 +785,17 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
         raise ValueError("x must be [tokens, hidden] and ids [tokens, top_k]")
     if x.requires_grad or weights.requires_grad or (out is not None and out.requires_grad):
         _refuse_grad("moe_experts")
-    if W13.scale_layout != "packed" or W2.scale_layout != "packed":
-        raise ValueError("W13 and W2 need packed scales (mx_quantize_rowwise_packed with groups=experts)")
     T, k = ids.shape
     H, I, dev = W13.cols, W2.cols, x.device
-    E = W2.rows // H
     if (x.shape != (T, H) or x.dtype != torch.bfloat16 or weights.shape != (T, k) or ids.dtype != torch.int32
             or weights.dtype != torch.float32 or not ids.is_contiguous() or not weights.is_contiguous()
             or not (x.is_cuda and ids.is_cuda and weights.is_cuda)):
         _refuse(x=(x, (T, H), torch.bfloat16, False), ids=(ids, (T, k), torch.int32, True),
                 weights=(weights, (T, k), torch.float32, True))
-    if W2.rows != E * H or W13.rows != E * 2 * I:
+    a, b = _expert_weights(W13), _expert_weights(W2)
+    E = b.rows // H
+    if b.rows != E * H or a.rows != E * 2 * I:
         raise ValueError("W13 must be [E * 2I, H] and W2 [E * H, I]")
-    # a packed byte for every 32 weights (rows and columns are multiples of 128)
-    if W13.scale.numel() < W13.rows * (H // 32) or W2.scale.numel() < W2.rows * (I // 32):
-        raise ValueError("packed scales are shorter than the weights need")
-    if not (W13.data.is_cuda and W13.scale.is_cuda and W2.data.is_cuda and W2.scale.is_cuda):
-        raise ValueError("libmxg operates on CUDA tensors only")
     lib = _lib.load()
     given = out
     if out is None:
@@ -793,7 +805,8 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W13: 
     stream = _raw_stream(dev)
     if workspace is None:
         workspace = _scratch(moe_experts_workspace_size(T, k, E, H, I), dev, stream)
-    a, b = W13.c(), W2.c()
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8")
     code = lib.moe_experts(x.data_ptr(), T, _row_ld(x, H), ids.data_ptr(), weights.data_ptr(), k, E, ctypes.byref(a),
                            ctypes.byref(b), out.data_ptr(), _row_ld(out, H), _OUT[out.dtype], workspace.data_ptr(),
                            workspace.numel(), _status_ptr(status, dev), stream)
@@ -851,6 +864,8 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     stream = _raw_stream(dev)
     if workspace is None:
         workspace = _scratch(lora_add_workspace_size(T, K, R), dev, stream)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8")
     code = lib.lora_add(y.data_ptr(), _row_ld(y, N), x.data_ptr(), _row_ld(x, K), A.data_ptr(), B.data_ptr(),
                         ids.data_ptr(), None if scale is None else scale.data_ptr(), T, N, K, R, n, dtype,
                         out.data_ptr(), _row_ld(out, N), workspace.data_ptr(), workspace.numel(),
