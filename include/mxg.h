@@ -495,7 +495,9 @@ mxg_status moe_route(const void* logits, int64_t tokens, int32_t experts, int64_
  * quotient by 1 + exp(-g) is within a few fp32 units for every g (it is taken by
  * exp(-|g|), so that it does not vanish where exp(-g) overflows).  A slot with a
  * negative id is empty; a token without slots gives zeros.  The result depends
- * on the inputs only, not on timing.
+ * on the inputs only, not on timing.  NaN stays NaN, and an infinity of x or of
+ * the product in front of hq becomes 448 * 2^120 (MXFP8 has none; as in the
+ * quantizers); neither reaches another token.
  *   x       : BF16 [tokens, hidden], row stride ld_x (% 8), 16-byte aligned
  *   ids, weights : [tokens, top_k] contiguous (as from moe_route)
  *   W13     : [experts * 2 * inter, hidden], W2: [experts * hidden, inter];

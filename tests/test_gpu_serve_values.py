@@ -152,3 +152,104 @@ def test_experts_gates_far_below_zero(fmt, up):
                              out_dtype=torch.float32, check=True)
     assert (want != 0).all()
     assert (np.abs(f64(got) - want) <= off + serve.U * np.abs(want)).all()
+
+
+GRID = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def expert_layer(T, E, k, H, I, fmt, seed, scale=1.0 / 16):
+    """(x, ids, weights, W13, W2) as numpy values that the formats hold exactly, and as the call's arguments."""
+    rng = np.random.default_rng(seed)
+    pick = lambda v, *s: rng.choice(v, s) * rng.choice([-1.0, 1.0], s)  # noqa: E731
+    x, w13, w2 = pick(GRID, T, H), pick(GRID, E * 2 * I, H) * scale, pick(GRID, E * H, I) * scale
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    wts = rng.random((T, k)).astype(np.float32) + 0.25
+    ops = operand(w13, fmt, E), operand(w2, fmt, E)
+    return x, ids, wts, w13, w2, ops
+
+
+def run_experts(x, ids, wts, ops, dtype=torch.float32):
+    return _mxg().moe_experts(torch.from_numpy(x).to(torch.bfloat16).to(DEV), torch.from_numpy(ids).to(DEV),
+                              torch.from_numpy(wts).to(DEV), *ops, out_dtype=dtype, check=True)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("T,E,k,H,I", [(5, 2, 2, 256, 128), (70, 3, 2, 384, 256), (200, 2, 1, 128, 256), (13, 3, 2, 4096, 512),
+                                       (9, 2, 1, 384, 4096)])
+def test_experts_nan_stays_with_its_token(T, E, k, H, I, fmt):
+    """NaN in a token (all of it, or one value) or in a routing weight reaches no other row: not through tiles that the
+    token shares, nor through what it leaves in the stage buffers, partial sums or the workspace."""
+    x, ids, wts, _, _, ops = expert_layer(T, E, k, H, I, fmt, seed=T)
+    ids[T - 1] = -1
+    want = run_experts(x, ids, wts, ops)
+    assert bool(want.isfinite().all()) and not want[T - 1].any()
+    bad = sorted({0, T // 3, T // 2, T - 2})
+    for t in bad:
+        x[t] = np.nan
+    x[bad[-1]] = 0.5
+    x[bad[-1], H - 1] = np.nan
+    x[T - 1] = np.nan  # no slot: still zeros
+    others = [t for t in range(T) if t not in bad]
+    for _ in range(2):
+        got = run_experts(x, ids, wts, ops)
+        assert bool(got[bad].isnan().all()) and torch.equal(got[others], want[others])
+    wts[1, 0] = np.nan
+    got = run_experts(x, ids, wts, ops)
+    others = [t for t in others if t != 1]
+    assert bool(got[1].isnan().all()) and torch.equal(got[others], want[others])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_experts_infinities_saturate(fmt, dtype):
+    """An infinite x, and a product silu(g) * u past the FP32 range, become 448 * 2^120 in MXFP8, as the quantizers
+    have it; the other tokens do not change."""
+    T, E, k, H, I = 12, 2, 2, 384, 256
+    x, ids, wts, w13, w2, ops = expert_layer(T, E, k, H, I, fmt, seed=3, scale=2.0 ** -16)
+    want = run_experts(x, ids, wts, ops, dtype)
+    hit = {2: (100, 1.0), 7: (383, -1.0)}
+    for t, (c, s) in hit.items():
+        x[t, c] = s * np.inf
+    got = run_experts(x, ids, wts, ops, dtype)
+    others = [t for t in range(T) if t not in hit]
+    assert torch.equal(got[others], want[others])
+    q = _mxg().mx_quantize_rowwise(torch.from_numpy(x).to(torch.bfloat16).to(DEV), "e4m3")
+    top = 448 * 2.0 ** 120
+    for t, (c, s) in hit.items():
+        codes, sc = q.data[t, c // 32 * 32: c // 32 * 32 + 32].cpu().numpy(), int(q.scale[t, c // 32])
+        assert sc == 247 and codes[c % 32] == (0x7E if s > 0 else 0xFE) and not (np.delete(codes, c % 32) & 0x7F).any()
+        xq = x[t].copy()
+        xq[c // 32 * 32: c // 32 * 32 + 32] = 0
+        xq[c] = s * top
+        row, bound = np.zeros(H), np.zeros(H)
+        for j, e in enumerate(ids[t]):
+            gu = w13[e * 2 * I:(e + 1) * 2 * I] @ xq
+            assert np.abs(gu).max() < 2.0 ** 126
+            with np.errstate(over="ignore"):
+                h = gu[:I] / (1.0 + np.exp(-gu[:I])) * gu[I:]
+            inf = np.abs(h) > np.finfo(np.float32).max
+            assert inf.reshape(-1, 32).any(1).all() and (np.abs(h[~inf]) < 2.0 ** 110).all()  # the rest rounds to 0
+            hq = np.where(inf, np.sign(h) * top, 0.0)
+            W = w2[e * H:(e + 1) * H]
+            row += wts[t, j] * (W @ hq)
+            bound += wts[t, j] * (I + 8) * serve.U * (np.abs(W) @ np.abs(hq))
+        tol = bound + np.abs(row) * (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -22)
+        assert np.isfinite(row).all() and (np.abs(f64(got[t]) - row) <= tol).all()
+
+
+# --------------------------------------------------------------------------- routing
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k", [(500, 2, 1), (500, 5, 2), (400, 32, 8), (300, 161, 6), (200, 512, 32)])
+def test_route_weights_within_their_own_terms(T, E, k, renorm):
+    """The weights' error by the terms that are summed: k or E additions, exp (2 units), its argument's rounding
+    (a unit of the difference of logits, in numerator and sum) and the division."""
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randn(T, E, generator=g)
+    ids, w = _mxg().moe_route(logits.to(DEV), k, renormalize=renorm)
+    want_ids, want = serve.route(f64(logits), k, renorm)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    spread = float((logits.max(1).values - logits.min(1).values).max())
+    rtol = ((k if renorm else E) + 6 + 2 * spread) * 2.0 ** -24
+    np.testing.assert_allclose(f64(w), want, rtol=rtol, atol=0)
