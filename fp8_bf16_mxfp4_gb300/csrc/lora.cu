@@ -1003,9 +1003,10 @@ int64_t lora_tile_adapters(int64_t T, int64_t n) {
   return n < tiles ? 1 : std::min<int64_t>({kTile, n, 2 + n / tiles});
 }
 
+// For every N: the per-token form's partial sums only where some N takes it.
 size_t lora_workspace_bytes(int64_t T, int64_t K, int R) {
   T = std::max<int64_t>(T, 1);
-  const int64_t split = std::max<int64_t>(tile_splits(T, K), T <= 65535 ? (K + kTokK - 1) / kTokK : 0);
+  const int64_t split = std::max<int64_t>(tile_splits(T, K), lora_per_token(T, 8, K, R) ? (K + kTokK - 1) / kTokK : 0);
   return (size_t)(split * T * R) * sizeof(float) + (size_t)T * sizeof(int32_t);  // u, order
 }
 

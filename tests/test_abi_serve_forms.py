@@ -42,3 +42,15 @@ def test_planned_adapters_of_a_tile(lib, T, n):
 
 def test_planned_adapters_of_no_tile(lib):
     assert lib.mxg_diag_lora_tile_adapters(0, 4) == 0 and lib.mxg_diag_lora_tile_adapters(4, 0) == 0
+
+
+@pytest.mark.parametrize("R", [8, 64, 128])
+@pytest.mark.parametrize("K", [8, 1000, 8192, 65536])
+@pytest.mark.parametrize("T", [1, 100, 3000, 8192, 32768, 65535, 65536, 200000])
+def test_lora_workspace_is_what_a_form_uses(lib, T, K, R):
+    """Partial sums of A x: one per 1024 elements of K where the per-token form may run (for some N), at most 16 in the
+    tiles; an order of the tokens beside them."""
+    size = lib.lora_add_workspace_size(T, K, R)
+    token = -(-K // 1024) if lib.lora_add_form(T, 8, K, R) == 1 else 0
+    least, most = max(token, 1), max(token, min(16, max(1, -(-K // 64) // 8)))
+    assert least * T * R * 4 + T * 4 <= size <= most * T * R * 4 + T * 4
