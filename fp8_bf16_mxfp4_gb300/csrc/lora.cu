@@ -8,8 +8,8 @@
 // Few tokens: a CTA works for one token, reads the token's adapter rows 16 bytes
 // a lane and multiplies in fp32.  Tokens that share an adapter read it again,
 // from L2; every load of a CTA is in flight at once.  64 tokens of 64 adapters
-// (K = N = 7168, rank 16): 6.2 us, two thirds of it the two launches; one token
-// 3.7 us.
+// (K = N = 7168, rank 16): 7.8 us from DRAM, 6.2 from L2, about half of it the two
+// launches; one token 3.8 us.
 //
 // Many tokens: the tokens are ordered by adapter (a third kernel), and a CTA
 // runs a tile of 128 of them against the adapters that occur in it on the
@@ -17,12 +17,15 @@
 // wanted cost little.  A row of the result is selected, never masked by a
 // product: an adapter's infinities or NaN reach its own tokens only.  u keeps its
 // fp32 accuracy as a sum of two BF16 terms (2^-17; BF16 output) or three (2^-25;
-// FP32 output).
-//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 237 us, 4.6 TB/s
-//   of the 1.09 GB it has to move (160 us at the copy rate).  Expand is about
+// FP32 output); a product that comes out infinite or NaN is done again in fp32.
+//   8192 tokens, 8192 x 28672, rank 32, prompts of 1024 tokens: 206 us, 5.4 TB/s
+//   of the 1.11 GB it has to move (164 us at the copy rate).  Expand is about
 //   three quarters of that; reads and writes of y share DRAM at 67 to 80 %.
 //   Left in the batch's order the same takes about 5 us less, but 1024 tokens of 64 mixed
-//   adapters (4096 x 4096, rank 16) take 200 us instead of 32.
+//   adapters (4096 x 4096, rank 16) take 200 us instead of 37.
+//   Tokens without an adapter are copied by the last tiles of a segment, a load
+//   behind each store: the first such tile lengthens a call by 30 to 120 us (206 ->
+//   318 here); in place there is nothing to copy.
 //   mma.sync runs at 1/16 of the tcgen05 rate here: a form on it took 264 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -927,6 +930,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 //   4096 x 4096, rank 64, 16 adapters: 64 tokens (67 MB) 21 / 20, 128 (134 MB)
 //   26 / 21, 256 (268 MB) 49 / 22
 //   2048 x 8192, rank 32, 32 adapters: 256 tokens (168 MB) 26 / 29, 512 47 / 31
+// The rule knows bytes alone: where few adapters or high ranks bring the tiles
+// ahead below it, it leaves 1 to 5 us.
 constexpr double kTokenBytes = 150e6;
 constexpr int kLoraSms = 152;
 

@@ -37,15 +37,15 @@
 // kernel's has left its SM), and only their activation and epilogue warps wait
 // for its results.
 //
-// Bound: HBM with E4M3 weights (4 tokens, top 2 of 8 experts, 4096 x 14336: 136 us
+// Bound: HBM with E4M3 weights (4 tokens, top 2 of 8 experts, 4096 x 14336: 137 us
 // for 0.85 GB of weights, 4 to 5 experts used, 6.2 TB/s).  E2M1 tiles cannot use the TMA for
 // the tensor core's layout at full rate (it moves a row of up to 128 bytes in
 // 2.9 ns an SM, so 64-byte rows stop at 3.3 TB/s); 8-byte copies out of L2 bring
 // them at about 20 bytes a clock an SM: 13 tokens, top 8 of 32 experts,
-// 7168 x 2048: 130 us, 5.6 TB/s; 128 tokens 152 us, joins and epilogues growing
-// with the tokens; 1 token 50 us for 0.19 GB, of which the four kernels' plans
+// 7168 x 2048: 133 us, 5.5 TB/s; 128 tokens 155 us, joins and epilogues growing
+// with the tokens; 1 token 52 us for 0.19 GB, of which the four kernels' plans
 // and tails are a third.  A small layer (33 tokens, top 3 of 12, 1152 x 640,
-// 27 MB) takes 15.5 us, nearly all of it latency.
+// 27 MB) takes 17 us, nearly all of it latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
