@@ -34,6 +34,8 @@ __all__ = [
     "bw_grouped_gemm_wgrad", "bw_quantize_1x128_pow2", "bw_quantize_128x128_pow2",
     "bw_quantize_colwise_padded_pow2", "bw_quantize_dual_padded",
     "moe_route", "moe_experts", "moe_experts_workspace_size", "lora_add", "lora_add_workspace_size",
+    "moe_sort", "moe_sort_workspace_size", "moe_gather", "moe_combine", "moe_combine_backward", "moe_route_backward",
+    "Int8Operand", "int8_quantize_rowwise", "int8_grouped_gemm_fwd", "int8_gemm_dense", "int8_gemm_workspace_size",
 ]
 
 ELEM = {"e2m1": 1, "e4m3": 2}
@@ -877,3 +879,335 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     if check:
         check_status(status, dev)
     return out
+
+
+# ----------------------------------------------------------------------------- tokens to the experts and back
+
+
+@functools.lru_cache(maxsize=1024)
+def moe_sort_workspace_size(tokens: int, top_k: int, experts: int) -> int:
+    return int(_lib.load().moe_sort_workspace_size(tokens, top_k, experts))
+
+
+def _given_workspace(workspace: torch.Tensor):
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8")
+
+
+def moe_sort(ids: torch.Tensor, experts: int, m_splits: torch.Tensor | None = None, rows: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, check: bool = False):
+    """Expert ids [T, top_k] (int32, as from ``moe_route``) -> (m_splits int32
+    [experts], rows int32 [T, top_k]): every slot's row in expert order, slots of
+    one expert in the order of their index.  An empty slot (negative id) owns a
+    row r behind all others and has the entry -1 - r; the last expert's split
+    counts these rows (zeros in the calls below), so that the splits add up to
+    T * top_k, as the grouped GEMMs and quantizers ask."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, top_k]")
+    T, k = ids.shape
+    i32, dev = torch.int32, ids.device
+    if ids.dtype != i32 or not ids.is_contiguous() or not ids.is_cuda:
+        _refuse(ids=(ids, (T, k), i32, True))
+    m_given, r_given = m_splits, rows
+    if m_splits is None:
+        m_splits = torch.empty((experts,), dtype=i32, device=dev)
+    elif m_splits.shape != (experts,) or m_splits.dtype != i32 or not m_splits.is_contiguous() or not m_splits.is_cuda:
+        _refuse(m_splits=(m_splits, (experts,), i32, True))
+    if rows is None:
+        rows = torch.empty((T, k), dtype=i32, device=dev)
+    elif rows.shape != (T, k) or rows.dtype != i32 or not rows.is_contiguous() or not rows.is_cuda:
+        _refuse(rows=(rows, (T, k), i32, True))
+    stream = _raw_stream(dev)
+    if workspace is None:
+        workspace = _scratch(moe_sort_workspace_size(T, k, experts), dev, stream)
+    else:
+        _given_workspace(workspace)
+    code = _lib.load().moe_sort(ids.data_ptr(), T, k, experts, m_splits.data_ptr(), rows.data_ptr(), workspace.data_ptr(),
+                                workspace.numel(), _status_ptr(status, dev), stream)
+    if code:
+        raise MXGError(code, "moe_sort")
+    if m_given is not None:
+        _written(m_splits)
+    if r_given is not None:
+        _written(rows)
+    if check:
+        check_status(status, dev)
+    return m_splits, rows
+
+
+def _slot_rows(rows: torch.Tensor):
+    if rows.dim() != 2 or rows.dtype != torch.int32 or not rows.is_contiguous() or not rows.is_cuda:
+        raise ValueError("rows must be contiguous int32 [tokens, top_k] on the GPU (from moe_sort)")
+    return rows.shape
+
+
+def _slot_values(name: str, t: torch.Tensor, shape):
+    """A contiguous FP32 value per slot."""
+    if t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda:
+        _refuse(**{name: (t, shape, torch.float32, True)})
+
+
+def _given_rows(name: str, t: torch.Tensor | None, shape, dtype, dev) -> torch.Tensor:
+    """The caller's output matrix, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        _refuse(**{name: (t, shape, dtype, False)})
+    return t
+
+
+def moe_gather(x: torch.Tensor, rows: torch.Tensor, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+               check: bool = False) -> torch.Tensor:
+    """x [T, H] (BF16 or FP32) -> [T * top_k, H] in expert order: out[rows[t, j]] =
+    x[t], zeros in the rows of empty slots.  ``rows`` from ``moe_sort``.  The
+    gradient is ``moe_combine(dout, rows)``.  H is a multiple of 8 (FP32: 4)."""
+    T, k = _slot_rows(rows)
+    dtype = _OUT.get(x.dtype)
+    if x.dim() != 2 or x.shape[0] != T or dtype is None or not x.is_cuda:
+        _refuse(x=(x, (T, x.shape[-1]), _OUT, False))
+    if x.requires_grad or (out is not None and out.requires_grad):
+        _refuse_grad("moe_gather")
+    H, dev, given = x.shape[1], x.device, out
+    out = _given_rows("out", out, (T * k, H), x.dtype, dev)
+    code = _lib.load().moe_gather(x.data_ptr(), _row_ld(x, H), rows.data_ptr(), T, k, H, dtype, out.data_ptr(),
+                                  _row_ld(out, H), _status_ptr(status, dev), _raw_stream(dev))
+    if code:
+        raise MXGError(code, "moe_gather")
+    if given is not None:
+        _written(out)
+    if check:
+        check_status(status, dev)
+    return out
+
+
+def moe_combine(y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                status: torch.Tensor | None = None, check: bool = False) -> torch.Tensor:
+    """Rows in expert order back to their tokens: out[t] = sum_j weights[t, j] *
+    y[rows[t, j]] (``weights`` None: 1), empty slots adding nothing.  ``y`` BF16 or
+    FP32 [rows, H]; ``weights`` FP32 [T, top_k] as from ``moe_route``.  Sums in FP32,
+    in the order of the slots, rounded once."""
+    T, k = _slot_rows(rows)
+    dtype = _OUT.get(y.dtype)
+    if y.dim() != 2 or dtype is None or not y.is_cuda:
+        _refuse(y=(y, (T * k, y.shape[-1]), _OUT, False))
+    if y.requires_grad or (weights is not None and weights.requires_grad) or (out is not None and out.requires_grad):
+        _refuse_grad("moe_combine")
+    if weights is not None:
+        _slot_values("weights", weights, (T, k))
+    n, H = y.shape
+    dev, given = y.device, out
+    out = _given_rows("out", out, (T, H), y.dtype, dev)
+    code = _lib.load().moe_combine(y.data_ptr(), _row_ld(y, H), n, rows.data_ptr(),
+                                   None if weights is None else weights.data_ptr(), T, k, H, dtype, out.data_ptr(),
+                                   _row_ld(out, H), _status_ptr(status, dev), _raw_stream(dev))
+    if code:
+        raise MXGError(code, "moe_combine")
+    if given is not None:
+        _written(out)
+    if check:
+        check_status(status, dev)
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
+                         dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None, check: bool = False):
+    """Gradients of ``moe_combine(y, rows, weights)`` -> (dy, dweights):
+    dy[rows[t, j]] = weights[t, j] * dout[t] (zeros in the rows of empty slots) and
+    dweights[t, j] = <dout[t], y[rows[t, j]]> (0 for an empty slot), FP32 sums.
+    ``dout`` [T, H] and ``y`` [T * top_k, H] of one type.  ``dy=y`` writes over y."""
+    T, k = _slot_rows(rows)
+    dtype = _OUT.get(y.dtype)
+    if y.dim() != 2 or y.shape[0] != T * k or dtype is None or not y.is_cuda:
+        _refuse(y=(y, (T * k, y.shape[-1]), _OUT, False))
+    H, dev = y.shape[1], y.device
+    if dout.shape != (T, H) or dout.dtype != y.dtype or not dout.is_cuda:
+        _refuse(dout=(dout, (T, H), y.dtype, False))
+    _slot_values("weights", weights, (T, k))
+    if (dout.requires_grad or y.requires_grad or weights.requires_grad or (dy is not None and dy.requires_grad)
+            or (dweights is not None and dweights.requires_grad)):
+        _refuse_grad("moe_combine_backward")
+    dy_given, dw_given = dy, dweights
+    dy = _given_rows("dy", dy, (T * k, H), y.dtype, dev)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        _slot_values("dweights", dweights, (T, k))
+    code = _lib.load().moe_combine_backward(dout.data_ptr(), _row_ld(dout, H), y.data_ptr(), _row_ld(y, H),
+                                            rows.data_ptr(), weights.data_ptr(), T, k, H, dtype, dy.data_ptr(),
+                                            _row_ld(dy, H), dweights.data_ptr(), _status_ptr(status, dev),
+                                            _raw_stream(dev))
+    if code:
+        raise MXGError(code, "moe_combine_backward")
+    if dy_given is not None:
+        _written(dy)
+    if dw_given is not None:
+        _written(dweights)
+    if check:
+        check_status(status, dev)
+    return dy, dweights
+
+
+def moe_route_backward(dweights: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, logits: torch.Tensor,
+                       renormalize: bool = True, dlogits: torch.Tensor | None = None,
+                       status: torch.Tensor | None = None, check: bool = False) -> torch.Tensor:
+    """Gradient of ``moe_route``'s weights for its logits: with s = sum_j weights_j
+    dweights_j over a token's slots, dlogits[id_j] = weights_j (dweights_j - s) and
+    zeros elsewhere (``renormalize``), or [e = id_j] weights_j dweights_j - p_e s with
+    p = softmax(logits).  ``ids`` and ``weights`` as ``moe_route`` returned them for
+    these ``logits`` [T, E] and this ``renormalize``; the result has the logits' type."""
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError("logits must be [tokens, experts] and ids [tokens, top_k]")
+    T, E = logits.shape
+    k, dev = ids.shape[1], logits.device
+    dtype = _OUT.get(logits.dtype)
+    if (dtype is None or not logits.is_cuda or ids.shape[0] != T or ids.dtype != torch.int32 or not ids.is_contiguous()
+            or not ids.is_cuda):
+        _refuse(logits=(logits, (T, E), _OUT, False), ids=(ids, (T, k), torch.int32, True))
+    _slot_values("dweights", dweights, (T, k))
+    _slot_values("weights", weights, (T, k))
+    if (dweights.requires_grad or weights.requires_grad or logits.requires_grad
+            or (dlogits is not None and dlogits.requires_grad)):
+        _refuse_grad("moe_route_backward")
+    given = dlogits
+    dlogits = _given_rows("dlogits", dlogits, (T, E), logits.dtype, dev)
+    code = _lib.load().moe_route_backward(dweights.data_ptr(), ids.data_ptr(), weights.data_ptr(), logits.data_ptr(),
+                                          _row_ld(logits, E), T, E, k, renormalize, dtype, dlogits.data_ptr(),
+                                          _row_ld(dlogits, E), _status_ptr(status, dev), _raw_stream(dev))
+    if code:
+        raise MXGError(code, "moe_route_backward")
+    if given is not None:
+        _written(dlogits)
+    if check:
+        check_status(status, dev)
+    return dlogits
+
+
+# ----------------------------------------------------------------------------- 8-bit integers
+
+_CODES = {"int8": torch.int8, "f16": torch.float16}
+_CODE_KIND = {torch.int8: 1, torch.float16: 2}
+
+
+@dataclass
+class Int8Operand:
+    """A K-major operand of 8-bit integers with one FP32 scale per row (token or
+    channel): codes [rows, cols] as int8, or as FP16 tensors of the same integers
+    (activations, the form the tensor core takes)."""
+    data: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def rows(self) -> int:
+        return self.data.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.data.shape[1]
+
+    def c(self) -> _lib.Int8OperandC:
+        data, scale = self.data, self.scale
+        kind = _CODE_KIND.get(data.dtype)
+        if data.dim() != 2 or kind is None or not data.is_cuda:
+            _refuse(codes=(data, data.shape[:2], _CODE_KIND, False))
+        rows, cols = data.shape
+        if scale.shape != (rows,) or scale.dtype != torch.float32 or not scale.is_contiguous() or not scale.is_cuda:
+            _refuse(scale=(scale, (rows,), torch.float32, True))
+        if rows > 0 and cols > 1 and data.stride(1) != 1:
+            raise ValueError("codes of a row must be contiguous")
+        ld = (data.stride(0) if rows > 1 else (cols + 15) & ~15) * kind
+        return _lib.Int8OperandC(data.data_ptr(), scale.data_ptr(), rows, cols, ld, kind, 0)
+
+
+def int8_quantize_rowwise(x: torch.Tensor, rows: torch.Tensor | None = None, codes: str = "int8",
+                          q: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None, check: bool = False) -> Int8Operand:
+    """BF16 [T, cols] -> 8-bit integers with a scale per row: scale = max(max |x|,
+    2^-100) / 127, codes to the nearest integer.  For activations, and for weights
+    per channel.  With ``rows`` (from ``moe_sort``) the rows come out in expert order
+    [T * top_k, cols], as from quantizing ``moe_gather(x, rows)``, from one read of
+    x.  ``codes="f16"`` writes the integers as FP16 values, which the GEMMs take
+    without widening them first.  A row with a NaN or an infinity gets the scale NaN."""
+    if codes not in _CODES:
+        raise ValueError(f"unknown codes {codes!r} (int8 or f16)")
+    if x.dim() != 2 or x.dtype != torch.bfloat16 or not x.is_cuda:
+        _refuse(x=(x, (x.shape[0], x.shape[-1]), torch.bfloat16, False))
+    if x.requires_grad or (scale is not None and scale.requires_grad) or (q is not None and q.requires_grad):
+        _refuse_grad("int8_quantize_rowwise")
+    T, K = x.shape
+    k, n = 1, T
+    if rows is not None:
+        t, k = _slot_rows(rows)
+        if t != T:
+            raise ValueError("rows must have a row for every token of x")
+        n = T * k
+    dev, dtype = x.device, _CODES[codes]
+    q_given, s_given = q, scale
+    q = _given_rows("q", q, (n, K), dtype, dev)
+    if scale is None:
+        scale = torch.empty((n,), dtype=torch.float32, device=dev)
+    else:
+        _slot_values("scale", scale, (n,))
+    op = Int8Operand(q, scale)
+    c = op.c()
+    code = _lib.load().int8_quantize_rowwise(x.data_ptr(), _row_ld(x, K), None if rows is None else rows.data_ptr(), T, k,
+                                             K, c.codes, c.data, c.ld, c.scale, _status_ptr(status, dev),
+                                             _raw_stream(dev))
+    if code:
+        raise MXGError(code, "int8_quantize_rowwise")
+    if q_given is not None:
+        _written(q)
+    if s_given is not None:
+        _written(scale)
+    if check:
+        check_status(status, dev)
+    return op
+
+
+@functools.lru_cache(maxsize=1024)
+def int8_gemm_workspace_size(G: int, S: int, N: int, K: int, codes: str = "int8") -> int:
+    return int(_lib.load().int8_gemm_workspace_size(G, S, N, K, _CODE_KIND[_CODES[codes]]))
+
+
+def _int8_gemm(name, A, W, m_splits, G, N, out_dtype, out, workspace, status, check):
+    a, w = A.c(), W.c()
+    if A.scale.requires_grad or W.scale.requires_grad or A.data.requires_grad or (out is not None and out.requires_grad):
+        _refuse_grad(name)
+    dev, lib, given = A.data.device, _lib.load(), out
+    if out is None:
+        out = torch.empty((a.rows, N), dtype=out_dtype, device=dev)
+    if out.shape != (a.rows, N) or out.dtype not in _OUT or not out.is_cuda:
+        _refuse(out=(out, (a.rows, N), _OUT, False))
+    stream = _raw_stream(dev)
+    if workspace is None:
+        workspace = _scratch(int8_gemm_workspace_size(G, a.rows, N, a.cols, "int8" if a.codes == 1 else "f16"), dev, stream)
+    else:
+        _given_workspace(workspace)
+    splits = () if m_splits is None else (m_splits.data_ptr(), G, N)
+    code = getattr(lib, name)(ctypes.byref(a), ctypes.byref(w), *splits, out.data_ptr(), _row_ld(out, N), _OUT[out.dtype],
+                              workspace.data_ptr(), workspace.numel(), _status_ptr(status, dev), stream)
+    if code:
+        raise MXGError(code, name)
+    if given is not None:
+        _written(out)
+    if check:
+        check_status(status, dev)
+    return out
+
+
+def int8_grouped_gemm_fwd(A: Int8Operand, W: Int8Operand, m_splits: torch.Tensor, N: int, out_dtype=torch.bfloat16,
+                          out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None, check: bool = False) -> torch.Tensor:
+    """Y[off_g+i, :] = A[off_g+i, :] @ W[g*N:(g+1)*N, :]^T for every expert g, both
+    operands standing for scale * codes; ``W`` int8 [G * N, K].  Codes' products are
+    exact and their sums in FP32.  Forward only."""
+    if m_splits.dim() != 1 or m_splits.dtype != torch.int32 or not m_splits.is_contiguous() or not m_splits.is_cuda:
+        _refuse(m_splits=(m_splits, (m_splits.numel(),), torch.int32, True))
+    return _int8_gemm("int8_grouped_gemm_fwd", A, W, m_splits, m_splits.numel(), N, out_dtype, out, workspace, status, check)
+
+
+def int8_gemm_dense(A: Int8Operand, B: Int8Operand, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                    check: bool = False) -> torch.Tensor:
+    """C[M, N] = A[M, K] @ B[N, K]^T of two 8-bit integer operands (``B`` int8)."""
+    return _int8_gemm("int8_gemm_dense", A, B, None, 1, B.rows, out_dtype, out, workspace, status, check)

@@ -48,6 +48,19 @@ class BwOperandC(ctypes.Structure):
     ]
 
 
+class Int8OperandC(ctypes.Structure):
+    """Mirror of ``mxg_i8_operand``."""
+    _fields_ = [
+        ("data", c_vp),
+        ("scale", c_vp),
+        ("rows", c_i64),
+        ("cols", c_i64),
+        ("ld", c_i64),
+        ("codes", c_i32),
+        ("reserved", c_i32),
+    ]
+
+
 # name -> (restype, argtypes); exactly the functions declared in include/mxg.h
 SIGNATURES = {
     "mx_quantize_rowwise": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp]),
@@ -119,6 +132,24 @@ SIGNATURES = {
     "lora_add": (
         c_i32, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i32, c_i32, c_i32, c_vp,
                 c_i64, c_vp, c_size, c_vp, c_vp]),
+    "moe_sort_workspace_size": (c_size, [c_i64, c_i32, c_i32]),
+    "moe_sort": (c_i32, [c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_size, c_vp, c_vp]),
+    "moe_gather": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp, c_vp]),
+    "moe_combine": (
+        c_i32, [c_vp, c_i64, c_i64, c_vp, c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp, c_vp]),
+    "moe_combine_backward": (
+        c_i32, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "moe_route_backward": (
+        c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp]),
+    "int8_quantize_rowwise": (
+        c_i32, [c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "int8_gemm_workspace_size": (c_size, [c_i32, c_i64, c_i64, c_i64, c_i32]),
+    "int8_grouped_gemm_fwd": (
+        c_i32, [ctypes.POINTER(Int8OperandC), ctypes.POINTER(Int8OperandC), c_vp, c_i32, c_i64, c_vp, c_i64, c_i32,
+                c_vp, c_size, c_vp, c_vp]),
+    "int8_gemm_dense": (
+        c_i32, [ctypes.POINTER(Int8OperandC), ctypes.POINTER(Int8OperandC), c_vp, c_i64, c_i32, c_vp, c_size, c_vp,
+                c_vp]),
     "mxg_check_status": (c_i32, [c_vp, c_vp]),
     "mxg_status_string": (ctypes.c_char_p, [c_i32]),
     "mxg_set_wait_timeout_ns": (None, [c_u64]),
@@ -127,6 +158,7 @@ SIGNATURES = {
     "mxg_get_gemm_cta_group": (c_i32, []),
     "mxg_diag_bounded_wait": (c_i32, [c_vp, c_u64, c_vp]),
     "mxg_diag_lora_tile_adapters": (c_i32, [c_i64, c_i32]),
+    "mxg_diag_int8_tile_tokens": (c_i32, [c_i32, c_i64, c_i64, c_i64]),
     "mxg_version": (c_i32, []),
 }
 

@@ -189,7 +189,7 @@ const char* mxg_status_string(mxg_status s) {
     case MXG_ERR_TIMEOUT: return "a bounded in-kernel wait ran out";
     case MXG_ERR_WORKSPACE: return "workspace missing or too small";
     case MXG_ERR_CAPACITY: return "padded rows exceed the output capacity";
-    case MXG_ERR_INDEX: return "an expert or adapter id is not below its count";
+    case MXG_ERR_INDEX: return "an expert or adapter id, or a row, is not below its count";
   }
   return "unknown status";
 }
@@ -956,6 +956,232 @@ mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, co
   a.dtype = dtype; a.out = out; a.ld_out = ld_out;
   a.ws = static_cast<float*>(ws); a.status = d_status;
   return cuda_status(launch_lora_add(a, static_cast<cudaStream_t>(stream), sms));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Tokens to the experts and back; products of 8-bit integers
+// ---------------------------------------------------------------------------
+namespace {
+
+bool slots_ok(int64_t tokens, int32_t top_k) {
+  return tokens >= 0 && top_k >= 1 && top_k <= kMaxTopK && tokens <= 0x7FFFFFFF / top_k;
+}
+inline int per16(int32_t dtype) { return dtype == MXG_OUT_BF16 ? 8 : 4; }  // elements of 16 bytes
+
+// A matrix of rows of `hidden` elements, 16-byte aligned.
+mxg_status check_rows(int64_t hidden, int32_t dtype, std::initializer_list<int64_t> lds) {
+  if (!valid_out_dtype(dtype)) return MXG_ERR_UNSUPPORTED;
+  if (hidden < 1 || hidden > 0x7FFFFFFF) return MXG_ERR_SHAPE;
+  for (int64_t ld : lds)
+    if (ld < hidden) return MXG_ERR_SHAPE;
+  if (hidden % per16(dtype) != 0) return MXG_ERR_SHAPE;
+  for (int64_t ld : lds)
+    if (ld % per16(dtype) != 0) return MXG_ERR_ALIGN;
+  return MXG_OK;
+}
+
+mxg_status check_i8_operand(const mxg_i8_operand* op) {
+  if (op == nullptr) return MXG_ERR_NULL;
+  if ((op->codes != MXG_CODES_INT8 && op->codes != MXG_CODES_F16) || op->reserved != 0) return MXG_ERR_UNSUPPORTED;
+  if (op->rows < 0 || op->rows > 0x7FFFFFFF || op->cols < 16 || op->cols > 0x7FFFFFFF || op->cols % 16 != 0 ||
+      op->ld < op->cols * op->codes)  // a code of kind c has c bytes
+    return MXG_ERR_SHAPE;
+  if (op->ld % 16 != 0) return MXG_ERR_ALIGN;
+  if (op->rows == 0) return MXG_OK;
+  if (op->data == nullptr || op->scale == nullptr) return MXG_ERR_NULL;
+  if (!aligned16(op->data) || !aligned(op->scale, 4)) return MXG_ERR_ALIGN;
+  return MXG_OK;
+}
+
+mxg_status int8_gemm_impl(const mxg_i8_operand* A, const mxg_i8_operand* W, const int32_t* d_m_splits, int32_t G,
+                          int64_t N, void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                          int32_t* d_status, void* stream) {
+  mxg_status st;
+  if ((st = check_i8_operand(A)) != MXG_OK || (st = check_i8_operand(W)) != MXG_OK) return st;
+  if (d_status == nullptr) return MXG_ERR_NULL;
+  if (W->codes != MXG_CODES_INT8 || !valid_out_dtype(out_dtype)) return MXG_ERR_UNSUPPORTED;
+  if (G < 1 || G > kMaxExperts || N < 8 || N % 8 != 0 || N > 0x7FFFFFFF / G || W->rows != (int64_t)G * N ||
+      A->cols != W->cols || ld_out < N || !int8_gemm_sizes_fit(A->rows, G, N, A->cols))
+    return MXG_ERR_SHAPE;
+  if (ld_out % per16(out_dtype) != 0) return MXG_ERR_ALIGN;
+  if (A->rows > 0 && out == nullptr) return MXG_ERR_NULL;
+  if (!aligned16(out)) return MXG_ERR_ALIGN;
+  if (ws == nullptr || ws_bytes < int8_gemm_workspace_bytes(A->rows, G, N, A->cols, A->codes)) return MXG_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if ((st = check_device({A->data, A->scale, W->data, W->scale, d_m_splits, out, ws, d_status}, &dev, &sms)) != MXG_OK)
+    return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  Int8GemmArgs a{};
+  a.a = static_cast<const uint8_t*>(A->data); a.ld_a = A->ld; a.codes = A->codes; a.sa = A->scale;
+  a.w = static_cast<const uint8_t*>(W->data); a.ld_w = W->ld; a.sw = W->scale;
+  a.splits = d_m_splits; a.G = G; a.S = A->rows; a.N = N; a.K = A->cols;
+  a.out = out; a.ld_out = ld_out; a.out_dtype = out_dtype;
+  a.ws = ws; a.status = d_status;
+  return launch_int8_gemm(a, static_cast<cudaStream_t>(stream), sms);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_sort_workspace_size(int64_t tokens, int32_t top_k, int32_t experts) {
+  if (!slots_ok(tokens, top_k) || experts < 1 || experts > kMaxExperts) return 0;
+  return moe_sort_workspace_bytes(tokens * top_k, experts);
+}
+
+mxg_status moe_sort(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t* m_splits,
+                    int32_t* rows, void* ws, size_t ws_bytes, int32_t* d_status, void* stream) {
+  if (d_status == nullptr || m_splits == nullptr) return MXG_ERR_NULL;
+  if (!slots_ok(tokens, top_k) || experts < 1 || experts > kMaxExperts) return MXG_ERR_SHAPE;
+  if (tokens > 0 && (ids == nullptr || rows == nullptr)) return MXG_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(m_splits, 4) || !aligned(rows, 4)) return MXG_ERR_ALIGN;
+  if (ws == nullptr || ws_bytes < moe_sort_workspace_bytes(tokens * top_k, experts)) return MXG_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  const void* in = tokens > 0 ? ids : nullptr;
+  const void* to = tokens > 0 ? rows : nullptr;
+  mxg_status st = check_device({in, m_splits, to, ws, d_status}, &dev, &sms);
+  if (st != MXG_OK) return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  return cuda_status(launch_moe_sort(ids, tokens * top_k, experts, m_splits, rows, ws, d_status,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+mxg_status moe_gather(const void* x, int64_t ld_x, const int32_t* rows, int64_t tokens, int32_t top_k, int64_t hidden,
+                      int32_t dtype, void* out, int64_t ld_out, int32_t* d_status, void* stream) {
+  if (d_status == nullptr) return MXG_ERR_NULL;
+  mxg_status st;
+  if ((st = check_rows(hidden, dtype, {ld_x, ld_out})) != MXG_OK) return st;
+  if (!slots_ok(tokens, top_k)) return MXG_ERR_SHAPE;
+  if (tokens == 0) return MXG_OK;
+  if (x == nullptr || rows == nullptr || out == nullptr) return MXG_ERR_NULL;
+  if (!aligned16(x) || !aligned16(out) || !aligned(rows, 4)) return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if ((st = check_device({x, rows, out, d_status}, &dev, &sms)) != MXG_OK) return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  const int n = per16(dtype);
+  return cuda_status(launch_moe_gather(x, ld_x / n, rows, tokens, top_k, hidden / n, out, ld_out / n, d_status,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+mxg_status moe_combine(const void* y, int64_t ld_y, int64_t y_rows, const int32_t* rows, const float* weights,
+                       int64_t tokens, int32_t top_k, int64_t hidden, int32_t dtype, void* out, int64_t ld_out,
+                       int32_t* d_status, void* stream) {
+  if (d_status == nullptr) return MXG_ERR_NULL;
+  mxg_status st;
+  if ((st = check_rows(hidden, dtype, {ld_y, ld_out})) != MXG_OK) return st;
+  if (!slots_ok(tokens, top_k) || y_rows < 0) return MXG_ERR_SHAPE;
+  if (tokens == 0) return MXG_OK;
+  if ((y_rows > 0 && y == nullptr) || rows == nullptr || out == nullptr) return MXG_ERR_NULL;
+  if (!aligned16(y) || !aligned16(out) || !aligned(rows, 4) || !aligned(weights, 4)) return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if ((st = check_device({y_rows > 0 ? y : nullptr, rows, weights, out, d_status}, &dev, &sms)) != MXG_OK) return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  const int n = per16(dtype);
+  return cuda_status(launch_moe_combine(y, ld_y / n, y_rows, rows, weights, tokens, top_k, hidden / n,
+                                        dtype == MXG_OUT_BF16, out, ld_out / n, d_status,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+mxg_status moe_combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y, const int32_t* rows,
+                                const float* weights, int64_t tokens, int32_t top_k, int64_t hidden, int32_t dtype,
+                                void* dy, int64_t ld_dy, float* dweights, int32_t* d_status, void* stream) {
+  if (d_status == nullptr) return MXG_ERR_NULL;
+  mxg_status st;
+  if ((st = check_rows(hidden, dtype, {ld_dout, ld_y, ld_dy})) != MXG_OK) return st;
+  if (!slots_ok(tokens, top_k) || (dy == y && ld_dy != ld_y)) return MXG_ERR_SHAPE;
+  if (tokens == 0) return MXG_OK;
+  if (dout == nullptr || y == nullptr || rows == nullptr || weights == nullptr || dy == nullptr || dweights == nullptr)
+    return MXG_ERR_NULL;
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(dy) || !aligned(rows, 4) || !aligned(weights, 4) ||
+      !aligned(dweights, 4))
+    return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  if ((st = check_device({dout, y, rows, weights, dy, dweights, d_status}, &dev, &sms)) != MXG_OK) return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  const int n = per16(dtype);
+  return cuda_status(launch_moe_combine_backward(dout, ld_dout / n, y, ld_y / n, rows, weights, tokens, top_k, hidden / n,
+                                                 dtype == MXG_OUT_BF16, dy, ld_dy / n, dweights, d_status,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+mxg_status moe_route_backward(const float* dweights, const int32_t* ids, const float* weights, const void* logits,
+                              int64_t ld_logits, int64_t tokens, int32_t experts, int32_t top_k, int32_t renormalize,
+                              int32_t dtype, void* dlogits, int64_t ld_dlogits, int32_t* d_status, void* stream) {
+  if (d_status == nullptr) return MXG_ERR_NULL;
+  if (!valid_out_dtype(dtype)) return MXG_ERR_UNSUPPORTED;
+  if (!slots_ok(tokens, top_k) || experts < 1 || experts > kMaxExperts || top_k > experts || ld_dlogits < experts ||
+      (renormalize == 0 && ld_logits < experts))
+    return MXG_ERR_SHAPE;
+  if (tokens == 0) return MXG_OK;
+  if (renormalize != 0) logits = nullptr;
+  if (dweights == nullptr || ids == nullptr || weights == nullptr || dlogits == nullptr ||
+      (renormalize == 0 && logits == nullptr))
+    return MXG_ERR_NULL;
+  const uintptr_t e = dtype == MXG_OUT_BF16 ? 2 : 4;
+  if (!aligned(dweights, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(logits, e) || !aligned(dlogits, e))
+    return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  mxg_status st = check_device({dweights, ids, weights, logits, dlogits, d_status}, &dev, &sms);
+  if (st != MXG_OK) return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  return cuda_status(launch_moe_route_backward(dweights, ids, weights, logits, tokens, experts, ld_logits,
+                                               dtype == MXG_OUT_BF16, top_k, dlogits, ld_dlogits, d_status,
+                                               static_cast<cudaStream_t>(stream), sms));
+}
+
+mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* rows, int64_t tokens, int32_t top_k,
+                                 int64_t cols, int32_t codes, void* q, int64_t ld_q, float* scale, int32_t* d_status,
+                                 void* stream) {
+  if (codes != MXG_CODES_INT8 && codes != MXG_CODES_F16) return MXG_ERR_UNSUPPORTED;
+  if (rows == nullptr) top_k = 1;
+  else if (d_status == nullptr) return MXG_ERR_NULL;
+  if (!slots_ok(tokens, top_k) || cols < 16 || cols > 0x7FFFFFFF || cols % 16 != 0 || ld_x < cols || ld_q < cols * codes)
+    return MXG_ERR_SHAPE;
+  if (ld_x % 8 != 0 || ld_q % 16 != 0) return MXG_ERR_ALIGN;
+  if (tokens == 0) return MXG_OK;
+  if (x == nullptr || q == nullptr || scale == nullptr) return MXG_ERR_NULL;
+  if (!aligned16(x) || !aligned16(q) || !aligned(scale, 4) || !aligned(rows, 4)) return MXG_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  mxg_status st = check_device({x, rows, q, scale, rows != nullptr ? d_status : nullptr}, &dev, &sms);
+  if (st != MXG_OK) return st;
+  DeviceGuard g(dev);
+  if (!g.ok) return MXG_ERR_CUDA;
+  return cuda_status(launch_int8_quantize(x, ld_x, rows, tokens, top_k, cols, codes, q, ld_q, scale, d_status,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t int8_gemm_workspace_size(int32_t G, int64_t S, int64_t N, int64_t K, int32_t a_codes) {
+  if (G < 1 || G > kMaxExperts || S < 0 || S > 0x7FFFFFFF || N < 8 || N % 8 != 0 || N > 0x7FFFFFFF / G || K < 16 ||
+      K > 0x7FFFFFFF || K % 16 != 0 || (a_codes != MXG_CODES_INT8 && a_codes != MXG_CODES_F16))
+    return 0;
+  return int8_gemm_workspace_bytes(S, G, N, K, a_codes);
+}
+
+int32_t mxg_diag_int8_tile_tokens(int32_t G, int64_t S, int64_t N, int64_t K) {
+  return int8_gemm_workspace_size(G, S, N, K, MXG_CODES_F16) == 0 ? 0 : int8_gemm_tile_tokens(S, G, N, K);
+}
+
+mxg_status int8_grouped_gemm_fwd(const mxg_i8_operand* A, const mxg_i8_operand* W, const int32_t* d_m_splits, int32_t G,
+                                 int64_t N, void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                                 int32_t* d_status, void* stream) {
+  if (d_m_splits == nullptr) return MXG_ERR_NULL;
+  if (!aligned(d_m_splits, 4)) return MXG_ERR_ALIGN;
+  return int8_gemm_impl(A, W, d_m_splits, G, N, out, ld_out, out_dtype, ws, ws_bytes, d_status, stream);
+}
+
+mxg_status int8_gemm_dense(const mxg_i8_operand* A, const mxg_i8_operand* B, void* out, int64_t ld_out, int32_t out_dtype,
+                           void* ws, size_t ws_bytes, int32_t* d_status, void* stream) {
+  return int8_gemm_impl(A, B, nullptr, 1, B == nullptr ? 0 : B->rows, out, ld_out, out_dtype, ws, ws_bytes, d_status, stream);
 }
 
 }  // extern "C"

@@ -111,6 +111,50 @@ mxg_status launch_grouped_bw_gemm(const BwGemmArgs& a, cudaStream_t stream, int 
 cudaError_t launch_moe_route(const void* logits, int64_t T, int E, int64_t ld, bool bf16, int k, bool renorm,
                              int32_t* ids, float* weights, cudaStream_t stream, int num_sms);
 
+cudaError_t launch_moe_route_backward(const float* dweights, const int32_t* ids, const float* weights, const void* logits,
+                                      int64_t T, int E, int64_t ld, bool bf16, int k, void* dlogits, int64_t ld_d,
+                                      int32_t* status, cudaStream_t stream, int num_sms);
+
+// Tokens to the experts and back.  See moe_dispatch.cu.  `pieces`: 16-byte pieces
+// of a row; strides in pieces.
+size_t moe_sort_workspace_bytes(int64_t P, int E);
+cudaError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* m_splits, int32_t* rows, void* ws,
+                            int32_t* status, cudaStream_t stream);
+cudaError_t launch_moe_gather(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int k, int64_t pieces,
+                              void* out, int64_t ld_out, int32_t* status, cudaStream_t stream);
+cudaError_t launch_moe_combine(const void* y, int64_t ld_y, int64_t y_rows, const int32_t* rows, const float* weights,
+                               int64_t T, int k, int64_t pieces, bool bf16, void* out, int64_t ld_out, int32_t* status,
+                               cudaStream_t stream);
+cudaError_t launch_moe_combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y,
+                                        const int32_t* rows, const float* weights, int64_t T, int k, int64_t pieces,
+                                        bool bf16, void* dy, int64_t ld_dy, float* dweights, int32_t* status,
+                                        cudaStream_t stream);
+
+// 8-bit integer products.  See gemm_i8.cu.
+cudaError_t launch_int8_quantize(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int k, int64_t cols,
+                                 int codes, void* q, int64_t ld_q, float* scale, int32_t* status, cudaStream_t stream);
+struct Int8GemmArgs {
+  const uint8_t* a;  // codes of the activations, row stride (bytes)
+  int64_t ld_a;
+  int codes;         // mxg_int_codes of the activations
+  const float* sa;
+  const uint8_t* w;
+  int64_t ld_w;
+  const float* sw;
+  const int32_t* splits;  // null: one expert of all rows
+  int G;
+  int64_t S, N, K;
+  void* out;
+  int64_t ld_out;
+  int out_dtype;
+  void* ws;
+  int32_t* status;
+};
+size_t int8_gemm_workspace_bytes(int64_t S, int G, int64_t N, int64_t K, int codes);
+int int8_gemm_tile_tokens(int64_t S, int G, int64_t N, int64_t K);
+bool int8_gemm_sizes_fit(int64_t S, int G, int64_t N, int64_t K);  // 32-bit counts of stages
+mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_sms);
+
 // The expert layer of a few tokens.  See moe_experts.cu.
 struct MoeArgs {
   const uint16_t* x;

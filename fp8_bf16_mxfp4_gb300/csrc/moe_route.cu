@@ -130,7 +130,109 @@ cudaError_t launch_route(const TIn* logits, int64_t T, int E, int64_t ld, int k,
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Gradient of the routing weights.  With s = sum_j w_j dw_j over a token's slots:
+//   weights over the chosen experts   dl[id_j] = w_j (dw_j - s), zeros elsewhere
+//   weights over all experts          dl_e = [e = id_j] w_j dw_j - p_e s,  p = softmax(l)
+// One warp per token.  The row is made in shared memory, the slots added to it in
+// order (so an expert that is named twice gets both, always the same way), and
+// written once.  p is made as the forward makes it: a logit of -inf or NaN has 0,
+// one that equals the maximum exp(0).
+// ---------------------------------------------------------------------------
+MXG_DEVINL void store_grad(float* p, float v) { *p = v; }
+MXG_DEVINL void store_grad(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+template <typename TIn, int kPer>
+__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(
+    const float* __restrict__ dweights, const int32_t* __restrict__ ids, const float* __restrict__ weights,
+    const TIn* __restrict__ logits, int64_t T, int E, int64_t ld, int k, TIn* __restrict__ dlogits, int64_t ld_d,
+    int32_t* __restrict__ status) {
+  __shared__ float rows[kRouteWarps][32 * kPer];
+  const int lane = threadIdx.x & 31;
+  float* row = rows[threadIdx.x >> 5];
+  const bool renorm = logits == nullptr;
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < T;
+       t += (int64_t)gridDim.x * kRouteWarps) {
+    float v[kPer], top = -INFINITY;
+    if (!renorm) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 32 * i;
+        v[i] = e < E ? load_logit(logits + t * ld + e) : -INFINITY;
+        if (v[i] > top) top = v[i];  // false for NaN
+      }
+    }
+    int id = lane < k ? __ldg(ids + t * k + lane) : -1;
+    if (id >= E) {
+      report(status, MXG_ERR_INDEX);
+      id = -1;
+    }
+    const float w = id >= 0 ? __ldg(weights + t * k + lane) : 0.0f;
+    const float dw = id >= 0 ? __ldg(dweights + t * k + lane) : 0.0f;
+    float s = w * dw;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+    const float add = renorm ? w * (dw - s) : w * dw;
+    if (renorm) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) row[lane + 32 * i] = 0.0f;
+    } else {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+      float total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        v[i] = v[i] > -INFINITY ? route_exp(v[i], top) : 0.0f;
+        total += v[i];
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+      const float per = total > 0.0f ? s / total : 0.0f;  // a row without logits has no slots
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) row[lane + 32 * i] = -v[i] * per;
+    }
+    __syncwarp();
+    for (int j = 0; j < k; ++j) {
+      const int e = __shfl_sync(kFull, id, j);
+      const float a = __shfl_sync(kFull, add, j);
+      if (e >= 0 && lane == (e & 31)) row[e] += a;  // the lane that wrote it, and that reads it
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = lane + 32 * i;
+      if (e < E) store_grad(dlogits + t * ld_d + e, row[e]);
+    }
+    __syncwarp();
+  }
+}
+
+template <typename TIn>
+cudaError_t launch_route_backward(const float* dweights, const int32_t* ids, const float* weights, const TIn* logits,
+                                  int64_t T, int E, int64_t ld, int k, TIn* dlogits, int64_t ld_d, int32_t* status,
+                                  cudaStream_t stream, int num_sms) {
+  const int per = (E + 31) / 32;
+  const auto fn = per <= 1   ? moe_route_backward_kernel<TIn, 1>
+                  : per <= 2 ? moe_route_backward_kernel<TIn, 2>
+                  : per <= 4 ? moe_route_backward_kernel<TIn, 4>
+                  : per <= 8 ? moe_route_backward_kernel<TIn, 8>
+                             : moe_route_backward_kernel<TIn, 16>;
+  const int64_t want = (T + kRouteWarps - 1) / kRouteWarps;
+  fn<<<(unsigned)std::min<int64_t>(want, (int64_t)num_sms * 8), kRouteWarps * 32, 0, stream>>>(
+      dweights, ids, weights, logits, T, E, ld, k, dlogits, ld_d, status);
+  return cudaGetLastError();
+}
+
 }  // namespace
+
+cudaError_t launch_moe_route_backward(const float* dweights, const int32_t* ids, const float* weights, const void* logits,
+                                      int64_t T, int E, int64_t ld, bool bf16, int k, void* dlogits, int64_t ld_d,
+                                      int32_t* status, cudaStream_t stream, int num_sms) {
+  if (bf16)
+    return launch_route_backward(dweights, ids, weights, static_cast<const __nv_bfloat16*>(logits), T, E, ld, k,
+                                 static_cast<__nv_bfloat16*>(dlogits), ld_d, status, stream, num_sms);
+  return launch_route_backward(dweights, ids, weights, static_cast<const float*>(logits), T, E, ld, k,
+                               static_cast<float*>(dlogits), ld_d, status, stream, num_sms);
+}
 
 cudaError_t launch_moe_route(const void* logits, int64_t T, int E, int64_t ld, bool bf16, int k, bool renorm,
                              int32_t* ids, float* weights, cudaStream_t stream, int num_sms) {

@@ -200,6 +200,9 @@ MXG_DEVINL void bulk_wait_group0() { asm volatile("cp.async.bulk.wait_group 0;" 
 MXG_DEVINL void ld_shared_v2_u64(uint32_t addr, uint64_t& a, uint64_t& b) {
   asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
+MXG_DEVINL void ld_shared_v4(uint32_t addr, uint32_t* v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+}
 MXG_DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
@@ -555,6 +558,42 @@ MXG_DEVINL void mma_f16_if(uint32_t e, uint32_t d, uint64_t adesc, uint64_t bdes
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
       : "memory");
+}
+
+// D(tmem) (+)= A(tmem) * B(smem), FP16 operands: A's rows are TMEM lanes, a column
+// holds two of its elements.  For a pair (kCta = 2) each CTA's TMEM has its own 128
+// rows of A and D, its shared memory half of B's rows.
+template <int kCta>
+MXG_DEVINL void mma_f16_ts_if(uint32_t e, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kCta == 1)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
+        : "memory");
+}
+// As tc_commit_pair, by the lane whose `e` is set.
+template <int kCta>
+MXG_DEVINL void tc_commit_pair_if(uint32_t e, uint32_t bar) {
+  if constexpr (kCta == 1) tc_commit_if(e, bar);
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+            bar),
+        "r"(e), "h"((uint16_t)0x3)
+        : "memory");
 }
 
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading

@@ -68,7 +68,7 @@ typedef enum mxg_status {
   MXG_ERR_TIMEOUT = 8,     /* device-side: a bounded wait ran out */
   MXG_ERR_WORKSPACE = 9,   /* workspace missing or smaller than required */
   MXG_ERR_CAPACITY = 10,   /* device-side: padded rows exceed the output capacity */
-  MXG_ERR_INDEX = 11       /* device-side: an expert or adapter id is not below its count */
+  MXG_ERR_INDEX = 11       /* device-side: an expert or adapter id, or a row, is not below its count */
 } mxg_status;
 
 typedef enum mxg_elem { MXG_E2M1 = 1, MXG_E4M3 = 2 } mxg_elem;
@@ -547,6 +547,130 @@ mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, co
                     int32_t* d_status, void* stream);
 
 /* --------------------------------------------------------------------------
+ * Tokens to the experts and back
+ *
+ * What surrounds the grouped GEMMs of a mixture-of-experts layer, forward and
+ * backward: `tokens` tokens of `top_k` slots each, P = tokens * top_k.  Strides
+ * are in elements; rows of BF16 or FP32 (`dtype`, mxg_out_dtype) are 16-byte
+ * aligned (hidden and strides % 8 for BF16, % 4 for FP32).  1 <= top_k <= 32,
+ * P < 2^31, tokens may be 0.  Sums are in fp32 in the order of the slots (of a
+ * fixed tree for dweights): results depend on the inputs only.  The operands of
+ * a call do not overlap, but where it says so.
+ * ------------------------------------------------------------------------ */
+
+/* Sorts the slots by expert: rows[t, j] is slot (t, j)'s row among the P rows in
+ * expert order, slots of one expert in the order of their index, and m_splits the
+ * rows of each expert, as the grouped GEMMs and quantizers take them.  A slot with
+ * a negative id is empty: it owns one of the rows behind all experts' slots, r
+ * (again in order), and its entry is -1 - r.  The last expert's split counts these
+ * rows, so that the splits add up to P; the calls below keep them zero.
+ *   ids      : int32 [tokens, top_k] contiguous
+ *   m_splits : int32 [experts]; rows: int32 [tokens, top_k] contiguous
+ *   ws       : at least moe_sort_workspace_size(...) bytes, 256-byte aligned
+ * 1 <= experts <= 512.  Device error: MXG_ERR_INDEX (an id >= experts; its slot is
+ * taken as empty). */
+size_t moe_sort_workspace_size(int64_t tokens, int32_t top_k, int32_t experts);
+mxg_status moe_sort(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t* m_splits,
+                    int32_t* rows, void* ws, size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* Rows in expert order: out[rows[t, j], :] = x[t, :], zeros in the rows of empty
+ * slots.  x: [tokens, hidden]; out: [P, hidden] of the same type, every row of
+ * which is written (rows as from moe_sort).  Its gradient is moe_combine of the
+ * gradient of out, without weights.  Device error: MXG_ERR_INDEX (a row >= P,
+ * which is not written). */
+mxg_status moe_gather(const void* x, int64_t ld_x, const int32_t* rows, int64_t tokens, int32_t top_k, int64_t hidden,
+                      int32_t dtype, void* out, int64_t ld_out, int32_t* d_status, void* stream);
+
+/* Back to the tokens: out[t, :] = sum over slots j of weights[t, j] * y[rows[t, j], :],
+ * empty slots (rows < 0) adding nothing, whatever their weight; rounded once.
+ *   y       : [y_rows, hidden]; out: [tokens, hidden] of the same type
+ *   weights : float [tokens, top_k] contiguous, or NULL for 1
+ * Device error: MXG_ERR_INDEX (a row >= y_rows, which adds nothing). */
+mxg_status moe_combine(const void* y, int64_t ld_y, int64_t y_rows, const int32_t* rows, const float* weights,
+                       int64_t tokens, int32_t top_k, int64_t hidden, int32_t dtype, void* out, int64_t ld_out,
+                       int32_t* d_status, void* stream);
+
+/* Gradients of moe_combine (with weights) for y of P rows:
+ *   dy[rows[t, j], :]  = weights[t, j] * dout[t, :],   zeros in the rows of empty slots
+ *   dweights[t, j]     = sum_h dout[t, h] * y[rows[t, j], h],   0 for an empty slot
+ * dout: [tokens, hidden]; y, dy: [P, hidden]; dweights: float [tokens, top_k].
+ * dy may be y (in place, with ld_dy = ld_y).  Device error: MXG_ERR_INDEX (a row >= P,
+ * which is not written; its dweights is 0). */
+mxg_status moe_combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y, const int32_t* rows,
+                                const float* weights, int64_t tokens, int32_t top_k, int64_t hidden, int32_t dtype,
+                                void* dy, int64_t ld_dy, float* dweights, int32_t* d_status, void* stream);
+
+/* Gradient of moe_route's weights with respect to the logits, s = sum_j weights_j dweights_j
+ * over a token's slots with ids >= 0:
+ *   renormalize != 0 : dlogits[id_j] = weights_j * (dweights_j - s), zeros elsewhere
+ *   renormalize == 0 : dlogits[e]    = [e = id_j] weights_j dweights_j - p_e s,
+ *                      p = softmax(logits[t, :]) as moe_route takes it (p of a logit of -inf or NaN is 0)
+ * computed in fp32 and rounded once; an expert that several slots name gets their sum.
+ *   dweights, ids, weights : [tokens, top_k] contiguous (ids and weights as from moe_route)
+ *   logits                 : [tokens, experts] of `dtype`, row stride ld_logits; not read with renormalize (may be NULL)
+ *   dlogits                : [tokens, experts] of `dtype`, row stride ld_dlogits >= experts; every element is written
+ * 1 <= experts <= 512, top_k <= experts.  Device error: MXG_ERR_INDEX (an id >= experts,
+ * whose slot is taken as empty). */
+mxg_status moe_route_backward(const float* dweights, const int32_t* ids, const float* weights, const void* logits,
+                              int64_t ld_logits, int64_t tokens, int32_t experts, int32_t top_k, int32_t renormalize,
+                              int32_t dtype, void* dlogits, int64_t ld_dlogits, int32_t* d_status, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Products of 8-bit integers (W8A8): a scale per token and per channel
+ *
+ * An operand is K-major: `rows` rows of `cols` codes q and one fp32 scale per row,
+ * standing for scale * q.  Codes are 8-bit integers in [-128, 127], or, for
+ * activations, the same integers as FP16 values (MXG_CODES_F16: what the tensor
+ * core takes; int8_quantize_rowwise writes either).  cols % 16 == 0; data 16-byte
+ * aligned; ld (row stride in BYTES) % 16 == 0 and at least a row's bytes.
+ * ------------------------------------------------------------------------ */
+typedef enum mxg_int_codes { MXG_CODES_INT8 = 1, MXG_CODES_F16 = 2 } mxg_int_codes;
+typedef struct mxg_i8_operand {
+  const void* data;
+  const float* scale; /* [rows] */
+  int64_t rows;
+  int64_t cols;
+  int64_t ld;
+  int32_t codes;    /* mxg_int_codes */
+  int32_t reserved; /* must be 0 */
+} mxg_i8_operand;
+
+/* Row-wise quantization of BF16 x [tokens, cols] (activations, or weights per
+ * channel): a = max(max |x[t, :]|, 2^-100), scale = a / 127 and r = 127 / a in fp32
+ * (correctly rounded), code = the integer nearest to the exact product x * r (ties
+ * to even; within [-127, 127]).  A row that holds a NaN or an infinity gets codes 0
+ * and the scale NaN, so that its products are NaN.
+ *   rows : NULL, or int32 [tokens, top_k] as from moe_sort: token t's row is written
+ *          to the output rows rows[t, j] -- the bytes of quantizing moe_gather(x, rows).
+ *          Device error: MXG_ERR_INDEX (a row >= P, which is not written; d_status
+ *          is required with rows).
+ *   x    : row stride ld_x elements (% 8), 16-byte aligned
+ *   q    : [tokens or P, cols] of `codes`, ld_q bytes; scale: float [tokens or P]
+ * cols % 16 == 0; tokens may be 0. */
+mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* rows, int64_t tokens, int32_t top_k,
+                                 int64_t cols, int32_t codes, void* q, int64_t ld_q, float* scale, int32_t* d_status,
+                                 void* stream);
+
+/* Y[off_g + i, n] = A.scale[off_g + i] * W.scale[g N + n] * sum_k A[off_g + i, k] W[g N + n, k]
+ * for every expert g, off the prefix sum of m_splits.  The products of the codes are
+ * exact, their sums in fp32 (exact while they stay below 2^24), the result rounded
+ * once to BF16 or, after two products in fp32, FP32.
+ *   A   : [S, K] codes of either kind; W: [G * N, K], MXG_CODES_INT8
+ *   out : [S, N] of out_dtype, row stride ld_out; rows 16-byte aligned; N % 8 == 0
+ *   ws  : at least int8_gemm_workspace_size(G, S, N, K, A->codes) bytes, 256-byte aligned
+ * Splits are checked as for grouped_gemm_fwd (MXG_ERR_SPLITS; nothing is written).
+ * Forward only: the gradients of a quantized layer are those of its unquantized weights. */
+size_t int8_gemm_workspace_size(int32_t G, int64_t S, int64_t N, int64_t K, int32_t a_codes);
+mxg_status int8_grouped_gemm_fwd(const mxg_i8_operand* A, const mxg_i8_operand* W, const int32_t* d_m_splits, int32_t G,
+                                 int64_t N, void* out, int64_t ld_out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                                 int32_t* d_status, void* stream);
+
+/* C[M, N] = A[M, K] * B[N, K]^T of two such operands: int8_grouped_gemm_fwd with one
+ * expert of all rows and no device m_splits. */
+mxg_status int8_gemm_dense(const mxg_i8_operand* A, const mxg_i8_operand* B, void* out, int64_t ld_out, int32_t out_dtype,
+                           void* ws, size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* --------------------------------------------------------------------------
  * Status and configuration
  * ------------------------------------------------------------------------ */
 
@@ -583,6 +707,11 @@ mxg_status mxg_diag_bounded_wait(int32_t* d_status, uint64_t timeout_ns, void* s
 /* Diagnostic: the number of adapters per tile of 128 tokens that lora_add plans
  * its work for (tokens on adapters at random), 0 where either is below 1. */
 int32_t mxg_diag_lora_tile_adapters(int64_t tokens, int32_t adapters);
+
+/* Diagnostic: the tokens of a tile of int8_grouped_gemm_fwd for these sizes: 16, 32,
+ * 64 or 128 (single CTAs, work cut into equal runs) or 256 (CTA pairs, whole tiles);
+ * 0 where the sizes are refused. */
+int32_t mxg_diag_int8_tile_tokens(int32_t G, int64_t S, int64_t N, int64_t K);
 
 /* ABI version: major*10000 + minor*100 + patch. */
 int32_t mxg_version(void);
