@@ -174,7 +174,6 @@ __global__ void __launch_bounds__(kPrepThreads) int8_prep_kernel(uint32_t* sync,
 // ---------------------------------------------------------------------------
 // Product
 // ---------------------------------------------------------------------------
-constexpr int kI8Threads = 448;
 constexpr int kChan = 128;                 // channels of a CTA's tile (TMEM lanes)
 constexpr int kStageK = 128;               // contraction elements of a stage
 constexpr int kWBytes = kChan * kStageK;
@@ -189,6 +188,10 @@ constexpr int kI8MinStages = 4;            // shortest run of cut units
 template <int kCta, int kTok>
 struct I8Cfg {
   static constexpr int kBufs = kTok == 256 ? 1 : 2;
+  // Groups of four widening warps.  A pair's stage lasts 1024 clocks, which one
+  // group keeps up with, and its epilogue needs the registers.
+  static constexpr int kGroups = kCta == 2 ? 1 : 2;
+  static constexpr int kThreads = 32 * (6 + 4 * kGroups);
   static constexpr int kRows = kTok / kCta;            // tokens whose elements this CTA loads
   static constexpr int kXBox = kRows * 128;            // 64 elements of each
   static constexpr int kStageBytes = kWBytes + 2 * kXBox;
@@ -202,7 +205,9 @@ struct I8Cfg {
   static constexpr int kMiscOff = kBarOff + ((kBars * 8 + 15) & ~15);
   static constexpr int kOffOff = kMiscOff + 16;                      // int32 [G + 1]: first row of each expert
   static constexpr int kTileOff = kOffOff + (kMaxExperts + 4) * 4;   // int32 [G + 1]: first unit of each expert
-  static constexpr int kTotal = kTileOff + (kMaxExperts + 4) * 4 + 1024;  // + alignment slack
+  static constexpr int kSaOff = kTileOff + (kMaxExperts + 4) * 4;    // float [4][256]: the tile's token scales (pairs)
+  static constexpr int kTotal = kSaOff + (kCta == 2 ? 4 * kTok * 4 : 0) + 1024;  // + alignment slack
+  static_assert(kSaOff % 16 == 0, "token scales are read 16 bytes at a time");
   static_assert(kBufs * kTok <= kACol && kACol + kStages * kACols <= kI8TmemCols, "TMEM holds accumulators and ring");
   static_assert(kStageBytes % 1024 == 0 && kXBox % 1024 == 0, "tiles keep the swizzle-atom alignment");
   static_assert(kTotal <= 232448, "fits the 227 KB of one CTA");
@@ -292,6 +297,11 @@ struct I8Walker {
   }
 };
 
+// Tokens that a pair's MMAs take: the tile's, to a multiple of 32 (half of them in
+// each CTA).  The last tile of an expert is often short: 8192 rows of 8 experts,
+// 4096 x 14336, take ZZ us with it and ZZ with 256 throughout.
+MXG_DEVINL int pair_tokens(int n) { return (n + 31) & ~31; }
+
 MXG_DEVINL uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -303,7 +313,7 @@ MXG_DEVINL uint32_t pack_bf16(float lo, float hi) {
 // epilogues of both arrive on the even CTA's barriers, and every commit reaches
 // the barriers of both.
 template <int kCta, int kTok>
-__global__ void __launch_bounds__(kI8Threads, 1)
+__global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const I8Params p) {
   using L = I8Cfg<kCta, kTok>;
   constexpr int kStages = L::kStages;
@@ -422,7 +432,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       bool ok = true;
       if (p.wide_from_prep) ptx::pdl_wait();  // the widened activations are complete
       while (ok && w.next(p, off, tile)) {
-        const int row_w = w.e * p.N + w.chan0 + rank * kChan, row_x = w.tok0 + rank * L::kRows;
+        const int row_w = w.e * p.N + w.chan0 + rank * kChan;
+        const int row_x = w.tok0 + (kCta == 2 ? rank * pair_tokens(w.n) / 2 : 0);
         for (int kc = w.k0; kc < w.k1; ++kc) {
           if (!ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
           const uint32_t fb = full_bar(stage);
@@ -460,6 +471,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t d = tm + buf * kTok;
+        const uint32_t idesc = kCta == 2 ? p.idesc | ((uint32_t)(pair_tokens(w.n) >> 3) << 17) : p.idesc;
         for (int kc = w.k0; kc < w.k1; ++kc) {
           ok = ptx::mbar_wait_warp(ready_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
           if (!ok) break;
@@ -468,7 +480,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           const uint64_t b = ptx::smem_desc(sbase + stage * L::kStageBytes + kWBytes, 16, 1024, 2);
 #pragma unroll
           for (int j = 0; j < 8; ++j)  // 16 contraction elements: 8 columns, 32 bytes of each token's row
-            ptx::mma_f16_ts_if<kCta>(el, d, a + 8 * j, b + (uint64_t)((j >> 2) * (L::kXBox >> 4) + 2 * (j & 3)), p.idesc,
+            ptx::mma_f16_ts_if<kCta>(el, d, a + 8 * j, b + (uint64_t)((j >> 2) * (L::kXBox >> 4) + 2 * (j & 3)), idesc,
                                      (kc != w.k0) || j != 0);
           issued = true;
           ptx::tc_commit_pair_if<kCta>(el, empty_bar(stage));
@@ -497,7 +509,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     bool ok = true;
     while (ok && w.next(p, off, tile)) {
       for (int kc = w.k0; kc < w.k1; ++kc) {
-        if ((stage & 1) == group) {
+        if (L::kGroups == 1 || (stage & 1) == group) {
           ok = ptx::mbar_wait_warp(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
           if (!ok) break;
           ptx::tc_fence_after();
@@ -536,10 +548,76 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       const int chan = w.chan0 + rank * kChan + quarter * 32 + lane;
       const bool in = chan < p.N;
       const float sw = in ? __ldg(p.sw + (int64_t)w.e * p.N + chan) : 0.0f;
+      float* sa_tile = reinterpret_cast<float*>(smem + L::kSaOff) + quarter * kTok;
+      if constexpr (kCta == 2) {  // the warp's copy of the token scales
+        __syncwarp();
+        for (int i = lane; i < kTok; i += 32) sa_tile[i] = i < w.n ? __ldg(p.sa + w.tok0 + i) : 0.0f;
+        __syncwarp();
+      }
       if (!ptx::mbar_wait_warp(acc_full(buf), round & 1u, abort_flag, p.status, p.timeout_ns)) break;
       ptx::tc_fence_after();
       ++count;
       const uint32_t d = tq + buf * kTok;
+      if constexpr (kCta == 2) {
+        // BF16: the tile's values as 128 pairs of tokens in registers, the
+        // accumulator handed back, then the stores, while the next tile's MMAs run.
+        auto release = [&]() {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_issuer(acc_empty(buf));
+        };
+        auto scaled = [&](int c, float* v) {  // columns 32 c .. 32 c + 31
+          __syncwarp();
+          ptx::tmem_ld_32x32b_x32(d + 32 * c, reinterpret_cast<uint32_t*>(v));
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 s = *reinterpret_cast<const float4*>(sa_tile + 32 * c + i);
+            v[i] = v[i] * sw * s.x;
+            v[i + 1] = v[i + 1] * sw * s.y;
+            v[i + 2] = v[i + 2] * sw * s.z;
+            v[i + 3] = v[i + 3] * sw * s.w;
+          }
+        };
+        if (p.out_f32) {
+          float* dst = static_cast<float*>(p.out) + (int64_t)w.tok0 * p.ld_out + chan;
+          for (int c = 0; 32 * c < w.n; ++c) {
+            float v[32];
+            scaled(c, v);
+            if (32 * c + 32 >= w.n) release();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ptx::st_f32_if(in && 32 * c + i < w.n, dst + (32 * c + i) * p.ld_out, v[i]);
+          }
+        } else {
+          uint32_t pk[kTok / 2];
+#pragma unroll
+          for (int c = 0; c < kTok / 32; ++c) {
+            if (32 * c < w.n) {
+              float v[32];
+              scaled(c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[16 * c + i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+            }
+          }
+          release();
+          // lanes 2 l and 2 l + 1 exchange: the even one takes the first token's two
+          // channels, the odd one the second's
+          const int odd = lane & 1;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (int64_t)(w.tok0 + odd) * p.ld_out + (chan - odd);
+#pragma unroll
+          for (int c = 0; c < kTok / 32; ++c) {
+            if (32 * c < w.n) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t mine = pk[16 * c + i], other = __shfl_xor_sync(kFull, mine, 1);
+                const int at = 32 * c + 2 * i;
+                ptx::st_u32_if(in && at + odd < w.n, dst + at * p.ld_out, __byte_perm(mine, other, odd ? 0x3276 : 0x5410));
+              }
+            }
+          }
+        }
+        continue;
+      }
       const bool whole = kCta == 2 || (w.k0 == 0 && w.k1 == runs.per_unit);
       auto read = [&](int c0, float* v) {
         __syncwarp();
@@ -594,7 +672,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
             const float r = v[i] * sw * __shfl_sync(kFull, sa, i);
-            if (in && c0 + i < w.n) dst[i * p.ld_out] = r;
+            ptx::st_f32_if(in && c0 + i < w.n, dst + i * p.ld_out, r);
           }
         } else {
           // two tokens at a time: the even lane of a pair takes the first one's two
@@ -606,7 +684,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             const float r0 = v[i] * sw * __shfl_sync(kFull, sa, i), r1 = v[i + 1] * sw * __shfl_sync(kFull, sa, i + 1);
             const float other = __shfl_xor_sync(kFull, odd ? r0 : r1, 1);
             const uint32_t o = odd ? pack_bf16(other, r1) : pack_bf16(r0, other);
-            if (in && c0 + i + odd < w.n) *reinterpret_cast<uint32_t*>(dst + i * p.ld_out) = o;
+            ptx::st_u32_if(in && c0 + i + odd < w.n, dst + i * p.ld_out, o);
           }
         }
       }
@@ -629,11 +707,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 // ---------------------------------------------------------------------------
 struct I8Form {
   const void* fn;
-  int cta, tok, smem;
+  int cta, tok, smem, threads;
 };
 template <int kCta, int kTok>
 I8Form form_of() {
-  return {(const void*)int8_gemm_kernel<kCta, kTok>, kCta, kTok, I8Cfg<kCta, kTok>::kTotal};
+  return {(const void*)int8_gemm_kernel<kCta, kTok>, kCta, kTok, I8Cfg<kCta, kTok>::kTotal,
+          I8Cfg<kCta, kTok>::kThreads};
 }
 constexpr int kI8Forms = 5;
 I8Form i8_form(int i) {
@@ -705,7 +784,7 @@ bool i8_ready(int form, int dev, int* pairs) {
       attr[0].val.clusterDim.y = 1;
       attr[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3(2);
-      cfg.blockDim = dim3(kI8Threads);
+      cfg.blockDim = dim3((unsigned)f.threads);
       cfg.dynamicSmemBytes = (size_t)f.smem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
@@ -772,7 +851,8 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
   p.timeout_ns = wait_timeout_ns();
   p.drain_ns = std::max<uint64_t>(p.timeout_ns, 200000000ull);
   // instruction descriptor: FP16 operands, K-major, fp32 sums
-  p.idesc = (1u << 4) | ((uint32_t)(f.tok >> 3) << 17) | ((uint32_t)((kChan * f.cta) >> 4) << 24);
+  p.idesc = (1u << 4) | ((uint32_t)((kChan * f.cta) >> 4) << 24);
+  if (f.cta == 1) p.idesc |= (uint32_t)(f.tok >> 3) << 17;  // a pair's tokens go by the tile
 
   const bool prep = f.cta == 1 || widen;
   if (prep) {
@@ -805,7 +885,7 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
     ++n;
   }
   cfg.gridDim = dim3((unsigned)(f.cta == 2 ? 2 * pairs : std::min(num_sms, kI8MaxCtas)));
-  cfg.blockDim = dim3(kI8Threads);
+  cfg.blockDim = dim3((unsigned)f.threads);
   cfg.dynamicSmemBytes = (size_t)f.smem;
   cfg.stream = stream;
   cfg.attrs = attr;

@@ -492,6 +492,14 @@ MXG_DEVINL void st_cg_f32_if(uint32_t pred, float* p, float v) {
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q st.global.cg.f32 [%1], %2;\n\t}" ::"r"(pred), "l"(p), "f"(v)
                : "memory");
 }
+MXG_DEVINL void st_f32_if(uint32_t pred, float* p, float v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q st.global.f32 [%1], %2;\n\t}" ::"r"(pred), "l"(p), "f"(v)
+               : "memory");
+}
+MXG_DEVINL void st_u32_if(uint32_t pred, void* p, uint32_t v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q st.global.b32 [%1], %2;\n\t}" ::"r"(pred), "l"(p), "r"(v)
+               : "memory");
+}
 MXG_DEVINL void st_v4_if(uint32_t pred, void* p, const uint4& v) {
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q st.global.v4.b32 [%1], {%2, %3, %4, %5};\n\t}" ::"r"(pred),
                "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
