@@ -11,18 +11,21 @@
 // tensor core reads from TMEM, so a warp that turns a row's bytes into FP16 writes
 // them where they are needed and shared memory never holds them twice as wide.
 // Activations are the N operand, from shared memory, as FP16 (the quantizer writes
-// them so, or a kernel in front widens them once).  One CTA per SM:
+// them so, or a kernel in front widens them once).  A pair of CTAs on neighbouring
+// SMs (a cluster) shares a tile of 256 channels through the 2-SM MMA: each has 128
+// channels and half of the tokens.  Per CTA:
 //   warp 0       producer: 128 channels x 128 bytes of weights and the tokens' 128
 //                elements a stage, by TMA;
-//   warp 1       TMEM owner and MMA issuer, 8 MMAs a stage;
+//   warp 1       TMEM owner; in the even CTA MMA issuer for both, 8 MMAs a stage;
 //   warps 2-5    epilogue, one per TMEM lane quarter (a lane is a channel);
 //   warps 6-13   weights to FP16, shared memory to TMEM: two groups of four warps
-//                take turns at the stages.
-// Two forms.  Few rows per expert: tiles of 16 to 128 tokens on single CTAs; the
-// stages of all units (expert, channel tile, token tile) are cut into one equal run
-// per CTA, so that every SM streams the same number of weight bytes, and cut units
-// are joined through fp32 partials, added in run order by the last to arrive.
-// Many rows: 256 channels x 256 tokens on CTA pairs (the 2-SM MMA), whole units.
+//                take turns at the stages (tiles of 256 tokens: one group, 6-9);
+//   warp 14      waits for the issuer (not with 256 tokens).
+// Two forms.  Few rows per expert: tiles of 16 to 128 tokens; the stages of all units
+// (expert, channel tile, token tile) are cut into one equal run per pair, so that
+// every SM streams the same number of weight bytes, and cut units are joined through
+// fp32 partials, added in run order by the last to arrive.  Many rows: 256 tokens,
+// whole units.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -171,46 +174,255 @@ __global__ void __launch_bounds__(kPrepThreads) int8_prep_kernel(uint32_t* sync,
   }
 }
 
+// One warp: the first row off[g] and first unit tile[g] of every expert, `per_tile`
+// units for every `tok` of its rows; *bad where a split is negative or they do not
+// add up to S.  Lane l has experts [l * per, l * per + per).
+MXG_DEVINL void plan_units(const int32_t* splits, int G, int S, int tok, int per_tile, int32_t* off, int32_t* tile, int* bad) {
+  const int lane = threadIdx.x & 31, per = (G + 31) >> 5;
+  int64_t rows = 0, units = 0;
+  bool neg = false;
+  auto split = [&](int g) -> int64_t { return splits != nullptr ? (int64_t)__ldg(splits + g) : (int64_t)S; };
+  auto units_of = [&](int64_t m) { return (m + tok - 1) / tok * per_tile; };
+  for (int i = 0; i < per; ++i) {
+    const int g = lane * per + i;
+    const int64_t m = g < G ? split(g) : 0;
+    neg |= m < 0;
+    rows += m;
+    units += units_of(m > 0 ? m : 0);
+  }
+  int64_t rs = rows, us = units;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t orow = __shfl_up_sync(kFull, rs, d), ou = __shfl_up_sync(kFull, us, d);
+    if (lane >= d) { rs += orow; us += ou; }
+  }
+  const bool wrong = __any_sync(kFull, neg) || __shfl_sync(kFull, rs, 31) != S;
+  rows = rs - rows;
+  units = us - units;
+  for (int i = 0; i < per && !wrong; ++i) {
+    const int g = lane * per + i;
+    if (g < G) {
+      off[g] = (int32_t)rows;
+      tile[g] = (int32_t)units;
+      const int64_t m = split(g);
+      rows += m;
+      units += units_of(m);
+    }
+  }
+  if (lane == 31) {
+    off[G] = (int32_t)rs;
+    tile[G] = (int32_t)us;
+    *bad = wrong;
+  }
+}
+
+MXG_DEVINL uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // ---------------------------------------------------------------------------
-// Product
+// A few rows per expert: integer dot products on the CUDA cores.  A unit is kDotRows
+// channels of one expert against up to 8 of its rows; its warp reads the channels'
+// codes once, 16 bytes a lane and channel, and the rows' bytes from shared memory,
+// where the CTA has put them (FP16 codes narrowed to bytes again).  Sums are 32-bit
+// integers.  A CTA takes an equal run of units, in the order expert, tile of rows,
+// channels.  Against the tensor-core form: no pipeline to fill, no join, one launch
+// (1 row, 4096 x 7168: ZZ us against ZZ); bound by HBM up to about 4 rows, then by
+// the dot products, one for 4 bytes and row (128 rows of 32 experts: ZZ against ZZ).
+// ---------------------------------------------------------------------------
+constexpr int kDotTok = 8;
+constexpr int kDotThreads = 256;
+constexpr int kDotWarps = kDotThreads / 32;
+constexpr int64_t kDotMaxK = 25600;  // 8 rows of it fit shared memory
+
+struct DotParams {
+  const int32_t* splits;
+  int G, S, N, K;
+  int per_tile;      // units of a tile of rows
+  const uint8_t* a;
+  int64_t ld_a;
+  int f16;           // the rows' codes are FP16
+  const float* sa;
+  const uint8_t* w;
+  int64_t ld_w;
+  const float* sw;
+  void* out;
+  int64_t ld_out;
+  int out_f32;
+  int32_t* status;
+};
+
+// 16 FP16 codes -> 16 bytes: q + 1536 has q in its low byte.
+MXG_DEVINL uint4 narrow16(const uint4& a, const uint4& b) {
+  const __half2 bias = __half2half2(__ushort_as_half(0x6600));
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2 s = __hadd2(*reinterpret_cast<const __half2*>(&w[i]), bias);
+    h[i] = *reinterpret_cast<const uint32_t*>(&s);
+  }
+  return make_uint4(__byte_perm(h[0], h[1], 0x6420), __byte_perm(h[2], h[3], 0x6420), __byte_perm(h[4], h[5], 0x6420),
+                    __byte_perm(h[6], h[7], 0x6420));
+}
+
+MXG_DEVINL uint4 ld_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// kR channels against n <= kT rows.
+template <int kR, int kT>
+MXG_DEVINL void dot_unit(const DotParams& p, const uint8_t* x, int e, int tok0, int n, int chan0) {
+  constexpr int kSteps = kR == 4 ? 4 : 8;  // 512 bytes of every channel each, in flight together
+  const int lane = threadIdx.x & 31;
+  const uint8_t* w[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) w[r] = p.w + ((int64_t)e * p.N + min(chan0 + r, p.N - 1)) * p.ld_w;
+  int acc[kR][kT];
+#pragma unroll
+  for (int r = 0; r < kR; ++r)
+#pragma unroll
+    for (int t = 0; t < kT; ++t) acc[r][t] = 0;
+  for (int k0 = lane * 16; k0 < p.K; k0 += 512 * kSteps) {
+    uint4 v[kSteps][kR];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+        v[s][r] = k0 + 512 * s < p.K ? ld_stream(w[r] + k0 + 512 * s) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      if (k0 + 512 * s < p.K) {
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          if (t < n) {
+            const uint4 a = *reinterpret_cast<const uint4*>(x + (int64_t)t * p.K + k0 + 512 * s);
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+              acc[r][t] = __dp4a((int)a.x, (int)v[s][r].x, acc[r][t]);
+              acc[r][t] = __dp4a((int)a.y, (int)v[s][r].y, acc[r][t]);
+              acc[r][t] = __dp4a((int)a.z, (int)v[s][r].z, acc[r][t]);
+              acc[r][t] = __dp4a((int)a.w, (int)v[s][r].w, acc[r][t]);
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  // lane t kR + r has channel r of row t
+  int sum = 0;
+#pragma unroll
+  for (int t = 0; t < kT; ++t)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const int v = __reduce_add_sync(kFull, acc[r][t]);
+      if (lane == t * kR + r) sum = v;
+    }
+  const int t = lane / kR, chan = chan0 + lane % kR;
+  if (t < n && t < kT && chan < p.N) {
+    const float y = (float)sum * __ldg(p.sw + (int64_t)e * p.N + chan) * __ldg(p.sa + tok0 + t);
+    const int64_t at = (int64_t)(tok0 + t) * p.ld_out + chan;
+    if (p.out_f32) static_cast<float*>(p.out)[at] = y;
+    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+  }
+}
+
+template <int kR>
+__global__ void __launch_bounds__(kDotThreads) int8_dot_kernel(const DotParams p) {
+  extern __shared__ __align__(16) uint8_t x[];  // [rows][K]
+  __shared__ int32_t off[kMaxExperts + 1], tile[kMaxExperts + 1];
+  __shared__ int bad;
+  const int warp = threadIdx.x >> 5;
+  if (warp == 0) plan_units(p.splits, p.G, p.S, kDotTok, p.per_tile, off, tile, &bad);
+  __syncthreads();
+  if (bad) {  // every CTA sees it: nothing is written
+    if (threadIdx.x == 0) report(p.status, MXG_ERR_SPLITS);
+    return;
+  }
+  const int64_t units = tile[p.G];
+  int u = (int)(units * blockIdx.x / gridDim.x);
+  const int end = (int)(units * (blockIdx.x + 1) / gridDim.x);
+  while (u < end) {  // a tile of rows at a time
+    const int e = find_prefix(tile, p.G, u), tt = (u - tile[e]) / p.per_tile;
+    const int first = tile[e] + tt * p.per_tile, last = min(end, first + p.per_tile);
+    const int tok0 = off[e] + tt * kDotTok, n = min(kDotTok, off[e + 1] - tok0);
+    __syncthreads();  // the rows before are no longer read
+    const int pieces = p.K / 16;
+    for (int i = threadIdx.x; i < n * pieces; i += kDotThreads) {
+      const int t = i / pieces, c = i - t * pieces;
+      const uint8_t* src = p.a + (int64_t)(tok0 + t) * p.ld_a;
+      uint4 v;
+      if (p.f16) {
+        const uint4* s = reinterpret_cast<const uint4*>(src) + 2 * c;
+        v = narrow16(__ldg(s), __ldg(s + 1));
+      } else {
+        v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+      }
+      reinterpret_cast<uint4*>(x)[i] = v;
+    }
+    __syncthreads();
+    for (int i = u + warp; i < last; i += kDotWarps) {
+      const int chan0 = (i - first) * kR;
+      if (n == 1) dot_unit<kR, 1>(p, x, e, tok0, n, chan0);
+      else if (n == 2) dot_unit<kR, 2>(p, x, e, tok0, n, chan0);
+      else if (n <= 4) dot_unit<kR, 4>(p, x, e, tok0, n, chan0);
+      else dot_unit<kR, 8>(p, x, e, tok0, n, chan0);
+    }
+    u = last;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Product on the tensor cores
 // ---------------------------------------------------------------------------
 constexpr int kChan = 128;                 // channels of a CTA's tile (TMEM lanes)
 constexpr int kStageK = 128;               // contraction elements of a stage
 constexpr int kWBytes = kChan * kStageK;
 constexpr int kI8TmemCols = 512;
 constexpr int kACols = kStageK / 2;        // TMEM columns of a stage's weights (two FP16 a column)
-constexpr int kI8MaxCtas = 160;            // partial buffers are sized for this many CTAs
-constexpr int kI8SyncWords = 4 * kI8MaxCtas;
+constexpr int kI8MaxPairs = 80;            // partial buffers are sized for this many pairs
+constexpr int kI8SyncWords = 8 * kI8MaxPairs;
 constexpr int kI8MinStages = 4;            // shortest run of cut units
+constexpr uint32_t kWatchBar = 1;          // named barrier of the issuer and the warp that waits for it
 
-// kCta: CTAs of a tile, kTok: its tokens.  Accumulators first (two of them, but
-// for the pairs' 256 columns), then the ring of widened weights.
-template <int kCta, int kTok>
+// kTok: the tokens of a tile.  Accumulators first (two of them, but for 256
+// columns), then the ring of widened weights.
+template <int kTok>
 struct I8Cfg {
   static constexpr int kBufs = kTok == 256 ? 1 : 2;
-  // Groups of four widening warps.  A pair's stage lasts 1024 clocks, which one
-  // group keeps up with, and its epilogue needs the registers.
-  static constexpr int kGroups = kCta == 2 ? 1 : 2;
-  static constexpr int kThreads = 32 * (6 + 4 * kGroups);
-  static constexpr int kRows = kTok / kCta;            // tokens whose elements this CTA loads
+  static constexpr bool kCut = kTok < 256;             // units may be cut over pairs
+  // Groups of four widening warps.  With 256 tokens a stage lasts 1024 clocks, which
+  // one group keeps up with, and the epilogue needs the registers.
+  static constexpr int kGroups = kTok == 256 ? 1 : 2;
+  static constexpr int kWatch = 6 + 4 * kGroups;       // the warp that waits for the issuer
+  static constexpr int kThreads = 32 * (kWatch + (kCut ? 1 : 0));
+  static constexpr int kRows = kTok / 2;               // tokens whose elements a CTA loads
   static constexpr int kXBox = kRows * 128;            // 64 elements of each
   static constexpr int kStageBytes = kWBytes + 2 * kXBox;
   static constexpr int kACol = kTok >= 128 ? 256 : (kTok >= 64 ? 128 : 64);
-  // An even number: each group of widening warps then has its own stages and waits
-  // for every round of them (a group that came to a stage every other round could
-  // take the round before for its own).
-  static constexpr int kStages = (kI8TmemCols - kACol) / kACols & ~1;
+  // Slots of widened weights in TMEM, and stages in shared memory: more of them
+  // where a stage is small, since the loads' latency under load (about 2.3 us) is
+  // most of a stage's time.  Both are even: each group of widening warps then has
+  // its own stages and slots and sees every round of them (a group that came to a
+  // stage every other round could take the round before for its own).
+  static constexpr int kSlots = (kI8TmemCols - kACol) / kACols & ~1;
+  static constexpr int kStages = kTok == 32 ? 10 : kTok == 64 ? 8 : kTok == 128 ? 6 : 4;
   static constexpr int kBarOff = kStages * kStageBytes;
   static constexpr int kBars = 3 * kStages + 5;
   static constexpr int kMiscOff = kBarOff + ((kBars * 8 + 15) & ~15);
   static constexpr int kOffOff = kMiscOff + 16;                      // int32 [G + 1]: first row of each expert
   static constexpr int kTileOff = kOffOff + (kMaxExperts + 4) * 4;   // int32 [G + 1]: first unit of each expert
-  static constexpr int kSaOff = kTileOff + (kMaxExperts + 4) * 4;    // float [4][256]: the tile's token scales (pairs)
-  static constexpr int kTotal = kSaOff + (kCta == 2 ? 4 * kTok * 4 : 0) + 1024;  // + alignment slack
+  static constexpr int kSaOff = kTileOff + (kMaxExperts + 4) * 4;    // float [4][256]: the tile's token scales (256 tokens)
+  static constexpr int kTotal = kSaOff + (kCut ? 0 : 4 * kTok * 4) + 1024;  // + alignment slack
   static_assert(kSaOff % 16 == 0, "token scales are read 16 bytes at a time");
-  static_assert(kBufs * kTok <= kACol && kACol + kStages * kACols <= kI8TmemCols, "TMEM holds accumulators and ring");
+  static_assert(kBufs * kTok <= kACol && kACol + kSlots * kACols <= kI8TmemCols, "TMEM holds accumulators and ring");
   static_assert(kStageBytes % 1024 == 0 && kXBox % 1024 == 0, "tiles keep the swizzle-atom alignment");
   static_assert(kTotal <= 232448, "fits the 227 KB of one CTA");
+  static_assert(kSlots % 2 == 0 && kStages % 2 == 0 && kSlots <= kStages, "see above");
 };
 
 struct I8Params {
@@ -222,28 +434,28 @@ struct I8Params {
   void* out;
   int64_t ld_out;
   int out_f32;
-  float* part;            // [2 * CTAs][kTok][128] partial sums of cut units
-  uint32_t* sync;         // [CTAs][4] arrivals at a cut unit
+  float* part;            // [2 * pairs][2][kTok][128] partial sums of cut units
+  uint32_t* sync;         // [pairs][8] arrivals at a cut unit
   int wide_from_prep;     // the activations come from the kernel before
   int32_t* status;
   uint64_t timeout_ns, drain_ns;
   uint32_t idesc;
 };
 
-// The stages of all units cut into equal runs (to one grain), one per CTA.
+// The stages of all units cut into equal runs (to one grain), one per pair.
 struct I8Runs {
-  int per_unit, grain, ctas, q, r;
-  MXG_DEVINL I8Runs(int units, int per_unit_, int tokens, int max_ctas) : per_unit(per_unit_) {
-    // whole units to every CTA, or units cut into equal runs: what ends sooner,
+  int per_unit, grain, pairs, q, r;
+  MXG_DEVINL I8Runs(int units, int per_unit_, int tokens, int max_pairs) : per_unit(per_unit_) {
+    // whole units to every pair, or units cut into equal runs: what ends sooner,
     // a join taking as long as some 8 + tokens / 4 stages
     const int total = units * per_unit;
-    const int whole = (units + max_ctas - 1) / max_ctas * per_unit;
-    const int run = max((total + max_ctas - 1) / max_ctas, kI8MinStages);
+    const int whole = (units + max_pairs - 1) / max_pairs * per_unit;
+    const int run = max((total + max_pairs - 1) / max_pairs, kI8MinStages);
     const int cut = run + (run >= 2 * per_unit ? 3 : 8 + tokens / 4);
     grain = whole <= cut ? per_unit : 1;
-    ctas = min(max_ctas, grain > 1 || per_unit == 1 ? units : (total + kI8MinStages - 1) / kI8MinStages);
-    q = ctas > 0 ? total / grain / ctas : 0;
-    r = ctas > 0 ? total / grain - q * ctas : 0;
+    pairs = min(max_pairs, grain > 1 || per_unit == 1 ? units : (total + kI8MinStages - 1) / kI8MinStages);
+    q = pairs > 0 ? total / grain / pairs : 0;
+    r = pairs > 0 ? total / grain - q * pairs : 0;
   }
   MXG_DEVINL int start(int b) const { return (b * q + min(b, r)) * grain; }
   MXG_DEVINL int owner(int s) const {
@@ -252,16 +464,16 @@ struct I8Runs {
   }
 };
 
-// Walks a CTA's units: of a run, the cut unit at its start, the cut unit at its
-// end, then the whole units; of a pair, every npairs-th unit.
-template <int kCta, int kTok>
+// Walks a pair's units: of a run, the cut unit at its start, the cut unit at its
+// end, then the whole units; with 256 tokens, every `per_unit`-th unit.
+template <int kTok>
 struct I8Walker {
-  int s, end, per_unit;      // what is left of the run (pairs: the next unit, all units, the stride)
+  int s, end, per_unit;      // what is left of the run (256 tokens: the next unit, all units, the stride)
   int unit, k0, k1;          // the current unit and its stages [k0, k1)
   int e, tok0, n, chan0;     // expert, first row, rows, first channel of the tile
   MXG_DEVINL bool next(const I8Params& p, const int32_t* off, const int32_t* tile) {
     if (s >= end) return false;
-    if constexpr (kCta == 2) {
+    if constexpr (!I8Cfg<kTok>::kCut) {
       unit = s;
       s += per_unit;
       k0 = 0;
@@ -292,36 +504,29 @@ struct I8Walker {
     const int rows = off[e + 1] - off[e];
     n = min(kTok, rows - tt * kTok);
     tok0 = off[e] + tt * kTok;
-    chan0 = ct * kChan * kCta;
+    chan0 = ct * 2 * kChan;
     return true;
   }
 };
 
-// Tokens that a pair's MMAs take: the tile's, to a multiple of 32 (half of them in
-// each CTA).  The last tile of an expert is often short: 8192 rows of 8 experts,
-// 4096 x 14336, take ZZ us with it and ZZ with 256 throughout.
-MXG_DEVINL int pair_tokens(int n) { return (n + 31) & ~31; }
+// Tokens that the MMAs of a tile take: its own, to a multiple of 16 (half of them
+// in each CTA).  An expert's last tile is often short.
+MXG_DEVINL int mma_tokens(int n) { return (n + 15) & ~15; }
 
-MXG_DEVINL uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-// A pair (kCta = 2, a cluster of two CTAs): the even CTA issues the MMAs of both
-// (M = 256: its TMEM has channels 0-127 of the tile, the odd CTA's 128-255; each
-// has half of the tokens' elements in shared memory).  The widening warps and the
-// epilogues of both arrive on the even CTA's barriers, and every commit reaches
-// the barriers of both.
-template <int kCta, int kTok>
-__global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
+// The even CTA issues the MMAs of both (M = 256: its TMEM has channels 0-127 of the
+// tile, the odd CTA's 128-255; each has half of the tokens' elements in shared
+// memory).  The widening warps and the epilogues of both arrive on the even CTA's
+// barriers, and every commit reaches the barriers of both.
+template <int kTok>
+__global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const I8Params p) {
-  using L = I8Cfg<kCta, kTok>;
+  using L = I8Cfg<kTok>;
   constexpr int kStages = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = ptx::smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kCta == 2 ? (int)ptx::cluster_ctarank() : 0;
+  const int rank = (int)ptx::cluster_ctarank();
 
   const uint32_t bar0 = sbase + L::kBarOff;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };                     // the stage's bytes are here
@@ -336,64 +541,23 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
   int32_t* off = reinterpret_cast<int32_t*>(smem + L::kOffOff);
   int32_t* tile = reinterpret_cast<int32_t*>(smem + L::kTileOff);
   // arrive on the issuing CTA's barrier (the even CTA of a pair)
-  auto arrive_issuer = [&](uint32_t bar) {
-    if constexpr (kCta == 2) ptx::mbar_arrive_cluster(ptx::mapa_shared(bar, 0));
-    else ptx::mbar_arrive(bar);
-  };
+  auto arrive_issuer = [&](uint32_t bar) { ptx::mbar_arrive_cluster(ptx::mapa_shared(bar, 0)); };
 
-  // ---------------------------------------------------------------- plan
-  if (warp == 0) {  // rows and units of every expert: lane l has experts [l * per, l * per + per)
-    const int per = (p.G + 31) >> 5;
-    int64_t rows = 0, units = 0;
-    bool neg = false;
-    auto split = [&](int g) -> int64_t { return p.splits != nullptr ? (int64_t)__ldg(p.splits + g) : (int64_t)p.S; };
-    auto units_of = [&](int64_t m) { return (m + kTok - 1) / kTok * p.n_chan; };
-    for (int i = 0; i < per; ++i) {
-      const int g = lane * per + i;
-      const int64_t m = g < p.G ? split(g) : 0;
-      neg |= m < 0;
-      rows += m;
-      units += units_of(m > 0 ? m : 0);
-    }
-    int64_t rs = rows, us = units;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t orow = __shfl_up_sync(kFull, rs, d), ou = __shfl_up_sync(kFull, us, d);
-      if (lane >= d) { rs += orow; us += ou; }
-    }
-    const bool bad = __any_sync(kFull, neg) || __shfl_sync(kFull, rs, 31) != p.S;
-    rows = rs - rows;
-    units = us - units;
-    for (int i = 0; i < per && !bad; ++i) {
-      const int g = lane * per + i;
-      if (g < p.G) {
-        off[g] = (int32_t)rows;
-        tile[g] = (int32_t)units;
-        const int64_t m = split(g);
-        rows += m;
-        units += units_of(m);
-      }
-    }
-    if (lane == 31) {
-      off[p.G] = (int32_t)rs;
-      tile[p.G] = (int32_t)us;
-    }
-    if (lane == 0) {
-      *bad_flag = bad;
-      *abort_flag = 0;
-    }
+  if (warp == 0) {
+    plan_units(p.splits, p.G, p.S, kTok, p.n_chan, off, tile, bad_flag);
+    if (lane == 0) *abort_flag = 0;
   } else if (warp == 1) {
-    ptx::tmem_alloc_g<kCta>(ptx::smem_u32(tmem_slot), kI8TmemCols);
-    ptx::tmem_relinquish_g<kCta>();
+    ptx::tmem_alloc_g<2>(ptx::smem_u32(tmem_slot), kI8TmemCols);
+    ptx::tmem_relinquish_g<2>();
   } else if (threadIdx.x == 64) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
-      ptx::mbar_init(ready_bar(s), 4 * kCta);
+      ptx::mbar_init(ready_bar(s), 8);  // four warps of either CTA
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(acc_full(b), 1);
-      ptx::mbar_init(acc_empty(b), 4 * kCta);
+      ptx::mbar_init(acc_empty(b), 8);
     }
     ptx::mbar_init(drain_bar, 1);
     ptx::fence_mbar_init();
@@ -403,25 +567,25 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   // the peer's barriers are initialised before any remote arrival or commit reaches them
-  if constexpr (kCta == 2) ptx::cluster_sync();
+  ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool bad = *bad_flag != 0;  // every CTA sees it: nothing is written
   if (bad && threadIdx.x == 0) report(p.status, MXG_ERR_SPLITS);
 
   const int units = bad ? 0 : tile[p.G];
-  const int cta = blockIdx.x;
-  const I8Runs runs(units, p.nk, units > 0 ? off[p.G] / (units / p.n_chan) : 0, gridDim.x);
-  I8Walker<kCta, kTok> w;
-  if constexpr (kCta == 2) {
-    w.s = (int)ptx::cluster_id_x();
-    w.end = units;
-    w.per_unit = (int)ptx::nclusters_x();
-  } else {
-    const bool active = cta < runs.ctas;
-    w.s = active ? runs.start(cta) : 0;
-    w.end = active ? runs.start(cta + 1) : 0;
+  const int pair = (int)ptx::cluster_id_x(), pairs = (int)ptx::nclusters_x();
+  const I8Runs runs(units, p.nk, units > 0 ? off[p.G] / (units / p.n_chan) : 0, pairs);
+  I8Walker<kTok> w;
+  if constexpr (L::kCut) {
+    const bool active = pair < runs.pairs;
+    w.s = active ? runs.start(pair) : 0;
+    w.end = active ? runs.start(pair + 1) : 0;
     w.per_unit = p.nk;
+  } else {
+    w.s = pair;
+    w.end = units;
+    w.per_unit = pairs;
   }
 
   if (warp == 0) {
@@ -433,7 +597,7 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
       if (p.wide_from_prep) ptx::pdl_wait();  // the widened activations are complete
       while (ok && w.next(p, off, tile)) {
         const int row_w = w.e * p.N + w.chan0 + rank * kChan;
-        const int row_x = w.tok0 + (kCta == 2 ? rank * pair_tokens(w.n) / 2 : 0);
+        const int row_x = w.tok0 + rank * mma_tokens(w.n) / 2;
         for (int kc = w.k0; kc < w.k1; ++kc) {
           if (!ptx::mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
           const uint32_t fb = full_bar(stage);
@@ -457,63 +621,90 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop in step (each wait ends in a vote) and one
-    // lane issues and hands the stages back.
+    // lane issues and hands the stages back.  A wait on an mbarrier by the thread
+    // that issues holds it until its MMAs are done.  256 tokens' MMAs take longer
+    // than that; for fewer a second warp waits and meets the issuer at a named
+    // barrier (32 experts of 4096 x 7168, 128 rows: ZZ us, ZZ with the waits here).
     if (rank == 0) {
       const uint32_t el = lane == 0;
       const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-      int stage = 0, count = 0;
+      int stage = 0, slot = 0, count = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false;
       while (ok && w.next(p, off, tile)) {
         const int buf = L::kBufs == 2 ? count & 1 : 0;
-        const uint32_t round = L::kBufs == 2 ? (uint32_t)(count >> 1) : (uint32_t)count;
-        ok = ptx::mbar_wait_warp(acc_empty(buf), (round & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns);
-        if (!ok) break;
-        ptx::tc_fence_after();
+        if constexpr (!L::kCut) {
+          ok = ptx::mbar_wait_warp(acc_empty(buf), (count & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns);
+          if (!ok) break;
+        }
         const uint32_t d = tm + buf * kTok;
-        const uint32_t idesc = kCta == 2 ? p.idesc | ((uint32_t)(pair_tokens(w.n) >> 3) << 17) : p.idesc;
+        const uint32_t idesc = p.idesc | ((uint32_t)(mma_tokens(w.n) >> 3) << 17);
         for (int kc = w.k0; kc < w.k1; ++kc) {
-          ok = ptx::mbar_wait_warp(ready_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
+          if constexpr (L::kCut) ok = !ptx::named_bar_or(kWatchBar, 64, false);
+          else ok = ptx::mbar_wait_warp(ready_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t a = tm + L::kACol + stage * kACols;
+          const uint32_t a = tm + L::kACol + slot * kACols;
           const uint64_t b = ptx::smem_desc(sbase + stage * L::kStageBytes + kWBytes, 16, 1024, 2);
 #pragma unroll
           for (int j = 0; j < 8; ++j)  // 16 contraction elements: 8 columns, 32 bytes of each token's row
-            ptx::mma_f16_ts_if<kCta>(el, d, a + 8 * j, b + (uint64_t)((j >> 2) * (L::kXBox >> 4) + 2 * (j & 3)), idesc,
-                                     (kc != w.k0) || j != 0);
+            ptx::mma_f16_ts_pair_if(el, d, a + 8 * j, b + (uint64_t)((j >> 2) * (L::kXBox >> 4) + 2 * (j & 3)), idesc,
+                                    (kc != w.k0) || j != 0);
           issued = true;
-          ptx::tc_commit_pair_if<kCta>(el, empty_bar(stage));
+          ptx::tc_commit_pair_if(el, empty_bar(stage));
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
+          if (++slot == L::kSlots) slot = 0;
         }
         if (!ok) break;
-        ptx::tc_commit_pair_if<kCta>(el, acc_full(buf));
+        ptx::tc_commit_pair_if(el, acc_full(buf));
         ++count;
       }
       if (issued) {  // every MMA has retired before TMEM is released
-        if (lane == 0) ptx::tc_commit_g<kCta>(drain_bar);
+        if (lane == 0) ptx::tc_commit_g<2>(drain_bar);
         volatile int no_abort = 0;
         ptx::mbar_wait(drain_bar, 0, &no_abort, p.status, p.drain_ns);
+      }
+    }
+  } else if (L::kCut && warp == L::kWatch) {
+    // ------------------------------------------------------------ the issuer's waits
+    if (rank == 0) {
+      int stage = 0, count = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && w.next(p, off, tile)) {
+        ok = ptx::mbar_wait_warp(acc_empty(count & 1), ((count >> 1) & 1u) ^ 1u, abort_flag, p.status, p.timeout_ns);
+        for (int kc = w.k0; kc < w.k1; ++kc) {
+          if (ok) ok = ptx::mbar_wait_warp(ready_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
+          if (ptx::named_bar_or(kWatchBar, 64, !ok)) break;  // the issuer leaves as well
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+        ++count;
       }
     }
   } else if (warp >= 6) {
     // ------------------------------------------------------------ weights to FP16
     // A thread takes a channel: 128 bytes of its row (16-byte piece c at
-    // c ^ (row % 8)) become 64 TMEM columns of its lane.  The stage's slot in TMEM
-    // is free: its bytes were loaded after the MMAs that read it had completed.
+    // c ^ (row % 8)) become 64 TMEM columns of its lane.  The slot there is free
+    // once the MMAs of kSlots stages ago have completed: they were committed to
+    // that stage's empty barrier (with as many slots as stages, before this
+    // stage's bytes were even loaded).
     const int group = (warp - 6) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16) + L::kACol;
     const uint32_t src0 = sbase + row * 128;
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
+    int stage = 0, slot = 0, old = 0;  // old: the stage of kSlots ago
+    uint32_t phase = 0, old_phase = 0;
+    bool ok = true, wrapped = false;   // wrapped: the slots have been used before
     while (ok && w.next(p, off, tile)) {
       for (int kc = w.k0; kc < w.k1; ++kc) {
         if (L::kGroups == 1 || (stage & 1) == group) {
           ok = ptx::mbar_wait_warp(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
           if (!ok) break;
+          if (L::kSlots < kStages && wrapped) {
+            ok = ptx::mbar_wait_warp(empty_bar(old), old_phase, abort_flag, p.status, p.timeout_ns);
+            if (!ok) break;
+          }
           ptx::tc_fence_after();
-          const uint32_t src = src0 + stage * L::kStageBytes, dst = tq + stage * kACols;
+          const uint32_t src = src0 + stage * L::kStageBytes, dst = tq + slot * kACols;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t o[32];
@@ -532,6 +723,8 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
           if (lane == 0) arrive_issuer(ready_bar(stage));
         }
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        if (wrapped && ++old == kStages) { old = 0; old_phase ^= 1u; }
+        if (++slot == L::kSlots) { slot = 0; wrapped = true; }
       }
     }
   } else {
@@ -539,9 +732,9 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
     // Warp q has TMEM lanes 32 q .. 32 q + 31: a lane is a channel, a column a token.
     const int quarter = warp & 3;
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
-    constexpr int kCols = kTok >= 32 ? 32 : 16;  // columns of a read
+    constexpr int kCols = 32;  // columns of a read
     int count = 0;
-    if constexpr (kCta == 1) ptx::pdl_wait();  // the kernel before has zeroed the counters
+    if constexpr (L::kCut) ptx::pdl_wait();  // the kernel before has zeroed the counters
     while (w.next(p, off, tile)) {
       const int buf = L::kBufs == 2 ? count & 1 : 0;
       const uint32_t round = L::kBufs == 2 ? (uint32_t)(count >> 1) : (uint32_t)count;
@@ -549,7 +742,7 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
       const bool in = chan < p.N;
       const float sw = in ? __ldg(p.sw + (int64_t)w.e * p.N + chan) : 0.0f;
       float* sa_tile = reinterpret_cast<float*>(smem + L::kSaOff) + quarter * kTok;
-      if constexpr (kCta == 2) {  // the warp's copy of the token scales
+      if constexpr (!L::kCut) {  // the warp's copy of the token scales
         __syncwarp();
         for (int i = lane; i < kTok; i += 32) sa_tile[i] = i < w.n ? __ldg(p.sa + w.tok0 + i) : 0.0f;
         __syncwarp();
@@ -558,7 +751,7 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
       ptx::tc_fence_after();
       ++count;
       const uint32_t d = tq + buf * kTok;
-      if constexpr (kCta == 2) {
+      if constexpr (!L::kCut) {
         // BF16: the tile's values as 128 pairs of tokens in registers, the
         // accumulator handed back, then the stores, while the next tile's MMAs run.
         auto release = [&]() {
@@ -618,15 +811,10 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
         }
         continue;
       }
-      const bool whole = kCta == 2 || (w.k0 == 0 && w.k1 == runs.per_unit);
+      const bool whole = w.k0 == 0 && w.k1 == runs.per_unit;
       auto read = [&](int c0, float* v) {
         __syncwarp();
-        if constexpr (kCols == 32) {
-          ptx::tmem_ld_32x32b_x32(d + c0, reinterpret_cast<uint32_t*>(v));
-        } else {
-          ptx::tmem_ld_32x32b_x8(d + c0, reinterpret_cast<uint32_t*>(v));
-          ptx::tmem_ld_32x32b_x8(d + c0 + 8, reinterpret_cast<uint32_t*>(v) + 8);
-        }
+        ptx::tmem_ld_32x32b_x32(d + c0, reinterpret_cast<uint32_t*>(v));
         ptx::tmem_ld_wait();
         if (c0 + kCols >= w.n) {  // last read: hand the accumulator back
           ptx::tc_fence_before();
@@ -634,9 +822,9 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
           if (lane == 0) arrive_issuer(acc_empty(buf));
         }
       };
-      int first = 0, last = -1;  // the CTAs of a cut unit
+      int first = 0, last = -1;  // the pairs of a cut unit
       if (!whole) {
-        float* mine = p.part + ((int64_t)(2 * cta + (w.k0 == 0)) * kTok) * kChan + quarter * 32 + lane;
+        float* mine = p.part + ((int64_t)(4 * pair + 2 * (w.k0 == 0) + rank) * kTok) * kChan + quarter * 32 + lane;
         for (int c0 = 0; c0 < w.n; c0 += kCols) {
           float v[kCols];
           read(c0, v);
@@ -648,7 +836,7 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
         __threadfence();
         __syncwarp();
         uint32_t got = 0;
-        if (lane == 0) got = atomicInc(p.sync + (first + 1) * 4 + quarter, (uint32_t)(last - first));
+        if (lane == 0) got = atomicInc(p.sync + (first + 1) * 8 + rank * 4 + quarter, (uint32_t)(last - first));
         got = __shfl_sync(kFull, got, 0);
         if (got != (uint32_t)(last - first)) continue;
         __threadfence();
@@ -661,12 +849,12 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) v[i] = 0.0f;
           for (int b = first; b <= last; ++b) {  // in run order: buffers 2 first + 1, 2 (first + 1), ...
-            const float* src = p.part + ((int64_t)(2 * b + (b == first)) * kTok + c0) * kChan + quarter * 32 + lane;
+            const float* src = p.part + ((int64_t)(4 * b + 2 * (b == first) + rank) * kTok + c0) * kChan + quarter * 32 + lane;
 #pragma unroll
             for (int i = 0; i < kCols; ++i) v[i] += c0 + i < w.n ? __ldcg(src + i * kChan) : 0.0f;
           }
         }
-        const float sa = c0 + lane < w.n && lane < kCols ? __ldg(p.sa + w.tok0 + c0 + lane) : 0.0f;
+        const float sa = c0 + lane < w.n ? __ldg(p.sa + w.tok0 + c0 + lane) : 0.0f;
         if (p.out_f32) {
           float* dst = static_cast<float*>(p.out) + (int64_t)(w.tok0 + c0) * p.ld_out + chan;
 #pragma unroll
@@ -694,11 +882,11 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   // neither CTA of a pair leaves while the other's MMAs or arrivals may reach it
-  if constexpr (kCta == 2) ptx::cluster_sync();
+  ptx::cluster_sync();
   if (warp == 1) {
     __syncwarp();
     ptx::tc_fence_after();
-    ptx::tmem_dealloc_g<kCta>(tmem, kI8TmemCols);
+    ptx::tmem_dealloc_g<2>(tmem, kI8TmemCols);
   }
 }
 
@@ -707,33 +895,34 @@ __global__ void __launch_bounds__(I8Cfg<kCta, kTok>::kThreads, 1)
 // ---------------------------------------------------------------------------
 struct I8Form {
   const void* fn;
-  int cta, tok, smem, threads;
+  int tok, smem, threads;
+  bool cut;
 };
-template <int kCta, int kTok>
+template <int kTok>
 I8Form form_of() {
-  return {(const void*)int8_gemm_kernel<kCta, kTok>, kCta, kTok, I8Cfg<kCta, kTok>::kTotal,
-          I8Cfg<kCta, kTok>::kThreads};
+  return {(const void*)int8_gemm_kernel<kTok>, kTok, I8Cfg<kTok>::kTotal, I8Cfg<kTok>::kThreads, I8Cfg<kTok>::kCut};
 }
-constexpr int kI8Forms = 5;
+constexpr int kI8Forms = 4;
 I8Form i8_form(int i) {
   switch (i) {
-    case 0: return form_of<1, 16>();
-    case 1: return form_of<1, 32>();
-    case 2: return form_of<1, 64>();
-    case 3: return form_of<1, 128>();
-    default: return form_of<2, 256>();
+    case 0: return form_of<32>();
+    case 1: return form_of<64>();
+    case 2: return form_of<128>();
+    default: return form_of<256>();
   }
 }
 
-// The form for S rows over G experts: tiles that hold half as many tokens again as
-// the mean expert's, pairs from there on.
+// The form for S rows over G experts, by the rows of the mean expert that has some:
+// dot products (-1) for very few; tiles that hold half as many again as the mean;
+// whole units of 256 from there on.
+constexpr int kDot = -1;
 int i8_choose(int64_t S, int G, int64_t N, int64_t K) {
   (void)N;
-  (void)K;
-  const int64_t mean = S / std::max<int64_t>(1, std::min<int64_t>(S, G));
-  for (int i = 0; i < 4; ++i)
+  const int64_t used = std::max<int64_t>(1, std::min<int64_t>(S, G)), mean = (S + used - 1) / used;
+  if (mean <= (G == 1 ? kDotTok : 4) && K <= kDotMaxK) return kDot;
+  for (int i = 0; i < 3; ++i)
     if (mean + mean / 2 <= i8_form(i).tok || (G == 1 && mean <= i8_form(i).tok)) return i;
-  return 4;
+  return 3;
 }
 
 struct I8Ws {
@@ -743,17 +932,20 @@ struct I8Ws {
   size_t total;
 };
 I8Ws i8_ws(int64_t S, int G, int64_t N, int64_t K, int codes, uint8_t* p) {
-  const I8Form f = i8_form(i8_choose(S, G, N, K));
+  const int form = i8_choose(S, G, N, K);
   I8Ws w{};
+  w.total = 256;
+  if (form == kDot) return w;  // needs none
+  const I8Form f = i8_form(form);
   size_t o = 0;
   auto take = [&](int64_t n) {
     uint8_t* r = p + o;
     o += ((size_t)n + 255) & ~(size_t)255;
     return r;
   };
-  if (f.cta == 1) {
+  if (f.cut) {
     w.sync = reinterpret_cast<uint32_t*>(take(kI8SyncWords * 4));
-    w.part = reinterpret_cast<float*>(take((int64_t)2 * kI8MaxCtas * f.tok * kChan * 4));
+    w.part = reinterpret_cast<float*>(take((int64_t)4 * kI8MaxPairs * f.tok * kChan * 4));
   }
   if (codes == MXG_CODES_INT8) w.wide = take(S * K * 2);
   w.total = std::max<size_t>(o, 256);
@@ -763,40 +955,39 @@ I8Ws i8_ws(int64_t S, int G, int64_t N, int64_t K, int codes, uint8_t* p) {
 constexpr int kI8MaxDevices = 64;
 std::mutex g_i8_mu;
 
+cudaLaunchAttribute pair_attr() {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = 2;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+
 // Per device and form, once: the dynamic shared-memory opt-in and the number of
-// pairs that can run together (0 where none can).
-bool i8_ready(int form, int dev, int* pairs) {
-  static bool done[kI8MaxDevices][kI8Forms] = {};
-  static int clusters[kI8MaxDevices] = {};
+// pairs that run together.  0 where none can.
+int i8_pairs(int form, int dev) {
+  static int pairs[kI8MaxDevices][kI8Forms] = {};
   std::lock_guard<std::mutex> lk(g_i8_mu);
-  if (dev < 0 || dev >= kI8MaxDevices) return false;
-  const I8Form f = i8_form(form);
-  if (!done[dev][form]) {
-    if (cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem) != cudaSuccess) {
+  if (dev < 0 || dev >= kI8MaxDevices) return 0;
+  int& n = pairs[dev][form];
+  if (n == 0) {
+    const I8Form f = i8_form(form);
+    cudaLaunchAttribute attr = pair_attr();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3((unsigned)f.threads);
+    cfg.dynamicSmemBytes = (size_t)f.smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, f.fn, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      return false;
+      n = 0;
     }
-    if (f.cta == 2) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(2);
-      cfg.blockDim = dim3((unsigned)f.threads);
-      cfg.dynamicSmemBytes = (size_t)f.smem;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&clusters[dev], f.fn, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-      }
-    }
-    done[dev][form] = true;
+    n = std::min(n, kI8MaxPairs);
   }
-  *pairs = clusters[dev];
-  return true;
+  return n;
 }
 
 // K-major FP16 map with a 128-byte swizzle: 64 elements x `box_rows`.
@@ -819,20 +1010,59 @@ cudaError_t launch_int8_quantize(const void* x, int64_t ld_x, const int32_t* row
 size_t int8_gemm_workspace_bytes(int64_t S, int G, int64_t N, int64_t K, int codes) {
   return i8_ws(S, G, N, K, codes, nullptr).total;
 }
-int int8_gemm_tile_tokens(int64_t S, int G, int64_t N, int64_t K) { return i8_form(i8_choose(S, G, N, K)).tok; }
-
-bool int8_gemm_sizes_fit(int64_t S, int G, int64_t N, int64_t K) {
-  const I8Form f = i8_form(i8_choose(S, G, N, K));
-  const int64_t units = (S / f.tok + std::min<int64_t>(S, G)) * cdiv(N, (int64_t)kChan * f.cta);
-  return units <= 0x7FFFFFFF / cdiv(K, kStageK);
+int int8_gemm_tile_tokens(int64_t S, int G, int64_t N, int64_t K) {
+  const int form = i8_choose(S, G, N, K);
+  return form == kDot ? kDotTok : i8_form(form).tok;
 }
 
+bool int8_gemm_sizes_fit(int64_t S, int G, int64_t N, int64_t K) {
+  const int form = i8_choose(S, G, N, K);
+  const int64_t tiles = S / (form == kDot ? kDotTok : i8_form(form).tok) + std::min<int64_t>(S, G);
+  if (form == kDot) return tiles <= 0x7FFFFFFF / cdiv(N, 2);
+  return tiles * cdiv(N, 2 * kChan) <= 0x7FFFFFFF / cdiv(K, kStageK);
+}
+
+namespace {
+mxg_status launch_int8_dot(const Int8GemmArgs& a, cudaStream_t stream, int num_sms, int dev) {
+  // Two channels a warp where four would leave warps without any.
+  const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(a.S, a.G));
+  const int slots = 2 * num_sms * kDotWarps;
+  const int per_warp = tiles * cdiv(a.N, 4) < slots ? 2 : 4;
+  const auto fn = per_warp == 2 ? int8_dot_kernel<2> : int8_dot_kernel<4>;
+  {
+    static bool done[kI8MaxDevices][2] = {};
+    std::lock_guard<std::mutex> lk(g_i8_mu);
+    if (dev < 0 || dev >= kI8MaxDevices) return MXG_ERR_CUDA;
+    bool& ready = done[dev][per_warp == 2];
+    if (!ready && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kDotTok * kDotMaxK)) != cudaSuccess) {
+      cudaGetLastError();
+      return MXG_ERR_CUDA;
+    }
+    ready = true;
+  }
+  DotParams p{};
+  p.splits = a.splits;
+  p.G = a.G; p.S = (int)a.S; p.N = (int)a.N; p.K = (int)a.K;
+  p.per_tile = (int)cdiv(a.N, per_warp);
+  p.a = a.a; p.ld_a = a.ld_a; p.f16 = a.codes == MXG_CODES_F16; p.sa = a.sa;
+  p.w = a.w; p.ld_w = a.ld_w; p.sw = a.sw;
+  p.out = a.out; p.ld_out = a.ld_out; p.out_f32 = a.out_dtype == MXG_OUT_F32;
+  p.status = a.status;
+  const size_t smem = (size_t)std::min<int64_t>(kDotTok, a.S) * a.K;
+  fn<<<2 * num_sms, kDotThreads, smem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return MXG_ERR_CUDA;
+  return MXG_OK;
+}
+}  // namespace
+
 mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_sms) {
-  int form = i8_choose(a.S, a.G, a.N, a.K);
-  const I8Form f = i8_form(form);
-  int dev = 0, pairs = 0;
+  const int form = i8_choose(a.S, a.G, a.N, a.K);
+  int dev = 0;
   cudaGetDevice(&dev);
-  if (!i8_ready(form, dev, &pairs) || (f.cta == 2 && pairs == 0)) return MXG_ERR_CUDA;
+  if (form == kDot) return launch_int8_dot(a, stream, num_sms, dev);
+  const I8Form f = i8_form(form);
+  const int pairs = i8_pairs(form, dev);
+  if (pairs == 0) return MXG_ERR_CUDA;
   const I8Ws ws = i8_ws(a.S, a.G, a.N, a.K, a.codes, static_cast<uint8_t*>(a.ws));
   const bool widen = a.codes == MXG_CODES_INT8 && a.S > 0;
 
@@ -840,7 +1070,7 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
   p.splits = a.splits;
   p.G = a.G; p.S = (int)a.S; p.N = (int)a.N;
   p.nk = (int)cdiv(a.K, kStageK);
-  p.n_chan = (int)cdiv(a.N, (int64_t)kChan * f.cta);
+  p.n_chan = (int)cdiv(a.N, 2 * kChan);
   // token tiles whose activations (about 32 MiB) stay in L2 over all channel tiles
   p.group_t = (int)std::max<int64_t>(1, (int64_t(32) << 20) / (f.tok * a.K * 2));
   p.sa = a.sa; p.sw = a.sw;
@@ -850,46 +1080,35 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
   p.status = a.status;
   p.timeout_ns = wait_timeout_ns();
   p.drain_ns = std::max<uint64_t>(p.timeout_ns, 200000000ull);
-  // instruction descriptor: FP16 operands, K-major, fp32 sums
-  p.idesc = (1u << 4) | ((uint32_t)((kChan * f.cta) >> 4) << 24);
-  if (f.cta == 1) p.idesc |= (uint32_t)(f.tok >> 3) << 17;  // a pair's tokens go by the tile
+  // instruction descriptor: FP16 operands, K-major, fp32 sums, M = 256 (N goes by the tile)
+  p.idesc = (1u << 4) | ((2 * kChan >> 4) << 24);
 
-  const bool prep = f.cta == 1 || widen;
+  const bool prep = f.cut || widen;
   if (prep) {
     const int64_t per_row = a.K / 16, items = std::max<int64_t>(widen ? a.S * per_row : 0, kI8SyncWords);
     const unsigned grid = (unsigned)std::min<int64_t>((items + kPrepThreads - 1) / kPrepThreads, (int64_t)num_sms * 16);
-    int8_prep_kernel<<<grid, kPrepThreads, 0, stream>>>(ws.sync, f.cta == 1 ? kI8SyncWords : 0, a.a, a.ld_a,
+    int8_prep_kernel<<<grid, kPrepThreads, 0, stream>>>(ws.sync, f.cut ? kI8SyncWords : 0, a.a, a.ld_a,
                                                         widen ? a.S : 0, per_row, reinterpret_cast<uint4*>(ws.wide));
     if (cudaGetLastError() != cudaSuccess) return MXG_ERR_CUDA;
   }
   CUtensorMap tmW, tmX;
   if (!make_tmap(&tmW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.K, (int64_t)a.G * a.N, a.ld_w, kStageK, kChan)) return MXG_ERR_CUDA;
   // without rows there is nothing to load and the map only has to be well formed
-  const bool ok = a.S == 0 ? make_f16_tmap(&tmX, a.w, 8, 1, 16, f.tok / f.cta)
-                  : widen  ? make_f16_tmap(&tmX, ws.wide, a.K, a.S, a.K * 2, f.tok / f.cta)
-                           : make_f16_tmap(&tmX, a.a, a.K, a.S, a.ld_a, f.tok / f.cta);
+  const bool ok = a.S == 0 ? make_f16_tmap(&tmX, a.w, 8, 1, 16, f.tok / 2)
+                  : widen  ? make_f16_tmap(&tmX, ws.wide, a.K, a.S, a.K * 2, f.tok / 2)
+                           : make_f16_tmap(&tmX, a.a, a.K, a.S, a.ld_a, f.tok / 2);
   if (!ok) return MXG_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (f.cta == 2) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = 2;
-    attr[n].val.clusterDim.y = 1;
-    attr[n].val.clusterDim.z = 1;
-    ++n;
-  } else {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  cfg.gridDim = dim3((unsigned)(f.cta == 2 ? 2 * pairs : std::min(num_sms, kI8MaxCtas)));
+  cudaLaunchAttribute attr[2] = {pair_attr()};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.blockDim = dim3((unsigned)f.threads);
   cfg.dynamicSmemBytes = (size_t)f.smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = n;
+  cfg.numAttrs = prep ? 2 : 1;
   void* args[] = {(void*)&tmW, (void*)&tmX, (void*)&p};
   if (cudaLaunchKernelExC(&cfg, f.fn, args) != cudaSuccess) {
     cudaGetLastError();

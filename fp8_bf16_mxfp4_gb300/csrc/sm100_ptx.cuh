@@ -521,6 +521,20 @@ MXG_DEVINL void named_bar_sync(uint32_t id, uint32_t threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// The same, and whether any of the threads came with `pred`.
+MXG_DEVINL bool named_bar_or(uint32_t id, uint32_t threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
+
 // One lane of a converged warp (1 there, 0 in the others).
 MXG_DEVINL uint32_t elect_one() {
   uint32_t e;
@@ -568,40 +582,27 @@ MXG_DEVINL void mma_f16_if(uint32_t e, uint32_t d, uint64_t adesc, uint64_t bdes
       : "memory");
 }
 
-// D(tmem) (+)= A(tmem) * B(smem), FP16 operands: A's rows are TMEM lanes, a column
-// holds two of its elements.  For a pair (kCta = 2) each CTA's TMEM has its own 128
-// rows of A and D, its shared memory half of B's rows.
-template <int kCta>
-MXG_DEVINL void mma_f16_ts_if(uint32_t e, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (kCta == 1)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
-        : "memory");
+// D(tmem) (+)= A(tmem) * B(smem) of a CTA pair, FP16 operands, by the lane whose `e`
+// is set: A's rows are TMEM lanes, a column holds two of its elements; each CTA's
+// TMEM has its own 128 rows of A and D, its shared memory half of B's rows.
+MXG_DEVINL void mma_f16_ts_pair_if(uint32_t e, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
+      : "memory");
 }
-// As tc_commit_pair, by the lane whose `e` is set.
-template <int kCta>
+// As tc_commit_pair of a pair, by the lane whose `e` is set.
 MXG_DEVINL void tc_commit_pair_if(uint32_t e, uint32_t bar) {
-  if constexpr (kCta == 1) tc_commit_if(e, bar);
-  else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
-            bar),
-        "r"(e), "h"((uint16_t)0x3)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+          bar),
+      "r"(e), "h"((uint16_t)0x3)
+      : "memory");
 }
 
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading
