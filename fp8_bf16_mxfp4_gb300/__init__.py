@@ -935,25 +935,9 @@ def moe_sort(ids: torch.Tensor, experts: int, m_splits: torch.Tensor | None = No
     return m_splits, rows
 
 
-def _slot_rows(rows: torch.Tensor):
-    if rows.dim() != 2 or rows.dtype != torch.int32 or not rows.is_contiguous() or not rows.is_cuda:
-        raise ValueError("rows must be contiguous int32 [tokens, top_k] on the GPU (from moe_sort)")
-    return rows.shape
-
-
-def _slot_values(name: str, t: torch.Tensor, shape):
-    """A contiguous FP32 value per slot."""
-    if t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous() or not t.is_cuda:
-        _refuse(**{name: (t, shape, torch.float32, True)})
-
-
-def _given_rows(name: str, t: torch.Tensor | None, shape, dtype, dev) -> torch.Tensor:
-    """The caller's output matrix, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
-        _refuse(**{name: (t, shape, dtype, False)})
-    return t
+def _refuse_rows(rows: torch.Tensor):
+    raise ValueError(f"rows must be contiguous int32 [tokens, top_k] on the GPU (from moe_sort), got {rows.dtype} of "
+                     f"shape {list(rows.shape)}")
 
 
 def moe_gather(x: torch.Tensor, rows: torch.Tensor, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
@@ -961,16 +945,22 @@ def moe_gather(x: torch.Tensor, rows: torch.Tensor, out: torch.Tensor | None = N
     """x [T, H] (BF16 or FP32) -> [T * top_k, H] in expert order: out[rows[t, j]] =
     x[t], zeros in the rows of empty slots.  ``rows`` from ``moe_sort``.  The
     gradient is ``moe_combine(dout, rows)``.  H is a multiple of 8 (FP32: 4)."""
-    T, k = _slot_rows(rows)
+    if rows.dim() != 2 or rows.dtype != torch.int32 or not rows.is_contiguous() or not rows.is_cuda:
+        _refuse_rows(rows)
+    T, k = rows.shape
     dtype = _OUT.get(x.dtype)
     if x.dim() != 2 or x.shape[0] != T or dtype is None or not x.is_cuda:
         _refuse(x=(x, (T, x.shape[-1]), _OUT, False))
     if x.requires_grad or (out is not None and out.requires_grad):
         _refuse_grad("moe_gather")
     H, dev, given = x.shape[1], x.device, out
-    out = _given_rows("out", out, (T * k, H), x.dtype, dev)
-    code = _lib.load().moe_gather(x.data_ptr(), _row_ld(x, H), rows.data_ptr(), T, k, H, dtype, out.data_ptr(),
-                                  _row_ld(out, H), _status_ptr(status, dev), _raw_stream(dev))
+    if out is None:
+        out = torch.empty((T * k, H), dtype=x.dtype, device=dev)
+    elif out.shape != (T * k, H) or out.dtype != x.dtype or not out.is_cuda:
+        _refuse(out=(out, (T * k, H), x.dtype, False))
+    code = _lib.load().moe_gather(x.data_ptr(), H if x.is_contiguous() else _row_ld(x, H), rows.data_ptr(), T, k, H, dtype,
+                                  out.data_ptr(), H if given is None else _row_ld(out, H), _status_ptr(status, dev),
+                                  _raw_stream(dev))
     if code:
         raise MXGError(code, "moe_gather")
     if given is not None:
@@ -986,20 +976,27 @@ def moe_combine(y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor | Non
     y[rows[t, j]] (``weights`` None: 1), empty slots adding nothing.  ``y`` BF16 or
     FP32 [rows, H]; ``weights`` FP32 [T, top_k] as from ``moe_route``.  Sums in FP32,
     in the order of the slots, rounded once."""
-    T, k = _slot_rows(rows)
+    if rows.dim() != 2 or rows.dtype != torch.int32 or not rows.is_contiguous() or not rows.is_cuda:
+        _refuse_rows(rows)
+    shape = rows.shape
+    T, k = shape
     dtype = _OUT.get(y.dtype)
     if y.dim() != 2 or dtype is None or not y.is_cuda:
         _refuse(y=(y, (T * k, y.shape[-1]), _OUT, False))
+    if weights is not None and (weights.shape != shape or weights.dtype != torch.float32 or not weights.is_contiguous()
+                                or not weights.is_cuda):
+        _refuse(weights=(weights, shape, torch.float32, True))
     if y.requires_grad or (weights is not None and weights.requires_grad) or (out is not None and out.requires_grad):
         _refuse_grad("moe_combine")
-    if weights is not None:
-        _slot_values("weights", weights, (T, k))
     n, H = y.shape
     dev, given = y.device, out
-    out = _given_rows("out", out, (T, H), y.dtype, dev)
-    code = _lib.load().moe_combine(y.data_ptr(), _row_ld(y, H), n, rows.data_ptr(),
+    if out is None:
+        out = torch.empty((T, H), dtype=y.dtype, device=dev)
+    elif out.shape != (T, H) or out.dtype != y.dtype or not out.is_cuda:
+        _refuse(out=(out, (T, H), y.dtype, False))
+    code = _lib.load().moe_combine(y.data_ptr(), H if y.is_contiguous() else _row_ld(y, H), n, rows.data_ptr(),
                                    None if weights is None else weights.data_ptr(), T, k, H, dtype, out.data_ptr(),
-                                   _row_ld(out, H), _status_ptr(status, dev), _raw_stream(dev))
+                                   H if given is None else _row_ld(out, H), _status_ptr(status, dev), _raw_stream(dev))
     if code:
         raise MXGError(code, "moe_combine")
     if given is not None:
@@ -1016,27 +1013,34 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, rows: torch.Tensor
     dy[rows[t, j]] = weights[t, j] * dout[t] (zeros in the rows of empty slots) and
     dweights[t, j] = <dout[t], y[rows[t, j]]> (0 for an empty slot), FP32 sums.
     ``dout`` [T, H] and ``y`` [T * top_k, H] of one type.  ``dy=y`` writes over y."""
-    T, k = _slot_rows(rows)
-    dtype = _OUT.get(y.dtype)
+    if rows.dim() != 2 or rows.dtype != torch.int32 or not rows.is_contiguous() or not rows.is_cuda:
+        _refuse_rows(rows)
+    shape = rows.shape
+    T, k = shape
+    f32, dt = torch.float32, y.dtype
+    dtype = _OUT.get(dt)
     if y.dim() != 2 or y.shape[0] != T * k or dtype is None or not y.is_cuda:
         _refuse(y=(y, (T * k, y.shape[-1]), _OUT, False))
     H, dev = y.shape[1], y.device
-    if dout.shape != (T, H) or dout.dtype != y.dtype or not dout.is_cuda:
-        _refuse(dout=(dout, (T, H), y.dtype, False))
-    _slot_values("weights", weights, (T, k))
+    if (dout.shape != (T, H) or dout.dtype != dt or not dout.is_cuda or weights.shape != shape or weights.dtype != f32
+            or not weights.is_contiguous() or not weights.is_cuda):
+        _refuse(dout=(dout, (T, H), dt, False), weights=(weights, shape, f32, True))
     if (dout.requires_grad or y.requires_grad or weights.requires_grad or (dy is not None and dy.requires_grad)
             or (dweights is not None and dweights.requires_grad)):
         _refuse_grad("moe_combine_backward")
     dy_given, dw_given = dy, dweights
-    dy = _given_rows("dy", dy, (T * k, H), y.dtype, dev)
+    if dy is None:
+        dy = torch.empty((T * k, H), dtype=dt, device=dev)
+    elif dy.shape != (T * k, H) or dy.dtype != dt or not dy.is_cuda:
+        _refuse(dy=(dy, (T * k, H), dt, False))
     if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    else:
-        _slot_values("dweights", dweights, (T, k))
-    code = _lib.load().moe_combine_backward(dout.data_ptr(), _row_ld(dout, H), y.data_ptr(), _row_ld(y, H),
-                                            rows.data_ptr(), weights.data_ptr(), T, k, H, dtype, dy.data_ptr(),
-                                            _row_ld(dy, H), dweights.data_ptr(), _status_ptr(status, dev),
-                                            _raw_stream(dev))
+        dweights = torch.empty(shape, dtype=f32, device=dev)
+    elif dweights.shape != shape or dweights.dtype != f32 or not dweights.is_contiguous() or not dweights.is_cuda:
+        _refuse(dweights=(dweights, shape, f32, True))
+    code = _lib.load().moe_combine_backward(
+        dout.data_ptr(), H if dout.is_contiguous() else _row_ld(dout, H), y.data_ptr(),
+        H if y.is_contiguous() else _row_ld(y, H), rows.data_ptr(), weights.data_ptr(), T, k, H, dtype, dy.data_ptr(),
+        H if dy.is_contiguous() else _row_ld(dy, H), dweights.data_ptr(), _status_ptr(status, dev), _raw_stream(dev))
     if code:
         raise MXGError(code, "moe_combine_backward")
     if dy_given is not None:
@@ -1059,21 +1063,27 @@ def moe_route_backward(dweights: torch.Tensor, ids: torch.Tensor, weights: torch
     if logits.dim() != 2 or ids.dim() != 2:
         raise ValueError("logits must be [tokens, experts] and ids [tokens, top_k]")
     T, E = logits.shape
-    k, dev = ids.shape[1], logits.device
-    dtype = _OUT.get(logits.dtype)
-    if (dtype is None or not logits.is_cuda or ids.shape[0] != T or ids.dtype != torch.int32 or not ids.is_contiguous()
-            or not ids.is_cuda):
-        _refuse(logits=(logits, (T, E), _OUT, False), ids=(ids, (T, k), torch.int32, True))
-    _slot_values("dweights", dweights, (T, k))
-    _slot_values("weights", weights, (T, k))
+    shape, dev, dt, f32 = ids.shape, logits.device, logits.dtype, torch.float32
+    dtype = _OUT.get(dt)
+    if (dtype is None or not logits.is_cuda or shape[0] != T or ids.dtype != torch.int32 or not ids.is_contiguous()
+            or not ids.is_cuda or dweights.shape != shape or dweights.dtype != f32 or not dweights.is_contiguous()
+            or not dweights.is_cuda or weights.shape != shape or weights.dtype != f32 or not weights.is_contiguous()
+            or not weights.is_cuda):
+        want = (T, shape[1])
+        _refuse(logits=(logits, (T, E), _OUT, False), ids=(ids, want, torch.int32, True),
+                dweights=(dweights, want, f32, True), weights=(weights, want, f32, True))
     if (dweights.requires_grad or weights.requires_grad or logits.requires_grad
             or (dlogits is not None and dlogits.requires_grad)):
         _refuse_grad("moe_route_backward")
     given = dlogits
-    dlogits = _given_rows("dlogits", dlogits, (T, E), logits.dtype, dev)
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=dt, device=dev)
+    elif dlogits.shape != (T, E) or dlogits.dtype != dt or not dlogits.is_cuda:
+        _refuse(dlogits=(dlogits, (T, E), dt, False))
     code = _lib.load().moe_route_backward(dweights.data_ptr(), ids.data_ptr(), weights.data_ptr(), logits.data_ptr(),
-                                          _row_ld(logits, E), T, E, k, renormalize, dtype, dlogits.data_ptr(),
-                                          _row_ld(dlogits, E), _status_ptr(status, dev), _raw_stream(dev))
+                                          E if logits.is_contiguous() else _row_ld(logits, E), T, E, shape[1], renormalize,
+                                          dtype, dlogits.data_ptr(), E if given is None else _row_ld(dlogits, E),
+                                          _status_ptr(status, dev), _raw_stream(dev))
     if code:
         raise MXGError(code, "moe_route_backward")
     if given is not None:
@@ -1086,7 +1096,7 @@ def moe_route_backward(dweights: torch.Tensor, ids: torch.Tensor, weights: torch
 # ----------------------------------------------------------------------------- 8-bit integers
 
 _CODES = {"int8": torch.int8, "f16": torch.float16}
-_CODE_KIND = {torch.int8: 1, torch.float16: 2}
+_CODE_KIND = {torch.int8: 1, torch.float16: 2}  # and a code's bytes
 
 
 @dataclass
@@ -1109,14 +1119,19 @@ class Int8Operand:
         data, scale = self.data, self.scale
         kind = _CODE_KIND.get(data.dtype)
         if data.dim() != 2 or kind is None or not data.is_cuda:
-            _refuse(codes=(data, data.shape[:2], _CODE_KIND, False))
+            _refuse(codes=(data, (data.shape[0], data.shape[-1]), _CODE_KIND, False))
         rows, cols = data.shape
         if scale.shape != (rows,) or scale.dtype != torch.float32 or not scale.is_contiguous() or not scale.is_cuda:
             _refuse(scale=(scale, (rows,), torch.float32, True))
-        if rows > 0 and cols > 1 and data.stride(1) != 1:
-            raise ValueError("codes of a row must be contiguous")
-        ld = (data.stride(0) if rows > 1 else (cols + 15) & ~15) * kind
+        ld = cols * kind if data.is_contiguous() else _code_ld(data, cols, kind)
         return _lib.Int8OperandC(data.data_ptr(), scale.data_ptr(), rows, cols, ld, kind, 0)
+
+
+def _code_ld(t: torch.Tensor, cols: int, kind: int) -> int:
+    """Row stride of codes in bytes; their rows must be contiguous."""
+    if t.shape[0] > 0 and cols > 1 and t.stride(1) != 1:
+        raise ValueError("codes of a row must be contiguous")
+    return (t.stride(0) if t.shape[0] > 1 else (cols + 15) & ~15) * kind
 
 
 def int8_quantize_rowwise(x: torch.Tensor, rows: torch.Tensor | None = None, codes: str = "int8",
@@ -1128,31 +1143,35 @@ def int8_quantize_rowwise(x: torch.Tensor, rows: torch.Tensor | None = None, cod
     [T * top_k, cols], as from quantizing ``moe_gather(x, rows)``, from one read of
     x.  ``codes="f16"`` writes the integers as FP16 values, which the GEMMs take
     without widening them first.  A row with a NaN or an infinity gets the scale NaN."""
-    if codes not in _CODES:
+    dtype = _CODES.get(codes)
+    if dtype is None:
         raise ValueError(f"unknown codes {codes!r} (int8 or f16)")
     if x.dim() != 2 or x.dtype != torch.bfloat16 or not x.is_cuda:
         _refuse(x=(x, (x.shape[0], x.shape[-1]), torch.bfloat16, False))
     if x.requires_grad or (scale is not None and scale.requires_grad) or (q is not None and q.requires_grad):
         _refuse_grad("int8_quantize_rowwise")
     T, K = x.shape
-    k, n = 1, T
+    n, k, dev, kind = T, 1, x.device, _CODE_KIND[dtype]
     if rows is not None:
-        t, k = _slot_rows(rows)
-        if t != T:
+        if rows.dim() != 2 or rows.dtype != torch.int32 or not rows.is_contiguous() or not rows.is_cuda:
+            _refuse_rows(rows)
+        if rows.shape[0] != T:
             raise ValueError("rows must have a row for every token of x")
+        k = rows.shape[1]
         n = T * k
-    dev, dtype = x.device, _CODES[codes]
     q_given, s_given = q, scale
-    q = _given_rows("q", q, (n, K), dtype, dev)
+    if q is None:
+        q = torch.empty((n, K), dtype=dtype, device=dev)
+    elif q.shape != (n, K) or q.dtype != dtype or not q.is_cuda:
+        _refuse(q=(q, (n, K), dtype, False))
     if scale is None:
         scale = torch.empty((n,), dtype=torch.float32, device=dev)
-    else:
-        _slot_values("scale", scale, (n,))
-    op = Int8Operand(q, scale)
-    c = op.c()
-    code = _lib.load().int8_quantize_rowwise(x.data_ptr(), _row_ld(x, K), None if rows is None else rows.data_ptr(), T, k,
-                                             K, c.codes, c.data, c.ld, c.scale, _status_ptr(status, dev),
-                                             _raw_stream(dev))
+    elif scale.shape != (n,) or scale.dtype != torch.float32 or not scale.is_contiguous() or not scale.is_cuda:
+        _refuse(scale=(scale, (n,), torch.float32, True))
+    code = _lib.load().int8_quantize_rowwise(x.data_ptr(), K if x.is_contiguous() else _row_ld(x, K),
+                                             None if rows is None else rows.data_ptr(), T, k, K, kind, q.data_ptr(),
+                                             K * kind if q_given is None else _code_ld(q, K, kind), scale.data_ptr(),
+                                             _status_ptr(status, dev), _raw_stream(dev))
     if code:
         raise MXGError(code, "int8_quantize_rowwise")
     if q_given is not None:
@@ -1161,7 +1180,7 @@ def int8_quantize_rowwise(x: torch.Tensor, rows: torch.Tensor | None = None, cod
         _written(scale)
     if check:
         check_status(status, dev)
-    return op
+    return Int8Operand(q, scale)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1169,23 +1188,23 @@ def int8_gemm_workspace_size(G: int, S: int, N: int, K: int, codes: str = "int8"
     return int(_lib.load().int8_gemm_workspace_size(G, S, N, K, _CODE_KIND[_CODES[codes]]))
 
 
-def _int8_gemm(name, A, W, m_splits, G, N, out_dtype, out, workspace, status, check):
+def _int8_gemm(name, fn, A, W, splits, G, N, out_dtype, out, workspace, status, check):
     a, w = A.c(), W.c()
     if A.scale.requires_grad or W.scale.requires_grad or A.data.requires_grad or (out is not None and out.requires_grad):
         _refuse_grad(name)
-    dev, lib, given = A.data.device, _lib.load(), out
+    dev, given, S = A.data.device, out, a.rows
     if out is None:
-        out = torch.empty((a.rows, N), dtype=out_dtype, device=dev)
-    if out.shape != (a.rows, N) or out.dtype not in _OUT or not out.is_cuda:
-        _refuse(out=(out, (a.rows, N), _OUT, False))
+        out = torch.empty((S, N), dtype=out_dtype, device=dev)
+    dtype = _OUT.get(out.dtype)
+    if out.shape != (S, N) or dtype is None or not out.is_cuda:
+        _refuse(out=(out, (S, N), _OUT, False))
     stream = _raw_stream(dev)
     if workspace is None:
-        workspace = _scratch(int8_gemm_workspace_size(G, a.rows, N, a.cols, "int8" if a.codes == 1 else "f16"), dev, stream)
+        workspace = _scratch(int8_gemm_workspace_size(G, S, N, a.cols, "int8" if a.codes == 1 else "f16"), dev, stream)
     else:
         _given_workspace(workspace)
-    splits = () if m_splits is None else (m_splits.data_ptr(), G, N)
-    code = getattr(lib, name)(ctypes.byref(a), ctypes.byref(w), *splits, out.data_ptr(), _row_ld(out, N), _OUT[out.dtype],
-                              workspace.data_ptr(), workspace.numel(), _status_ptr(status, dev), stream)
+    code = fn(ctypes.byref(a), ctypes.byref(w), *splits, out.data_ptr(), N if given is None else _row_ld(out, N), dtype,
+              workspace.data_ptr(), workspace.numel(), _status_ptr(status, dev), stream)
     if code:
         raise MXGError(code, name)
     if given is not None:
@@ -1203,11 +1222,14 @@ def int8_grouped_gemm_fwd(A: Int8Operand, W: Int8Operand, m_splits: torch.Tensor
     exact and their sums in FP32.  Forward only."""
     if m_splits.dim() != 1 or m_splits.dtype != torch.int32 or not m_splits.is_contiguous() or not m_splits.is_cuda:
         _refuse(m_splits=(m_splits, (m_splits.numel(),), torch.int32, True))
-    return _int8_gemm("int8_grouped_gemm_fwd", A, W, m_splits, m_splits.numel(), N, out_dtype, out, workspace, status, check)
+    G = m_splits.numel()
+    return _int8_gemm("int8_grouped_gemm_fwd", _lib.load().int8_grouped_gemm_fwd, A, W, (m_splits.data_ptr(), G, N), G, N,
+                      out_dtype, out, workspace, status, check)
 
 
 def int8_gemm_dense(A: Int8Operand, B: Int8Operand, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
                     check: bool = False) -> torch.Tensor:
     """C[M, N] = A[M, K] @ B[N, K]^T of two 8-bit integer operands (``B`` int8)."""
-    return _int8_gemm("int8_gemm_dense", A, B, None, 1, B.rows, out_dtype, out, workspace, status, check)
+    return _int8_gemm("int8_gemm_dense", _lib.load().int8_gemm_dense, A, B, (), 1, B.rows, out_dtype, out, workspace,
+                      status, check)

@@ -40,27 +40,40 @@ int64_t sort_chunk(int64_t P) {
 }
 int64_t sort_chunks(int64_t P) { const int64_t c = sort_chunk(P); return (P + c - 1) / c; }
 
-// The expert of slot i, E for an empty slot (and for an id that is not below E).
-MXG_DEVINL int slot_key(const int32_t* ids, int64_t i, int64_t end, int E, bool& bad) {
-  if (i >= end) return -1;
-  const int e = __ldg(ids + i);
-  bad |= e >= E;
-  return e < 0 || e >= E ? E : e;
-}
-
-// cnt[warp][0..E]: the slots of each expert in the warp's run.
-MXG_DEVINL bool count_run(const int32_t* ids, int64_t i0, int64_t i1, int E, uint32_t* cnt) {
+// Calls f(i, e) for every 32 slots of [i0, i1), a slot per lane: e is the slot's
+// expert, E for an empty one (and for an id that is not below E), -1 past the end.
+// Four loads are in flight.
+constexpr int kSortFlight = 4;
+template <typename F>
+MXG_DEVINL bool for_slots(const int32_t* ids, int64_t i0, int64_t i1, int E, F f) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
-  for (int64_t i = i0; i < i1; i += 32) {
-    const int e = slot_key(ids, i + lane, i1, E, bad);
-    const uint32_t same = __match_any_sync(kFull, e);
-    if (e >= 0 && lane == __ffs(same) - 1) cnt[e] += __popc(same);
-    __syncwarp();
+  for (int64_t i = i0; i < i1; i += 32 * kSortFlight) {
+    int id[kSortFlight];
+#pragma unroll
+    for (int q = 0; q < kSortFlight; ++q) id[q] = i + 32 * q + lane < i1 ? __ldg(ids + i + 32 * q + lane) : -1;
+#pragma unroll
+    for (int q = 0; q < kSortFlight; ++q) {
+      const int64_t at = i + 32 * q + lane;
+      if (at - lane >= i1) break;
+      bad |= id[q] >= E;
+      f(at, at >= i1 ? -1 : id[q] < 0 || id[q] >= E ? E : id[q]);
+    }
   }
   return bad;
 }
 
+// cnt[0..E]: the slots of each expert in the warp's run.
+MXG_DEVINL bool count_run(const int32_t* ids, int64_t i0, int64_t i1, int E, uint32_t* cnt) {
+  const int lane = threadIdx.x & 31;
+  return for_slots(ids, i0, i1, E, [&](int64_t, int e) {
+    const uint32_t same = __match_any_sync(kFull, e);
+    if (e >= 0 && lane == __ffs(same) - 1) cnt[e] += __popc(same);
+    __syncwarp();
+  });
+}
+
+// counts[e][chunk], e = 0 .. E
 __global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(const int32_t* __restrict__ ids, int64_t P, int E,
                                                                       int64_t chunk, int32_t* counts) {
   extern __shared__ uint32_t cnt[];  // [warps][E + 1]
@@ -76,7 +89,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(const int3
     uint32_t v = 0;
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) v += cnt[w * keys + e];
-    counts[(int64_t)blockIdx.x * keys + e] = (int32_t)v;
+    counts[(int64_t)e * gridDim.x + blockIdx.x] = (int32_t)v;
   }
 }
 
@@ -85,6 +98,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
                                                                       int32_t* __restrict__ m_splits,
                                                                       int32_t* __restrict__ rows, int32_t* status) {
   extern __shared__ uint32_t cnt[];  // [warps][E + 1]
+  __shared__ uint32_t total[2 * kSortThreads], before[2 * kSortThreads];  // of a key: all slots, those of earlier chunks
   __shared__ uint32_t warp_sum[kSortWarps];
   const int keys = E + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < kSortWarps * keys; i += kSortThreads) cnt[i] = 0;
@@ -94,32 +108,38 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
   const bool bad = count_run(ids, i0, i1, E, cnt + warp * keys);
   if (__syncthreads_or(bad) && threadIdx.x == 0) report(status, MXG_ERR_INDEX);
 
-  // Thread t has the two keys 2 t and 2 t + 1 (at most 513): their totals over
-  // all chunks and what earlier chunks have of them.
-  const int key0 = 2 * (int)threadIdx.x;
-  uint32_t total[2] = {0, 0}, before[2] = {0, 0};
-  if (gridDim.x > 1) ptx::pdl_wait();  // the counts are complete
+  if (gridDim.x == 1) {
+    for (int e = threadIdx.x; e < keys; e += kSortThreads) {
+      uint32_t v = 0;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int e = key0 + q;
-    if (e >= keys) continue;
-    if (gridDim.x == 1) {
-#pragma unroll
-      for (int w = 0; w < kSortWarps; ++w) total[q] += cnt[w * keys + e];
-    } else {
-      for (unsigned c = 0; c < gridDim.x; c += 8) {
-        uint32_t v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = c + u < gridDim.x ? (uint32_t)__ldcg(counts + (int64_t)(c + u) * keys + e) : 0u;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          total[q] += v[u];
-          if (c + u < blockIdx.x) before[q] += v[u];
-        }
+      for (int w = 0; w < kSortWarps; ++w) v += cnt[w * keys + e];
+      total[e] = v;
+      before[e] = 0;
+    }
+  } else {
+    ptx::pdl_wait();  // the counts are complete
+    const int chunks = (int)gridDim.x;
+#pragma unroll 4
+    for (int e = warp; e < keys; e += kSortWarps) {  // a warp takes a key, its lanes the chunks
+      uint32_t all = 0, early = 0;
+      for (int c = lane; c < chunks; c += 32) {
+        const uint32_t v = (uint32_t)__ldcg(counts + (int64_t)e * chunks + c);
+        all += v;
+        if (c < (int)blockIdx.x) early += v;
+      }
+      all = __reduce_add_sync(kFull, all);
+      early = __reduce_add_sync(kFull, early);
+      if (lane == 0) {
+        total[e] = all;
+        before[e] = early;
       }
     }
   }
-  uint32_t incl = total[0] + total[1];
+  __syncthreads();
+  // Thread t has the two keys 2 t and 2 t + 1 (at most 513).
+  const int key0 = 2 * (int)threadIdx.x;
+  const uint32_t t0 = key0 < keys ? total[key0] : 0u, t1 = key0 + 1 < keys ? total[key0 + 1] : 0u;
+  uint32_t incl = t0 + t1;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t o = __shfl_up_sync(kFull, incl, d);
@@ -127,7 +147,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  uint32_t at = incl - total[0] - total[1];
+  uint32_t at = incl - t0 - t1;
   for (int w = 0; w < warp; ++w) at += warp_sum[w];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -135,10 +155,10 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
     if (e < keys) {
       if (blockIdx.x == 0) {
         // the tail of empty slots counts as the last expert's
-        if (e < E - 1) m_splits[e] = (int32_t)total[q];
+        if (e < E - 1) m_splits[e] = (int32_t)(q ? t1 : t0);
         else if (e == E - 1) m_splits[e] = (int32_t)((uint32_t)P - at);
       }
-      uint32_t pos = at + before[q];
+      uint32_t pos = at + before[e];
 #pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t m = cnt[w * keys + e];
@@ -146,25 +166,23 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
         pos += m;
       }
     }
-    at += total[q];
+    at += q ? t1 : t0;
   }
   __syncthreads();
 
   uint32_t* mine = cnt + warp * keys;
-  bool ignored = false;
-  for (int64_t i = i0; i < i1; i += 32) {
-    const int e = slot_key(ids, i + lane, i1, E, ignored);
+  for_slots(ids, i0, i1, E, [&](int64_t i, int e) {
     const uint32_t same = __match_any_sync(kFull, e);
     const int rank = __popc(same & ((1u << lane) - 1u));
     const uint32_t first = e >= 0 ? mine[e] : 0u;
     __syncwarp();
     if (e >= 0) {
       const int r = (int)(first + rank);
-      rows[i + lane] = e == E ? -1 - r : r;
+      rows[i] = e == E ? -1 - r : r;
       if (rank == 0) mine[e] = first + __popc(same);
     }
     __syncwarp();
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -207,7 +225,12 @@ MXG_DEVINL uint4 narrow(const float* v) {
 
 // A CTA takes one token and `threads` pieces of its row at a time.
 constexpr int kRowThreads = 256;
-int row_threads(int64_t pieces) { return (int)std::min<int64_t>(kRowThreads, (pieces + 31) / 32 * 32); }
+// As many threads as share a row's pieces equally (896 pieces: 4 times 224; with
+// 256 threads combine takes 186 us instead of 173 for 65536 rows of 7168).
+int row_threads(int64_t pieces) {
+  const int64_t turns = (pieces + kRowThreads - 1) / kRowThreads;
+  return (int)(((pieces + turns - 1) / turns + 31) / 32 * 32);
+}
 
 __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const uint4* __restrict__ x, int64_t ld_x,
                                                                  const int32_t* __restrict__ rows, int k, int64_t P,
@@ -250,7 +273,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* _
           const int64_t r = e >= 0 ? row_of(e, y_rows, status) : -1;
           on[j] = r >= 0;
           if (on[j]) {
-            v[j] = __ldg(y + r * ld_y + c);
+            v[j] = __ldcs(y + r * ld_y + c);
             w[j] = weights != nullptr ? __ldg(weights + t * k + j0 + j) : 1.0f;
           }
         }
@@ -264,7 +287,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* _
         for (int i = 0; i < n; ++i) s[i] = fmaf(w[j], f[i], s[i]);
       }
     }
-    out[t * ld_out + c] = narrow<T>(s);
+    __stcs(out + t * ld_out + c, narrow<T>(s));
   }
 }
 
@@ -277,7 +300,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(
     const float* __restrict__ weights, int k, int64_t P, int64_t pieces, uint4* dy, int64_t ld_dy,
     float* __restrict__ dweights, int32_t* status) {
   constexpr int n = Piece<T>::n;
-  constexpr int kFlight = 8;
+  constexpr int kFlight = 4;  // slots at a time; with 8 there are too few warps (65536 rows of 4096: 199 us, 173)
   __shared__ float part[kRowThreads / 32][kFlight];
   const int64_t t = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
