@@ -1157,7 +1157,7 @@ mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* row
   DeviceGuard g(dev);
   if (!g.ok) return MXG_ERR_CUDA;
   return cuda_status(launch_int8_quantize(x, ld_x, rows, tokens, top_k, cols, codes, q, ld_q, scale, d_status,
-                                          static_cast<cudaStream_t>(stream)));
+                                          static_cast<cudaStream_t>(stream), sms));
 }
 
 size_t int8_gemm_workspace_size(int32_t G, int64_t S, int64_t N, int64_t K, int32_t a_codes) {

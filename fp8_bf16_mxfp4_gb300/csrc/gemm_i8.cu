@@ -49,6 +49,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kQThreads = 256;
 constexpr int kQKeep = 4;  // 16-byte pieces of a row that a thread keeps between its two passes
 
+// A CTA takes a token (and, where there are few, every gridDim.y-th of its slots):
+// its largest value, then its codes, once for every output row.
+
 // q = rint(x r) in the low 16 bits: the sum with 1.5 2^23 rounds the exact product
 // to an integer, to nearest even, in one step.
 MXG_DEVINL uint32_t round_code(float x, float r) { return __float_as_uint(fmaf(x, r, 12582912.0f)); }
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const uint4* _
     on = e >= 0;
     return at < out_rows ? at : -1;
   };
-  for (int j = threadIdx.x; j < k; j += blockDim.x) {
+  for (int j = blockIdx.y + threadIdx.x * gridDim.y; j < k; j += blockDim.x * gridDim.y) {
     bool on;
     const int64_t at = row_at(j, on);
     if (at >= 0) scale[at] = on ? s : kLeast;
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const uint4* _
       if constexpr (kF16) o = make_uint4(h[0], h[1], h[2], h[3]);
       else o = make_uint4(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410), 0, 0);
     }
-    for (int j = 0; j < k; ++j) {
+    for (int j = blockIdx.y; j < k; j += gridDim.y) {
       bool on;
       const int64_t at = row_at(j, on);
       if (at < 0) continue;
@@ -174,6 +177,12 @@ __global__ void __launch_bounds__(kPrepThreads) int8_prep_kernel(uint32_t* sync,
   }
 }
 
+MXG_DEVINL uint4 ld_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // One warp: the first row off[g] and first unit tile[g] of every expert, `per_tile`
 // units for every `tok` of its rows; *bad where a split is negative or they do not
 // add up to S.  Lane l has experts [l * per, l * per + per).
@@ -222,24 +231,32 @@ MXG_DEVINL uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------------------
-// A few rows per expert: integer dot products on the CUDA cores.  A unit is kDotRows
-// channels of one expert against up to 8 of its rows; its warp reads the channels'
-// codes once, 16 bytes a lane and channel, and the rows' bytes from shared memory,
-// where the CTA has put them (FP16 codes narrowed to bytes again).  Sums are 32-bit
-// integers.  A CTA takes an equal run of units, in the order expert, tile of rows,
-// channels.  Against the tensor-core form: no pipeline to fill, no join, one launch
-// (1 row, 4096 x 7168: ZZ us against ZZ); bound by HBM up to about 4 rows, then by
-// the dot products, one for 4 bytes and row (128 rows of 32 experts: ZZ against ZZ).
+// A few rows per expert.  A unit is 16 channels of one expert against a tile of up
+// to 16 of its rows.  Weights go from global memory to registers, 16 bytes a lane,
+// and are widened there to the A fragments of mma.sync (m16n8k16, FP16): a lane has
+// the same four bytes of a channel that it has of a row, in whatever order mma.sync
+// numbers them, so nothing is moved between lanes.  The rows' bytes are in shared
+// memory (FP16 codes narrowed again: half the room) and are widened as they are used.
+// A CTA has 16 warps: `split` of them share a unit's contraction, 128 elements in
+// turn, and 16 / split units are on their way at a time; partial sums are added
+// through shared memory in the warps' order.  A CTA takes an equal run of units, in
+// the order expert, tile of rows, channels, and its loads run ahead over units.
+// mma.sync makes 974 products of FP16 codes a clock and SM (of 8-bit integers 255, as
+// does dp4a), of which 8 rows at the rate of memory need 190: bound by HBM.
+// 1 row, 4096 x 7168: ZZ us; 128 rows of 32 experts: ZZ us, ZZ TB/s.
 // ---------------------------------------------------------------------------
-constexpr int kDotTok = 8;
-constexpr int kDotThreads = 256;
-constexpr int kDotWarps = kDotThreads / 32;
-constexpr int64_t kDotMaxK = 25600;  // 8 rows of it fit shared memory
+constexpr int kFewThreads = 512;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewChan = 16;
+constexpr int kFewDepth = 4;   // chunks of 128 elements that a warp has in flight
+constexpr int kFewCol = 20;    // words between columns of a partial tile (16 channels each): 4 columns, 32 banks
 
-struct DotParams {
+struct FewParams {
   const int32_t* splits;
   int G, S, N, K;
+  int tok;           // rows of a tile: 8 or 16
   int per_tile;      // units of a tile of rows
+  int split;         // warps of a unit, a power of two up to 16
   const uint8_t* a;
   int64_t ld_a;
   int f16;           // the rows' codes are FP16
@@ -252,6 +269,11 @@ struct DotParams {
   int out_f32;
   int32_t* status;
 };
+
+// Bytes between rows in shared memory: 64 past a multiple of 128, so that two rows'
+// 64 bytes are in different banks.
+__host__ __device__ inline int few_stride(int64_t K) { return (int)((K + 127) / 128 * 128) + 64; }
+inline int64_t few_part_bytes(int tok) { return (int64_t)2 * kFewWarps * tok * kFewCol * 4; }
 
 // 16 FP16 codes -> 16 bytes: q + 1536 has q in its low byte.
 MXG_DEVINL uint4 narrow16(const uint4& a, const uint4& b) {
@@ -267,111 +289,155 @@ MXG_DEVINL uint4 narrow16(const uint4& a, const uint4& b) {
                     __byte_perm(h[6], h[7], 0x6420));
 }
 
-MXG_DEVINL uint4 ld_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// The tile's rows to shared memory, as bytes.
+MXG_DEVINL void few_stage(const FewParams& p, uint8_t* x, int tok0, int n) {
+  const int pieces = p.K / 16, stride = few_stride(p.K);
+  __syncthreads();  // the rows before are no longer read
+  for (int i = threadIdx.x; i < n * pieces; i += kFewThreads) {
+    const int t = i / pieces, c = i - t * pieces;
+    const uint8_t* src = p.a + (int64_t)(tok0 + t) * p.ld_a;
+    uint4 r;
+    if (p.f16) {
+      const uint4* s = reinterpret_cast<const uint4*>(src) + 2 * c;
+      r = narrow16(__ldg(s), __ldg(s + 1));
+    } else {
+      r = __ldg(reinterpret_cast<const uint4*>(src) + c);
+    }
+    *reinterpret_cast<uint4*>(x + t * stride + c * 16) = r;
+  }
+  __syncthreads();
 }
 
-// kR channels against n <= kT rows.
-template <int kR, int kT>
-MXG_DEVINL void dot_unit(const DotParams& p, const uint8_t* x, int e, int tok0, int n, int chan0) {
-  constexpr int kSteps = kR == 4 ? 4 : 8;  // 512 bytes of every channel each, in flight together
-  const int lane = threadIdx.x & 31;
-  const uint8_t* w[kR];
+// Channels [c0, c1) of one expert for a tile of n <= 8 kNT rows.
+template <int kNT>
+MXG_DEVINL void few_tile(const FewParams& p, uint8_t* x, float* part, int e, int tok0, int n, int c0, int c1) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q16 = (lane & 3) * 16;
+  const int split = p.split, kp = warp & (split - 1), ug = warp / split, at_once = kFewWarps / split;
+  const int chunks = (p.K + 127) >> 7, turns = (chunks + split - 1) / split;  // a warp's chunks: kp, kp + split, ...
+  const int slots = (turns + kFewDepth - 1) / kFewDepth * kFewDepth;  // of the ring, for one unit
+  const int step = at_once * kFewChan, iters = (c1 - c0 + step - 1) / step;
+  const int stride = few_stride(p.K);
+
+  // what is loaded next: chunk kp + split l_i of this warp's unit of turn l_it
+  int l_it = 0, l_i = 0;
+  const uint8_t *w0 = nullptr, *w8 = nullptr;  // this lane's rows: channels g and g + 8 of the unit
+  auto point = [&]() {  // past the last channel: not stored
+    const int chan = c0 + (l_it * at_once + ug) * kFewChan + g;
+    w0 = p.w + ((int64_t)e * p.N + min(chan, c1 - 1)) * p.ld_w + q16;
+    w8 = p.w + ((int64_t)e * p.N + min(chan + 8, c1 - 1)) * p.ld_w + q16;
+  };
+  point();
+  uint4 v[kFewDepth][4];
+  auto load = [&](uint4* d) {  // channel g, g + 8 of bytes 0-63, then 64-127 of the chunk
+    const int k = (kp + split * l_i) << 7;
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    const bool on = l_i < turns && l_it < iters;
+    const bool lo = on && k + q16 < p.K, hi = on && k + q16 + 64 < p.K;
+    d[0] = lo ? ld_stream(w0 + k) : z;
+    d[1] = lo ? ld_stream(w8 + k) : z;
+    d[2] = hi ? ld_stream(w0 + k + 64) : z;
+    d[3] = hi ? ld_stream(w8 + k + 64) : z;
+    if (++l_i == slots) {
+      l_i = 0;
+      ++l_it;
+      point();
+    }
+  };
 #pragma unroll
-  for (int r = 0; r < kR; ++r) w[r] = p.w + ((int64_t)e * p.N + min(chan0 + r, p.N - 1)) * p.ld_w;
-  int acc[kR][kT];
+  for (int s = 0; s < kFewDepth; ++s) load(v[s]);
+
+  few_stage(p, x, tok0, n);  // while the first weights are on their way
+
+  float acc[kNT][4];
 #pragma unroll
-  for (int r = 0; r < kR; ++r)
+  for (int t = 0; t < kNT; ++t)
 #pragma unroll
-    for (int t = 0; t < kT; ++t) acc[r][t] = 0;
-  for (int k0 = lane * 16; k0 < p.K; k0 += 512 * kSteps) {
-    uint4 v[kSteps][kR];
+    for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+  const uint32_t xs = ptx::smem_u32(x) + g * stride + q16;
+  auto multiply = [&](const uint4* d, int k) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int h = 0; h < 2; ++h) {
+      uint32_t b[kNT][4];
 #pragma unroll
-      for (int r = 0; r < kR; ++r)
-        v[s][r] = k0 + 512 * s < p.K ? ld_stream(w[r] + k0 + 512 * s) : make_uint4(0, 0, 0, 0);
+      for (int t = 0; t < kNT; ++t) ptx::ld_shared_v4(xs + t * 8 * stride + k + h * 64, b[t]);
+      const uint32_t r0[4] = {d[2 * h].x, d[2 * h].y, d[2 * h].z, d[2 * h].w};
+      const uint32_t r8[4] = {d[2 * h + 1].x, d[2 * h + 1].y, d[2 * h + 1].z, d[2 * h + 1].w};
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (k0 + 512 * s < p.K) {
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a0, a1, a2, a3;
+        widen4(r0[j], a0, a2);
+        widen4(r8[j], a1, a3);
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
-          if (t < n) {
-            const uint4 a = *reinterpret_cast<const uint4*>(x + (int64_t)t * p.K + k0 + 512 * s);
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-              acc[r][t] = __dp4a((int)a.x, (int)v[s][r].x, acc[r][t]);
-              acc[r][t] = __dp4a((int)a.y, (int)v[s][r].y, acc[r][t]);
-              acc[r][t] = __dp4a((int)a.z, (int)v[s][r].z, acc[r][t]);
-              acc[r][t] = __dp4a((int)a.w, (int)v[s][r].w, acc[r][t]);
-            }
-          }
+        for (int t = 0; t < kNT; ++t) {
+          uint32_t b0, b1;
+          widen4(b[t][j], b0, b1);
+          asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                       : "+f"(acc[t][0]), "+f"(acc[t][1]), "+f"(acc[t][2]), "+f"(acc[t][3])
+                       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
         }
       }
     }
-  }
-  __syncwarp();
-  // lane t kR + r has channel r of row t
-  int sum = 0;
+  };
+  for (int it = 0; it < iters; ++it) {
+    for (int i = 0; i < turns; i += kFewDepth) {
 #pragma unroll
-  for (int t = 0; t < kT; ++t)
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const int v = __reduce_add_sync(kFull, acc[r][t]);
-      if (lane == t * kR + r) sum = v;
+      for (int s = 0; s < kFewDepth; ++s) {
+        const int c = kp + split * (i + s);
+        if (c < chunks) multiply(v[s], c << 7);
+        load(v[s]);
+      }
     }
-  const int t = lane / kR, chan = chan0 + lane % kR;
-  if (t < n && t < kT && chan < p.N) {
-    const float y = (float)sum * __ldg(p.sw + (int64_t)e * p.N + chan) * __ldg(p.sa + tok0 + t);
-    const int64_t at = (int64_t)(tok0 + t) * p.ld_out + chan;
-    if (p.out_f32) static_cast<float*>(p.out)[at] = y;
-    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+    // partial tiles: lane (g, q) has channels g and g + 8 of columns 2 q and 2 q + 1
+    float* to_part = part + ((it & 1) * kFewWarps + warp) * (kNT * 8 * kFewCol);
+    const int col = (lane & 3) * 2;
+#pragma unroll
+    for (int t = 0; t < kNT; ++t) {
+      float* at = to_part + (t * 8 + col) * kFewCol + g;
+      at[0] = acc[t][0];
+      at[kFewCol] = acc[t][1];
+      at[8] = acc[t][2];
+      at[kFewCol + 8] = acc[t][3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+    }
+    __syncthreads();  // (the buffer is written again after the next one)
+    for (int o = threadIdx.x; o < at_once * kNT * 128; o += kFewThreads) {
+      const int which = o / (kNT * 128), t = (o >> 4) & (kNT * 8 - 1), r = o & 15;
+      const int chan = c0 + (it * at_once + which) * kFewChan + r;
+      if (t >= n || chan >= c1) continue;
+      const float* src = part + ((it & 1) * kFewWarps + which * split) * (kNT * 8 * kFewCol) + t * kFewCol + r;
+      float sum = 0.0f;
+      for (int q = 0; q < split; ++q) sum += src[q * (kNT * 8 * kFewCol)];
+      const float y = sum * __ldg(p.sw + (int64_t)e * p.N + chan) * __ldg(p.sa + tok0 + t);
+      const int64_t to = (int64_t)(tok0 + t) * p.ld_out + chan;
+      if (p.out_f32) static_cast<float*>(p.out)[to] = y;
+      else static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
+    }
   }
 }
 
-template <int kR>
-__global__ void __launch_bounds__(kDotThreads) int8_dot_kernel(const DotParams p) {
-  extern __shared__ __align__(16) uint8_t x[];  // [rows][K]
+__global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const FewParams p) {
+  extern __shared__ __align__(16) uint8_t few_smem[];  // rows [tok][stride], then partial tiles
   __shared__ int32_t off[kMaxExperts + 1], tile[kMaxExperts + 1];
   __shared__ int bad;
-  const int warp = threadIdx.x >> 5;
-  if (warp == 0) plan_units(p.splits, p.G, p.S, kDotTok, p.per_tile, off, tile, &bad);
+  if (threadIdx.x < 32) plan_units(p.splits, p.G, p.S, p.tok, p.per_tile, off, tile, &bad);
   __syncthreads();
   if (bad) {  // every CTA sees it: nothing is written
     if (threadIdx.x == 0) report(p.status, MXG_ERR_SPLITS);
     return;
   }
+  uint8_t* x = few_smem;
+  float* part = reinterpret_cast<float*>(few_smem + p.tok * few_stride(p.K));
   const int64_t units = tile[p.G];
   int u = (int)(units * blockIdx.x / gridDim.x);
   const int end = (int)(units * (blockIdx.x + 1) / gridDim.x);
   while (u < end) {  // a tile of rows at a time
     const int e = find_prefix(tile, p.G, u), tt = (u - tile[e]) / p.per_tile;
     const int first = tile[e] + tt * p.per_tile, last = min(end, first + p.per_tile);
-    const int tok0 = off[e] + tt * kDotTok, n = min(kDotTok, off[e + 1] - tok0);
-    __syncthreads();  // the rows before are no longer read
-    const int pieces = p.K / 16;
-    for (int i = threadIdx.x; i < n * pieces; i += kDotThreads) {
-      const int t = i / pieces, c = i - t * pieces;
-      const uint8_t* src = p.a + (int64_t)(tok0 + t) * p.ld_a;
-      uint4 v;
-      if (p.f16) {
-        const uint4* s = reinterpret_cast<const uint4*>(src) + 2 * c;
-        v = narrow16(__ldg(s), __ldg(s + 1));
-      } else {
-        v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-      }
-      reinterpret_cast<uint4*>(x)[i] = v;
-    }
-    __syncthreads();
-    for (int i = u + warp; i < last; i += kDotWarps) {
-      const int chan0 = (i - first) * kR;
-      if (n == 1) dot_unit<kR, 1>(p, x, e, tok0, n, chan0);
-      else if (n == 2) dot_unit<kR, 2>(p, x, e, tok0, n, chan0);
-      else if (n <= 4) dot_unit<kR, 4>(p, x, e, tok0, n, chan0);
-      else dot_unit<kR, 8>(p, x, e, tok0, n, chan0);
-    }
+    const int tok0 = off[e] + tt * p.tok, n = min(p.tok, off[e + 1] - tok0);
+    const int c0 = (u - first) * kFewChan, c1 = min(p.N, (last - first) * kFewChan);
+    if (n <= 8) few_tile<1>(p, x, part, e, tok0, n, c0, c1);
+    else few_tile<2>(p, x, part, e, tok0, n, c0, c1);
     u = last;
   }
 }
@@ -912,14 +978,23 @@ I8Form i8_form(int i) {
   }
 }
 
+// Rows of a tile of the few-rows form: 16 where they fit shared memory, else 8; 0
+// where not even these do.
+int few_tok(int64_t S, int64_t K) {
+  for (int tok = S > 8 ? 16 : 8; tok >= 8; tok -= 8)
+    if (tok * (int64_t)few_stride(K) + few_part_bytes(tok) <= 216 * 1024) return tok;
+  return 0;
+}
+
 // The form for S rows over G experts, by the rows of the mean expert that has some:
-// dot products (-1) for very few; tiles that hold half as many again as the mean;
-// whole units of 256 from there on.
-constexpr int kDot = -1;
+// the few-rows form (-1; at a mean of 8 rows of 32 experts, 4096 x 7168, it takes the
+// 189 us of the next one, at 16 253 us); tiles that hold half as many again as the mean; whole
+// units of 256 from there on.
+constexpr int kFew = -1;
 int i8_choose(int64_t S, int G, int64_t N, int64_t K) {
   (void)N;
   const int64_t used = std::max<int64_t>(1, std::min<int64_t>(S, G)), mean = (S + used - 1) / used;
-  if (mean <= (G == 1 ? kDotTok : 4) && K <= kDotMaxK) return kDot;
+  if (K <= 0x7FFFFF && mean <= (G == 1 ? 16 : 8) && few_tok(S, K) > 0) return kFew;
   for (int i = 0; i < 3; ++i)
     if (mean + mean / 2 <= i8_form(i).tok || (G == 1 && mean <= i8_form(i).tok)) return i;
   return 3;
@@ -935,7 +1010,7 @@ I8Ws i8_ws(int64_t S, int G, int64_t N, int64_t K, int codes, uint8_t* p) {
   const int form = i8_choose(S, G, N, K);
   I8Ws w{};
   w.total = 256;
-  if (form == kDot) return w;  // needs none
+  if (form == kFew) return w;  // needs none
   const I8Form f = i8_form(form);
   size_t o = 0;
   auto take = [&](int64_t n) {
@@ -998,11 +1073,12 @@ bool make_f16_tmap(CUtensorMap* m, const void* base, int64_t cols, int64_t rows,
 }  // namespace
 
 cudaError_t launch_int8_quantize(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int k, int64_t cols,
-                                 int codes, void* q, int64_t ld_q, float* scale, int32_t* status, cudaStream_t stream) {
+                                 int codes, void* q, int64_t ld_q, float* scale, int32_t* status, cudaStream_t stream, int num_sms) {
   const int64_t pieces = cols / 8;
   const int threads = (int)std::min<int64_t>(kQThreads, (pieces + 31) / 32 * 32);
   const auto fn = codes == MXG_CODES_F16 ? int8_quantize_kernel<true> : int8_quantize_kernel<false>;
-  fn<<<(unsigned)T, threads, 0, stream>>>(static_cast<const uint4*>(x), ld_x / 8, rows, k, T * k, pieces,
+  const dim3 grid((unsigned)T, (unsigned)std::max<int64_t>(1, std::min<int64_t>(k, 2 * num_sms / T)));
+  fn<<<grid, threads, 0, stream>>>(static_cast<const uint4*>(x), ld_x / 8, rows, k, T * k, pieces,
                                           static_cast<uint8_t*>(q), ld_q, scale, status);
   return cudaGetLastError();
 }
@@ -1012,44 +1088,44 @@ size_t int8_gemm_workspace_bytes(int64_t S, int G, int64_t N, int64_t K, int cod
 }
 int int8_gemm_tile_tokens(int64_t S, int G, int64_t N, int64_t K) {
   const int form = i8_choose(S, G, N, K);
-  return form == kDot ? kDotTok : i8_form(form).tok;
+  return form == kFew ? few_tok(S, K) : i8_form(form).tok;
 }
 
 bool int8_gemm_sizes_fit(int64_t S, int G, int64_t N, int64_t K) {
   const int form = i8_choose(S, G, N, K);
-  const int64_t tiles = S / (form == kDot ? kDotTok : i8_form(form).tok) + std::min<int64_t>(S, G);
-  if (form == kDot) return tiles <= 0x7FFFFFFF / cdiv(N, 2);
+  const int64_t tiles = S / (form == kFew ? 8 : i8_form(form).tok) + std::min<int64_t>(S, G);
+  if (form == kFew) return tiles <= 0x7FFFFFFF / cdiv(N, kFewChan);
   return tiles * cdiv(N, 2 * kChan) <= 0x7FFFFFFF / cdiv(K, kStageK);
 }
 
 namespace {
-mxg_status launch_int8_dot(const Int8GemmArgs& a, cudaStream_t stream, int num_sms, int dev) {
-  // Two channels a warp where four would leave warps without any.
-  const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(a.S, a.G));
-  const int slots = 2 * num_sms * kDotWarps;
-  const int per_warp = tiles * cdiv(a.N, 4) < slots ? 2 : 4;
-  const auto fn = per_warp == 2 ? int8_dot_kernel<2> : int8_dot_kernel<4>;
+mxg_status launch_int8_few(const Int8GemmArgs& a, cudaStream_t stream, int num_sms, int dev) {
   {
-    static bool done[kI8MaxDevices][2] = {};
+    static bool ready[kI8MaxDevices] = {};
     std::lock_guard<std::mutex> lk(g_i8_mu);
     if (dev < 0 || dev >= kI8MaxDevices) return MXG_ERR_CUDA;
-    bool& ready = done[dev][per_warp == 2];
-    if (!ready && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kDotTok * kDotMaxK)) != cudaSuccess) {
+    if (!ready[dev] && cudaFuncSetAttribute(int8_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024) != cudaSuccess) {
       cudaGetLastError();
       return MXG_ERR_CUDA;
     }
-    ready = true;
+    ready[dev] = true;
   }
-  DotParams p{};
+  FewParams p{};
   p.splits = a.splits;
   p.G = a.G; p.S = (int)a.S; p.N = (int)a.N; p.K = (int)a.K;
-  p.per_tile = (int)cdiv(a.N, per_warp);
+  p.tok = few_tok(a.S, a.K);
+  p.per_tile = (int)cdiv(a.N, kFewChan);
+  // all warps on a unit, or fewer where that leaves a warp less than its loads in
+  // flight and there are units for every CTA all the same
+  const int64_t units = std::max<int64_t>(1, std::min<int64_t>(a.S, a.G)) * cdiv(a.N, kFewChan);
+  p.split = kFewWarps;
+  while (p.split > 1 && cdiv(a.K, 128) < p.split * kFewDepth && units >= 2 * (int64_t)num_sms * (2 * kFewWarps / p.split)) p.split /= 2;
   p.a = a.a; p.ld_a = a.ld_a; p.f16 = a.codes == MXG_CODES_F16; p.sa = a.sa;
   p.w = a.w; p.ld_w = a.ld_w; p.sw = a.sw;
   p.out = a.out; p.ld_out = a.ld_out; p.out_f32 = a.out_dtype == MXG_OUT_F32;
   p.status = a.status;
-  const size_t smem = (size_t)std::min<int64_t>(kDotTok, a.S) * a.K;
-  fn<<<2 * num_sms, kDotThreads, smem, stream>>>(p);
+  const size_t smem = (size_t)(p.tok * (int64_t)few_stride(a.K) + few_part_bytes(p.tok));
+  int8_few_kernel<<<num_sms, kFewThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return MXG_ERR_CUDA;
   return MXG_OK;
 }
@@ -1059,7 +1135,7 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
   const int form = i8_choose(a.S, a.G, a.N, a.K);
   int dev = 0;
   cudaGetDevice(&dev);
-  if (form == kDot) return launch_int8_dot(a, stream, num_sms, dev);
+  if (form == kFew) return launch_int8_few(a, stream, num_sms, dev);
   const I8Form f = i8_form(form);
   const int pairs = i8_pairs(form, dev);
   if (pairs == 0) return MXG_ERR_CUDA;

@@ -132,7 +132,8 @@ cudaError_t launch_moe_combine_backward(const void* dout, int64_t ld_dout, const
 
 // 8-bit integer products.  See gemm_i8.cu.
 cudaError_t launch_int8_quantize(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int k, int64_t cols,
-                                 int codes, void* q, int64_t ld_q, float* scale, int32_t* status, cudaStream_t stream);
+                                 int codes, void* q, int64_t ld_q, float* scale, int32_t* status, cudaStream_t stream,
+                                 int num_sms);
 struct Int8GemmArgs {
   const uint8_t* a;  // codes of the activations, row stride (bytes)
   int64_t ld_a;

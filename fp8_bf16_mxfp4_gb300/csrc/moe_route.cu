@@ -162,13 +162,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(
         if (v[i] > top) top = v[i];  // false for NaN
       }
     }
-    int id = lane < k ? __ldg(ids + t * k + lane) : -1;
+    int id = -1;
+    float w = 0.0f, dw = 0.0f;
+    if (lane < k) {  // loaded together, before it is known whether the slot is empty
+      id = __ldg(ids + t * k + lane);
+      w = __ldg(weights + t * k + lane);
+      dw = __ldg(dweights + t * k + lane);
+    }
     if (id >= E) {
       report(status, MXG_ERR_INDEX);
       id = -1;
     }
-    const float w = id >= 0 ? __ldg(weights + t * k + lane) : 0.0f;
-    const float dw = id >= 0 ? __ldg(dweights + t * k + lane) : 0.0f;
+    if (id < 0) w = dw = 0.0f;
     float s = w * dw;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);

@@ -708,8 +708,8 @@ mxg_status mxg_diag_bounded_wait(int32_t* d_status, uint64_t timeout_ns, void* s
  * its work for (tokens on adapters at random), 0 where either is below 1. */
 int32_t mxg_diag_lora_tile_adapters(int64_t tokens, int32_t adapters);
 
-/* Diagnostic: the rows of a tile of int8_grouped_gemm_fwd for these sizes: 8 (dot
- * products), 32, 64 or 128 (tensor cores, work cut into equal runs) or 256 (whole
+/* Diagnostic: the rows of a tile of int8_grouped_gemm_fwd for these sizes: 8 or 16
+ * (the form for few rows), 32, 64 or 128 (work cut into equal runs) or 256 (whole
  * tiles); 0 where the sizes are refused. */
 int32_t mxg_diag_int8_tile_tokens(int32_t G, int64_t S, int64_t N, int64_t K);
 

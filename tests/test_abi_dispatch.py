@@ -112,7 +112,7 @@ def _op(rows, cols, codes=1, data=FAKE, scale=FAKE, ld=None, reserved=0):
 def test_int8_gemm_refusals(lib):
     f, g = lib.int8_grouped_gemm_fwd, lib.int8_gemm_dense
     p = ctypes.byref
-    G, S, N, K = 3, 40, 64, 128
+    G, S, N, K = 3, 400, 64, 128
     need = lib.int8_gemm_workspace_size(G, S, N, K, 1)
     assert need >= S * K * 2 and 0 < lib.int8_gemm_workspace_size(G, S, N, K, 2) < need
     a, w = _op(S, K), _op(G * N, K)
@@ -140,8 +140,8 @@ def test_int8_gemm_refusals(lib):
 
 def test_int8_tiles_go_by_the_rows_of_an_expert(lib):
     f = lib.mxg_diag_int8_tile_tokens
-    got = {f(G, S, 4096, 4096) for G, S in ((1, 1), (8, 160), (4, 160), (2, 160), (2, 4096))}
-    assert got == {8, 32, 64, 128, 256}
+    got = {f(G, S, 4096, 4096) for G, S in ((1, 1), (1, 9), (8, 160), (4, 160), (2, 160), (2, 4096))}
+    assert got == {8, 16, 32, 64, 128, 256}
     assert f(0, 1, 64, 64) == 0 and f(1, -1, 64, 64) == 0
 
 
