@@ -985,7 +985,8 @@ mxg_status check_rows(int64_t hidden, int32_t dtype, std::initializer_list<int64
 mxg_status check_i8_operand(const mxg_i8_operand* op) {
   if (op == nullptr) return MXG_ERR_NULL;
   if ((op->codes != MXG_CODES_INT8 && op->codes != MXG_CODES_F16) || op->reserved != 0) return MXG_ERR_UNSUPPORTED;
-  if (op->rows < 0 || op->rows > 0x7FFFFFFF || op->cols < 16 || op->cols > 0x7FFFFFFF || op->cols % 16 != 0 ||
+  // 32-bit tile coordinates: up to 256 rows past the last one
+  if (op->rows < 0 || op->rows > 0x7FFFFFFF - 256 || op->cols < 16 || op->cols > 0x7FFFFFFF || op->cols % 16 != 0 ||
       op->ld < op->cols * op->codes)  // a code of kind c has c bytes
     return MXG_ERR_SHAPE;
   if (op->ld % 16 != 0) return MXG_ERR_ALIGN;
@@ -1002,7 +1003,7 @@ mxg_status int8_gemm_impl(const mxg_i8_operand* A, const mxg_i8_operand* W, cons
   if ((st = check_i8_operand(A)) != MXG_OK || (st = check_i8_operand(W)) != MXG_OK) return st;
   if (d_status == nullptr) return MXG_ERR_NULL;
   if (W->codes != MXG_CODES_INT8 || !valid_out_dtype(out_dtype)) return MXG_ERR_UNSUPPORTED;
-  if (G < 1 || G > kMaxExperts || N < 8 || N % 8 != 0 || N > 0x7FFFFFFF / G || W->rows != (int64_t)G * N ||
+  if (G < 1 || G > kMaxExperts || N < 8 || N % 8 != 0 || N > (0x7FFFFFFF - 256) / G || W->rows != (int64_t)G * N ||
       A->cols != W->cols || ld_out < N || !int8_gemm_sizes_fit(A->rows, G, N, A->cols))
     return MXG_ERR_SHAPE;
   if (ld_out % per16(out_dtype) != 0) return MXG_ERR_ALIGN;
@@ -1161,7 +1162,8 @@ mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* row
 }
 
 size_t int8_gemm_workspace_size(int32_t G, int64_t S, int64_t N, int64_t K, int32_t a_codes) {
-  if (G < 1 || G > kMaxExperts || S < 0 || S > 0x7FFFFFFF || N < 8 || N % 8 != 0 || N > 0x7FFFFFFF / G || K < 16 ||
+  if (G < 1 || G > kMaxExperts || S < 0 || S > 0x7FFFFFFF - 256 || N < 8 || N % 8 != 0 ||
+      N > (0x7FFFFFFF - 256) / G || K < 16 ||
       K > 0x7FFFFFFF || K % 16 != 0 || (a_codes != MXG_CODES_INT8 && a_codes != MXG_CODES_F16))
     return 0;
   return int8_gemm_workspace_bytes(S, G, N, K, a_codes);

@@ -134,9 +134,9 @@ cudaError_t launch_route(const TIn* logits, int64_t T, int E, int64_t ld, int k,
 // Gradient of the routing weights.  With s = sum_j w_j dw_j over a token's slots:
 //   weights over the chosen experts   dl[id_j] = w_j (dw_j - s), zeros elsewhere
 //   weights over all experts          dl_e = [e = id_j] w_j dw_j - p_e s,  p = softmax(l)
-// One warp per token.  The row is made in shared memory, the slots added to it in
-// order (so an expert that is named twice gets both, always the same way), and
-// written once.  p is made as the forward makes it: a logit of -inf or NaN has 0,
+// One warp per token, a lane holding the experts lane, lane + 32, ...: the slots are
+// added to the row in order (so an expert that is named twice gets both, always the
+// same way), and it is written once.  p is made as the forward makes it: a logit of -inf or NaN has 0,
 // one that equals the maximum exp(0).
 // ---------------------------------------------------------------------------
 MXG_DEVINL void store_grad(float* p, float v) { *p = v; }
@@ -147,9 +147,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(
     const float* __restrict__ dweights, const int32_t* __restrict__ ids, const float* __restrict__ weights,
     const TIn* __restrict__ logits, int64_t T, int E, int64_t ld, int k, TIn* __restrict__ dlogits, int64_t ld_d,
     int32_t* __restrict__ status) {
-  __shared__ float rows[kRouteWarps][32 * kPer];
   const int lane = threadIdx.x & 31;
-  float* row = rows[threadIdx.x >> 5];
   const bool renorm = logits == nullptr;
   for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < T;
        t += (int64_t)gridDim.x * kRouteWarps) {
@@ -180,7 +178,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(
     const float add = renorm ? w * (dw - s) : w * dw;
     if (renorm) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) row[lane + 32 * i] = 0.0f;
+      for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
     } else {
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
@@ -194,20 +192,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(
       for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
       const float per = total > 0.0f ? s / total : 0.0f;  // a row without logits has no slots
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) row[lane + 32 * i] = -v[i] * per;
+      for (int i = 0; i < kPer; ++i) v[i] *= -per;
     }
-    __syncwarp();
     for (int j = 0; j < k; ++j) {
       const int e = __shfl_sync(kFull, id, j);
       const float a = __shfl_sync(kFull, add, j);
-      if (e >= 0 && lane == (e & 31)) row[e] += a;  // the lane that wrote it, and that reads it
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (e == lane + 32 * i) v[i] += a;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = lane + 32 * i;
-      if (e < E) store_grad(dlogits + t * ld_d + e, row[e]);
+      if (e < E) store_grad(dlogits + t * ld_d + e, v[i]);
     }
-    __syncwarp();
   }
 }
 
