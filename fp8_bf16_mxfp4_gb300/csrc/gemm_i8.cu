@@ -4,28 +4,19 @@
 //   quantize   a = max(max |x[t]|, 2^-100), s = a / 127, q = rint(x (127 / a))
 //   product    y[i, n] = sa[i] sw[g N + n] sum_k qa[i, k] qw[g N + n, k],  g row i's expert
 //
-// sm_103a has no integer kind of tcgen05.mma, and its mma.sync runs at a small
-// fraction of the tensor cores' rate.  Every integer up to 2048 is an FP16 value,
-// so the products are taken by kind::f16: exact, with fp32 sums (exact up to 2^24).
-// Weights stay 8-bit integers as far as the SM: they are the M operand, which the
-// tensor core reads from TMEM, so a warp that turns a row's bytes into FP16 writes
-// them where they are needed and shared memory never holds them twice as wide.
-// Activations are the N operand, from shared memory, as FP16 (the quantizer writes
-// them so, or a kernel in front widens them once).  A pair of CTAs on neighbouring
-// SMs (a cluster) shares a tile of 256 channels through the 2-SM MMA: each has 128
-// channels and half of the tokens.  Per CTA:
-//   warp 0       producer: 128 channels x 128 bytes of weights and the tokens' 128
-//                elements a stage, by TMA;
-//   warp 1       TMEM owner; in the even CTA MMA issuer for both, 8 MMAs a stage;
-//   warps 2-5    epilogue, one per TMEM lane quarter (a lane is a channel);
-//   warps 6-13   weights to FP16, shared memory to TMEM: two groups of four warps
-//                take turns at the stages (tiles of 256 tokens: one group, 6-9);
-//   warp 14      waits for the issuer (not with 256 tokens).
-// Two forms.  Few rows per expert: tiles of 16 to 128 tokens; the stages of all units
-// (expert, channel tile, token tile) are cut into one equal run per pair, so that
-// every SM streams the same number of weight bytes, and cut units are joined through
-// fp32 partials, added in run order by the last to arrive.  Many rows: 256 tokens,
-// whole units.
+// sm_103a has no integer kind of tcgen05.mma, and its integer mma.sync runs at the
+// rate of dp4a.  Every integer up to 2048 is an FP16 value, so products are taken as
+// FP16's: exact, with fp32 sums (exact up to 2^24).  Weights stay 8-bit integers as
+// far as the SM.  Three forms, by the rows of the mean expert:
+//
+//   few      tiles of 8 or 16 rows, mma.sync, weights from global memory to registers;
+//   cut      tiles of 32, 64 or 128 rows on the tensor cores, the contraction of all
+//            tiles cut into equal runs;
+//   whole    tiles of 256 rows on the tensor cores.
+//
+// 8192 rows of 8 experts, 4096 x 14336: 530 us, 1.82 PFLOP/s (0.96 of what torch's
+// BF16 product of two such matrices reaches), where tensor pipe and shared memory are
+// each busy 80 % of the time.  128 rows of 32 experts, 4096 x 7168: 155 us, 6.1 TB/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -243,7 +234,10 @@ MXG_DEVINL uint32_t pack_bf16(float lo, float hi) {
 // the order expert, tile of rows, channels, and its loads run ahead over units.
 // mma.sync makes 974 products of FP16 codes a clock and SM (of 8-bit integers 255, as
 // does dp4a), of which 8 rows at the rate of memory need 190: bound by HBM.
-// 1 row, 4096 x 7168: ZZ us; 128 rows of 32 experts: ZZ us, ZZ TB/s.
+// 128 rows of 32 experts, 4096 x 7168: 155 us, 6.1 TB/s (167 with dp4a, 184 in the
+// form for more rows); 1 row, 28672 x 8192: 43 us, of which 6 are start and end; 1
+// row, 4096 x 7168: 11 us.  Loads of 32 bytes a lane, 8 warps with twice the loads in
+// flight, and joins that no warp waits for measured the same or worse.
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
@@ -443,7 +437,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const FewParam
 }
 
 // ---------------------------------------------------------------------------
-// Product on the tensor cores
+// Product on the tensor cores (tcgen05, kind::f16)
+//
+// Weights are the M operand, which the tensor core reads from TMEM: a warp that turns
+// a row's bytes into FP16 writes them where they are needed, and shared memory never
+// holds them twice as wide.  Activations are the N operand, from shared memory, as
+// FP16 (the quantizer writes them so, or a kernel in front widens them once).  A pair
+// of CTAs on neighbouring SMs (a cluster) shares a tile of 256 channels through the
+// 2-SM MMA: each has 128 channels and half of the rows, so that shared memory takes
+// 96 bytes a clock; a single CTA's 160 would not fit its 128.  Per CTA:
+//   warp 0       producer: 128 channels x 128 bytes of weights and the rows' 128
+//                elements a stage, by TMA;
+//   warp 1       TMEM owner; in the even CTA MMA issuer for both, 8 MMAs a stage;
+//   warps 2-5    epilogue, one per TMEM lane quarter (a lane is a channel);
+//   warps 6-9    weights to FP16, shared memory to TMEM;
+//   warp 10      waits for the issuer (cut form).
+// Cut form: the stages of all units (expert, channel tile, row tile) are cut into one
+// equal run per pair, so that every SM streams the same number of weight bytes; cut
+// units are joined through fp32 partials, added in run order by the last to arrive.
+// Bound there: an MMA of 16 contraction elements takes about 110 clocks whatever its
+// rows while the widening warps write TMEM (152 us for 1024 rows of 32 experts, 4096 x
+// 7168, without those writes; 184 with them; 138 of HBM).  One row tile of few rows is
+// latency: 20 rows, 4096 x 4096, 16 us, of which 4 are the loads', 1 the start, 3 the
+// join and 3 two launches.
 // ---------------------------------------------------------------------------
 constexpr int kChan = 128;                 // channels of a CTA's tile (TMEM lanes)
 constexpr int kStageK = 128;               // contraction elements of a stage
@@ -461,10 +477,7 @@ template <int kTok>
 struct I8Cfg {
   static constexpr int kBufs = kTok == 256 ? 1 : 2;
   static constexpr bool kCut = kTok < 256;             // units may be cut over pairs
-  // Groups of four widening warps.  With 256 tokens a stage lasts 1024 clocks, which
-  // one group keeps up with, and the epilogue needs the registers.
-  static constexpr int kGroups = kTok == 256 ? 1 : 2;
-  static constexpr int kWatch = 6 + 4 * kGroups;       // the warp that waits for the issuer
+  static constexpr int kWatch = 10;                    // the warp that waits for the issuer
   static constexpr int kThreads = 32 * (kWatch + (kCut ? 1 : 0));
   static constexpr int kRows = kTok / 2;               // tokens whose elements a CTA loads
   static constexpr int kXBox = kRows * 128;            // 64 elements of each
@@ -472,10 +485,8 @@ struct I8Cfg {
   static constexpr int kACol = kTok >= 128 ? 256 : (kTok >= 64 ? 128 : 64);
   // Slots of widened weights in TMEM, and stages in shared memory: more of them
   // where a stage is small, since the loads' latency under load (about 2.3 us) is
-  // most of a stage's time.  Both are even: each group of widening warps then has
-  // its own stages and slots and sees every round of them (a group that came to a
-  // stage every other round could take the round before for its own).
-  static constexpr int kSlots = (kI8TmemCols - kACol) / kACols & ~1;
+  // most of a stage's time.
+  static constexpr int kSlots = (kI8TmemCols - kACol) / kACols;
   static constexpr int kStages = kTok == 32 ? 10 : kTok == 64 ? 8 : kTok == 128 ? 6 : 4;
   static constexpr int kBarOff = kStages * kStageBytes;
   static constexpr int kBars = 3 * kStages + 5;
@@ -488,7 +499,7 @@ struct I8Cfg {
   static_assert(kBufs * kTok <= kACol && kACol + kSlots * kACols <= kI8TmemCols, "TMEM holds accumulators and ring");
   static_assert(kStageBytes % 1024 == 0 && kXBox % 1024 == 0, "tiles keep the swizzle-atom alignment");
   static_assert(kTotal <= 232448, "fits the 227 KB of one CTA");
-  static_assert(kSlots % 2 == 0 && kStages % 2 == 0 && kSlots <= kStages, "see above");
+  static_assert(kSlots <= kStages, "a slot's MMAs are those of an earlier stage of the ring");
 };
 
 struct I8Params {
@@ -690,7 +701,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
     // lane issues and hands the stages back.  A wait on an mbarrier by the thread
     // that issues holds it until its MMAs are done.  256 tokens' MMAs take longer
     // than that; for fewer a second warp waits and meets the issuer at a named
-    // barrier (32 experts of 4096 x 7168, 128 rows: ZZ us, ZZ with the waits here).
+    // barrier (128 rows of 32 experts, 4096 x 7168: 184 us, 201 with the waits here).
     if (rank == 0) {
       const uint32_t el = lane == 0;
       const uint32_t tm = __shfl_sync(kFull, tmem, 0);
@@ -754,7 +765,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
     // once the MMAs of kSlots stages ago have completed: they were committed to
     // that stage's empty barrier (with as many slots as stages, before this
     // stage's bytes were even loaded).
-    const int group = (warp - 6) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16) + L::kACol;
     const uint32_t src0 = sbase + row * 128;
     int stage = 0, slot = 0, old = 0;  // old: the stage of kSlots ago
@@ -762,32 +773,27 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
     bool ok = true, wrapped = false;   // wrapped: the slots have been used before
     while (ok && w.next(p, off, tile)) {
       for (int kc = w.k0; kc < w.k1; ++kc) {
-        if (L::kGroups == 1 || (stage & 1) == group) {
-          ok = ptx::mbar_wait_warp(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
+        ok = ptx::mbar_wait_warp(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns);
+        if (!ok) break;
+        if (L::kSlots < kStages && wrapped) {
+          ok = ptx::mbar_wait_warp(empty_bar(old), old_phase, abort_flag, p.status, p.timeout_ns);
           if (!ok) break;
-          if (L::kSlots < kStages && wrapped) {
-            ok = ptx::mbar_wait_warp(empty_bar(old), old_phase, abort_flag, p.status, p.timeout_ns);
-            if (!ok) break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t src = src0 + stage * L::kStageBytes, dst = tq + slot * kACols;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t o[32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[4];
-              ptx::ld_shared_v4(src + (((4 * h + c) ^ (row & 7)) << 4), v);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) widen4(v[i], o[8 * c + 2 * i], o[8 * c + 2 * i + 1]);
-            }
-            ptx::tmem_st_32x32b_x32(dst + 32 * h, o);
-          }
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_issuer(ready_bar(stage));
         }
+        ptx::tc_fence_after();
+        const uint32_t src = src0 + stage * L::kStageBytes, dst = tq + slot * kACols;
+        uint32_t o[64];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[4];
+          ptx::ld_shared_v4(src + ((c ^ (row & 7)) << 4), v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) widen4(v[i], o[8 * c + 2 * i], o[8 * c + 2 * i + 1]);
+        }
+        ptx::tmem_st_32x32b_x64(dst, o);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_issuer(ready_bar(stage));
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
         if (wrapped && ++old == kStages) { old = 0; old_phase ^= 1u; }
         if (++slot == L::kSlots) { slot = 0; wrapped = true; }
@@ -914,10 +920,17 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < kCols; ++i) v[i] = 0.0f;
-          for (int b = first; b <= last; ++b) {  // in run order: buffers 2 first + 1, 2 (first + 1), ...
-            const float* src = p.part + ((int64_t)(4 * b + 2 * (b == first) + rank) * kTok + c0) * kChan + quarter * 32 + lane;
+          // in run order: buffers 2 first + 1, 2 (first + 1), ...; two of them in flight
+          for (int b = first; b <= last; b += 2) {
+            const float* s0 = p.part + ((int64_t)(4 * b + 2 * (b == first) + rank) * kTok + c0) * kChan + quarter * 32 + lane;
+            const float* s1 = p.part + ((int64_t)(4 * (b + 1) + rank) * kTok + c0) * kChan + quarter * 32 + lane;
+            float a0[kCols], a1[kCols];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) v[i] += c0 + i < w.n ? __ldcg(src + i * kChan) : 0.0f;
+            for (int i = 0; i < kCols; ++i) a0[i] = c0 + i < w.n ? __ldcg(s0 + i * kChan) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) a1[i] = b < last && c0 + i < w.n ? __ldcg(s1 + i * kChan) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) v[i] = v[i] + a0[i] + a1[i];
           }
         }
         const float sa = c0 + lane < w.n ? __ldg(p.sa + w.tok0 + c0 + lane) : 0.0f;
