@@ -532,3 +532,47 @@ def test_arguments_that_do_not_fit_are_refused(name):
         for bad in (t.double() if t.is_floating_point() else t.long(), t.cpu(), t.unsqueeze(0), wide, wide[..., ::2]):
             with pytest.raises((ValueError, _mxg().MXGError)):
                 fn(**{**args, k: bad})
+
+
+def test_workspace_and_status():
+    mxg = _mxg()
+    u8 = torch.uint8
+    ids = torch.zeros(3000, 2, dtype=torch.int32, device=DEV)
+    a = mxg.Int8Operand(torch.zeros(700, 64, dtype=torch.int8, device=DEV), torch.ones(700, device=DEV))
+    b = mxg.Int8Operand(torch.zeros(64, 64, dtype=torch.int8, device=DEV), torch.ones(64, device=DEV))
+    for fn, args, need in ((mxg.moe_sort, (ids, 7), mxg.moe_sort_workspace_size(3000, 2, 7)),
+                           (mxg.int8_gemm_dense, (a, b), mxg.int8_gemm_workspace_size(1, 700, 64, 64, "int8"))):
+        whole = torch.zeros(2 * need + 256, dtype=u8, device=DEV)
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        fn(*args, workspace=whole[256:256 + need], status=st, check=True)
+        for bad in (torch.zeros(1, dtype=u8, device=DEV).expand(need), whole[: 2 * need: 2], whole[: need // 4 * 4].view(F32),
+                    whole[: need - 1], whole[8: need + 8], whole.cpu()):
+            with pytest.raises((ValueError, mxg.MXGError)):
+                fn(*args, workspace=bad)
+        for bad in (torch.zeros(1, dtype=u8, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)):
+            with pytest.raises(ValueError):
+                fn(*args, status=bad)
+
+
+def test_two_threads_on_one_stream():
+    """Each thread's calls have a workspace of their own."""
+    import threading
+    mxg = _mxg()
+    data = [inputs(7), inputs(8)]
+    want = [step(mxg, s) for s in data]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        for _ in range(40):
+            got = step(mxg, data[i])
+            torch.cuda.synchronize()
+            if not all(torch.equal(x, y) for x, y in zip(got, want[i])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
