@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const uint4* _
                                                                   int64_t pieces, uint8_t* __restrict__ q, int64_t ld_q,
                                                                   float* __restrict__ scale, int32_t* status) {
   __shared__ uint32_t part[kQThreads / 32];
+  ptx::pdl_launch_dependents();
   const int64_t t = blockIdx.x;
   const uint4* src = x + t * ld_x;
   uint4 keep[kQKeep];
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const FewParam
   extern __shared__ __align__(16) uint8_t few_smem[];  // rows [tok][stride], then partial tiles
   __shared__ int32_t off[kMaxExperts + 1], tile[kMaxExperts + 1];
   __shared__ int bad;
+  ptx::pdl_wait();  // all operands may come from the kernel before
   if (threadIdx.x < 32) plan_units(p.splits, p.G, p.S, p.tok, p.per_tile, off, tile, &bad);
   __syncthreads();
   if (bad) {  // every CTA sees it: nothing is written
@@ -1144,8 +1146,21 @@ mxg_status launch_int8_few(const Int8GemmArgs& a, cudaStream_t stream, int num_s
   p.out = a.out; p.ld_out = a.ld_out; p.out_f32 = a.out_dtype == MXG_OUT_F32;
   p.status = a.status;
   const size_t smem = (size_t)(p.tok * (int64_t)few_stride(a.K) + few_part_bytes(p.tok));
-  int8_few_kernel<<<num_sms, kFewThreads, smem, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return MXG_ERR_CUDA;
+  // started while the kernel before ends (1 token's quantizer and product: 12.7 us, 13.3 without)
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)num_sms);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, int8_few_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return MXG_ERR_CUDA;
+  }
   return MXG_OK;
 }
 }  // namespace
