@@ -950,7 +950,7 @@ def moe_gather(x: torch.Tensor, rows: torch.Tensor, out: torch.Tensor | None = N
     T, k = rows.shape
     dtype = _OUT.get(x.dtype)
     if x.dim() != 2 or x.shape[0] != T or dtype is None or not x.is_cuda:
-        _refuse(x=(x, (T, x.shape[-1]), _OUT, False))
+        _refuse(x=(x, (T, *x.shape[-1:]), _OUT, False))
     if x.requires_grad or (out is not None and out.requires_grad):
         _refuse_grad("moe_gather")
     H, dev, given = x.shape[1], x.device, out
@@ -982,7 +982,7 @@ def moe_combine(y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor | Non
     T, k = shape
     dtype = _OUT.get(y.dtype)
     if y.dim() != 2 or dtype is None or not y.is_cuda:
-        _refuse(y=(y, (T * k, y.shape[-1]), _OUT, False))
+        _refuse(y=(y, (T * k, *y.shape[-1:]), _OUT, False))
     if weights is not None and (weights.shape != shape or weights.dtype != torch.float32 or not weights.is_contiguous()
                                 or not weights.is_cuda):
         _refuse(weights=(weights, shape, torch.float32, True))
@@ -1020,7 +1020,7 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, rows: torch.Tensor
     f32, dt = torch.float32, y.dtype
     dtype = _OUT.get(dt)
     if y.dim() != 2 or y.shape[0] != T * k or dtype is None or not y.is_cuda:
-        _refuse(y=(y, (T * k, y.shape[-1]), _OUT, False))
+        _refuse(y=(y, (T * k, *y.shape[-1:]), _OUT, False))
     H, dev = y.shape[1], y.device
     if (dout.shape != (T, H) or dout.dtype != dt or not dout.is_cuda or weights.shape != shape or weights.dtype != f32
             or not weights.is_contiguous() or not weights.is_cuda):
@@ -1119,7 +1119,7 @@ class Int8Operand:
         data, scale = self.data, self.scale
         kind = _CODE_KIND.get(data.dtype)
         if data.dim() != 2 or kind is None or not data.is_cuda:
-            _refuse(codes=(data, (data.shape[0], data.shape[-1]), _CODE_KIND, False))
+            _refuse(codes=(data, (*data.shape[:1], *data.shape[1:][-1:]), _CODE_KIND, False))
         rows, cols = data.shape
         if scale.shape != (rows,) or scale.dtype != torch.float32 or not scale.is_contiguous() or not scale.is_cuda:
             _refuse(scale=(scale, (rows,), torch.float32, True))
@@ -1147,7 +1147,7 @@ def int8_quantize_rowwise(x: torch.Tensor, rows: torch.Tensor | None = None, cod
     if dtype is None:
         raise ValueError(f"unknown codes {codes!r} (int8 or f16)")
     if x.dim() != 2 or x.dtype != torch.bfloat16 or not x.is_cuda:
-        _refuse(x=(x, (x.shape[0], x.shape[-1]), torch.bfloat16, False))
+        _refuse(x=(x, (*x.shape[:1], *x.shape[1:][-1:]), torch.bfloat16, False))
     if x.requires_grad or (scale is not None and scale.requires_grad) or (q is not None and q.requires_grad):
         _refuse_grad("int8_quantize_rowwise")
     T, K = x.shape

@@ -27,6 +27,10 @@ constexpr uint32_t kFull = 0xffffffffu;
 // chunk to its warps, and a warp takes its run 32 slots at a time, where
 // __match_any finds the slots of one expert.  A slot's row is the rows of lower
 // experts, of earlier chunks, of earlier warps and of earlier slots of its run.
+// Up to 4096 slots are one CTA's; above, a first kernel leaves every chunk's counts
+// and the second, which counts its own chunk again while that one ends, adds up those
+// of the chunks before.  Bound by latency: 64 slots 2.5 us, 65536 slots of 32 experts
+// 11 us (4 and 7, overlapping); no atomics, so equal ids keep their order.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -196,7 +200,6 @@ MXG_DEVINL int64_t row_of(int32_t entry, int64_t count, int32_t* status) {
   return -1;
 }
 
-
 template <typename T>
 struct Piece {
   static constexpr int n = 16 / sizeof(T);
@@ -232,6 +235,8 @@ int row_threads(int64_t pieces) {
   return (int)(((pieces + turns - 1) / turns + 31) / 32 * 32);
 }
 
+// A token's row is read once and written to its k rows.  Bound by HBM: 8192 tokens of
+// 7168, top 8, 162 us, 6.5 TB/s, nearly all of it writes.
 __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const uint4* __restrict__ x, int64_t ld_x,
                                                                  const int32_t* __restrict__ rows, int k, int64_t P,
                                                                  int64_t pieces, uint4* __restrict__ out, int64_t ld_out,
@@ -248,6 +253,9 @@ __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const uint4* __
   }
 }
 
+// A thread sums one piece over the slots, eight rows in flight.  Every row is read once
+// and not again, so the loads and stores are marked as streaming: 65536 rows of 7168 to
+// 8192, 162 us, 6.5 TB/s; 173 with plain ones.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* __restrict__ y, int64_t ld_y, int64_t y_rows,
                                                                   const int32_t* __restrict__ rows,
@@ -293,7 +301,8 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* _
 
 // A CTA takes a token: its pieces of dout once for every kFlight slots, whose
 // products with y it sums per thread, then over the CTA in a fixed order.  y and
-// dy may be one buffer: a piece is read by the thread that writes it.
+// dy may be one buffer: a piece is read by the thread that writes it.  Bound by HBM:
+// 65536 rows of 4096, 172 us, 6.6 TB/s (177 with streaming loads and stores).
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(
     const uint4* __restrict__ dout, int64_t ld_dout, const uint4* y, int64_t ld_y, const int32_t* __restrict__ rows,

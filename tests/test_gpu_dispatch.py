@@ -529,7 +529,8 @@ def test_arguments_that_do_not_fit_are_refused(name):
         if not isinstance(t, torch.Tensor):
             continue
         wide = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype, device=DEV)
-        for bad in (t.double() if t.is_floating_point() else t.long(), t.cpu(), t.unsqueeze(0), wide, wide[..., ::2]):
+        for bad in (t.double() if t.is_floating_point() else t.long(), t.cpu(), t.unsqueeze(0), wide, wide[..., ::2],
+                    t.new_zeros(())):
             with pytest.raises((ValueError, _mxg().MXGError)):
                 fn(**{**args, k: bad})
 

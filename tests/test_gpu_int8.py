@@ -243,10 +243,11 @@ def test_bad_splits_write_nothing(splits, S):
 
 
 def test_rows_and_channels_that_are_not_finite():
-    """A scale of NaN or infinity, or an FP16 code that is not an integer's, stays in its row or channel."""
+    """A scale of NaN or infinity stays in its row or channel; so does, in tiles of 32 rows and more, an FP16 code that
+    is no integer's."""
     mxg = _mxg()
     rng = np.random.default_rng(3)
-    for S in (20, 600):
+    for S in (8, 20, 600):
         qa, sa, qw, sw = operands(rng, [S], 136, 256)
         clean = product(qa, sa, qw, sw, [S], 136, F32)
         sa[3], sw[7] = np.nan, np.inf
@@ -254,6 +255,8 @@ def test_rows_and_channels_that_are_not_finite():
         keep = torch.ones_like(clean, dtype=torch.bool)
         keep[3], keep[:, 7] = False, False
         assert torch.equal(got[keep], clean[keep]) and got[3].isnan().all() and not got[:, 7].isfinite().any()
+        if S == 8:  # codes that are no integers are not for this form
+            continue
         a = dev(qa, torch.float16)
         a[5, 100] = float("inf")
         sa[3], sw[7] = 1, 1
