@@ -1111,7 +1111,7 @@ mxg_status moe_combine_backward(const void* dout, int64_t ld_dout, const void* y
   const int n = per16(dtype);
   return cuda_status(launch_moe_combine_backward(dout, ld_dout / n, y, ld_y / n, rows, weights, tokens, top_k, hidden / n,
                                                  dtype == MXG_OUT_BF16, dy, ld_dy / n, dweights, d_status,
-                                                 static_cast<cudaStream_t>(stream)));
+                                                 static_cast<cudaStream_t>(stream), sms));
 }
 
 mxg_status moe_route_backward(const float* dweights, const int32_t* ids, const float* weights, const void* logits,

@@ -128,7 +128,7 @@ cudaError_t launch_moe_combine(const void* y, int64_t ld_y, int64_t y_rows, cons
 cudaError_t launch_moe_combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y,
                                         const int32_t* rows, const float* weights, int64_t T, int k, int64_t pieces,
                                         bool bf16, void* dy, int64_t ld_dy, float* dweights, int32_t* status,
-                                        cudaStream_t stream);
+                                        cudaStream_t stream, int num_sms);
 
 // 8-bit integer products.  See gemm_i8.cu.
 cudaError_t launch_int8_quantize(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int k, int64_t cols,

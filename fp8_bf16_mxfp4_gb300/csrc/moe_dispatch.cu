@@ -123,19 +123,33 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
   } else {
     ptx::pdl_wait();  // the counts are complete
     const int chunks = (int)gridDim.x;
-#pragma unroll 4
-    for (int e = warp; e < keys; e += kSortWarps) {  // a warp takes a key, its lanes the chunks
-      uint32_t all = 0, early = 0;
+    constexpr int kKeys = 8;  // keys of a warp in flight, its lanes the chunks
+    for (int e0 = warp; e0 < keys; e0 += kSortWarps * kKeys) {
+      uint32_t all[kKeys], early[kKeys];
+#pragma unroll
+      for (int q = 0; q < kKeys; ++q) all[q] = early[q] = 0;
       for (int c = lane; c < chunks; c += 32) {
-        const uint32_t v = (uint32_t)__ldcg(counts + (int64_t)e * chunks + c);
-        all += v;
-        if (c < (int)blockIdx.x) early += v;
+        uint32_t v[kKeys];
+#pragma unroll
+        for (int q = 0; q < kKeys; ++q) {
+          const int e = e0 + q * kSortWarps;
+          v[q] = e < keys ? (uint32_t)__ldcg(counts + (int64_t)e * chunks + c) : 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < kKeys; ++q) {
+          all[q] += v[q];
+          if (c < (int)blockIdx.x) early[q] += v[q];
+        }
       }
-      all = __reduce_add_sync(kFull, all);
-      early = __reduce_add_sync(kFull, early);
-      if (lane == 0) {
-        total[e] = all;
-        before[e] = early;
+#pragma unroll
+      for (int q = 0; q < kKeys; ++q) {
+        const int e = e0 + q * kSortWarps;
+        all[q] = __reduce_add_sync(kFull, all[q]);
+        early[q] = __reduce_add_sync(kFull, early[q]);
+        if (lane == 0 && e < keys) {
+          total[e] = all[q];
+          before[e] = early[q];
+        }
       }
     }
   }
@@ -162,12 +176,13 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
         if (e < E - 1) m_splits[e] = (int32_t)(q ? t1 : t0);
         else if (e == E - 1) m_splits[e] = (int32_t)((uint32_t)P - at);
       }
-      uint32_t pos = at + before[e];
+      uint32_t pos = at + before[e], m[kSortWarps];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) m[w] = cnt[w * keys + e];
 #pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t m = cnt[w * keys + e];
         cnt[w * keys + e] = pos;
-        pos += m;
+        pos += m[w];
       }
     }
     at += q ? t1 : t0;
@@ -226,22 +241,30 @@ MXG_DEVINL uint4 narrow(const float* v) {
   }
 }
 
-// A CTA takes one token and `threads` pieces of its row at a time.
+// Gather and combine: blockDim.x threads share a row's pieces, blockDim.y tokens a CTA.
 constexpr int kRowThreads = 256;
 // As many threads as share a row's pieces equally (896 pieces: 4 times 224; with
-// 256 threads combine takes 186 us instead of 173 for 65536 rows of 7168).
-int row_threads(int64_t pieces) {
+// 256 threads combine takes 186 us instead of 173 for 65536 rows of 7168), and as many
+// tokens as make up a CTA (8 rows of 32 BF16 values for each of 32768 tokens: ZZ us, ZZ
+// with a CTA for every token).
+dim3 row_block(int64_t pieces) {
   const int64_t turns = (pieces + kRowThreads - 1) / kRowThreads;
-  return (int)(((pieces + turns - 1) / turns + 31) / 32 * 32);
+  const unsigned x = (unsigned)((pieces + turns - 1) / turns);
+  return x > kRowThreads / 4 ? dim3((x + 31) / 32 * 32) : dim3(x, kRowThreads / x);
+}
+dim3 row_grid(int64_t tokens, int64_t pieces, dim3 block) {
+  return dim3((unsigned)((tokens + block.y - 1) / block.y),
+              (unsigned)std::min<int64_t>(65535, (pieces + block.x - 1) / block.x));
 }
 
 // A token's row is read once and written to its k rows.  Bound by HBM: 8192 tokens of
 // 7168, top 8, 162 us, 6.5 TB/s, nearly all of it writes.
 __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const uint4* __restrict__ x, int64_t ld_x,
-                                                                 const int32_t* __restrict__ rows, int k, int64_t P,
+                                                                 const int32_t* __restrict__ rows, int64_t T, int k,
                                                                  int64_t pieces, uint4* __restrict__ out, int64_t ld_out,
                                                                  int32_t* status) {
-  const int64_t t = blockIdx.x;
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, P = T * k;
+  if (t >= T) return;
   const int32_t* mine = rows + t * k;
   for (int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; c < pieces; c += (int64_t)gridDim.y * blockDim.x) {
     const uint4 v = __ldg(x + t * ld_x + c);
@@ -253,18 +276,21 @@ __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const uint4* __
   }
 }
 
-// A thread sums one piece over the slots, eight rows in flight.  Every row is read once
-// and not again, so the loads and stores are marked as streaming: 65536 rows of 7168 to
-// 8192, 162 us, 6.5 TB/s; 173 with plain ones.
-template <typename T>
+// A thread sums one piece over a token's slots, eight rows in flight.  Every row is read
+// once and not again, so the loads and stores are marked as streaming: 65536 rows of
+// 7168 to 8192, 162 us, 6.5 TB/s; 173 with plain ones.  kShort: rows so short that a CTA
+// has several tokens (apart, because the other form takes 72 registers: four CTAs of 224
+// threads an SM; with 75 there are three and it takes 194 us).
+template <typename T, bool kShort>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* __restrict__ y, int64_t ld_y, int64_t y_rows,
                                                                   const int32_t* __restrict__ rows,
-                                                                  const float* __restrict__ weights, int k,
+                                                                  const float* __restrict__ weights, int64_t tokens, int k,
                                                                   int64_t pieces, uint4* __restrict__ out,
                                                                   int64_t ld_out, int32_t* status) {
   constexpr int n = Piece<T>::n;
   constexpr int kFlight = 8;  // rows in flight
-  const int64_t t = blockIdx.x;
+  const int64_t t = kShort ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
+  if (kShort && t >= tokens) return;
   for (int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; c < pieces; c += (int64_t)gridDim.y * blockDim.x) {
     float s[n];
 #pragma unroll
@@ -299,20 +325,80 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* _
   }
 }
 
-// A CTA takes a token: its pieces of dout once for every kFlight slots, whose
-// products with y it sums per thread, then over the CTA in a fixed order.  y and
-// dy may be one buffer: a piece is read by the thread that writes it.  Bound by HBM:
-// 65536 rows of 4096, 172 us, 6.6 TB/s (177 with streaming loads and stores).
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(
+// The same for up to kSlots slots, of kTokens tokens at a time, so that there are as
+// many rows in flight: 32768 rows of 2048, one a token, take ZZ us, 94 with the above.
+template <typename T, int kTokens, int kSlots>
+__global__ void __launch_bounds__(kRowThreads) moe_combine_few_kernel(const uint4* __restrict__ y, int64_t ld_y,
+                                                                      int64_t y_rows, const int32_t* __restrict__ rows,
+                                                                      const float* __restrict__ weights, int64_t tokens,
+                                                                      int k, int pieces, uint4* __restrict__ out,
+                                                                      int64_t ld_out, int32_t* status) {
+  constexpr int n = Piece<T>::n;
+  const int64_t t0 = (int64_t)blockIdx.x * (blockDim.y * kTokens) + threadIdx.y;  // then every blockDim.y-th
+  int64_t row[kTokens][kSlots];
+  float w[kTokens][kSlots];
+#pragma unroll
+  for (int u = 0; u < kTokens; ++u) {
+    const int64_t t = t0 + (int64_t)u * blockDim.y;
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      row[u][j] = -1;
+      w[u][j] = 1.0f;
+      if (t < tokens && j < k) {
+        const int32_t e = __ldg(rows + t * k + j);
+        if (weights != nullptr) w[u][j] = __ldg(weights + t * k + j);
+        if (e >= 0) row[u][j] = row_of(e, y_rows, status);
+      }
+    }
+  }
+  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < pieces; c += gridDim.y * blockDim.x) {
+    uint4 v[kTokens][kSlots];
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u)
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (row[u][j] >= 0) v[u][j] = __ldcs(y + row[u][j] * ld_y + c);
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u) {
+      float s[n];
+#pragma unroll
+      for (int i = 0; i < n; ++i) s[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        if (row[u][j] < 0) continue;
+        float f[n];
+        widen<T>(v[u][j], f);
+#pragma unroll
+        for (int i = 0; i < n; ++i) s[i] = fmaf(w[u][j], f[i], s[i]);
+      }
+      const int64_t t = t0 + (int64_t)u * blockDim.y;
+      if (t < tokens) __stcs(out + t * ld_out + c, narrow<T>(s));
+    }
+  }
+}
+
+// `share` threads take a token: kPieces pieces of dout at a time, once for every kFlight
+// slots, whose products with y they sum, then over the threads in a fixed order.  share
+// is a power of two up to 32 (lanes of a warp, 256 / share tokens a CTA) or the whole
+// CTA.  y and dy may be one buffer: a piece is read by the thread that writes it.
+// Bound by HBM: 65536 rows of 4096, 172 us, 6.6 TB/s (177 with streaming loads and
+// stores, 199 with eight slots in flight and fewer warps for it).
+template <typename T, int kPieces, int kFlight, int kThreads, bool kLanes>
+__global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(
     const uint4* __restrict__ dout, int64_t ld_dout, const uint4* y, int64_t ld_y, const int32_t* __restrict__ rows,
-    const float* __restrict__ weights, int k, int64_t P, int64_t pieces, uint4* dy, int64_t ld_dy,
+    const float* __restrict__ weights, int64_t tokens, int k, int pieces, int share, uint4* dy, int64_t ld_dy,
     float* __restrict__ dweights, int32_t* status) {
   constexpr int n = Piece<T>::n;
-  constexpr int kFlight = 4;  // slots at a time; with 8 there are too few warps (65536 rows of 4096: 199 us, 173)
-  __shared__ float part[kRowThreads / 32][kFlight];
-  const int64_t t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  __shared__ float part[kThreads / 32][kFlight];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int me = kLanes ? threadIdx.x & (share - 1) : threadIdx.x;
+  const int64_t t = kLanes ? (int64_t)blockIdx.x * (blockDim.x / share) + threadIdx.x / share : blockIdx.x;
+  const int last = !kLanes || t < tokens ? pieces : 0;  // all threads of a warp take part in its sums
+  const int slots = !kLanes || t < tokens ? k : 0;
+  rows += t * k;
+  weights += t * k;
+  dweights += t * k;
+  dout += t * ld_dout;
   for (int j0 = 0; j0 < k; j0 += kFlight) {
     int64_t at[kFlight];
     float w[kFlight], dot[kFlight];
@@ -322,50 +408,70 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(
       at[j] = -1;
       on[j] = false;
       w[j] = dot[j] = 0.0f;
-      if (j0 + j < k) {
-        const int32_t e = __ldg(rows + t * k + j0 + j);
-        at[j] = row_of(e, P, status);
+      if (j0 + j < slots) {
+        const int32_t e = __ldg(rows + j0 + j);
+        at[j] = row_of(e, tokens * k, status);
         on[j] = e >= 0 && at[j] >= 0;
-        if (on[j]) w[j] = __ldg(weights + t * k + j0 + j);
+        if (on[j]) w[j] = __ldg(weights + j0 + j);
       }
     }
-    for (int64_t c = threadIdx.x; c < pieces; c += blockDim.x) {
-      float d[n];
-      widen<T>(__ldg(dout + t * ld_dout + c), d);
-      uint4 v[kFlight];
+    for (int c0 = me; c0 < last; c0 += kPieces * share) {
+      uint4 d4[kPieces], v[kPieces][kFlight];
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        const int c = c0 + q * share;
+        if (kPieces == 1 || c < pieces) {
+          d4[q] = __ldg(dout + c);
+#pragma unroll
+          for (int j = 0; j < kFlight; ++j)
+            if (on[j]) v[q][j] = y[at[j] * ld_y + c];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        const int c = c0 + q * share;
+        if (kPieces == 1 || c < pieces) {
+          float d[n];
+          widen<T>(d4[q], d);
+#pragma unroll
+          for (int j = 0; j < kFlight; ++j) {
+            float f[n];
+            if (on[j]) {
+              widen<T>(v[q][j], f);
+#pragma unroll
+              for (int i = 0; i < n; ++i) {
+                dot[j] = fmaf(d[i], f[i], dot[j]);
+                f[i] = w[j] * d[i];
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < n; ++i) f[i] = 0.0f;
+            }
+            if (at[j] >= 0) dy[at[j] * ld_dy + c] = narrow<T>(f);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j)
+      for (int s = kLanes ? share >> 1 : 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(kFull, dot[j], s);
+    if constexpr (kLanes) {
 #pragma unroll
       for (int j = 0; j < kFlight; ++j)
-        if (on[j]) v[j] = y[at[j] * ld_y + c];
+        if (me == 0 && j0 + j < slots) dweights[j0 + j] = dot[j];
+    } else {
+      if (lane == 0) {
 #pragma unroll
-      for (int j = 0; j < kFlight; ++j) {
-        float f[n];
-        if (on[j]) {
-          widen<T>(v[j], f);
-#pragma unroll
-          for (int i = 0; i < n; ++i) {
-            dot[j] = fmaf(d[i], f[i], dot[j]);
-            f[i] = w[j] * d[i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < n; ++i) f[i] = 0.0f;
-        }
-        if (at[j] >= 0) dy[at[j] * ld_dy + c] = narrow<T>(f);
+        for (int j = 0; j < kFlight; ++j) part[warp][j] = dot[j];
       }
+      __syncthreads();
+      if (threadIdx.x < kFlight && j0 + (int)threadIdx.x < k) {
+        float s = 0.0f;
+        for (int q = 0; q < (int)(blockDim.x >> 5); ++q) s += part[q][threadIdx.x];
+        dweights[j0 + threadIdx.x] = s;
+      }
+      __syncthreads();
     }
-#pragma unroll
-    for (int j = 0; j < kFlight; ++j) {
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(kFull, dot[j], s);
-      if (lane == 0) part[warp][j] = dot[j];
-    }
-    __syncthreads();
-    if (threadIdx.x < kFlight && j0 + (int)threadIdx.x < k) {
-      float s = 0.0f;
-      for (int q = 0; q < warps; ++q) s += part[q][threadIdx.x];
-      dweights[t * k + j0 + threadIdx.x] = s;
-    }
-    __syncthreads();
   }
 }
 
@@ -412,33 +518,80 @@ cudaError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* m_spl
 
 cudaError_t launch_moe_gather(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int k, int64_t pieces,
                               void* out, int64_t ld_out, int32_t* status, cudaStream_t stream) {
-  const int threads = row_threads(pieces);
-  const dim3 grid((unsigned)T, (unsigned)std::min<int64_t>(65535, (pieces + threads - 1) / threads));
-  moe_gather_kernel<<<grid, threads, 0, stream>>>(static_cast<const uint4*>(x), ld_x, rows, k, T * k, pieces,
-                                                  static_cast<uint4*>(out), ld_out, status);
+  const dim3 block = row_block(pieces);
+  moe_gather_kernel<<<row_grid(T, pieces, block), block, 0, stream>>>(static_cast<const uint4*>(x), ld_x, rows, T, k, pieces,
+                                                                      static_cast<uint4*>(out), ld_out, status);
   return cudaGetLastError();
 }
+
+namespace {
+template <typename T>
+cudaError_t combine(const void* y, int64_t ld_y, int64_t y_rows, const int32_t* rows, const float* weights, int64_t tokens,
+                    int k, int64_t pieces, void* out, int64_t ld_out, int32_t* status, cudaStream_t stream) {
+  const dim3 block = row_block(pieces);
+  const uint4* from = static_cast<const uint4*>(y);
+  uint4* to = static_cast<uint4*>(out);
+  if (k > 4) {
+    const auto fn = block.y > 1 ? moe_combine_kernel<T, true> : moe_combine_kernel<T, false>;
+    fn<<<row_grid(tokens, pieces, block), block, 0, stream>>>(from, ld_y, y_rows, rows, weights, tokens, k, pieces, to,
+                                                             ld_out, status);
+    return cudaGetLastError();
+  }
+  const int each = k > 2 ? 2 : 4;  // tokens of a thread
+  const auto fn = k > 2 ? moe_combine_few_kernel<T, 2, 4> : k > 1 ? moe_combine_few_kernel<T, 4, 2> : moe_combine_few_kernel<T, 4, 1>;
+  fn<<<row_grid((tokens + each - 1) / each, pieces, block), block, 0, stream>>>(from, ld_y, y_rows, rows, weights, tokens, k,
+                                                                               (int)pieces, to, ld_out, status);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y, const int32_t* rows,
+                             const float* weights, int64_t tokens, int k, int64_t pieces, void* dy, int64_t ld_dy,
+                             float* dweights, int32_t* status, cudaStream_t stream, int num_sms) {
+  // Four rows of a thread in flight: of four slots, or of fewer slots' pieces.  A token
+  // has lanes of a warp, or a CTA of as many threads as share its pieces equally: up
+  // to 256, or 1024 where there are few tokens (64 of 7168, top 8: ZZ us, 11.9).
+  const int each = k > 2 ? 1 : k > 1 ? 2 : 4;
+  const int64_t want = (pieces + each - 1) / each;
+  const bool lanes = want <= 32, few = !lanes && tokens < 4 * num_sms;
+  int share = 1, threads = kRowThreads;
+  if (lanes) {
+    while (share < want) share *= 2;
+  } else {
+    const int64_t most = few ? 1024 : kRowThreads, turns = (want + most - 1) / most;
+    share = threads = (int)(((want + turns - 1) / turns + 31) / 32 * 32);
+  }
+  const auto pick = [&](auto one, auto two, auto four) { return each == 1 ? one : each == 2 ? two : four; };
+  const auto fn = lanes ? pick(moe_combine_backward_kernel<T, 1, 4, kRowThreads, true>,
+                               moe_combine_backward_kernel<T, 2, 2, kRowThreads, true>,
+                               moe_combine_backward_kernel<T, 4, 1, kRowThreads, true>)
+                  : few ? pick(moe_combine_backward_kernel<T, 1, 4, 1024, false>,
+                               moe_combine_backward_kernel<T, 2, 2, 1024, false>,
+                               moe_combine_backward_kernel<T, 4, 1, 1024, false>)
+                        : pick(moe_combine_backward_kernel<T, 1, 4, kRowThreads, false>,
+                               moe_combine_backward_kernel<T, 2, 2, kRowThreads, false>,
+                               moe_combine_backward_kernel<T, 4, 1, kRowThreads, false>);
+  const int64_t ctas = lanes ? (tokens + threads / share - 1) / (threads / share) : tokens;
+  fn<<<(unsigned)ctas, threads, 0, stream>>>(static_cast<const uint4*>(dout), ld_dout, static_cast<const uint4*>(y), ld_y,
+                                             rows, weights, tokens, k, (int)pieces, share, static_cast<uint4*>(dy), ld_dy,
+                                             dweights, status);
+  return cudaGetLastError();
+}
+}  // namespace
 
 cudaError_t launch_moe_combine(const void* y, int64_t ld_y, int64_t y_rows, const int32_t* rows, const float* weights,
                                int64_t T, int k, int64_t pieces, bool bf16, void* out, int64_t ld_out, int32_t* status,
                                cudaStream_t stream) {
-  const int threads = row_threads(pieces);
-  const dim3 grid((unsigned)T, (unsigned)std::min<int64_t>(65535, (pieces + threads - 1) / threads));
-  const auto fn = bf16 ? moe_combine_kernel<__nv_bfloat16> : moe_combine_kernel<float>;
-  fn<<<grid, threads, 0, stream>>>(static_cast<const uint4*>(y), ld_y, y_rows, rows, weights, k, pieces,
-                                   static_cast<uint4*>(out), ld_out, status);
-  return cudaGetLastError();
+  const auto fn = bf16 ? combine<__nv_bfloat16> : combine<float>;
+  return fn(y, ld_y, y_rows, rows, weights, T, k, pieces, out, ld_out, status, stream);
 }
 
 cudaError_t launch_moe_combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y,
                                         const int32_t* rows, const float* weights, int64_t T, int k, int64_t pieces,
                                         bool bf16, void* dy, int64_t ld_dy, float* dweights, int32_t* status,
-                                        cudaStream_t stream) {
-  const auto fn = bf16 ? moe_combine_backward_kernel<__nv_bfloat16> : moe_combine_backward_kernel<float>;
-  fn<<<(unsigned)T, row_threads(pieces), 0, stream>>>(static_cast<const uint4*>(dout), ld_dout,
-                                                      static_cast<const uint4*>(y), ld_y, rows, weights, k, T * k, pieces,
-                                                      static_cast<uint4*>(dy), ld_dy, dweights, status);
-  return cudaGetLastError();
+                                        cudaStream_t stream, int num_sms) {
+  const auto fn = bf16 ? combine_backward<__nv_bfloat16> : combine_backward<float>;
+  return fn(dout, ld_dout, y, ld_y, rows, weights, T, k, pieces, dy, ld_dy, dweights, status, stream, num_sms);
 }
 
 }  // namespace mxg

@@ -117,7 +117,8 @@ def test_sort_into_given_outputs():
 
 # --------------------------------------------------------------------------- gather and combine
 
-SIZES = [(1, 1, 1, 8, "all"), (1, 8, 32, 64, "all"), (2, 3, 4, 256, "none"), (7, 2, 3, 40, "holes"), (33, 6, 5, 1160, "holes"),
+SIZES = [(700, 1, 5, 24, "holes"), (90, 2, 4, 1032, "holes"), (1300, 4, 9, 264, "holes"), (40, 3, 4, 520, "all"),
+         (650, 2, 3, 2048, "holes"), (1, 1, 1, 8, "all"), (1, 8, 32, 64, "all"), (2, 3, 4, 256, "none"), (7, 2, 3, 40, "holes"), (33, 6, 5, 1160, "holes"),
          (16, 32, 64, 104, "holes"), (129, 9, 16, 2056, "all"), (300, 1, 7, 16, "holes"), (5, 8, 9, 7168, "holes"),
          (3, 17, 8, 20000, "all")]
 
@@ -315,6 +316,28 @@ def test_route_backward_against_differences(renorm):
         step[e] = h
         loss = [float((mxg.moe_route(logits + s * step, 3, renormalize=renorm)[1].double() * d).sum()) for s in (1, -1)]
         assert abs((loss[0] - loss[1]) / (2 * h) - float(got[e])) < 2.0 ** -9
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E", [128, 256, 264, 512])
+def test_route_backward_of_rows_at_any_offset(E, dtype):
+    """Rows that 16-byte pieces fit, and the same values in rows that they do not."""
+    mxg = _mxg()
+    g = torch.Generator().manual_seed(E)
+    logits = (2 * torch.randn(19, E, generator=g)).to(dtype).to(DEV)
+    ids, w = mxg.moe_route(logits, 8, renormalize=False)
+    d = torch.randn(19, 8, generator=g).to(DEV)
+    want = mxg.moe_route_backward(d, ids, w, logits, renormalize=False, check=True)
+    oracle, bound = dispatch.route_backward(f64(d), ids.cpu().numpy(), f64(w), f64(logits), E, False)
+    close(want, oracle, bound, dtype)
+    for at, room in ((1, 3), (16, 32), (4, 12)):
+        big, out = torch.zeros(19, E + room, dtype=dtype, device=DEV), torch.full((19, E + room), 9.0, dtype=dtype, device=DEV)
+        big[:, at:at + E] = logits
+        for dst in (None, out[:, at:at + E]):
+            got = mxg.moe_route_backward(d, ids, w, big[:, at:at + E], renormalize=False, dlogits=dst, check=True)
+            close(got, oracle, bound, dtype)
+        out[:, at:at + E] = 9.0
+        assert (out == 9.0).all()
 
 
 def test_route_backward_special_cases():
