@@ -28,14 +28,17 @@ constexpr uint32_t kFull = 0xffffffffu;
 // __match_any finds the slots of one expert.  A slot's row is the rows of lower
 // experts, of earlier chunks, of earlier warps and of earlier slots of its run.
 // Up to 4096 slots are one CTA's; above, a first kernel leaves every chunk's counts
-// and the second, which counts its own chunk again while that one ends, adds up those
-// of the chunks before.  Bound by latency: 64 slots 2.5 us, 65536 slots of 32 experts
-// 11 us (4 and 7, overlapping); no atomics, so equal ids keep their order.
+// and the last, which counts its own chunk again while the one before ends, adds up
+// those of the chunks before.  Where that is much for every CTA, a kernel between the
+// two adds them up once.  Bound by latency: 64 slots 2.5 us, 65536 slots of 32 experts
+// 10 us, 262144 of 512 15 us (29 without the kernel between); no atomics, so equal ids
+// keep their order.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortChunk = 2048;  // least slots of a chunk, where there are several
 constexpr int kSortMaxChunks = 256;
+constexpr int64_t kSortScan = 8192;  // counts from which on they are added up by a kernel of their own
 
 int64_t sort_chunk(int64_t P) {
   if (P <= 2 * kSortChunk) return 2 * kSortChunk;  // one CTA, one launch
@@ -97,8 +100,37 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(const int3
   }
 }
 
+// counts[e][.] -> their exclusive prefix sums, totals[e].  A warp takes a key.
+__global__ void __launch_bounds__(kSortThreads) moe_sort_scan_kernel(int32_t* counts, int32_t* totals, int keys, int chunks) {
+  const int lane = threadIdx.x & 31, e = blockIdx.x * kSortWarps + (threadIdx.x >> 5);
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait();
+  if (e >= keys) return;
+  uint32_t v[kSortMaxChunks / 32], at = 0;
+#pragma unroll
+  for (int i = 0; i < kSortMaxChunks / 32; ++i) {
+    const int c = 32 * i + lane;
+    v[i] = c < chunks ? (uint32_t)__ldcg(counts + (int64_t)e * chunks + c) : 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < kSortMaxChunks / 32; ++i) {
+    if (32 * i >= chunks) break;
+    uint32_t incl = v[i];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += o;
+    }
+    const int c = 32 * i + lane;
+    if (c < chunks) counts[(int64_t)e * chunks + c] = (int32_t)(at + incl - v[i]);
+    at += __shfl_sync(kFull, incl, 31);
+  }
+  if (lane == 0) totals[e] = (int32_t)at;
+}
+
 __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int32_t* __restrict__ ids, int64_t P, int E,
                                                                       int64_t chunk, const int32_t* counts,
+                                                                      const int32_t* totals,  // with prefix sums in counts
                                                                       int32_t* __restrict__ m_splits,
                                                                       int32_t* __restrict__ rows, int32_t* status) {
   extern __shared__ uint32_t cnt[];  // [warps][E + 1]
@@ -119,6 +151,12 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
       for (int w = 0; w < kSortWarps; ++w) v += cnt[w * keys + e];
       total[e] = v;
       before[e] = 0;
+    }
+  } else if (totals != nullptr) {
+    ptx::pdl_wait();  // the counts are complete
+    for (int e = threadIdx.x; e < keys; e += kSortThreads) {
+      total[e] = (uint32_t)__ldcg(totals + e);
+      before[e] = (uint32_t)__ldcg(counts + (int64_t)e * gridDim.x + blockIdx.x);
     }
   } else {
     ptx::pdl_wait();  // the counts are complete
@@ -245,7 +283,7 @@ MXG_DEVINL uint4 narrow(const float* v) {
 constexpr int kRowThreads = 256;
 // As many threads as share a row's pieces equally (896 pieces: 4 times 224; with
 // 256 threads combine takes 186 us instead of 173 for 65536 rows of 7168), and as many
-// tokens as make up a CTA (8 rows of 32 BF16 values for each of 32768 tokens: ZZ us, ZZ
+// tokens as make up a CTA (8 rows of 32 BF16 values for each of 32768 tokens: 7.0 us, 19.7
 // with a CTA for every token).
 dim3 row_block(int64_t pieces) {
   const int64_t turns = (pieces + kRowThreads - 1) / kRowThreads;
@@ -326,7 +364,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* _
 }
 
 // The same for up to kSlots slots, of kTokens tokens at a time, so that there are as
-// many rows in flight: 32768 rows of 2048, one a token, take ZZ us, 94 with the above.
+// many rows in flight: 32768 rows of 2048, one a token, take 44 us, 94 with the above.
 template <typename T, int kTokens, int kSlots>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_few_kernel(const uint4* __restrict__ y, int64_t ld_y,
                                                                       int64_t y_rows, const int32_t* __restrict__ rows,
@@ -496,7 +534,7 @@ cudaError_t launch_overlapped(void (*fn)(P...), dim3 grid, int threads, size_t s
 
 size_t moe_sort_workspace_bytes(int64_t P, int E) {
   const int64_t n = sort_chunks(P);
-  return std::max<size_t>(256, n > 1 ? (size_t)n * (E + 1) * sizeof(int32_t) : 0);
+  return std::max<size_t>(256, n > 1 ? ((size_t)n + 1) * (E + 1) * sizeof(int32_t) : 0);  // counts, totals
 }
 
 cudaError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* m_splits, int32_t* rows, void* ws,
@@ -506,14 +544,22 @@ cudaError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* m_spl
   const size_t smem = (size_t)kSortWarps * (E + 1) * sizeof(uint32_t);
   int32_t* counts = static_cast<int32_t*>(ws);
   if (chunks == 1) {
-    moe_sort_place_kernel<<<1, kSortThreads, smem, stream>>>(ids, P, E, chunk, counts, m_splits, rows, status);
+    moe_sort_place_kernel<<<1, kSortThreads, smem, stream>>>(ids, P, E, chunk, counts, nullptr, m_splits, rows, status);
     return cudaGetLastError();
   }
   moe_sort_count_kernel<<<chunks, kSortThreads, smem, stream>>>(ids, P, E, chunk, counts);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  const int32_t* totals = nullptr;
+  if ((int64_t)chunks * (E + 1) > kSortScan) {
+    int32_t* sums = counts + (int64_t)chunks * (E + 1);
+    const cudaError_t s = launch_overlapped(moe_sort_scan_kernel, dim3((unsigned)((E + kSortWarps) / kSortWarps)), kSortThreads,
+                                            0, stream, counts, sums, E + 1, (int)chunks);
+    if (s != cudaSuccess) return s;
+    totals = sums;
+  }
   return launch_overlapped(moe_sort_place_kernel, dim3(chunks), kSortThreads, smem, stream, ids, P, E, chunk,
-                           static_cast<const int32_t*>(counts), m_splits, rows, status);
+                           static_cast<const int32_t*>(counts), totals, m_splits, rows, status);
 }
 
 cudaError_t launch_moe_gather(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int k, int64_t pieces,
@@ -550,7 +596,7 @@ cudaError_t combine_backward(const void* dout, int64_t ld_dout, const void* y, i
                              float* dweights, int32_t* status, cudaStream_t stream, int num_sms) {
   // Four rows of a thread in flight: of four slots, or of fewer slots' pieces.  A token
   // has lanes of a warp, or a CTA of as many threads as share its pieces equally: up
-  // to 256, or 1024 where there are few tokens (64 of 7168, top 8: ZZ us, 11.9).
+  // to 256, or 1024 where there are few tokens (64 of 7168, top 8: 8.2 us, 11.9).
   const int each = k > 2 ? 1 : k > 1 ? 2 : 4;
   const int64_t want = (pieces + each - 1) / each;
   const bool lanes = want <= 32, few = !lanes && tokens < 4 * num_sms;
