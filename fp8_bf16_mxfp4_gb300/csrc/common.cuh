@@ -103,4 +103,21 @@ MXG_DEVINL uint32_t cvt_e4m3x4(float a0, float a1, float a2, float a3) {
   return r;
 }
 
+// Launch with programmatic stream serialization: the kernel starts while the one
+// before it ends, and waits for its results itself.
+template <typename... P, typename... A>
+inline cudaError_t launch_overlapped(void (*fn)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
 }  // namespace mxg

@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const uint4* _
                                                                   float* __restrict__ scale, int32_t* status) {
   __shared__ uint32_t part[kQThreads / 32];
   ptx::pdl_launch_dependents();
+  ptx::pdl_wait();  // rows, and x too, may come from the kernel before
   const int64_t t = blockIdx.x;
   const uint4* src = x + t * ld_x;
   uint4 keep[kQKeep];
@@ -64,11 +65,11 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const uint4* _
 #pragma unroll
   for (int i = 0; i < kQKeep; ++i) {
     const int64_t c = threadIdx.x + (int64_t)i * blockDim.x;
-    keep[i] = c < pieces ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    keep[i] = c < pieces ? ptx::ld_global_v4(src + c) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < kQKeep; ++i) amax(keep[i]);
-  for (int64_t c = threadIdx.x + (int64_t)kQKeep * blockDim.x; c < pieces; c += blockDim.x) amax(__ldg(src + c));
+  for (int64_t c = threadIdx.x + (int64_t)kQKeep * blockDim.x; c < pieces; c += blockDim.x) amax(ptx::ld_global_v4(src + c));
   m = __reduce_max_sync(kFull, max(m & 0xFFFFu, m >> 16));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const uint4* _
   const int64_t first = rows != nullptr ? t * k : t;
   auto row_at = [&](int j, bool& on) -> int64_t {
     if (rows == nullptr) { on = true; return t; }
-    const int32_t e = __ldg(rows + first + j);
+    const int32_t e = ptx::ld_global_s32(rows + first + j);
     const int64_t at = e < 0 ? -1 - (int64_t)e : e;
     on = e >= 0;
     return at < out_rows ? at : -1;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kQThreads) int8_quantize_kernel(const uint4* _
     const int64_t c = threadIdx.x + (int64_t)i * blockDim.x;
     if (c < pieces) emit(c, keep[i]);
   }
-  for (int64_t c = threadIdx.x + (int64_t)kQKeep * blockDim.x; c < pieces; c += blockDim.x) emit(c, __ldg(src + c));
+  for (int64_t c = threadIdx.x + (int64_t)kQKeep * blockDim.x; c < pieces; c += blockDim.x) emit(c, ptx::ld_global_v4(src + c));
 }
 
 // Four 8-bit integers -> four FP16 values: with the sign bit flipped a byte is
@@ -169,12 +170,6 @@ __global__ void __launch_bounds__(kPrepThreads) int8_prep_kernel(uint32_t* sync,
   }
 }
 
-MXG_DEVINL uint4 ld_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
 // One warp: the first row off[g] and first unit tile[g] of every expert, `per_tile`
 // units for every `tok` of its rows; *bad where a split is negative or they do not
 // add up to S.  Lane l has experts [l * per, l * per + per).
@@ -182,7 +177,7 @@ MXG_DEVINL void plan_units(const int32_t* splits, int G, int S, int tok, int per
   const int lane = threadIdx.x & 31, per = (G + 31) >> 5;
   int64_t rows = 0, units = 0;
   bool neg = false;
-  auto split = [&](int g) -> int64_t { return splits != nullptr ? (int64_t)__ldg(splits + g) : (int64_t)S; };
+  auto split = [&](int g) -> int64_t { return splits != nullptr ? (int64_t)ptx::ld_global_s32(splits + g) : (int64_t)S; };
   auto units_of = [&](int64_t m) { return (m + tok - 1) / tok * per_tile; };
   for (int i = 0; i < per; ++i) {
     const int g = lane * per + i;
@@ -294,9 +289,9 @@ MXG_DEVINL void few_stage(const FewParams& p, uint8_t* x, int tok0, int n) {
     uint4 r;
     if (p.f16) {
       const uint4* s = reinterpret_cast<const uint4*>(src) + 2 * c;
-      r = narrow16(__ldg(s), __ldg(s + 1));
+      r = narrow16(s[0], s[1]);
     } else {
-      r = __ldg(reinterpret_cast<const uint4*>(src) + c);
+      r = reinterpret_cast<const uint4*>(src)[c];
     }
     *reinterpret_cast<uint4*>(x + t * stride + c * 16) = r;
   }
@@ -328,10 +323,10 @@ MXG_DEVINL void few_tile(const FewParams& p, uint8_t* x, float* part, int e, int
     const uint4 z = make_uint4(0, 0, 0, 0);
     const bool on = l_i < turns && l_it < iters;
     const bool lo = on && k + q16 < p.K, hi = on && k + q16 + 64 < p.K;
-    d[0] = lo ? ld_stream(w0 + k) : z;
-    d[1] = lo ? ld_stream(w8 + k) : z;
-    d[2] = hi ? ld_stream(w0 + k + 64) : z;
-    d[3] = hi ? ld_stream(w8 + k + 64) : z;
+    d[0] = lo ? ptx::ld_global_v4(w0 + k) : z;
+    d[1] = lo ? ptx::ld_global_v4(w8 + k) : z;
+    d[2] = hi ? ptx::ld_global_v4(w0 + k + 64) : z;
+    d[3] = hi ? ptx::ld_global_v4(w8 + k + 64) : z;
     if (++l_i == slots) {
       l_i = 0;
       ++l_it;
@@ -403,7 +398,7 @@ MXG_DEVINL void few_tile(const FewParams& p, uint8_t* x, float* part, int e, int
       const float* src = part + ((it & 1) * kFewWarps + which * split) * (kNT * 8 * kFewCol) + t * kFewCol + r;
       float sum = 0.0f;
       for (int q = 0; q < split; ++q) sum += src[q * (kNT * 8 * kFewCol)];
-      const float y = sum * __ldg(p.sw + (int64_t)e * p.N + chan) * __ldg(p.sa + tok0 + t);
+      const float y = sum * p.sw[(int64_t)e * p.N + chan] * p.sa[tok0 + t];
       const int64_t to = (int64_t)(tok0 + t) * p.ld_out + chan;
       if (p.out_f32) static_cast<float*>(p.out)[to] = y;
       else static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
@@ -1099,9 +1094,8 @@ cudaError_t launch_int8_quantize(const void* x, int64_t ld_x, const int32_t* row
   const int threads = (int)std::min<int64_t>(kQThreads, ((pieces + each - 1) / each + 31) / 32 * 32);
   const auto fn = codes == MXG_CODES_F16 ? int8_quantize_kernel<true> : int8_quantize_kernel<false>;
   const dim3 grid((unsigned)T, (unsigned)std::max<int64_t>(1, std::min<int64_t>(k, 2 * num_sms / T)));
-  fn<<<grid, threads, 0, stream>>>(static_cast<const uint4*>(x), ld_x / 8, rows, k, T * k, pieces,
-                                          static_cast<uint8_t*>(q), ld_q, scale, status);
-  return cudaGetLastError();
+  return launch_overlapped(fn, grid, dim3((unsigned)threads), 0, stream, static_cast<const uint4*>(x), ld_x / 8, rows, k, T * k, pieces,
+                           static_cast<uint8_t*>(q), ld_q, scale, status);
 }
 
 size_t int8_gemm_workspace_bytes(int64_t S, int G, int64_t N, int64_t K, int codes) {
@@ -1147,17 +1141,7 @@ mxg_status launch_int8_few(const Int8GemmArgs& a, cudaStream_t stream, int num_s
   p.status = a.status;
   const size_t smem = (size_t)(p.tok * (int64_t)few_stride(a.K) + few_part_bytes(p.tok));
   // started while the kernel before ends (1 token's quantizer and product: 12.7 us, 13.3 without)
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_sms);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, int8_few_kernel, p) != cudaSuccess) {
+  if (launch_overlapped(int8_few_kernel, dim3((unsigned)num_sms), dim3(kFewThreads), smem, stream, p) != cudaSuccess) {
     cudaGetLastError();
     return MXG_ERR_CUDA;
   }

@@ -27,18 +27,19 @@ constexpr uint32_t kFull = 0xffffffffu;
 // chunk to its warps, and a warp takes its run 32 slots at a time, where
 // __match_any finds the slots of one expert.  A slot's row is the rows of lower
 // experts, of earlier chunks, of earlier warps and of earlier slots of its run.
-// Up to 4096 slots are one CTA's; above, a first kernel leaves every chunk's counts
-// and the last, which counts its own chunk again while the one before ends, adds up
-// those of the chunks before.  Where that is much for every CTA, a kernel between the
-// two adds them up once.  Bound by latency: 64 slots 2.5 us, 65536 slots of 32 experts
-// 10 us, 262144 of 512 15 us (29 without the kernel between); no atomics, so equal ids
-// keep their order.
+// Up to 1024 slots are one CTA's; above, a first kernel leaves every chunk's counts
+// and the last, which counts its own chunk again while the one before ends, needs the
+// sums over those of the chunks before.  Where a warp has all chunks of eight keys in
+// one load each CTA adds them up itself; a kernel between the two does it for more.
+// Bound by latency: 512 slots of 32 experts 3.4 us, 16384 4.8, 65536 6.1 (7.5 without
+// the kernel between); 65536 of 512 7.8 (17).  Chunks of 2048 slots: 7.2, 7.2 and
+// 10.2.  No atomics, so equal ids keep their order.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortChunk = 2048;  // least slots of a chunk, where there are several
+constexpr int kSortChunk = 512;  // least slots of a chunk, where there are several
 constexpr int kSortMaxChunks = 256;
-constexpr int64_t kSortScan = 8192;  // counts from which on they are added up by a kernel of their own
+constexpr int kSortKeys = 128;  // the most keys whose counts every CTA adds up itself, of at most 32 chunks
 
 int64_t sort_chunk(int64_t P) {
   if (P <= 2 * kSortChunk) return 2 * kSortChunk;  // one CTA, one launch
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_scan_kernel(int32_t* co
 #pragma unroll
   for (int i = 0; i < kSortMaxChunks / 32; ++i) {
     const int c = 32 * i + lane;
-    v[i] = c < chunks ? (uint32_t)__ldcg(counts + (int64_t)e * chunks + c) : 0u;
+    v[i] = c < chunks ? (uint32_t)ptx::ld_global_s32(counts + (int64_t)e * chunks + c) : 0u;
   }
 #pragma unroll
   for (int i = 0; i < kSortMaxChunks / 32; ++i) {
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
   __shared__ uint32_t total[2 * kSortThreads], before[2 * kSortThreads];  // of a key: all slots, those of earlier chunks
   __shared__ uint32_t warp_sum[kSortWarps];
   const int keys = E + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::pdl_launch_dependents();
   for (int i = threadIdx.x; i < kSortWarps * keys; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * chunk, run = chunk / kSortWarps;
@@ -155,39 +157,27 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
   } else if (totals != nullptr) {
     ptx::pdl_wait();  // the counts are complete
     for (int e = threadIdx.x; e < keys; e += kSortThreads) {
-      total[e] = (uint32_t)__ldcg(totals + e);
-      before[e] = (uint32_t)__ldcg(counts + (int64_t)e * gridDim.x + blockIdx.x);
+      total[e] = (uint32_t)ptx::ld_global_s32(totals + e);
+      before[e] = (uint32_t)ptx::ld_global_s32(counts + (int64_t)e * gridDim.x + blockIdx.x);
     }
   } else {
     ptx::pdl_wait();  // the counts are complete
+    // at most kSortKeys keys and 32 chunks: eight keys of a warp in flight, its lanes the chunks
     const int chunks = (int)gridDim.x;
-    constexpr int kKeys = 8;  // keys of a warp in flight, its lanes the chunks
-    for (int e0 = warp; e0 < keys; e0 += kSortWarps * kKeys) {
-      uint32_t all[kKeys], early[kKeys];
+    uint32_t v[kSortKeys / kSortWarps];
 #pragma unroll
-      for (int q = 0; q < kKeys; ++q) all[q] = early[q] = 0;
-      for (int c = lane; c < chunks; c += 32) {
-        uint32_t v[kKeys];
+    for (int q = 0; q < kSortKeys / kSortWarps; ++q) {
+      const int e = warp + q * kSortWarps;
+      v[q] = e < keys && lane < chunks ? (uint32_t)ptx::ld_global_s32(counts + (int64_t)e * chunks + lane) : 0u;
+    }
 #pragma unroll
-        for (int q = 0; q < kKeys; ++q) {
-          const int e = e0 + q * kSortWarps;
-          v[q] = e < keys ? (uint32_t)__ldcg(counts + (int64_t)e * chunks + c) : 0u;
-        }
-#pragma unroll
-        for (int q = 0; q < kKeys; ++q) {
-          all[q] += v[q];
-          if (c < (int)blockIdx.x) early[q] += v[q];
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < kKeys; ++q) {
-        const int e = e0 + q * kSortWarps;
-        all[q] = __reduce_add_sync(kFull, all[q]);
-        early[q] = __reduce_add_sync(kFull, early[q]);
-        if (lane == 0 && e < keys) {
-          total[e] = all[q];
-          before[e] = early[q];
-        }
+    for (int q = 0; q < kSortKeys / kSortWarps; ++q) {
+      const int e = warp + q * kSortWarps;
+      const uint32_t all = __reduce_add_sync(kFull, v[q]);
+      const uint32_t early = __reduce_add_sync(kFull, lane < (int)blockIdx.x ? v[q] : 0u);
+      if (lane == 0 && e < keys) {
+        total[e] = all;
+        before[e] = early;
       }
     }
   }
@@ -304,10 +294,11 @@ __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const uint4* __
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, P = T * k;
   if (t >= T) return;
   const int32_t* mine = rows + t * k;
+  ptx::pdl_wait();  // rows, and x too, may come from the kernel before
   for (int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; c < pieces; c += (int64_t)gridDim.y * blockDim.x) {
-    const uint4 v = __ldg(x + t * ld_x + c);
+    const uint4 v = ptx::ld_global_v4(x + t * ld_x + c);
     for (int j = 0; j < k; ++j) {
-      const int32_t e = __ldg(mine + j);
+      const int32_t e = ptx::ld_global_s32(mine + j);
       const int64_t r = row_of(e, P, status);
       if (r >= 0) out[r * ld_out + c] = e >= 0 ? v : make_uint4(0, 0, 0, 0);
     }
@@ -513,23 +504,6 @@ __global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(
   }
 }
 
-// Launch with programmatic stream serialization: the kernel starts while the one
-// before it ends, and waits for its results itself.
-template <typename... P, typename... A>
-cudaError_t launch_overlapped(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
-}
-
 }  // namespace
 
 size_t moe_sort_workspace_bytes(int64_t P, int E) {
@@ -551,23 +525,22 @@ cudaError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* m_spl
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int32_t* totals = nullptr;
-  if ((int64_t)chunks * (E + 1) > kSortScan) {
+  if (chunks > 32 || E + 1 > kSortKeys) {
     int32_t* sums = counts + (int64_t)chunks * (E + 1);
-    const cudaError_t s = launch_overlapped(moe_sort_scan_kernel, dim3((unsigned)((E + kSortWarps) / kSortWarps)), kSortThreads,
+    const cudaError_t s = launch_overlapped(moe_sort_scan_kernel, dim3((unsigned)((E + kSortWarps) / kSortWarps)), dim3(kSortThreads),
                                             0, stream, counts, sums, E + 1, (int)chunks);
     if (s != cudaSuccess) return s;
     totals = sums;
   }
-  return launch_overlapped(moe_sort_place_kernel, dim3(chunks), kSortThreads, smem, stream, ids, P, E, chunk,
+  return launch_overlapped(moe_sort_place_kernel, dim3(chunks), dim3(kSortThreads), smem, stream, ids, P, E, chunk,
                            static_cast<const int32_t*>(counts), totals, m_splits, rows, status);
 }
 
 cudaError_t launch_moe_gather(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int k, int64_t pieces,
                               void* out, int64_t ld_out, int32_t* status, cudaStream_t stream) {
   const dim3 block = row_block(pieces);
-  moe_gather_kernel<<<row_grid(T, pieces, block), block, 0, stream>>>(static_cast<const uint4*>(x), ld_x, rows, T, k, pieces,
-                                                                      static_cast<uint4*>(out), ld_out, status);
-  return cudaGetLastError();
+  return launch_overlapped(moe_gather_kernel, row_grid(T, pieces, block), block, 0, stream, static_cast<const uint4*>(x), ld_x, rows, T, k,
+                           pieces, static_cast<uint4*>(out), ld_out, status);
 }
 
 namespace {

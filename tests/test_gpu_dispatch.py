@@ -61,8 +61,9 @@ def choose(rng, T, k, E, how):
 @pytest.mark.parametrize("T,k,E,how", [
     (1, 1, 1, "all"), (1, 8, 32, "all"), (3, 2, 1, "holes"), (8, 8, 32, "all"), (33, 3, 31, "holes"), (31, 1, 32, "one"),
     (64, 32, 512, "all"), (128, 32, 7, "holes"), (128, 32, 511, "all"), (1, 32, 512, "none"), (100, 2, 3, "first"),
-    # more than one chunk of slots: just past 4096, odd tails, chunks of one expert, none
-    (4097, 1, 5, "all"), (1366, 3, 512, "holes"), (2500, 2, 33, "one"), (3000, 3, 64, "none"), (5001, 7, 161, "holes"),
+    # more than one chunk of slots: around 1024 slots, 32 chunks and 128 keys, odd tails, chunks of one expert, none
+    (1024, 1, 7, "holes"), (1025, 1, 7, "holes"), (683, 3, 126, "holes"), (2048, 8, 127, "all"), (2048, 8, 128, "all"),
+    (16384, 1, 16, "holes"), (16385, 1, 16, "holes"), (16385, 1, 127, "all"), (131073, 1, 3, "holes"), (4097, 1, 5, "all"), (1366, 3, 512, "holes"), (2500, 2, 33, "one"), (3000, 3, 64, "none"), (5001, 7, 161, "holes"),
     (20000, 8, 32, "all"), (75000, 8, 512, "holes")])
 def test_sort(T, k, E, how):
     rng = np.random.default_rng(T + k + E)
