@@ -341,6 +341,22 @@ def test_route_backward_of_rows_at_any_offset(E, dtype):
         assert (out == 9.0).all()
 
 
+@pytest.mark.parametrize("E,k", [(7, 5), (40, 32), (100, 3), (256, 32), (500, 17)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_backward_of_experts_named_several_times(E, k, renorm):
+    mxg = _mxg()
+    g = torch.Generator().manual_seed(E + k)
+    logits = (2 * torch.randn(41, E, generator=g)).to(DEV)
+    ids = torch.randint(-1, E, (41, k), generator=g, dtype=torch.int32).to(DEV)
+    ids[3] = E - 1
+    w, d = torch.rand(41, k, generator=g).to(DEV), torch.randn(41, k, generator=g).to(DEV)
+    got = mxg.moe_route_backward(d, ids, w, logits, renormalize=renorm, check=True)
+    want, bound = dispatch.route_backward(f64(d), ids.cpu().numpy(), f64(w), f64(logits), E, renorm)
+    close(got, want, bound, F32)
+    for _ in range(3):  # adds in the order of the slots
+        assert torch.equal(got, mxg.moe_route_backward(d, ids, w, logits, renormalize=renorm))
+
+
 def test_route_backward_special_cases():
     mxg = _mxg()
     nan, inf = float("nan"), float("inf")
