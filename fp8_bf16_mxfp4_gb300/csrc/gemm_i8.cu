@@ -155,11 +155,12 @@ __global__ void __launch_bounds__(kPrepThreads) int8_prep_kernel(uint32_t* sync,
                                                                  int64_t ld_a, int64_t S, int64_t per_row,
                                                                  uint4* __restrict__ wide) {
   ptx::pdl_launch_dependents();
+  ptx::pdl_wait();  // the activations may come from the kernel before, which may also be at work with the counters
   const int64_t i0 = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x;
   if (i0 < words) sync[i0] = 0;
   for (int64_t i = i0; i < S * per_row; i += (int64_t)gridDim.x * kPrepThreads) {
     const int64_t r = i / per_row, c = i - r * per_row;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a + r * ld_a) + c);
+    const uint4 v = ptx::ld_global_v4(a + r * ld_a + c * 16);
     uint32_t o[8];
     widen4(v.x, o[0], o[1]);
     widen4(v.y, o[2], o[3]);
@@ -510,7 +511,6 @@ struct I8Params {
   int out_f32;
   float* part;            // [2 * pairs][2][kTok][128] partial sums of cut units
   uint32_t* sync;         // [pairs][8] arrivals at a cut unit
-  int wide_from_prep;     // the activations come from the kernel before
   int32_t* status;
   uint64_t timeout_ns, drain_ns;
   uint32_t idesc;
@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
   auto arrive_issuer = [&](uint32_t bar) { ptx::mbar_arrive_cluster(ptx::mapa_shared(bar, 0)); };
 
   if (warp == 0) {
+    ptx::pdl_wait();  // all operands may come from the kernel before
     plan_units(p.splits, p.G, p.S, kTok, p.n_chan, off, tile, bad_flag);
     if (lane == 0) *abort_flag = 0;
   } else if (warp == 1) {
@@ -646,6 +647,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
   // the peer's barriers are initialised before any remote arrival or commit reaches them
   ptx::cluster_sync();
   ptx::tc_fence_after();
+  ptx::pdl_wait();
   const uint32_t tmem = *tmem_slot;
   const bool bad = *bad_flag != 0;  // every CTA sees it: nothing is written
   if (bad && threadIdx.x == 0) report(p.status, MXG_ERR_SPLITS);
@@ -671,7 +673,6 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_phase = 0;
       bool ok = true;
-      if (p.wide_from_prep) ptx::pdl_wait();  // the widened activations are complete
       while (ok && w.next(p, off, tile)) {
         const int row_w = w.e * p.N + w.chan0 + rank * kChan;
         const int row_x = w.tok0 + rank * mma_tokens(w.n) / 2;
@@ -806,17 +807,16 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
     constexpr int kCols = 32;  // columns of a read
     int count = 0;
-    if constexpr (L::kCut) ptx::pdl_wait();  // the kernel before has zeroed the counters
     while (w.next(p, off, tile)) {
       const int buf = L::kBufs == 2 ? count & 1 : 0;
       const uint32_t round = L::kBufs == 2 ? (uint32_t)(count >> 1) : (uint32_t)count;
       const int chan = w.chan0 + rank * kChan + quarter * 32 + lane;
       const bool in = chan < p.N;
-      const float sw = in ? __ldg(p.sw + (int64_t)w.e * p.N + chan) : 0.0f;
+      const float sw = in ? p.sw[(int64_t)w.e * p.N + chan] : 0.0f;
       float* sa_tile = reinterpret_cast<float*>(smem + L::kSaOff) + quarter * kTok;
       if constexpr (!L::kCut) {  // the warp's copy of the token scales
         __syncwarp();
-        for (int i = lane; i < kTok; i += 32) sa_tile[i] = i < w.n ? __ldg(p.sa + w.tok0 + i) : 0.0f;
+        for (int i = lane; i < kTok; i += 32) sa_tile[i] = i < w.n ? p.sa[w.tok0 + i] : 0.0f;
         __syncwarp();
       }
       if (!ptx::mbar_wait_warp(acc_full(buf), round & 1u, abort_flag, p.status, p.timeout_ns)) break;
@@ -933,7 +933,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
             for (int i = 0; i < kCols; ++i) v[i] = v[i] + a0[i] + a1[i];
           }
         }
-        const float sa = c0 + lane < w.n ? __ldg(p.sa + w.tok0 + c0 + lane) : 0.0f;
+        const float sa = c0 + lane < w.n ? p.sa[w.tok0 + c0 + lane] : 0.0f;
         if (p.out_f32) {
           float* dst = static_cast<float*>(p.out) + (int64_t)(w.tok0 + c0) * p.ld_out + chan;
 #pragma unroll
@@ -1170,7 +1170,6 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
   p.sa = a.sa; p.sw = a.sw;
   p.out = a.out; p.ld_out = a.ld_out; p.out_f32 = a.out_dtype == MXG_OUT_F32;
   p.part = ws.part; p.sync = ws.sync;
-  p.wide_from_prep = widen;
   p.status = a.status;
   p.timeout_ns = wait_timeout_ns();
   p.drain_ns = std::max<uint64_t>(p.timeout_ns, 200000000ull);
@@ -1181,9 +1180,11 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
   if (prep) {
     const int64_t per_row = a.K / 16, items = std::max<int64_t>(widen ? a.S * per_row : 0, kI8SyncWords);
     const unsigned grid = (unsigned)std::min<int64_t>((items + kPrepThreads - 1) / kPrepThreads, (int64_t)num_sms * 16);
-    int8_prep_kernel<<<grid, kPrepThreads, 0, stream>>>(ws.sync, f.cut ? kI8SyncWords : 0, a.a, a.ld_a,
-                                                        widen ? a.S : 0, per_row, reinterpret_cast<uint4*>(ws.wide));
-    if (cudaGetLastError() != cudaSuccess) return MXG_ERR_CUDA;
+    if (launch_overlapped(int8_prep_kernel, dim3(grid), dim3(kPrepThreads), 0, stream, ws.sync, f.cut ? kI8SyncWords : 0, a.a, a.ld_a,
+                          widen ? a.S : 0, per_row, reinterpret_cast<uint4*>(ws.wide)) != cudaSuccess) {
+      cudaGetLastError();
+      return MXG_ERR_CUDA;
+    }
   }
   CUtensorMap tmW, tmX;
   if (!make_tmap(&tmW, a.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.K, (int64_t)a.G * a.N, a.ld_w, kStageK, kChan)) return MXG_ERR_CUDA;
@@ -1202,7 +1203,7 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
   cfg.dynamicSmemBytes = (size_t)f.smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = prep ? 2 : 1;
+  cfg.numAttrs = 2;
   void* args[] = {(void*)&tmW, (void*)&tmX, (void*)&p};
   if (cudaLaunchKernelExC(&cfg, f.fn, args) != cudaSuccess) {
     cudaGetLastError();
