@@ -449,7 +449,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const FewParam
 //   warp 1       TMEM owner; in the even CTA MMA issuer for both, 8 MMAs a stage;
 //   warps 2-5    epilogue, one per TMEM lane quarter (a lane is a channel);
 //   warps 6-9    weights to FP16, shared memory to TMEM;
-//   warp 10      waits for the issuer (cut form).
+//   warp 10      waits for the issuer (cut form);
+//   warps 10-13  epilogue (whole tiles): with one accumulator the next tile waits
+//                for it (1024 rows of 32 experts each, 2048 x 1024: 97 us, 119 with four
+//                warps; x 2048, 4096 channels: 302, 306).
 // Cut form: the stages of all units (expert, channel tile, row tile) are cut into one
 // equal run per pair, so that every SM streams the same number of weight bytes; cut
 // units are joined through fp32 partials, added in run order by the last to arrive.
@@ -476,7 +479,8 @@ struct I8Cfg {
   static constexpr int kBufs = kTok == 256 ? 1 : 2;
   static constexpr bool kCut = kTok < 256;             // units may be cut over pairs
   static constexpr int kWatch = 10;                    // the warp that waits for the issuer
-  static constexpr int kThreads = 32 * (kWatch + (kCut ? 1 : 0));
+  static constexpr int kEpi = kCut ? 4 : 8;            // epilogue warps
+  static constexpr int kThreads = 32 * (kWatch + (kCut ? 1 : 4));
   static constexpr int kRows = kTok / 2;               // tokens whose elements a CTA loads
   static constexpr int kXBox = kRows * 128;            // 64 elements of each
   static constexpr int kStageBytes = kWBytes + 2 * kXBox;
@@ -491,7 +495,7 @@ struct I8Cfg {
   static constexpr int kMiscOff = kBarOff + ((kBars * 8 + 15) & ~15);
   static constexpr int kOffOff = kMiscOff + 16;                      // int32 [G + 1]: first row of each expert
   static constexpr int kTileOff = kOffOff + (kMaxExperts + 4) * 4;   // int32 [G + 1]: first unit of each expert
-  static constexpr int kSaOff = kTileOff + (kMaxExperts + 4) * 4;    // float [4][256]: the tile's token scales (256 tokens)
+  static constexpr int kSaOff = kTileOff + (kMaxExperts + 4) * 4;    // float [8][128]: the tile's token scales (256 tokens)
   static constexpr int kTotal = kSaOff + (kCut ? 0 : 4 * kTok * 4) + 1024;  // + alignment slack
   static_assert(kSaOff % 16 == 0, "token scales are read 16 bytes at a time");
   static_assert(kBufs * kTok <= kACol && kACol + kSlots * kACols <= kI8TmemCols, "TMEM holds accumulators and ring");
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(acc_full(b), 1);
-      ptx::mbar_init(acc_empty(b), 8);
+      ptx::mbar_init(acc_empty(b), 2 * L::kEpi);  // the epilogue warps of either CTA
     }
     ptx::mbar_init(drain_bar, 1);
     ptx::fence_mbar_init();
@@ -759,7 +763,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
         ++count;
       }
     }
-  } else if (warp >= 6) {
+  } else if (warp >= 6 && warp < 10) {
     // ------------------------------------------------------------ weights to FP16
     // A thread takes a channel: 128 bytes of its row (16-byte piece c at
     // c ^ (row % 8)) become 64 TMEM columns of its lane.  The slot there is free
@@ -801,7 +805,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
       }
     }
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2-5)
+    // ------------------------------------------------------------ epilogue (warps 2-5; 256 tokens: 10-13 too)
     // Warp q has TMEM lanes 32 q .. 32 q + 31: a lane is a channel, a column a token.
     const int quarter = warp & 3;
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -813,10 +817,12 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
       const int chan = w.chan0 + rank * kChan + quarter * 32 + lane;
       const bool in = chan < p.N;
       const float sw = in ? p.sw[(int64_t)w.e * p.N + chan] : 0.0f;
-      float* sa_tile = reinterpret_cast<float*>(smem + L::kSaOff) + quarter * kTok;
+      // 256 tokens: of a quarter's two warps each takes every second 32 columns
+      const int half = warp >= 10;
+      float* sa_tile = reinterpret_cast<float*>(smem + L::kSaOff) + (2 * quarter + half) * (kTok / 2);
       if constexpr (!L::kCut) {  // the warp's copy of the token scales
         __syncwarp();
-        for (int i = lane; i < kTok; i += 32) sa_tile[i] = i < w.n ? p.sa[w.tok0 + i] : 0.0f;
+        for (int i = 32 * half + lane; i < kTok; i += 64) sa_tile[(i >> 6) * 32 + lane] = i < w.n ? p.sa[w.tok0 + i] : 0.0f;
         __syncwarp();
       }
       if (!ptx::mbar_wait_warp(acc_full(buf), round & 1u, abort_flag, p.status, p.timeout_ns)) break;
@@ -824,16 +830,16 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
       ++count;
       const uint32_t d = tq + buf * kTok;
       if constexpr (!L::kCut) {
-        // BF16: the tile's values as 128 pairs of tokens in registers, the
+        // BF16: the warp's values as 64 pairs of tokens in registers, the
         // accumulator handed back, then the stores, while the next tile's MMAs run.
         auto release = [&]() {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_issuer(acc_empty(buf));
         };
-        auto scaled = [&](int c, float* v) {  // columns 32 c .. 32 c + 31
+        auto scaled = [&](int c, float* v) {  // the warp's c-th 32 columns
           __syncwarp();
-          ptx::tmem_ld_32x32b_x32(d + 32 * c, reinterpret_cast<uint32_t*>(v));
+          ptx::tmem_ld_32x32b_x32(d + 64 * c + 32 * half, reinterpret_cast<uint32_t*>(v));
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
@@ -846,18 +852,20 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
         };
         if (p.out_f32) {
           float* dst = static_cast<float*>(p.out) + (int64_t)w.tok0 * p.ld_out + chan;
-          for (int c = 0; 32 * c < w.n; ++c) {
+          if (32 * half >= w.n) release();  // nothing for this warp
+          for (int c = 0; 64 * c + 32 * half < w.n; ++c) {
+            const int at = 64 * c + 32 * half;
             float v[32];
             scaled(c, v);
-            if (32 * c + 32 >= w.n) release();
+            if (at + 64 >= w.n) release();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ptx::st_f32_if(in && 32 * c + i < w.n, dst + (32 * c + i) * p.ld_out, v[i]);
+            for (int i = 0; i < 32; ++i) ptx::st_f32_if(in && at + i < w.n, dst + (at + i) * p.ld_out, v[i]);
           }
         } else {
-          uint32_t pk[kTok / 2];
+          uint32_t pk[kTok / 4];
 #pragma unroll
-          for (int c = 0; c < kTok / 32; ++c) {
-            if (32 * c < w.n) {
+          for (int c = 0; c < kTok / 64; ++c) {
+            if (64 * c + 32 * half < w.n) {
               float v[32];
               scaled(c, v);
 #pragma unroll
@@ -870,12 +878,12 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
           const int odd = lane & 1;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (int64_t)(w.tok0 + odd) * p.ld_out + (chan - odd);
 #pragma unroll
-          for (int c = 0; c < kTok / 32; ++c) {
-            if (32 * c < w.n) {
+          for (int c = 0; c < kTok / 64; ++c) {
+            if (64 * c + 32 * half < w.n) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const uint32_t mine = pk[16 * c + i], other = __shfl_xor_sync(kFull, mine, 1);
-                const int at = 32 * c + 2 * i;
+                const int at = 64 * c + 32 * half + 2 * i;
                 ptx::st_u32_if(in && at + odd < w.n, dst + at * p.ld_out, __byte_perm(mine, other, odd ? 0x3276 : 0x5410));
               }
             }
