@@ -366,6 +366,84 @@ def test_two_streams_at_once(S):
     assert all(torch.equal(g, want[i]) for i in (0, 1) for g in got[i])
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T", [4, 90, 800])  # 2 experts: 4, 90 and 800 rows each
+def test_operands_of_the_operations_just_before(T, captured):
+    """Calls whose inputs come from a copy, a fill, another stream, or from the call before, right before each of them:
+    nothing is read before it is there.  (Kernels of these calls start while the kernel before them ends.)"""
+    mxg = _mxg()
+    rng = np.random.default_rng(T)
+    E, K, N = 2, 1040, 520
+    side = torch.cuda.Stream()
+    slow = torch.randn(2048, 2048, device=DEV)
+    new = []  # an iteration's inputs
+    for i in range(4):
+        new.append((torch.randn(T, K, device=DEV).bfloat16(), dev(rng.integers(0, E, (T, 2)).astype(np.int32)),
+                    torch.randn(E * N, K, device=DEV).bfloat16()))
+    x, ids, w = (torch.zeros_like(t) for t in new[0])
+    splits = torch.empty(E, dtype=torch.int32, device=DEV)
+    rows = torch.empty(T, 2, dtype=torch.int32, device=DEV)
+    q, sc = torch.empty(2 * T, K, dtype=torch.float16, device=DEV), torch.empty(2 * T, device=DEV)
+    wq, ws = torch.empty(E * N, K, dtype=torch.int8, device=DEV), torch.empty(E * N, device=DEV)
+    xs, out = torch.empty(2 * T, K, dtype=torch.bfloat16, device=DEV), torch.empty(2 * T, N, dtype=torch.bfloat16, device=DEV)
+    staged = [torch.empty_like(t) for t in (splits, rows)]
+
+    def chain(src):
+        here = torch.cuda.current_stream()
+        ids.copy_(src[1])
+        mxg.moe_sort(ids, E, m_splits=staged[0], rows=staged[1])
+        rows.copy_(staged[1])                                  # a copy, then the gather of its rows
+        side.wait_stream(here)
+        with torch.cuda.stream(side):                          # x from another stream, late
+            y = slow
+            for _ in range(4):
+                y = y @ slow
+            x.copy_(src[0])
+        mxg.moe_sort(ids, E, m_splits=splits)                  # a kernel that the next one may overtake
+        here.wait_stream(side)
+        mxg.moe_gather(x, rows, out=xs)
+        w.copy_(src[2])
+        mxg.int8_quantize_rowwise(x, rows=rows, codes="f16", q=q, scale=sc)
+        mxg.int8_quantize_rowwise(w, q=wq, scale=ws)           # weights from the kernel before the product
+        mxg.int8_grouped_gemm_fwd(mxg.Int8Operand(q, sc), mxg.Int8Operand(wq, ws), splits, N, out=out)
+        first = out.clone()
+        out.zero_()
+        mxg.moe_sort(ids, E, m_splits=splits)                  # splits from the kernel before
+        mxg.int8_grouped_gemm_fwd(mxg.Int8Operand(q, sc), mxg.Int8Operand(wq, ws), splits, N, out=out)
+        return first
+
+    want = []
+    for s in new:  # every operation by itself
+        def alone(f, *a, **k):
+            r = f(*a, **k)
+            torch.cuda.synchronize()
+            return r
+        sp, ro = alone(mxg.moe_sort, s[1], E)
+        g = alone(mxg.moe_gather, s[0], ro)
+        a = alone(mxg.int8_quantize_rowwise, s[0], rows=ro, codes="f16")
+        b = alone(mxg.int8_quantize_rowwise, s[2])
+        want.append((g, alone(mxg.int8_grouped_gemm_fwd, a, b, sp, N)))
+    chain(new[0])
+    torch.cuda.synchronize()
+    if captured:
+        inputs = [torch.empty_like(t) for t in new[0]]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            first = chain(inputs)
+    for i in (1, 2, 3, 0, 2):
+        for t in (splits, *staged, rows, xs, q, out):  # what a call that came too early would find
+            t.zero_()
+        if captured:
+            for d, s in zip(inputs, new[i]):
+                d.copy_(s)
+            graph.replay()
+        else:
+            first = chain(new[i])
+        torch.cuda.synchronize()
+        assert torch.equal(xs, want[i][0]), i
+        assert torch.equal(first, want[i][1]) and torch.equal(out, want[i][1]), i
+
+
 @pytest.mark.parametrize("S,N,K", [(20, 4104, 8208), (3000, 2056, 8208)])
 def test_waits_that_run_out(S, N, K):
     """With a limit of 1 ns a call finishes or gives up cleanly; either way the next one is right."""
