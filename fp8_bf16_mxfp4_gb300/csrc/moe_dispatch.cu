@@ -25,15 +25,18 @@ constexpr uint32_t kFull = 0xffffffffu;
 // ---------------------------------------------------------------------------
 // Sort: a stable counting sort.  Chunks of the slots go to CTAs, equal runs of a
 // chunk to its warps, and a warp takes its run 32 slots at a time, where
-// __match_any finds the slots of one expert.  A slot's row is the rows of lower
+// votes find the slots of one expert.  A slot's row is the rows of lower
 // experts, of earlier chunks, of earlier warps and of earlier slots of its run.
 // Up to 1024 slots are one CTA's; above, a first kernel leaves every chunk's counts
 // and the last, which counts its own chunk again while the one before ends, needs the
 // sums over those of the chunks before.  Where a warp has all chunks of eight keys in
 // one load each CTA adds them up itself; a kernel between the two does it for more.
-// Bound by latency: 512 slots of 32 experts 3.4 us, 16384 4.8, 65536 6.1 (7.5 without
-// the kernel between); 65536 of 512 7.8 (17).  Chunks of 2048 slots: 7.2, 7.2 and
-// 10.2.  No atomics, so equal ids keep their order.
+// Bound by latency: 512 slots of 32 experts 2.8 us, 16384 4.1, 65536 5.1, of 512
+// experts 6.8; 262144 of 512 9.8.  (Chunks of 2048 slots, one CTA up to 4096: 4096 of
+// 32 experts 8.4 us instead of 4.7; without the kernel between 65536 of 32 7.5 instead
+// of 6.1; votes again for the placement and counters without atomics: 5.5 and 7.2 for
+// the 5.1 and 6.8.)  Atomics only add within a warp's own counters, so equal ids keep
+// their order.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -48,9 +51,9 @@ int64_t sort_chunk(int64_t P) {
 }
 int64_t sort_chunks(int64_t P) { const int64_t c = sort_chunk(P); return (P + c - 1) / c; }
 
-// Calls f(i, e) for every 32 slots of [i0, i1), a slot per lane: e is the slot's
+// Calls f(q, i, e) for every 32 slots of [i0, i1), a slot per lane: e is the slot's
 // expert, E for an empty one (and for an id that is not below E), -1 past the end.
-// Four loads are in flight.
+// Four loads are in flight, q counts them.
 constexpr int kSortFlight = 4;
 template <typename F>
 MXG_DEVINL bool for_slots(const int32_t* ids, int64_t i0, int64_t i1, int E, F f) {
@@ -65,19 +68,37 @@ MXG_DEVINL bool for_slots(const int32_t* ids, int64_t i0, int64_t i1, int E, F f
       const int64_t at = i + 32 * q + lane;
       if (at - lane >= i1) break;
       bad |= id[q] >= E;
-      f(at, at >= i1 ? -1 : id[q] < 0 || id[q] >= E ? E : id[q]);
+      f(q, at, at >= i1 ? -1 : id[q] < 0 || id[q] >= E ? E : id[q]);
     }
   }
   return bad;
 }
 
-// cnt[0..E]: the slots of each expert in the warp's run.
-MXG_DEVINL bool count_run(const int32_t* ids, int64_t i0, int64_t i1, int E, uint32_t* cnt) {
-  const int lane = threadIdx.x & 31;
-  return for_slots(ids, i0, i1, E, [&](int64_t, int e) {
-    const uint32_t same = __match_any_sync(kFull, e);
-    if (e >= 0 && lane == __ffs(same) - 1) cnt[e] += __popc(same);
-    __syncwarp();
+// The lanes whose slot has this one's expert: a vote for each bit of e, of which
+// those past the end (-1) have all, the others not.  (__match_any takes 200 clocks
+// for 32 different experts: 262144 slots of 512 experts 9.8 us, 10.5 with it; 1048576
+// of 8 13.7, 11.2.)
+MXG_DEVINL uint32_t same_expert(int e, int bits) {
+  uint32_t same = kFull;
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
+    if (b >= bits) break;
+    const bool on = (e >> b) & 1;
+    const uint32_t with = __ballot_sync(kFull, on);
+    same &= on ? with : ~with;
+  }
+  return same;
+}
+MXG_DEVINL int expert_bits(int E) { return 32 - __clz(E + 1); }
+
+// cnt[0..E]: the slots of each expert in the warp's run.  Of its last 32 kSortFlight
+// slots e and same are the experts and the lanes that share them.
+MXG_DEVINL bool count_run(const int32_t* ids, int64_t i0, int64_t i1, int E, uint32_t* cnt, int* e, uint32_t* same) {
+  const int lane = threadIdx.x & 31, bits = expert_bits(E);
+  return for_slots(ids, i0, i1, E, [&](int q, int64_t, int at) {
+    e[q] = at;
+    same[q] = same_expert(at, bits);
+    if (at >= 0 && lane == __ffs(same[q]) - 1) atomicAdd(cnt + at, __popc(same[q]));
   });
 }
 
@@ -91,7 +112,9 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(const int3
   __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * chunk, run = chunk / kSortWarps;
   const int64_t i0 = min(P, c0 + warp * run), i1 = min(P, i0 + run);
-  count_run(ids, i0, i1, E, cnt + warp * keys);
+  int e_of[kSortFlight];
+  uint32_t same_of[kSortFlight];
+  count_run(ids, i0, i1, E, cnt + warp * keys, e_of, same_of);
   __syncthreads();
   for (int e = threadIdx.x; e < keys; e += kSortThreads) {
     uint32_t v = 0;
@@ -143,7 +166,9 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
   __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * chunk, run = chunk / kSortWarps;
   const int64_t i0 = min(P, c0 + warp * run), i1 = min(P, i0 + run);
-  const bool bad = count_run(ids, i0, i1, E, cnt + warp * keys);
+  int e_of[kSortFlight];
+  uint32_t same_of[kSortFlight];
+  const bool bad = count_run(ids, i0, i1, E, cnt + warp * keys, e_of, same_of);
   if (__syncthreads_or(bad) && threadIdx.x == 0) report(status, MXG_ERR_INDEX);
 
   if (gridDim.x == 1) {
@@ -218,18 +243,25 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const int3
   __syncthreads();
 
   uint32_t* mine = cnt + warp * keys;
-  for_slots(ids, i0, i1, E, [&](int64_t i, int e) {
-    const uint32_t same = __match_any_sync(kFull, e);
+  auto place = [&](int64_t i, int e, uint32_t same) {
     const int rank = __popc(same & ((1u << lane) - 1u));
-    const uint32_t first = e >= 0 ? mine[e] : 0u;
-    __syncwarp();
+    uint32_t first = 0;
+    if (e >= 0 && rank == 0) first = atomicAdd(mine + e, __popc(same));
+    first = __shfl_sync(kFull, first, __ffs(same) - 1);
     if (e >= 0) {
       const int r = (int)(first + rank);
       rows[i] = e == E ? -1 - r : r;
-      if (rank == 0) mine[e] = first + __popc(same);
     }
-    __syncwarp();
-  });
+    __syncwarp();  // one 32 slots after another
+  };
+  if (run <= 32 * kSortFlight) {  // as counted
+#pragma unroll
+    for (int q = 0; q < kSortFlight; ++q)
+      if (i0 + 32 * q < i1) place(i0 + 32 * q + lane, e_of[q], same_of[q]);
+  } else {
+    const int bits = expert_bits(E);
+    for_slots(ids, i0, i1, E, [&](int, int64_t i, int e) { place(i, e, same_expert(e, bits)); });
+  }
 }
 
 // ---------------------------------------------------------------------------
