@@ -520,26 +520,48 @@ struct I8Params {
   uint32_t idesc;
 };
 
-// The stages of all units cut into equal runs (to one grain), one per pair.
+// How the stages of all units are shared out, a run per pair: whole units; or cut into
+// equal runs wherever these end; or, where there are pairs for it, every unit into
+// `parts` equal runs of its own.  What ends soonest, in stages (0.46 us): a unit that
+// is joined costs 4, and 0.6 for each run and 32 tokens of it, which the last to
+// arrive adds up (100 rows, K = 16384, 256 channels: 46 us in runs of 4 stages, 25 in
+// runs of 16 to 24; 100 rows, 1024 x 7168: 29 and 21).
 struct I8Runs {
-  int per_unit, grain, pairs, q, r;
-  MXG_DEVINL I8Runs(int units, int per_unit_, int tokens, int max_pairs) : per_unit(per_unit_) {
-    // whole units to every pair, or units cut into equal runs: what ends sooner,
-    // a join taking as long as some 8 + tokens / 4 stages
-    const int total = units * per_unit;
-    const int whole = (units + max_pairs - 1) / max_pairs * per_unit;
-    const int run = max((total + max_pairs - 1) / max_pairs, kI8MinStages);
-    const int cut = run + (run >= 2 * per_unit ? 3 : 8 + tokens / 4);
+  int per_unit, grain, pairs, q, r, parts;  // parts > 0: of every unit
+  MXG_DEVINL I8Runs(int units, int per_unit_, int tokens, int max_pairs) : per_unit(per_unit_), parts(0) {
+    const int total = units * per_unit, c32 = max((tokens + 31) >> 5, 1);
+    const int whole = (int)((unsigned)(units + max_pairs - 1) / (unsigned)max_pairs) * per_unit;
+    const int run = max((int)((unsigned)(total + max_pairs - 1) / (unsigned)max_pairs), kI8MinStages);
+    // (estimates need no exact quotients)
+    const int cut = run + (run >= 2 * per_unit ? 3 : 8 + c32 * ((int)__fdividef((float)per_unit, (float)run) + 3) * 5 / 8);
     grain = whole <= cut ? per_unit : 1;
     pairs = min(max_pairs, grain > 1 || per_unit == 1 ? units : (total + kI8MinStages - 1) / kI8MinStages);
-    q = pairs > 0 ? total / grain / pairs : 0;
-    r = pairs > 0 ? total / grain - q * pairs : 0;
+    if (units > 0 && 2 * units <= max_pairs && per_unit > 1) {
+      const float each = (float)per_unit;
+      int n = min((int)__fdividef((float)max_pairs + 0.5f, (float)units),
+                  max(2, (int)(sqrtf(__fdividef(1.6f * each, (float)c32)) + 0.5f)));
+      if (n * units > max_pairs) --n;
+      n = min(n, per_unit);
+      if ((int)__fdividef(each, (float)n) + 5 + c32 * n * 5 / 8 < min(whole, cut)) {
+        parts = n;
+        grain = 1;
+        pairs = units * n;
+      }
+    }
+    const int items = parts > 0 ? per_unit : grain > 1 ? units : total, to = parts > 0 ? parts : pairs;
+    q = to > 0 ? (int)((unsigned)items / (unsigned)to) : 0;
+    r = items - q * to;
   }
-  MXG_DEVINL int start(int b) const { return (b * q + min(b, r)) * grain; }
-  MXG_DEVINL int owner(int s) const {
-    const int g = s / grain;
-    return g < r * (q + 1) ? g / (q + 1) : r + (g - r * (q + 1)) / q;
+  // pair b's run
+  MXG_DEVINL void run(int b, int& s, int& end) const {
+    const int u = parts > 0 ? (int)((unsigned)b / (unsigned)parts) : 0, i = b - u * parts;
+    s = u * per_unit + (i * q + min(i, r)) * grain;
+    end = s + (q + (i < r)) * grain;
   }
+  // the first and the last pair of a cut unit
+  MXG_DEVINL int owner(int s) const { return s < r * (q + 1) ? s / (q + 1) : r + (s - r * (q + 1)) / q; }
+  MXG_DEVINL int first(int unit) const { return parts > 0 ? unit * parts : owner(unit * per_unit); }
+  MXG_DEVINL int last(int unit) const { return parts > 0 ? unit * parts + parts - 1 : owner(unit * per_unit + per_unit - 1); }
 };
 
 // Walks a pair's units: of a run, the cut unit at its start, the cut unit at its
@@ -661,9 +683,8 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
   const I8Runs runs(units, p.nk, units > 0 ? off[p.G] / (units / p.n_chan) : 0, pairs);
   I8Walker<kTok> w;
   if constexpr (L::kCut) {
-    const bool active = pair < runs.pairs;
-    w.s = active ? runs.start(pair) : 0;
-    w.end = active ? runs.start(pair + 1) : 0;
+    w.s = w.end = 0;
+    if (pair < runs.pairs) runs.run(pair, w.s, w.end);
     w.per_unit = p.nk;
   } else {
     w.s = pair;
@@ -911,8 +932,8 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) ptx::st_cg_f32_if(c0 + i < w.n, mine + (c0 + i) * kChan, v[i]);
         }
-        first = runs.owner(w.unit * runs.per_unit);
-        last = runs.owner(w.unit * runs.per_unit + runs.per_unit - 1);
+        first = runs.first(w.unit);
+        last = runs.last(w.unit);
         __threadfence();
         __syncwarp();
         uint32_t got = 0;
