@@ -7,7 +7,7 @@
 // sm_103a has no integer kind of tcgen05.mma, and its integer mma.sync runs at the
 // rate of dp4a.  Every integer up to 2048 is an FP16 value, so products are taken as
 // FP16's: exact, with fp32 sums (exact up to 2^24).  Weights stay 8-bit integers as
-// far as the SM.  Three forms, by the rows of the mean expert:
+// far as the SM.  Three forms:
 //
 //   few      tiles of 8 or 16 rows, mma.sync, weights from global memory to registers;
 //   cut      tiles of 32, 64 or 128 rows on the tensor cores, the contraction of all
@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const FewParam
 // Bound there: an MMA of 16 contraction elements takes about 110 clocks whatever its
 // rows while the widening warps write TMEM (152 us for 1024 rows of 32 experts, 4096 x
 // 7168, without those writes; 184 with them; 138 of HBM).  One row tile of few rows is
-// latency: 20 rows, 4096 x 4096, 16 us, of which 4 are the loads', 1 the start, 3 the
+// latency: 20 rows, 4096 x 4096, 14 us, of which 4 are the loads', 1 the start, 3 the
 // join and 3 two launches.
 // ---------------------------------------------------------------------------
 constexpr int kChan = 128;                 // channels of a CTA's tile (TMEM lanes)
@@ -1028,18 +1029,45 @@ int few_tok(int64_t S, int64_t K) {
   return 0;
 }
 
-// The form for S rows over G experts, by the rows of the mean expert that has some:
-// the few-rows form (-1; at a mean of 8 rows of 32 experts, 4096 x 7168, it takes the
-// 189 us of the next one, at 16 253 us); tiles that hold half as many again as the mean; whole
-// units of 256 from there on.
+// Microseconds that S rows over G experts take in a tensor-core form, as far as sizes
+// tell: the stages of the longest run (I8Runs) and the epilogues of its units, with
+// constants fitted to 150 shapes of 1 to 64 experts, where the form so chosen is 1.6 %
+// slower than the best one in the geometric mean (8.8 % by the mean expert's rows
+// alone: 150 rows, 1024 x 7168, 33.5 us in whole tiles of 256, 18.4 in cut ones of
+// 64).  An expert of routed rows has half a short tile.
+double i8_cost(int form, int64_t S, int G, int64_t N, int64_t K) {
+  constexpr double kPairs = 76, kStage[3] = {0.434, 0.443, 0.482}, kUnit[3] = {0.92, 1.35, 2.03};
+  const int tok = i8_form(form).tok;
+  const double used = (double)std::max<int64_t>(1, std::min<int64_t>(S, G)), nk = (double)cdiv(K, kStageK);
+  const double tiles = G == 1 ? (double)std::max<int64_t>(1, cdiv(S, tok)) : used * std::max(1.0, S / used / tok + 0.53);
+  const double units = tiles * cdiv(N, 2 * kChan), rounds = std::max(1.0, std::ceil(units / kPairs - 0.02));
+  if (form == 3) return 3.8 + rounds * (0.514 * nk + 2.56);
+  const double c32 = std::max(1.0, std::ceil(S / tiles / 32)), run = std::max(units * nk / kPairs, (double)kI8MinStages);
+  double stages = std::min(rounds * nk, run + (run >= 2 * nk ? 3 : 8 + 0.625 * c32 * (nk / run + 3)));
+  if (2 * units <= kPairs && nk > 1) {
+    const double parts = std::min({std::floor(kPairs / units), nk, std::max(2.0, std::round(std::sqrt(1.6 * nk / c32)))});
+    stages = std::min(stages, nk / parts + 4 + 0.625 * c32 * parts);
+  }
+  return 7.2 + kStage[form] * stages + kUnit[form] * units / kPairs;
+}
+
+// The form for S rows over G experts: the few-rows form (-1) up to 8 rows of the mean
+// expert that has some, 16 of a single one (at 8 rows of 32 experts, 4096 x 7168, it
+// takes the 189 us of the next one, at 16 253 us); above, what takes the least time.
 constexpr int kFew = -1;
 int i8_choose(int64_t S, int G, int64_t N, int64_t K) {
-  (void)N;
   const int64_t used = std::max<int64_t>(1, std::min<int64_t>(S, G)), mean = (S + used - 1) / used;
   if (K <= 0x7FFFFF && mean <= (G == 1 ? 16 : 8) && few_tok(S, K) > 0) return kFew;
-  for (int i = 0; i < 3; ++i)
-    if (mean + mean / 2 <= i8_form(i).tok || (G == 1 && mean <= i8_form(i).tok)) return i;
-  return 3;
+  int best = 0;
+  double least = i8_cost(0, S, G, N, K);
+  for (int i = 1; i < kI8Forms; ++i) {
+    const double c = i8_cost(i, S, G, N, K);
+    if (c < least) {
+      least = c;
+      best = i;
+    }
+  }
+  return best;
 }
 
 struct I8Ws {

@@ -162,10 +162,30 @@ def test_product(splits, N, K, out_dtype):
     assert torch.equal(got, product(*ops, splits, N, out_dtype, codes="int8"))
 
 
+CUT = [  # splits, N, K, tile: few units, whose contraction is cut
+    ([17], 40, 2064, 32), ([33], 264, 8208, 32), ([20, 0, 41], 776, 2064, 32), ([500], 40, 4112, 32), ([1, 280, 19], 264, 4112, 32),
+    ([65], 2056, 2064, 64), ([129], 776, 8208, 64), ([90, 200, 3], 776, 4112, 64), ([64, 0, 64, 65, 1], 520, 8208, 64),
+    ([1000], 264, 4112, 64), ([129], 2056, 4112, 128), ([300], 2056, 8208, 128), ([150, 350, 0], 776, 4112, 128),
+    ([900], 776, 8208, 128), ([1, 127, 600, 172], 520, 8208, 128)]
+
+
 def test_every_form_is_among_the_cases():
     from fp8_bf16_mxfp4_gb300 import _lib
     f = _lib.load().mxg_diag_int8_tile_tokens
-    assert {f(len(s), sum(s), N, K) for s, N, K in CASES if sum(s)} == {8, 16, 32, 64, 128, 256}
+    assert {f(len(s), sum(s), N, K) for s, N, K in CASES if sum(s)} >= {8, 16, 256}
+    assert [f(len(s), sum(s), N, K) for s, N, K, _ in CUT] == [tile for *_, tile in CUT]
+
+
+@pytest.mark.parametrize("splits,N,K,tile", CUT)
+def test_cut_forms(splits, N, K, tile):
+    """Small codes, whose sums are exact whatever the order: every part of every unit is in the result, once."""
+    rng = np.random.default_rng(N + K)
+    ops = operands(rng, splits, N, K, most=20)
+    want = torch.from_numpy(in_order(*ops, splits, N))
+    for codes in ("f16", "int8"):
+        assert torch.equal(product(*ops, splits, N, F32, codes=codes).cpu(), want)
+    got = product(*ops, splits, N, BF)
+    assert torch.equal(got.cpu(), want.to(BF)) and torch.equal(got, product(*ops, splits, N, BF))
 
 
 @pytest.mark.parametrize("S", [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 600])
