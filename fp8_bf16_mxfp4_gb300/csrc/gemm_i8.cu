@@ -1058,14 +1058,22 @@ constexpr int kFew = -1;
 int i8_choose(int64_t S, int G, int64_t N, int64_t K) {
   const int64_t used = std::max<int64_t>(1, std::min<int64_t>(S, G)), mean = (S + used - 1) / used;
   if (K <= 0x7FFFFF && mean <= (G == 1 ? 16 : 8) && few_tok(S, K) > 0) return kFew;
-  int best = 0;
-  double least = i8_cost(0, S, G, N, K);
-  for (int i = 1; i < kI8Forms; ++i) {
-    const double c = i8_cost(i, S, G, N, K);
-    if (c < least) {
-      least = c;
-      best = i;
+  thread_local int64_t of[4] = {};  // a call asks for its form several times
+  thread_local int best = 0;
+  if (of[0] != S || of[1] != G || of[2] != N || of[3] != K) {
+    best = 0;
+    double least = i8_cost(0, S, G, N, K);
+    for (int i = 1; i < kI8Forms; ++i) {
+      const double c = i8_cost(i, S, G, N, K);
+      if (c < least) {
+        least = c;
+        best = i;
+      }
     }
+    of[0] = S;
+    of[1] = G;
+    of[2] = N;
+    of[3] = K;
   }
   return best;
 }
