@@ -337,11 +337,11 @@ __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const uint4* __
   }
 }
 
-// A thread sums one piece over a token's slots, eight rows in flight.  Every row is read
+// A thread sums one piece over a token's slots, four rows in flight (8192 tokens, top 8
+// of 4096: 6.2 TB/s, 5.8 with eight, which take more registers).  Every row is read
 // once and not again, so the loads and stores are marked as streaming: 65536 rows of
-// 7168 to 8192, 162 us, 6.5 TB/s; 173 with plain ones.  kShort: rows so short that a CTA
-// has several tokens (apart, because the other form takes 72 registers: four CTAs of 224
-// threads an SM; with 75 there are three and it takes 194 us).
+// 7168 to 8192, 163 us, 6.5 TB/s; 173 with plain ones.  kShort: rows so short that a CTA
+// has several tokens.
 template <typename T, bool kShort>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* __restrict__ y, int64_t ld_y, int64_t y_rows,
                                                                   const int32_t* __restrict__ rows,
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* _
                                                                   int64_t pieces, uint4* __restrict__ out,
                                                                   int64_t ld_out, int32_t* status) {
   constexpr int n = Piece<T>::n;
-  constexpr int kFlight = 8;  // rows in flight
+  constexpr int kFlight = 4;  // rows in flight
   const int64_t t = kShort ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
   if (kShort && t >= tokens) return;
   for (int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; c < pieces; c += (int64_t)gridDim.y * blockDim.x) {
@@ -386,8 +386,10 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const uint4* _
   }
 }
 
-// The same for up to kSlots slots, of kTokens tokens at a time, so that there are as
-// many rows in flight: 32768 rows of 2048, one a token, take 44 us, 94 with the above.
+// The same for up to kSlots slots, all in flight, of kTokens tokens at a time: four where
+// there is one slot (32768 rows of 2048: 44 us, 94 with the above), else one, which
+// leaves room for more CTAs (top 4 of 4096: 6.0 TB/s, 4.6 with two; top 2: 6.2, 5.0 with
+// four; top 6: 5.9, 5.8 with the above).
 template <typename T, int kTokens, int kSlots>
 __global__ void __launch_bounds__(kRowThreads) moe_combine_few_kernel(const uint4* __restrict__ y, int64_t ld_y,
                                                                       int64_t y_rows, const int32_t* __restrict__ rows,
@@ -582,14 +584,19 @@ cudaError_t combine(const void* y, int64_t ld_y, int64_t y_rows, const int32_t* 
   const dim3 block = row_block(pieces);
   const uint4* from = static_cast<const uint4*>(y);
   uint4* to = static_cast<uint4*>(out);
-  if (k > 4) {
+  if (k > 6) {
     const auto fn = block.y > 1 ? moe_combine_kernel<T, true> : moe_combine_kernel<T, false>;
     fn<<<row_grid(tokens, pieces, block), block, 0, stream>>>(from, ld_y, y_rows, rows, weights, tokens, k, pieces, to,
                                                              ld_out, status);
     return cudaGetLastError();
   }
-  const int each = k > 2 ? 2 : 4;  // tokens of a thread
-  const auto fn = k > 2 ? moe_combine_few_kernel<T, 2, 4> : k > 1 ? moe_combine_few_kernel<T, 4, 2> : moe_combine_few_kernel<T, 4, 1>;
+  const int each = k > 1 ? 1 : 4;  // tokens of a thread
+  const auto fn = k > 5   ? moe_combine_few_kernel<T, 1, 6>
+                  : k > 4 ? moe_combine_few_kernel<T, 1, 5>
+                  : k > 3 ? moe_combine_few_kernel<T, 1, 4>
+                  : k > 2 ? moe_combine_few_kernel<T, 1, 3>
+                  : k > 1 ? moe_combine_few_kernel<T, 1, 2>
+                          : moe_combine_few_kernel<T, 4, 1>;
   fn<<<row_grid((tokens + each - 1) / each, pieces, block), block, 0, stream>>>(from, ld_y, y_rows, rows, weights, tokens, k,
                                                                                (int)pieces, to, ld_out, status);
   return cudaGetLastError();
@@ -599,9 +606,10 @@ template <typename T>
 cudaError_t combine_backward(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y, const int32_t* rows,
                              const float* weights, int64_t tokens, int k, int64_t pieces, void* dy, int64_t ld_dy,
                              float* dweights, int32_t* status, cudaStream_t stream, int num_sms) {
-  // Four rows of a thread in flight: of four slots, or of fewer slots' pieces.  A token
-  // has lanes of a warp, or a CTA of as many threads as share its pieces equally: up
-  // to 256, or 1024 where there are few tokens (64 of 7168, top 8: 8.2 us, 11.9).
+  // Four rows of a thread in flight: of four slots, of three where that leaves fewer
+  // unused (top 6 of 2880: 6.4 TB/s, 6.0 with four), or of fewer slots' pieces.  A
+  // token has lanes of a warp, or a CTA of as many threads as share its pieces equally:
+  // up to 256, or 1024 where there are few tokens (64 of 7168, top 8: 8.2 us, 11.9).
   const int each = k > 2 ? 1 : k > 1 ? 2 : 4;
   const int64_t want = (pieces + each - 1) / each;
   const bool lanes = want <= 32, few = !lanes && tokens < 4 * num_sms;
@@ -612,14 +620,20 @@ cudaError_t combine_backward(const void* dout, int64_t ld_dout, const void* y, i
     const int64_t most = few ? 1024 : kRowThreads, turns = (want + most - 1) / most;
     share = threads = (int)(((want + turns - 1) / turns + 31) / 32 * 32);
   }
-  const auto pick = [&](auto one, auto two, auto four) { return each == 1 ? one : each == 2 ? two : four; };
+  const bool three = (k + 2) / 3 * 3 < (k + 3) / 4 * 4;
+  const auto pick = [&](auto one, auto one3, auto two, auto four) {
+    return each == 1 ? (three ? one3 : one) : each == 2 ? two : four;
+  };
   const auto fn = lanes ? pick(moe_combine_backward_kernel<T, 1, 4, kRowThreads, true>,
+                               moe_combine_backward_kernel<T, 1, 3, kRowThreads, true>,
                                moe_combine_backward_kernel<T, 2, 2, kRowThreads, true>,
                                moe_combine_backward_kernel<T, 4, 1, kRowThreads, true>)
                   : few ? pick(moe_combine_backward_kernel<T, 1, 4, 1024, false>,
+                               moe_combine_backward_kernel<T, 1, 3, 1024, false>,
                                moe_combine_backward_kernel<T, 2, 2, 1024, false>,
                                moe_combine_backward_kernel<T, 4, 1, 1024, false>)
                         : pick(moe_combine_backward_kernel<T, 1, 4, kRowThreads, false>,
+                               moe_combine_backward_kernel<T, 1, 3, kRowThreads, false>,
                                moe_combine_backward_kernel<T, 2, 2, kRowThreads, false>,
                                moe_combine_backward_kernel<T, 4, 1, kRowThreads, false>);
   const int64_t ctas = lanes ? (tokens + threads / share - 1) / (threads / share) : tokens;
