@@ -304,13 +304,14 @@ MXG_DEVINL uint4 narrow(const float* v) {
 // Gather and combine: blockDim.x threads share a row's pieces, blockDim.y tokens a CTA.
 constexpr int kRowThreads = 256;
 // As many threads as share a row's pieces equally (896 pieces: 4 times 224; with
-// 256 threads combine takes 186 us instead of 173 for 65536 rows of 7168), and as many
-// tokens as make up a CTA (8 rows of 32 BF16 values for each of 32768 tokens: 7.0 us, 19.7
-// with a CTA for every token).
+// 256 threads combine takes 186 us instead of 173 for 65536 rows of 7168); of short rows
+// as many tokens as make up a CTA of 128 (8 rows of 32 BF16 values for each of 32768
+// tokens: 5.6 us, 19.7 with a CTA for every token; top 8 of 256 6.1 TB/s, 5.7 with 256
+// threads).
 dim3 row_block(int64_t pieces) {
   const int64_t turns = (pieces + kRowThreads - 1) / kRowThreads;
   const unsigned x = (unsigned)((pieces + turns - 1) / turns);
-  return x > kRowThreads / 4 ? dim3((x + 31) / 32 * 32) : dim3(x, kRowThreads / x);
+  return x > kRowThreads / 4 ? dim3((x + 31) / 32 * 32) : dim3(x, kRowThreads / 2 / x);
 }
 dim3 row_grid(int64_t tokens, int64_t pieces, dim3 block) {
   return dim3((unsigned)((tokens + block.y - 1) / block.y),
@@ -609,10 +610,11 @@ cudaError_t combine_backward(const void* dout, int64_t ld_dout, const void* y, i
   // Four rows of a thread in flight: of four slots, of three where that leaves fewer
   // unused (top 6 of 2880: 6.4 TB/s, 6.0 with four), or of fewer slots' pieces.  A
   // token has lanes of a warp, or a CTA of as many threads as share its pieces equally:
-  // up to 256, or 1024 where there are few tokens (64 of 7168, top 8: 8.2 us, 11.9).
+  // from 32 (top 8 of 256: 6.1 TB/s, 4.9 with eight tokens' warps in a CTA) up to 256,
+  // or 1024 where there are few tokens (64 of 7168, top 8: 8.2 us, 11.9).
   const int each = k > 2 ? 1 : k > 1 ? 2 : 4;
   const int64_t want = (pieces + each - 1) / each;
-  const bool lanes = want <= 32, few = !lanes && tokens < 4 * num_sms;
+  const bool lanes = want <= 16, few = !lanes && tokens < 4 * num_sms;
   int share = 1, threads = kRowThreads;
   if (lanes) {
     while (share < want) share *= 2;
