@@ -1052,12 +1052,16 @@ double i8_cost(int form, int64_t S, int G, int64_t N, int64_t K) {
 }
 
 // The form for S rows over G experts: the few-rows form (-1) up to 8 rows of the mean
-// expert that has some, 16 of a single one (at 8 rows of 32 experts, 4096 x 7168, it
-// takes the 189 us of the next one, at 16 253 us); above, what takes the least time.
+// expert that has some, more where there are so few of these that none is far above the
+// mean (two of 10 rows, 2048 x 7168: 15.3 us, 17.6 in the next form; four of 12, 592 x
+// 6256: 11.9, 14.9, of 14 15.3, 15.0; six of 12 19.8, 17.1; at 8 rows of 32, 4096 x
+// 7168, it takes the 189 us of the next one, at 16 253 us); above, what takes the least
+// time.
 constexpr int kFew = -1;
 int i8_choose(int64_t S, int G, int64_t N, int64_t K) {
   const int64_t used = std::max<int64_t>(1, std::min<int64_t>(S, G)), mean = (S + used - 1) / used;
-  if (K <= 0x7FFFFF && mean <= (G == 1 ? 16 : 8) && few_tok(S, K) > 0) return kFew;
+  const int64_t most = used == 1 ? 16 : used == 2 ? 14 : used <= 4 ? 12 : 8;
+  if (K <= 0x7FFFFF && mean <= most && few_tok(S, K) > 0) return kFew;
   thread_local int64_t of[4] = {};  // a call asks for its form several times
   thread_local int best = 0;
   if (of[0] != S || of[1] != G || of[2] != N || of[3] != K) {

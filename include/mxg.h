@@ -659,7 +659,7 @@ mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* row
  *   out : [S, N] of out_dtype, row stride ld_out; rows 16-byte aligned; N % 8 == 0
  *   ws  : at least int8_gemm_workspace_size(G, S, N, K, A->codes) bytes, 256-byte aligned
  * Splits are checked as for grouped_gemm_fwd (MXG_ERR_SPLITS; nothing is written).
- * From 17 rows (or a mean of 9 rows an expert) on the product runs on CTA pairs;
+ * From 17 rows (or a mean of 9 to 15 rows an expert) on the product runs on CTA pairs;
  * mxg_set_gemm_cta_group has no effect on it.
  * Forward only: the gradients of a quantized layer are those of its unquantized weights. */
 size_t int8_gemm_workspace_size(int32_t G, int64_t S, int64_t N, int64_t K, int32_t a_codes);
