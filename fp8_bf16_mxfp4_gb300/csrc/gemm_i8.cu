@@ -14,9 +14,9 @@
 //            tiles cut into equal runs;
 //   whole    tiles of 256 rows on the tensor cores.
 //
-// 8192 rows of 8 experts, 4096 x 14336: 530 us, 1.82 PFLOP/s (0.96 of what torch's
-// BF16 product of two such matrices reaches), where tensor pipe and shared memory are
-// each busy 80 % of the time.  128 rows of 32 experts, 4096 x 7168: 155 us, 6.1 TB/s.
+// 8192 rows of 8 experts, 4096 x 14336: 505 us, 1.9 PFLOP/s (0.95 and more of what
+// torch's BF16 product of two such matrices reaches), where the tensor pipe is busy 81 %
+// of the time.  128 rows of 32 experts, 4096 x 7168: 155 us, 6.1 TB/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
