@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "tile_walk.h"
 
 namespace mxg {
 namespace {
@@ -171,21 +172,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* __res
   }
 }
 
-// Tile order inside an expert: groups of `group_m` m-tiles; inside a group m
-// runs fastest and n outer, so CTAs running at the same time share a B tile
-// and the group's A rows stay in L2 across all of its n-tiles (B is then read
-// once per group instead of once per m-tile).
-MXG_DEVINL void tile_mn(int local, int expert_tiles, int ntn, int group_m, int& mt, int& nt) {
-  const int mtn = expert_tiles / ntn;
-  const int span = group_m * ntn;
-  const int grp = local / span;
-  const int first = grp * group_m;
-  const int rows = min(group_m, mtn - first);
-  const int idx = local - grp * span;
-  mt = first + idx % rows;
-  nt = idx / rows;
-}
-
 // Host: group size that keeps about 32 MiB of A rows (128-row strips of
 // `a_row_bytes` each) resident.
 inline int tile_group_m(double a_row_bytes) {
@@ -193,16 +179,6 @@ inline int tile_group_m(double a_row_bytes) {
   const double g = (32.0 * 1024 * 1024) / strip;
   return g < 1.0 ? 1 : (g > 4096.0 ? 4096 : (int)g);
 }
-
-MXG_DEVINL int find_prefix(const int32_t* pre, int G, int x) {  // last g with pre[g] <= x
-  int lo = 0, hi = G - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
 
 // ---------------------------------------------------------------------------
 // Host: tensor maps (driver entry point looked up through the runtime, so the

@@ -314,9 +314,9 @@ MXG_DEVINL void few_tile(const FewParams& p, uint8_t* x, float* part, int e, int
   int l_it = 0, l_i = 0;
   const uint8_t *w0 = nullptr, *w8 = nullptr;  // this lane's rows: channels g and g + 8 of the unit
   auto point = [&]() {  // past the last channel: not stored
-    const int chan = c0 + (l_it * at_once + ug) * kFewChan + g;
-    w0 = p.w + ((int64_t)e * p.N + min(chan, c1 - 1)) * p.ld_w + q16;
-    w8 = p.w + ((int64_t)e * p.N + min(chan + 8, c1 - 1)) * p.ld_w + q16;
+    const uint32_t chan = c0 + ((uint32_t)l_it * at_once + ug) * kFewChan + g, most = c1 - 1;  // up to 512 above N
+    w0 = p.w + ((int64_t)e * p.N + min(chan, most)) * p.ld_w + q16;
+    w8 = p.w + ((int64_t)e * p.N + min(chan + 8, most)) * p.ld_w + q16;
   };
   point();
   uint4 v[kFewDepth][4];
@@ -463,8 +463,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const FewParam
 // latency: 20 rows, 4096 x 4096, 14 us, of which 4 are the loads', 1 the start, 3 the
 // join and 3 two launches.
 // ---------------------------------------------------------------------------
-constexpr int kChan = 128;                 // channels of a CTA's tile (TMEM lanes)
-constexpr int kStageK = 128;               // contraction elements of a stage
+constexpr int kChan = kUnitChan / 2;       // channels of a CTA's tile (TMEM lanes)
 constexpr int kWBytes = kChan * kStageK;
 constexpr int kI8TmemCols = 512;
 constexpr int kACols = kStageK / 2;        // TMEM columns of a stage's weights (two FP16 a column)
@@ -505,10 +504,9 @@ struct I8Cfg {
   static_assert(kSlots <= kStages, "a slot's MMAs are those of an earlier stage of the ring");
 };
 
-struct I8Params {
+struct I8Params : I8Order {
   const int32_t* splits;  // null: one expert of all S rows
-  int G, S, N, nk, n_chan;  // nk: stages of a unit; n_chan: channel tiles
-  int group_t;            // token tiles per group of the unit order
+  int S, N;
   const float* sa;
   const float* sw;
   void* out;
@@ -563,54 +561,6 @@ struct I8Runs {
   MXG_DEVINL int owner(int s) const { return s < r * (q + 1) ? s / (q + 1) : r + (s - r * (q + 1)) / q; }
   MXG_DEVINL int first(int unit) const { return parts > 0 ? unit * parts : owner(unit * per_unit); }
   MXG_DEVINL int last(int unit) const { return parts > 0 ? unit * parts + parts - 1 : owner(unit * per_unit + per_unit - 1); }
-};
-
-// Walks a pair's units: of a run, the cut unit at its start, the cut unit at its
-// end, then the whole units; with 256 tokens, every `per_unit`-th unit.
-template <int kTok>
-struct I8Walker {
-  int s, end, per_unit;      // what is left of the run (256 tokens: the next unit, all units, the stride)
-  int unit, k0, k1;          // the current unit and its stages [k0, k1)
-  int e, tok0, n, chan0;     // expert, first row, rows, first channel of the tile
-  MXG_DEVINL bool next(const I8Params& p, const int32_t* off, const int32_t* tile) {
-    if (s >= end) return false;
-    if constexpr (!I8Cfg<kTok>::kCut) {
-      unit = s;
-      s += per_unit;
-      k0 = 0;
-      k1 = p.nk;
-    } else {
-      const int first = s / per_unit, last = end / per_unit;
-      const int head = s - first * per_unit, tail = end - last * per_unit;
-      if (head != 0 || first == last) {  // up to the unit's end, or the run's
-        unit = first;
-        k0 = head;
-        k1 = first == last ? tail : per_unit;
-        s += k1 - k0;
-      } else if (tail != 0) {
-        unit = last;
-        k0 = 0;
-        k1 = tail;
-        end -= tail;
-      } else {
-        unit = first;
-        k0 = 0;
-        k1 = per_unit;
-        s += k1;
-      }
-    }
-    e = find_prefix(tile, p.G, unit);
-    // The expert's full tiles, then its short ones: in the order of the tiles every
-    // second unit would be short where there are two, and always the same pairs'
-    // (12000 rows of 32 experts, 4096 x 7168: 447 us, 481).
-    const int rows = off[e + 1] - off[e], local = unit - tile[e], whole = rows / kTok * p.n_chan;
-    int tt = rows / kTok, ct = local - whole;
-    if (local < whole) tile_mn(local, whole, p.n_chan, p.group_t, tt, ct);
-    n = min(kTok, rows - tt * kTok);
-    tok0 = off[e] + tt * kTok;
-    chan0 = ct * 2 * kChan;
-    return true;
-  }
 };
 
 // Tokens that the MMAs of a tile take: its own, to a multiple of 16 (half of them
@@ -682,7 +632,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
   const int units = bad ? 0 : tile[p.G];
   const int pair = (int)ptx::cluster_id_x(), pairs = (int)ptx::nclusters_x();
   const I8Runs runs(units, p.nk, units > 0 ? off[p.G] / (units / p.n_chan) : 0, pairs);
-  I8Walker<kTok> w;
+  I8Walker<kTok, L::kCut> w;
   if constexpr (L::kCut) {
     w.s = w.end = 0;
     if (pair < runs.pairs) runs.run(pair, w.s, w.end);
@@ -1179,7 +1129,7 @@ bool int8_gemm_sizes_fit(int64_t S, int G, int64_t N, int64_t K) {
   const int form = i8_choose(S, G, N, K);
   const int64_t tiles = S / (form == kFew ? 8 : i8_form(form).tok) + std::min<int64_t>(S, G);
   if (form == kFew) return tiles <= 0x7FFFFFFF / cdiv(N, kFewChan);
-  return tiles * cdiv(N, 2 * kChan) <= 0x7FFFFFFF / cdiv(K, kStageK);
+  return tiles * cdiv(N, 2 * kChan) <= (0x7FFFFFFF - 256) / cdiv(K, kStageK);  // (sums of them and the pairs are taken too)
 }
 
 namespace {
@@ -1231,11 +1181,8 @@ mxg_status launch_int8_gemm(const Int8GemmArgs& a, cudaStream_t stream, int num_
 
   I8Params p{};
   p.splits = a.splits;
-  p.G = a.G; p.S = (int)a.S; p.N = (int)a.N;
-  p.nk = (int)cdiv(a.K, kStageK);
-  p.n_chan = (int)cdiv(a.N, 2 * kChan);
-  // token tiles whose activations (about 32 MiB) stay in L2 over all channel tiles
-  p.group_t = (int)std::max<int64_t>(1, (int64_t(32) << 20) / (f.tok * a.K * 2));
+  static_cast<I8Order&>(p) = i8_order(a.G, a.N, a.K, f.tok);
+  p.S = (int)a.S; p.N = (int)a.N;
   p.sa = a.sa; p.sw = a.sw;
   p.out = a.out; p.ld_out = a.ld_out; p.out_f32 = a.out_dtype == MXG_OUT_F32;
   p.part = ws.part; p.sync = ws.sync;
