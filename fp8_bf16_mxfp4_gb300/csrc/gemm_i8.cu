@@ -971,11 +971,14 @@ I8Form i8_form(int i) {
   }
 }
 
-// Rows of a tile of the few-rows form: 16 where they fit shared memory, else 8; 0
-// where not even these do.
+// Rows of a tile of the few-rows form: 16 where they fit its share of shared memory,
+// else 8; 0 where not even these do.  What shared memory takes is missing from L1,
+// through which the weights' loads pass (one row, 8192 channels, tiles of 8: K = 16384,
+// 149 KB, 31 us, 36 in the next form; 18432, 165 KB, 41 and 40; 22016, 193 KB, 73 and 45).
+constexpr int64_t kFewSmem = 156 * 1024;
 int few_tok(int64_t S, int64_t K) {
   for (int tok = S > 8 ? 16 : 8; tok >= 8; tok -= 8)
-    if (tok * (int64_t)few_stride(K) + few_part_bytes(tok) <= 216 * 1024) return tok;
+    if (tok * (int64_t)few_stride(K) + few_part_bytes(tok) <= kFewSmem) return tok;
   return 0;
 }
 
@@ -1001,17 +1004,39 @@ double i8_cost(int form, int64_t S, int G, int64_t N, int64_t K) {
   return 7.2 + kStage[form] * stages + kUnit[form] * units / kPairs;
 }
 
-// The form for S rows over G experts: the few-rows form (-1) up to 8 rows of the mean
-// expert that has some, more where there are so few of these that none is far above the
-// mean (two of 10 rows, 2048 x 7168: 15.3 us, 17.6 in the next form; four of 12, 592 x
-// 6256: 11.9, 14.9, of 14 15.3, 15.0; six of 12 19.8, 17.1; at 8 rows of 32, 4096 x
-// 7168, it takes the 189 us of the next one, at 16 253 us); above, what takes the least
-// time.
+// The most rows of the mean expert that has some for which the few-rows form is taken.
+// It reads an expert's weights once for every tile of its rows, widens them once for
+// every 8, and ends with its fullest expert, which routing makes the fuller the more
+// experts there are.  us in this form and in the next one, rows at random where there are
+// several experts (at mean rows):
+//   up to 8 experts: 8 (8 of 6, 4096 x 7168: 45.9, 54.5, of 8: 54.4, 54.5); above: 4
+//     (32 of 4, 4096 x 7168: 179.7, 179.4, of 2: 138, 159; 64 of 5, 1024 x 1024: 28.4, 23.0);
+//   tiles of 8 alone, where 16 rows do not fit: one expert's 8 (4096 x 14336: 20.1, 23.0;
+//     9 rows 28.5, 22.9), else 6 (8 of 6, 4096 x 14336: 84.3, 95.4, of 7: 107, 96; 32 of 6:
+//     322, 345); 16 of one expert of 20 MB (1024 x 16384: 15.1, 16.7; 4096 x 11264: 24.3, 20.5);
+//   tiles of 16 and few experts, 16, 14 or 12, where an expert's weights are small: 60 MB
+//     of one or two (16 rows, 14336 x 4096: 19.8, 22.2, 8192 x 8192: 25.9, 23.9; two of 14,
+//     14336 x 4096: 31.5, 32.8, 28672 x 8192: 101.6, 95.4), 16 MB of three or four (three of 12,
+//     2048 x 2048: 10.3, 12.6, 11008 x 2048: 28.9, 23.4; four of 12, 2048 x 7168: 22.7, 23.2).
+// Over 463 such products 1.1 % slower than the faster of the two in the geometric mean.
+int few_most(int64_t used, int tok, int64_t N, int64_t K) {
+  const int64_t weights = N * K;
+  if (used == 1 && tok == 8) return weights <= 20'000'000 ? 16 : 8;
+  if (tok == 8) return 6;
+  if (used <= 2 && weights <= 60'000'000) return used == 1 ? 16 : 14;
+  if (used > 2 && used <= 4 && weights <= 16'000'000) return 12;
+  return used <= 8 ? 8 : 4;
+}
+
+// The form for S rows over G experts: the few-rows form (-1) up to few_most rows of the
+// mean expert that has some; above, what takes the least time.
 constexpr int kFew = -1;
 int i8_choose(int64_t S, int G, int64_t N, int64_t K) {
   const int64_t used = std::max<int64_t>(1, std::min<int64_t>(S, G)), mean = (S + used - 1) / used;
-  const int64_t most = used == 1 ? 16 : used == 2 ? 14 : used <= 4 ? 12 : 8;
-  if (K <= 0x7FFFFF && mean <= most && few_tok(S, K) > 0) return kFew;
+  if (mean <= 16 && K <= 0x7FFFFF) {
+    const int tok = few_tok(S, K);
+    if (tok > 0 && mean <= few_most(used, tok, N, K)) return kFew;
+  }
   thread_local int64_t of[4] = {};  // a call asks for its form several times
   thread_local int best = 0;
   if (of[0] != S || of[1] != G || of[2] != N || of[3] != K) {
@@ -1138,7 +1163,7 @@ mxg_status launch_int8_few(const Int8GemmArgs& a, cudaStream_t stream, int num_s
     static bool ready[kI8MaxDevices] = {};
     std::lock_guard<std::mutex> lk(g_i8_mu);
     if (dev < 0 || dev >= kI8MaxDevices) return MXG_ERR_CUDA;
-    if (!ready[dev] && cudaFuncSetAttribute(int8_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024) != cudaSuccess) {
+    if (!ready[dev] && cudaFuncSetAttribute(int8_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem) != cudaSuccess) {
       cudaGetLastError();
       return MXG_ERR_CUDA;
     }
