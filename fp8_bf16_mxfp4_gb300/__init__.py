@@ -1219,7 +1219,8 @@ def int8_grouped_gemm_fwd(A: Int8Operand, W: Int8Operand, m_splits: torch.Tensor
                           status: torch.Tensor | None = None, check: bool = False) -> torch.Tensor:
     """Y[off_g+i, :] = A[off_g+i, :] @ W[g*N:(g+1)*N, :]^T for every expert g, both
     operands standing for scale * codes; ``W`` int8 [G * N, K].  Codes' products are
-    exact and their sums in FP32.  Forward only."""
+    exact and their sums in FP32: exact below 2^24, above within 2^-23 of the largest
+    partial sum for every 16 elements.  Forward only."""
     if m_splits.dim() != 1 or m_splits.dtype != torch.int32 or not m_splits.is_contiguous() or not m_splits.is_cuda:
         _refuse(m_splits=(m_splits, (m_splits.numel(),), torch.int32, True))
     G = m_splits.numel()

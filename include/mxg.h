@@ -653,8 +653,11 @@ mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* row
 
 /* Y[off_g + i, n] = A.scale[off_g + i] * W.scale[g N + n] * sum_k A[off_g + i, k] W[g N + n, k]
  * for every expert g, off the prefix sum of m_splits.  The products of the codes are
- * exact, their sums in fp32 (exact while they stay below 2^24), the result rounded
- * once to BF16 or, after two products in fp32, FP32.
+ * exact, their sums in fp32: exact while they stay below 2^24; above, every 16
+ * elements of the contraction lose less than 2^-23 of the largest partial sum, cut
+ * off rather than rounded (codes of 64 to 127 of one sign: 3.4e-6 of the sum for
+ * K = 7168, 1.9e-5 for 20000; a tenth of that where the contraction is cut into many
+ * runs).  The result is rounded once to BF16 or, after two products in fp32, FP32.
  *   A   : [S, K] codes of either kind; W: [G * N, K], MXG_CODES_INT8
  *   out : [S, N] of out_dtype, row stride ld_out; rows 16-byte aligned; N % 8 == 0
  *   ws  : at least int8_gemm_workspace_size(G, S, N, K, A->codes) bytes, 256-byte aligned
