@@ -1164,7 +1164,8 @@ mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* row
 size_t int8_gemm_workspace_size(int32_t G, int64_t S, int64_t N, int64_t K, int32_t a_codes) {
   if (G < 1 || G > kMaxExperts || S < 0 || S > 0x7FFFFFFF - 256 || N < 8 || N % 8 != 0 ||
       N > (0x7FFFFFFF - 256) / G || K < 16 ||
-      K > 0x7FFFFFFF || K % 16 != 0 || (a_codes != MXG_CODES_INT8 && a_codes != MXG_CODES_F16))
+      K > 0x7FFFFFFF || K % 16 != 0 || (a_codes != MXG_CODES_INT8 && a_codes != MXG_CODES_F16) ||
+      !int8_gemm_sizes_fit(S, G, N, K))
     return 0;
   return int8_gemm_workspace_bytes(S, G, N, K, a_codes);
 }

@@ -662,8 +662,10 @@ mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* row
  *   out : [S, N] of out_dtype, row stride ld_out; rows 16-byte aligned; N % 8 == 0
  *   ws  : at least int8_gemm_workspace_size(G, S, N, K, A->codes) bytes, 256-byte aligned
  * Splits are checked as for grouped_gemm_fwd (MXG_ERR_SPLITS; nothing is written).
- * From 17 rows (or a mean of 9 to 15 rows an expert) on the product runs on CTA pairs;
- * mxg_set_gemm_cta_group has no effect on it.
+ * Few rows (a mean of up to 4 to 16 for an expert, by sizes; K <= 17280) run on single
+ * CTAs, others on CTA pairs (mxg_diag_int8_tile_tokens); mxg_set_gemm_cta_group has no
+ * effect on either.  Sizes whose count of tiles does not fit 32 bits are refused
+ * (MXG_ERR_SHAPE; int8_gemm_workspace_size returns 0).
  * Forward only: the gradients of a quantized layer are those of its unquantized weights. */
 size_t int8_gemm_workspace_size(int32_t G, int64_t S, int64_t N, int64_t K, int32_t a_codes);
 mxg_status int8_grouped_gemm_fwd(const mxg_i8_operand* A, const mxg_i8_operand* W, const int32_t* d_m_splits, int32_t G,
@@ -715,7 +717,7 @@ int32_t mxg_diag_lora_tile_adapters(int64_t tokens, int32_t adapters);
 
 /* Diagnostic: the rows of a tile of int8_grouped_gemm_fwd for these sizes: 8 or 16
  * (the form for few rows), 32, 64 or 128 (work cut into equal runs) or 256 (whole
- * tiles); 0 where the sizes are refused. */
+ * tiles); 0 where the call refuses the sizes. */
 int32_t mxg_diag_int8_tile_tokens(int32_t G, int64_t S, int64_t N, int64_t K);
 
 /* ABI version: major*10000 + minor*100 + patch. */
