@@ -468,9 +468,6 @@ constexpr int kChan = kUnitChan / 2;       // channels of a CTA's tile (TMEM lan
 constexpr int kWBytes = kChan * kStageK;
 constexpr int kI8TmemCols = 512;
 constexpr int kACols = kStageK / 2;        // TMEM columns of a stage's weights (two FP16 a column)
-constexpr int kI8MaxPairs = 80;            // partial buffers are sized for this many pairs
-constexpr int kI8SyncWords = 8 * kI8MaxPairs;
-constexpr int kI8MinStages = 4;            // shortest run of cut units
 constexpr uint32_t kWatchBar = 1;          // named barrier of the issuer and the warp that waits for it
 
 // kTok: the tokens of a tile.  Accumulators first (two of them, but for 256
@@ -518,50 +515,6 @@ struct I8Params : I8Order {
   int32_t* status;
   uint64_t timeout_ns, drain_ns;
   uint32_t idesc;
-};
-
-// How the stages of all units are shared out, a run per pair: whole units; or cut into
-// equal runs wherever these end; or, where there are pairs for it, every unit into
-// `parts` equal runs of its own.  What ends soonest, in stages (0.46 us): a unit that
-// is joined costs 4, and 0.6 for each run and 32 tokens of it, which the last to
-// arrive adds up (100 rows, K = 16384, 256 channels: 46 us in runs of 4 stages, 25 in
-// runs of 16 to 24; 100 rows, 1024 x 7168: 29 and 21).
-struct I8Runs {
-  int per_unit, grain, pairs, q, r, parts;  // parts > 0: of every unit
-  MXG_DEVINL I8Runs(int units, int per_unit_, int tokens, int max_pairs) : per_unit(per_unit_), parts(0) {
-    const int total = units * per_unit, c32 = max((tokens + 31) >> 5, 1);
-    const int whole = (int)((unsigned)(units + max_pairs - 1) / (unsigned)max_pairs) * per_unit;
-    const int run = max((int)((unsigned)(total + max_pairs - 1) / (unsigned)max_pairs), kI8MinStages);
-    // (estimates need no exact quotients)
-    const int cut = run + (run >= 2 * per_unit ? 3 : 8 + c32 * ((int)__fdividef((float)per_unit, (float)run) + 3) * 5 / 8);
-    grain = whole <= cut ? per_unit : 1;
-    pairs = min(max_pairs, grain > 1 || per_unit == 1 ? units : (total + kI8MinStages - 1) / kI8MinStages);
-    if (units > 0 && 2 * units <= max_pairs && per_unit > 1) {
-      const float each = (float)per_unit;
-      int n = min((int)__fdividef((float)max_pairs + 0.5f, (float)units),
-                  max(2, (int)(sqrtf(__fdividef(1.6f * each, (float)c32)) + 0.5f)));
-      if (n * units > max_pairs) --n;
-      n = min(n, per_unit);
-      if ((int)__fdividef(each, (float)n) + 5 + c32 * n * 5 / 8 < min(whole, cut)) {
-        parts = n;
-        grain = 1;
-        pairs = units * n;
-      }
-    }
-    const int items = parts > 0 ? per_unit : grain > 1 ? units : total, to = parts > 0 ? parts : pairs;
-    q = to > 0 ? (int)((unsigned)items / (unsigned)to) : 0;
-    r = items - q * to;
-  }
-  // pair b's run
-  MXG_DEVINL void run(int b, int& s, int& end) const {
-    const int u = parts > 0 ? (int)((unsigned)b / (unsigned)parts) : 0, i = b - u * parts;
-    s = u * per_unit + (i * q + min(i, r)) * grain;
-    end = s + (q + (i < r)) * grain;
-  }
-  // the first and the last pair of a cut unit
-  MXG_DEVINL int owner(int s) const { return s < r * (q + 1) ? s / (q + 1) : r + (s - r * (q + 1)) / q; }
-  MXG_DEVINL int first(int unit) const { return parts > 0 ? unit * parts : owner(unit * per_unit); }
-  MXG_DEVINL int last(int unit) const { return parts > 0 ? unit * parts + parts - 1 : owner(unit * per_unit + per_unit - 1); }
 };
 
 // Tokens that the MMAs of a tile take: its own, to a multiple of 16 (half of them
@@ -632,7 +585,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
 
   const int units = bad ? 0 : tile[p.G];
   const int pair = (int)ptx::cluster_id_x(), pairs = (int)ptx::nclusters_x();
-  const I8Runs runs(units, p.nk, units > 0 ? off[p.G] / (units / p.n_chan) : 0, pairs);
+  const I8Runs runs(units, p.nk, units > 0 ? off[p.G] / (units / p.n_chan) : 0, pairs);  // (the mean rows of a tile)
   I8Walker<kTok, L::kCut> w;
   if constexpr (L::kCut) {
     w.s = w.end = 0;
@@ -877,7 +830,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
       };
       int first = 0, last = -1;  // the pairs of a cut unit
       if (!whole) {
-        float* mine = p.part + ((int64_t)(4 * pair + 2 * (w.k0 == 0) + rank) * kTok) * kChan + quarter * 32 + lane;
+        float* mine = p.part + (int64_t)(2 * I8Runs::buffer(pair, w.k0 == 0) + rank) * kTok * kChan + quarter * 32 + lane;
         for (int c0 = 0; c0 < w.n; c0 += kCols) {
           float v[kCols];
           read(c0, v);
@@ -889,7 +842,7 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
         __threadfence();
         __syncwarp();
         uint32_t got = 0;
-        if (lane == 0) got = atomicInc(p.sync + (first + 1) * 8 + rank * 4 + quarter, (uint32_t)(last - first));
+        if (lane == 0) got = atomicInc(p.sync + I8Runs::counter(first) + rank * 4 + quarter, (uint32_t)(last - first));
         got = __shfl_sync(kFull, got, 0);
         if (got != (uint32_t)(last - first)) continue;
         __threadfence();
@@ -901,10 +854,10 @@ __global__ void __launch_bounds__(I8Cfg<kTok>::kThreads, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < kCols; ++i) v[i] = 0.0f;
-          // in run order: buffers 2 first + 1, 2 (first + 1), ...; two of them in flight
+          // in run order, the first pair's from the unit's start; two of them in flight
           for (int b = first; b <= last; b += 2) {
-            const float* s0 = p.part + ((int64_t)(4 * b + 2 * (b == first) + rank) * kTok + c0) * kChan + quarter * 32 + lane;
-            const float* s1 = p.part + ((int64_t)(4 * (b + 1) + rank) * kTok + c0) * kChan + quarter * 32 + lane;
+            const float* s0 = p.part + ((int64_t)(2 * I8Runs::buffer(b, b == first) + rank) * kTok + c0) * kChan + quarter * 32 + lane;
+            const float* s1 = p.part + ((int64_t)(2 * I8Runs::buffer(b + 1, false) + rank) * kTok + c0) * kChan + quarter * 32 + lane;
             float a0[kCols], a1[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) a0[i] = c0 + i < w.n ? __ldcg(s0 + i * kChan) : 0.0f;
@@ -1078,7 +1031,7 @@ I8Ws i8_ws(int64_t S, int G, int64_t N, int64_t K, int codes, uint8_t* p) {
   };
   if (f.cut) {
     w.sync = reinterpret_cast<uint32_t*>(take(kI8SyncWords * 4));
-    w.part = reinterpret_cast<float*>(take((int64_t)4 * kI8MaxPairs * f.tok * kChan * 4));
+    w.part = reinterpret_cast<float*>(take((int64_t)2 * I8Runs::buffer(kI8MaxPairs, false) * f.tok * kChan * 4));
   }
   if (codes == MXG_CODES_INT8) w.wide = take(S * K * 2);
   w.total = std::max<size_t>(o, 256);
