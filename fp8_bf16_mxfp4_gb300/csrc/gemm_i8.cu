@@ -958,39 +958,62 @@ double i8_cost(int form, int64_t S, int G, int64_t N, int64_t K) {
   return 7.2 + kStage[form] * stages + kUnit[form] * units / kPairs;
 }
 
-// The most rows of the mean expert that has some for which the few-rows form is taken.
-// It reads an expert's weights once for every tile of its rows, widens them once for
-// every 8, and ends with its fullest expert, which routing makes the fuller the more
-// experts there are.  us in this form and in the next one, rows at random where there are
-// several experts (at mean rows):
-//   up to 8 experts: 8 (8 of 6, 4096 x 7168: 45.9, 54.5, of 8: 54.4, 54.5); above: 4
-//     (32 of 4, 4096 x 7168: 179.7, 179.4, of 2: 138, 159; 64 of 5, 1024 x 1024: 28.4, 23.0);
-//   tiles of 8 alone, where 16 rows do not fit: one expert's 8 (4096 x 14336: 20.1, 23.0;
-//     9 rows 28.5, 22.9), else 6 (8 of 6, 4096 x 14336: 84.3, 95.4, of 7: 107, 96; 32 of 6:
-//     322, 345); 16 of one expert of 20 MB (1024 x 16384: 15.1, 16.7; 4096 x 11264: 24.3, 20.5);
-//   tiles of 16 and few experts, 16, 14 or 12, where an expert's weights are small: 60 MB
-//     of one or two (16 rows, 14336 x 4096: 19.8, 22.2, 8192 x 8192: 25.9, 23.9; two of 14,
-//     14336 x 4096: 31.5, 32.8, 28672 x 8192: 101.6, 95.4), 16 MB of three or four (three of 12,
-//     2048 x 2048: 10.3, 12.6, 11008 x 2048: 28.9, 23.4; four of 12, 2048 x 7168: 22.7, 23.2).
-// Over 463 such products 1.1 % slower than the faster of the two in the geometric mean.
-int few_most(int64_t used, int tok, int64_t N, int64_t K) {
-  const int64_t weights = N * K;
-  if (used == 1 && tok == 8) return weights <= 20'000'000 ? 16 : 8;
-  if (tok == 8) return 6;
-  if (used <= 2 && weights <= 60'000'000) return used == 1 ? 16 : 14;
-  if (used > 2 && used <= 4 && weights <= 16'000'000) return 12;
-  return used <= 8 ? 8 : 4;
+// Warps of a unit in the few-rows form: all, or fewer where that leaves a warp less than
+// its loads in flight and there are units for every CTA all the same.
+int few_split(int64_t S, int G, int64_t N, int64_t K, int num_sms) {
+  const int64_t units = std::max<int64_t>(1, std::min<int64_t>(S, G)) * cdiv(N, kFewChan);
+  int split = kFewWarps;
+  while (split > 1 && cdiv(K, 128) < split * kFewDepth && units >= 2 * (int64_t)num_sms * (2 * kFewWarps / split)) split /= 2;
+  return split;
 }
 
-// The form for S rows over G experts: the few-rows form (-1) up to few_most rows of the
-// mean expert that has some; above, what takes the least time.
+// Microseconds in the few-rows form, in tiles of `tok` rows, as they compare with
+// i8_cost: the iterations of the longest run of units, without the weights' stream,
+// which is the same in all forms.  Rows fall to experts at random (Poisson); more than 8
+// of a tile of 16 are widened and multiplied twice, and a run inside one expert's channels
+// is as slow as that expert's.  A run that ends in another expert than it began (never
+// where the SMs are a multiple of the tiles) starts its loads again.
+double few_cost(int64_t S, int G, int64_t N, int64_t K, int tok) {
+  constexpr int kSms = 152;
+  double tiles = (double)cdiv(S, tok), over = S > 8, over_used = over;  // over: the share of experts with more than 8 rows
+  if (G > 1) {
+    const double mean = (double)S / G, none = std::exp(-mean);
+    double p = none;
+    tiles = over = 0;
+    for (int i = 1; i < 64; ++i) {
+      p *= mean / i;
+      tiles += G * p * ((i + tok - 1) / tok);
+      if (i > 8) over += p;
+    }
+    over_used = over / (1 - none);
+  }
+  const int split = few_split(S, G, N, K, kSms), at_once = kFewWarps / split;
+  const int64_t turns = cdiv(cdiv(K, 128), split), slots = cdiv(turns, kFewDepth) * kFewDepth;
+  const double chans = (double)cdiv(N, kFewChan), run = std::max(1.0, std::ceil(std::max(1.0, tiles) * chans / kSms - 0.02));
+  double iters, two = over_used;
+  if (tiles <= 1 && G == 1) {
+    iters = std::ceil(run / at_once);
+  } else if (run <= chans) {
+    const bool ends_elsewhere = kSms % std::max<int64_t>(1, std::llround(tiles)) != 0;
+    iters = std::max(1.0, run / at_once + 0.48 + (ends_elsewhere ? 0.75 : 0.0));
+    if (G > 1) two = 1 - std::pow(1 - over, 0.42 * G);
+  } else {
+    iters = run / chans * std::ceil(chans / at_once);
+  }
+  if (tok == 8) two = 0;
+  return 3.0 + iters * (at_once * (0.14 + 0.097 * two) + 0.11 * slots + (0.58 + 0.31 * two) * turns);
+}
+
+// The form for S rows over G experts: what takes the least time by these estimates, the
+// few-rows form (-1) up to a mean of 16 rows for an expert that has some.  Of 2855
+// products of 1 to 16 rows for each of 1 to 256 experts the form so chosen is 0.7 % slower
+// than the faster of the two in the geometric mean, 65 of them by more than 10 % (with a
+// limit of 8 to 16 rows for any size 3.6 %).  Both sides, this form and the next: 12
+// rows, 4096 x 14336 (tiles of 8): 27.5 us, 22.9; 8 rows 20.1, 23.0; three experts of 12,
+// 11008 x 2048: 28.9, 23.4, 2048 x 2048: 10.3, 12.6; 8 of 6, 4096 x 7168: 46, 55; 64 of 5,
+// 1024 x 1024: 28.4, 23.0; 22 of 4, 96 x 2336: 6.4, 13.0.
 constexpr int kFew = -1;
 int i8_choose(int64_t S, int G, int64_t N, int64_t K) {
-  const int64_t used = std::max<int64_t>(1, std::min<int64_t>(S, G)), mean = (S + used - 1) / used;
-  if (mean <= 16 && K <= 0x7FFFFF) {
-    const int tok = few_tok(S, K);
-    if (tok > 0 && mean <= few_most(used, tok, N, K)) return kFew;
-  }
   thread_local int64_t of[4] = {};  // a call asks for its form several times
   thread_local int best = 0;
   if (of[0] != S || of[1] != G || of[2] != N || of[3] != K) {
@@ -1003,6 +1026,9 @@ int i8_choose(int64_t S, int G, int64_t N, int64_t K) {
         best = i;
       }
     }
+    const int64_t used = std::max<int64_t>(1, std::min<int64_t>(S, G));
+    const int tok = K <= 0x7FFFFF && S <= 16 * used ? few_tok(S, K) : 0;
+    if (tok > 0 && (S == 0 || few_cost(S, G, N, K, tok) < least)) best = kFew;
     of[0] = S;
     of[1] = G;
     of[2] = N;
@@ -1128,11 +1154,7 @@ mxg_status launch_int8_few(const Int8GemmArgs& a, cudaStream_t stream, int num_s
   p.G = a.G; p.S = (int)a.S; p.N = (int)a.N; p.K = (int)a.K;
   p.tok = few_tok(a.S, a.K);
   p.per_tile = (int)cdiv(a.N, kFewChan);
-  // all warps on a unit, or fewer where that leaves a warp less than its loads in
-  // flight and there are units for every CTA all the same
-  const int64_t units = std::max<int64_t>(1, std::min<int64_t>(a.S, a.G)) * cdiv(a.N, kFewChan);
-  p.split = kFewWarps;
-  while (p.split > 1 && cdiv(a.K, 128) < p.split * kFewDepth && units >= 2 * (int64_t)num_sms * (2 * kFewWarps / p.split)) p.split /= 2;
+  p.split = few_split(a.S, a.G, a.N, a.K, num_sms);
   p.a = a.a; p.ld_a = a.ld_a; p.f16 = a.codes == MXG_CODES_F16; p.sa = a.sa;
   p.w = a.w; p.ld_w = a.ld_w; p.sw = a.sw;
   p.out = a.out; p.ld_out = a.ld_out; p.out_f32 = a.out_dtype == MXG_OUT_F32;

@@ -662,7 +662,7 @@ mxg_status int8_quantize_rowwise(const void* x, int64_t ld_x, const int32_t* row
  *   out : [S, N] of out_dtype, row stride ld_out; rows 16-byte aligned; N % 8 == 0
  *   ws  : at least int8_gemm_workspace_size(G, S, N, K, A->codes) bytes, 256-byte aligned
  * Splits are checked as for grouped_gemm_fwd (MXG_ERR_SPLITS; nothing is written).
- * Few rows (a mean of up to 4 to 16 for an expert, by sizes; K <= 17280) run on single
+ * Few rows (a mean of up to 16 for an expert, by sizes; K <= 17280) run on single
  * CTAs, others on CTA pairs (mxg_diag_int8_tile_tokens); mxg_set_gemm_cta_group has no
  * effect on either.  Sizes whose count of tiles does not fit 32 bits are refused
  * (MXG_ERR_SHAPE; int8_gemm_workspace_size returns 0).

@@ -22,10 +22,10 @@ def mxg():
 
 CASES = [  # splits, N, K, rows of a tile (0: of the tensor-core forms, 32 and more)
     ([57, 0, 0, 3, 0, 0, 4, 0], 264, 272, 16), ([0] * 31 + [100], 1096, 1040, 16), ([128] + [0] * 31, 520, 272, 16),
-    ([33, 0, 1], 4104, 528, 16), ([0, 0, 36], 8, 16, 16), ([9, 7, 8, 24, 0, 0, 0, 16], 2056, 2064, 16),
+    ([33, 0, 1], 2056, 2064, 16), ([0, 0, 36], 8, 16, 16), ([9, 7, 8, 24, 0, 0, 0, 16], 1032, 2064, 16),
     ([1, 17, 0, 30], 1096, 656, 16), ([25, 3], 72, 7168, 16), ([17, 0, 2, 0, 0, 1, 0, 4], 136, 14336, 8),
     ([0, 31, 0, 17, 0, 0, 0, 0], 1032, 9008, 8), ([12], 264, 14336, 8), ([16], 1048, 16384, 8), ([9], 40, 17280, 8),
-    ([12], 4096, 14336, 0), ([33, 0, 1], 136, 14336, 0), ([5], 136, 17296, 0)]
+    ([12], 4096, 14336, 0), ([33, 0, 1], 136, 14336, 8), ([33, 0, 1], 136, 17296, 0), ([5], 136, 17296, 0)]
 
 
 @pytest.mark.parametrize("splits,N,K,tile", CASES)
