@@ -234,8 +234,8 @@ MXG_DEVINL uint32_t pack_bf16(float lo, float hi) {
 // mma.sync makes 974 products of FP16 codes a clock and SM (of 8-bit integers 255, as
 // does dp4a), of which 8 rows at the rate of memory need 190: bound by HBM.
 // 128 rows of 32 experts, 4096 x 7168: 155 us, 6.1 TB/s (167 with dp4a, 184 in the
-// form for more rows); 1 row, 28672 x 8192: 43 us, of which 6 are start and end; 1
-// row, 4096 x 7168: 11 us.  Loads of 32 bytes a lane, 8 warps with twice the loads in
+// form for more rows; 180 where one expert has 9 rows); 1 row, 28672 x 8192: 43 us, of
+// which 6 are start and end; 1 row, 4096 x 7168: 11 us.  Loads of 32 bytes a lane, 8 warps with twice the loads in
 // flight, and joins that no warp waits for measured the same or worse.
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 512;
@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) int8_few_kernel(const FewParam
 //   warp 10      waits for the issuer (cut form);
 //   warps 10-13  epilogue (whole tiles): with one accumulator the next tile waits
 //                for it (1024 rows of 32 experts each, 2048 x 1024: 97 us, 119 with four
-//                warps; x 2048, 4096 channels: 302, 306).
+//                warps; x 2048, 4096 channels: 302, 306; 14 warps leave 128 registers a
+//                thread, of which 60 bytes spill).
 // Cut form: the stages of all units (expert, channel tile, row tile) are cut into one
 // equal run per pair, so that every SM streams the same number of weight bytes; cut
 // units are joined through fp32 partials, added in run order by the last to arrive.

@@ -139,9 +139,10 @@ cudaError_t launch_route(const TIn* logits, int64_t T, int E, int64_t ld, int k,
 // An expert that is named twice (its lanes do not read back what they wrote) gets both
 // in the order of the slots.  p is made as the forward makes it: a logit of -inf or NaN
 // has 0, one that equals the maximum exp(0).  Bound by issue and latency: 16384 tokens
-// of 256 experts, 34 MB, 8.4 us (12.2 with every slot offered to every expert in
-// registers and a maximum of shuffles); 77 tokens 2.1 us, a launch.  Two or four tokens
-// of a warp at once: 12.8 and 17; two experts in one load: 8.4, with BF16 12.1 for 9.7.
+// of 256 experts, 34 MB, 8.2 us (12.2 with every slot offered to every expert in
+// registers and a maximum of shuffles), with weights over the chosen experts 5.7; 77
+// tokens 2.1 us, a launch.  Two or four tokens of a warp at once: 12.8 and 17; two
+// experts in one load: the same, with BF16 12.1 for 9.6.
 // ---------------------------------------------------------------------------
 MXG_DEVINL void store_grad(float* p, float v) { *p = v; }
 MXG_DEVINL void store_grad(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }

@@ -563,7 +563,8 @@ mxg_status lora_add(const void* y, int64_t ld_y, const void* x, int64_t ld_x, co
  * rows of each expert, as the grouped GEMMs and quantizers take them.  A slot with
  * a negative id is empty: it owns one of the rows behind all experts' slots, r
  * (again in order), and its entry is -1 - r.  The last expert's split counts these
- * rows, so that the splits add up to P; the calls below keep them zero.
+ * rows, so that the splits add up to P; the calls below keep them zero (and the
+ * products multiply them as any other row).
  *   ids      : int32 [tokens, top_k] contiguous
  *   m_splits : int32 [experts]; rows: int32 [tokens, top_k] contiguous
  *   ws       : at least moe_sort_workspace_size(...) bytes, 256-byte aligned
