@@ -981,7 +981,7 @@ double few_cost(int64_t S, int G, int64_t N, int64_t K, int tok) {
     const double mean = (double)S / G, none = std::exp(-mean);
     double p = none;
     tiles = over = 0;
-    for (int i = 1; i < 64; ++i) {
+    for (int i = 1; i < mean || p > 1e-7; ++i) {
       p *= mean / i;
       tiles += G * p * ((i + tok - 1) / tok);
       if (i > 8) over += p;
